@@ -12,10 +12,14 @@ Names and semantics follow include/qlora.h:
     qlora_linear_bwd_multi, qlora_merge_workspace_bytes, qlora_merge,
     qlora_noalloc_scratch_bytes, qlora_linear_fwd_noalloc, qlora_workspace_bytes_flags,
     nf4_quantize_weight_nodq, nf4_code_buckets,
+    qlora_fp8_storage_bytes, qlora_fp8_quantize, qlora_fp8_quantize_weight, qlora_fp8_dequantize,
+    qlora_fp8_workspace_bytes, qlora_fp8_linear_fwd, qlora_fp8_linear_bwd,
+    qlora_moe_route, qlora_moe_route_bwd, qlora_moe_workspace_bytes, qlora_moe_fwd,
     nf4_codebook, nf4_code_thresholds, qlora_status_string
 """
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 
@@ -116,6 +120,35 @@ _lib.nf4_code_thresholds.argtypes = [ctypes.POINTER(ctypes.c_float)]
 _lib.nf4_code_thresholds.restype = None
 _lib.qlora_status_string.argtypes = [ctypes.c_int]
 _lib.qlora_status_string.restype = ctypes.c_char_p
+
+
+class _FP8WeightC(ctypes.Structure):
+    _fields_ = [("codes", _p), ("scales", _p), ("rows", _i64), ("cols", _i64), ("flags", ctypes.c_uint32)]
+
+
+_lib.qlora_fp8_storage_bytes.argtypes = [_i64, _i64, ctypes.POINTER(_sz), ctypes.POINTER(_sz)]
+_lib.qlora_fp8_storage_bytes.restype = ctypes.c_int
+_lib.qlora_fp8_quantize.argtypes = [_p, _i64, _i64, _p, _p, _p]
+_lib.qlora_fp8_quantize.restype = ctypes.c_int
+_lib.qlora_fp8_dequantize.argtypes = [_p, _p, _i64, _i64, _p, _p]
+_lib.qlora_fp8_dequantize.restype = ctypes.c_int
+_lib.qlora_fp8_workspace_bytes.argtypes = [_i64, _i64, _i64, _i64, ctypes.c_int]
+_lib.qlora_fp8_workspace_bytes.restype = _sz
+_lib.qlora_fp8_linear_fwd.argtypes = [ctypes.POINTER(_FP8WeightC), _p, _i64, _p, _p, _i64, ctypes.c_float,
+                                      _p, _p, _sz, _p]
+_lib.qlora_fp8_linear_fwd.restype = ctypes.c_int
+_lib.qlora_fp8_linear_bwd.argtypes = [ctypes.POINTER(_FP8WeightC), _p, _p, _i64, _p, _p, _i64, ctypes.c_float,
+                                      _p, _p, _p, _p, _sz, _p]
+_lib.qlora_fp8_linear_bwd.restype = ctypes.c_int
+_lib.qlora_moe_route.argtypes = [_p, _i64, _i64, _i64, ctypes.c_int, _p, _p, _p]
+_lib.qlora_moe_route.restype = ctypes.c_int
+_lib.qlora_moe_route_bwd.argtypes = [_p, _p, _p, _i64, _i64, _i64, ctypes.c_int, _p, _p]
+_lib.qlora_moe_route_bwd.restype = ctypes.c_int
+_lib.qlora_moe_workspace_bytes.argtypes = [_i64, _i64, _i64, _i64]
+_lib.qlora_moe_workspace_bytes.restype = _sz
+_lib.qlora_moe_fwd.argtypes = [ctypes.POINTER(_NF4WeightC), ctypes.POINTER(_NF4WeightC), _i64, _p, _i64, _p, _p,
+                               _i64, _p, _p, _sz, _p]
+_lib.qlora_moe_fwd.restype = ctypes.c_int
 
 
 def _status_string(status: int) -> str:
@@ -521,3 +554,256 @@ def nf4_code_thresholds():
     out = (ctypes.c_float * 15)()
     _lib.nf4_code_thresholds(out)
     return [float(v) for v in out]
+
+
+# ---------------------------------------------------------------------------
+# The 8-bit linear layer and the mixture-of-experts operators.  Every tensor of
+# a call lies on one GPU, which becomes the current one for the call; the work
+# goes to that GPU's current stream.
+# ---------------------------------------------------------------------------
+@dataclass
+class FP8Weight:
+    """Frozen 8-bit weight [rows = out_features, cols = in_features]: e4m3
+    codes, one power-of-two scale byte per 128 x 128 block."""
+    codes: torch.Tensor   # uint8 [rows, cols]
+    scales: torch.Tensor  # uint8 [ceil(rows/128), ceil(cols/128)]
+    rows: int
+    cols: int
+
+    def _c(self):
+        return _FP8WeightC(self.codes.data_ptr(), self.scales.data_ptr(), self.rows, self.cols, 0)
+
+
+def _arg(t, dtype, shape, name: str, dev):
+    """A contiguous tensor of this type, device and number of elements
+    (shape: its sizes, or its element count)."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.device != dev or dev.type != "cuda":
+        raise ValueError(f"{name}: on {t.device}, the call runs on {dev} (a GPU is needed)")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+    if isinstance(shape, int):
+        if t.numel() != shape:
+            raise ValueError(f"{name}: expected {shape} elements, got {t.numel()}")
+    elif tuple(t.shape) != shape:
+        raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
+
+
+def _matrix(t, name: str):
+    """(rows, cols) of a 2-D tensor."""
+    if t.dim() != 2:
+        raise ValueError(f"{name}: must be 2-D, got {t.dim()}-D")
+    return t.shape
+
+
+def _on(dev, fn, where: str, *args):
+    """Calls fn(*args, stream) with dev current, on dev's current stream."""
+    if torch.cuda.current_device() == dev.index:
+        st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    if st != QLORA_OK:
+        raise QloraError(st, where)
+
+
+_SCRATCH = {}
+
+
+def _scratch(ws, need: int, where: str, dev):
+    """The caller's workspace, or one kept per (device, stream).  Under graph
+    capture it is a new allocation of the graph's own pool: a replay then
+    shares no scratch with eager calls or with other graphs."""
+    if ws is not None:
+        if ws.device != dev:
+            raise ValueError(f"ws: on {ws.device}, the call runs on {dev}")
+        if not ws.is_contiguous():
+            raise ValueError("ws: must be contiguous")
+        return ws
+    if need == 0:  # refused shapes: the library says why
+        return make_workspace(256, dev)
+    if torch.cuda.is_current_stream_capturing():
+        return make_workspace(need, dev)
+    key = (dev.index, torch.cuda.current_stream(dev).cuda_stream)
+    ws = _SCRATCH.get(key)
+    if ws is None or ws.numel() < need:
+        ws = make_workspace(need, dev)
+        _SCRATCH[key] = ws
+    return ws
+
+
+def qlora_fp8_storage_bytes(rows: int, cols: int):
+    c, s = _sz(), _sz()
+    _check(_lib.qlora_fp8_storage_bytes(rows, cols, ctypes.byref(c), ctypes.byref(s)), "qlora_fp8_storage_bytes")
+    return c.value, s.value
+
+
+def qlora_fp8_quantize(w: torch.Tensor, codes=None, scales=None):
+    """fp32 device tensor [rows, cols] (multiples of 64) -> (codes uint8 [rows,
+    cols], scales uint8 [ceil(rows/128), ceil(cols/128)])."""
+    rows, cols = _matrix(w, "w")
+    dev = w.device
+    _arg(w, torch.float32, rows * cols, "w", dev)
+    qlora_fp8_storage_bytes(rows, cols)  # refuses other sizes
+    grid = (-(-rows // 128), -(-cols // 128))
+    if codes is None:
+        codes = torch.empty(rows, cols, dtype=torch.uint8, device=dev)
+    if scales is None:
+        scales = torch.empty(grid, dtype=torch.uint8, device=dev)
+    _arg(codes, torch.uint8, rows * cols, "codes", dev)
+    _arg(scales, torch.uint8, grid[0] * grid[1], "scales", dev)
+    _on(dev, _lib.qlora_fp8_quantize, "qlora_fp8_quantize", w.data_ptr(), rows, cols, codes.data_ptr(),
+        scales.data_ptr())
+    return codes, scales
+
+
+def qlora_fp8_quantize_weight(w: torch.Tensor) -> FP8Weight:
+    """Quantizes a [out, in] fp32 weight into an FP8Weight."""
+    codes, scales = qlora_fp8_quantize(w)
+    return FP8Weight(codes, scales, w.shape[0], w.shape[1])
+
+
+def qlora_fp8_dequantize(codes, scales, rows: int, cols: int, out=None):
+    """-> bf16 device tensor [rows, cols]."""
+    dev = codes.device
+    _, sb = qlora_fp8_storage_bytes(rows, cols)
+    _arg(codes, torch.uint8, rows * cols, "codes", dev)
+    _arg(scales, torch.uint8, sb, "scales", dev)
+    if out is None:
+        out = torch.empty(rows, cols, dtype=torch.bfloat16, device=dev)
+    _arg(out, torch.bfloat16, rows * cols, "out", dev)
+    _on(dev, _lib.qlora_fp8_dequantize, "qlora_fp8_dequantize", codes.data_ptr(), scales.data_ptr(), rows, cols,
+        out.data_ptr())
+    return out
+
+
+@functools.lru_cache(maxsize=4096)
+def qlora_fp8_workspace_bytes(T: int, in_features: int, out_features: int, r: int, backward: bool) -> int:
+    return int(_lib.qlora_fp8_workspace_bytes(T, in_features, out_features, r, 1 if backward else 0))
+
+
+def _fp8_args(W, X, A, B, r, dev, T):
+    blocks = -(-W.rows // 128) * -(-W.cols // 128)
+    _arg(W.codes, torch.uint8, W.rows * W.cols, "W.codes", dev)
+    _arg(W.scales, torch.uint8, blocks, "W.scales", dev)
+    if r > 0:
+        _arg(A, torch.bfloat16, r * W.cols, "A", dev)
+        _arg(B, torch.bfloat16, W.rows * r, "B", dev)
+
+
+def qlora_fp8_linear_fwd(W: FP8Weight, X, A, B, r: int, alpha: float, Y=None, ws=None):
+    """Y [T, out] bf16 = X_hat W_hat^T + (alpha/r) (X A^T) B^T, X_hat = X
+    quantized per row and 128 columns; r = 0: no adapter (A, B None)."""
+    T, _ = _matrix(X, "X")
+    dev = X.device
+    _arg(X, torch.bfloat16, (T, W.cols), "X", dev)
+    _fp8_args(W, X, A, B, r, dev, T)
+    if Y is None:
+        Y = torch.empty(T, W.rows, dtype=torch.bfloat16, device=dev)
+    _arg(Y, torch.bfloat16, T * W.rows, "Y", dev)
+    ws = _scratch(ws, qlora_fp8_workspace_bytes(T, W.cols, W.rows, r, False), "qlora_fp8_linear_fwd", dev)
+    _on(dev, _lib.qlora_fp8_linear_fwd, "qlora_fp8_linear_fwd", ctypes.byref(W._c()), X.data_ptr(), T,
+        A.data_ptr() if r > 0 else None, B.data_ptr() if r > 0 else None, r, float(alpha), Y.data_ptr(),
+        ws.data_ptr(), ws.numel() * ws.element_size())
+    return Y
+
+
+def qlora_fp8_linear_bwd(W: FP8Weight, X, dY, A, B, r: int, alpha: float, dX=None, dA=None, dB=None, ws=None):
+    """-> (dX [T, in] bf16, dA [r, in] fp32, dB [out, r] fp32); r = 0: (dX,
+    None, None), and X, A, B may be None."""
+    T, _ = _matrix(dY, "dY")
+    dev = dY.device
+    _arg(dY, torch.bfloat16, (T, W.rows), "dY", dev)
+    if r > 0:
+        _arg(X, torch.bfloat16, (T, W.cols), "X", dev)
+    _fp8_args(W, X, A, B, r, dev, T)
+    if dX is None:
+        dX = torch.empty(T, W.cols, dtype=torch.bfloat16, device=dev)
+    _arg(dX, torch.bfloat16, T * W.cols, "dX", dev)
+    if r > 0:
+        if dA is None:
+            dA = torch.empty(r, W.cols, dtype=torch.float32, device=dev)
+        if dB is None:
+            dB = torch.empty(W.rows, r, dtype=torch.float32, device=dev)
+        _arg(dA, torch.float32, r * W.cols, "dA", dev)
+        _arg(dB, torch.float32, W.rows * r, "dB", dev)
+    else:
+        X = A = B = dA = dB = None
+    ws = _scratch(ws, qlora_fp8_workspace_bytes(T, W.cols, W.rows, r, True), "qlora_fp8_linear_bwd", dev)
+    ptr = (lambda t: t.data_ptr() if t is not None else None)
+    _on(dev, _lib.qlora_fp8_linear_bwd, "qlora_fp8_linear_bwd", ctypes.byref(W._c()), ptr(X), dY.data_ptr(), T,
+        ptr(A), ptr(B), r, float(alpha), dX.data_ptr(), ptr(dA), ptr(dB), ws.data_ptr(),
+        ws.numel() * ws.element_size())
+    return dX, dA, dB
+
+
+def qlora_moe_route(logits, k: int, renormalize: bool = True, ids=None, weights=None):
+    """fp32 logits [T, E] -> (ids int32 [T, k], weights fp32 [T, k]): the k
+    largest (ties to the lower index) and their softmax weights, over the k
+    chosen (renormalize) or over all E."""
+    T, E = _matrix(logits, "logits")
+    dev = logits.device
+    _arg(logits, torch.float32, T * E, "logits", dev)
+    if ids is None:
+        ids = torch.empty(T, max(k, 0), dtype=torch.int32, device=dev)
+    if weights is None:
+        weights = torch.empty(T, max(k, 0), dtype=torch.float32, device=dev)
+    _arg(ids, torch.int32, T * k, "ids", dev)
+    _arg(weights, torch.float32, T * k, "weights", dev)
+    _on(dev, _lib.qlora_moe_route, "qlora_moe_route", logits.data_ptr(), T, E, k, 1 if renormalize else 0,
+        ids.data_ptr(), weights.data_ptr())
+    return ids, weights
+
+
+def qlora_moe_route_bwd(logits, ids, dweights, renormalize: bool = True, dlogits=None):
+    """-> dlogits fp32 [T, E] for the gradient dweights [T, k] of the weights."""
+    T, E = _matrix(logits, "logits")
+    _, k = _matrix(ids, "ids")
+    dev = logits.device
+    _arg(logits, torch.float32, T * E, "logits", dev)
+    _arg(ids, torch.int32, (T, k), "ids", dev)
+    _arg(dweights, torch.float32, (T, k), "dweights", dev)
+    if dlogits is None:
+        dlogits = torch.empty(T, E, dtype=torch.float32, device=dev)
+    _arg(dlogits, torch.float32, T * E, "dlogits", dev)
+    _on(dev, _lib.qlora_moe_route_bwd, "qlora_moe_route_bwd", logits.data_ptr(), ids.data_ptr(),
+        dweights.data_ptr(), T, E, k, 1 if renormalize else 0, dlogits.data_ptr())
+    return dlogits
+
+
+@functools.lru_cache(maxsize=4096)
+def qlora_moe_workspace_bytes(T: int, hidden: int, inter: int, k: int) -> int:
+    return int(_lib.qlora_moe_workspace_bytes(T, hidden, inter, k))
+
+
+def _nf4_arg(W, name, dev):
+    n = W.rows * W.cols
+    _arg(W.codes, torch.uint8, n // 2, name + ".codes", dev)
+    if W.flags == 0:
+        _arg(W.absmax_q, torch.uint8, n // 64, name + ".absmax_q", dev)
+        _arg(W.absmax_scale, torch.float32, -(-n // 16384), name + ".absmax_scale", dev)
+
+
+def qlora_moe_fwd(gate_up: NF4Weight, down: NF4Weight, experts: int, X, ids, weights, Y=None, ws=None):
+    """Y [T, hidden] bf16: the expert layer for up to 64 tokens, Y_t = sum_j
+    weights[t, j] Wd_e (silu(Wg_e x_t) * (Wu_e x_t)), e = ids[t, j].  gate_up
+    [experts * 2 * inter, hidden] (an expert's gate rows, then its up rows),
+    down [experts * hidden, inter]; an id outside [0, experts) adds nothing."""
+    T, _ = _matrix(X, "X")
+    _, k = _matrix(ids, "ids")
+    dev = X.device
+    hidden, inter = gate_up.cols, down.cols
+    _arg(X, torch.bfloat16, (T, hidden), "X", dev)
+    _arg(ids, torch.int32, (T, k), "ids", dev)
+    _arg(weights, torch.float32, (T, k), "weights", dev)
+    _nf4_arg(gate_up, "gate_up", dev)
+    _nf4_arg(down, "down", dev)
+    if Y is None:
+        Y = torch.empty(T, hidden, dtype=torch.bfloat16, device=dev)
+    _arg(Y, torch.bfloat16, T * hidden, "Y", dev)
+    ws = _scratch(ws, qlora_moe_workspace_bytes(T, hidden, inter, k), "qlora_moe_fwd", dev)
+    _on(dev, _lib.qlora_moe_fwd, "qlora_moe_fwd", ctypes.byref(gate_up._c()), ctypes.byref(down._c()), experts,
+        X.data_ptr(), T, ids.data_ptr(), weights.data_ptr(), k, Y.data_ptr(), ws.data_ptr(),
+        ws.numel() * ws.element_size())
+    return Y

@@ -178,6 +178,69 @@ hipError_t launch_gemm_nf4t(int64_t M, int64_t N, int nproj, const Nf4Proj* proj
                             const uint8_t* keep = nullptr, int64_t ldk = 0, float keep_scale = 1.f,
                             float* part = nullptr, size_t part_bytes = 0);
 
+// C[m][n] = bf16(sum over z < S of part[z][m][n]), added in order (N % 8 == 0)
+hipError_t launch_split_sum(const float* part, int S, int64_t M, int64_t N, uint16_t* C, int64_t ldc,
+                            hipStream_t s);
+
+// The 8-bit format (fp8_format.hpp).  Weights: codes [rows][cols], scale
+// bytes [ceil(rows / 128)][ceil(cols / 128)].
+hipError_t launch_fp8_quantize(const float* w, int64_t rows, int64_t cols, uint8_t* codes, uint8_t* scales,
+                               hipStream_t s);
+hipError_t launch_fp8_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols,
+                                 uint16_t* out, hipStream_t s);
+// Activations x [T][ldx] (K columns, K % 8 == 0) -> codes [T][K rounded up to
+// 128, the rest zero], scale bytes [T][ldsc] (one per 128 columns).
+hipError_t launch_fp8_rows(const uint16_t* x, int64_t ldx, int64_t T, int64_t K, uint8_t* codes, uint8_t* scales,
+                           int64_t ldsc, hipStream_t s);
+// C [M][N] bf16 = activations (codes, scales as launch_fp8_rows writes them)
+// times the 8-bit weight (not transposed: N = rows, K = cols; transposed: N =
+// cols, K = rows) plus the adapter segment (K1 = 0: none; as in
+// launch_gemm_nt), rounded once.  part: fp8_split_bytes(M, N, K) bytes.
+struct F8Gemm {
+  int64_t M;
+  const uint8_t* codes; const uint8_t* scales;
+  int64_t rows, cols;
+  bool transposed;
+  const uint8_t* xq; const uint8_t* xs;
+  int64_t ldxs;
+  const uint16_t* act1; int64_t lda1;
+  const uint16_t* wt1; int64_t ldw1;
+  int64_t K1;
+  uint16_t* C;
+  float* part;
+};
+int fp8_splits(int64_t M, int64_t N, int64_t K);
+size_t fp8_split_bytes(int64_t M, int64_t N, int64_t K);
+hipError_t launch_fp8_gemm(const F8Gemm& g, hipStream_t s);
+
+// Mixture of experts.  The router: the k largest of each row of logits [T][E]
+// (E <= kMoeMaxExperts, k <= min(kMoeMaxChoices, E)), their weights, and the
+// gradient of the logits.
+constexpr int kMoeMaxExperts = 1024;
+constexpr int kMoeMaxChoices = 16;
+constexpr int kMoeMaxTokens = 64;
+constexpr int kMoeMaxPairs = 512;  // T * k of one expert-layer call
+hipError_t launch_moe_route(const float* logits, int64_t T, int E, int k, bool renorm, int* ids, float* weights,
+                            hipStream_t s);
+hipError_t launch_moe_route_bwd(const float* logits, const int* ids, const float* dw, int64_t T, int E, int k,
+                                bool renorm, float* dlogits, hipStream_t s);
+// The expert layer for a few tokens: gate_up [E * 2 I][H] (expert e's gate
+// rows, then its up rows), down [E * H][I], both double-quantized NF4; h is
+// [T k][2][I] bf16 scratch (hi plane, lo plane of each pair).
+struct MoeWeight {
+  const uint8_t* codes; const uint8_t* absmax_q; const float* scale;
+};
+struct MoeArgs {
+  MoeWeight gate_up, down;
+  const uint16_t* X;
+  const int* ids; const float* weights;
+  uint16_t* h;
+  uint16_t* Y;
+  int T, E, k, H, I;
+  int by_expert;  // set by the launcher
+};
+hipError_t launch_moe(MoeArgs a, hipStream_t s);
+
 // W_merged[m][n] = bf16(W_hat[m][n] + s * sum_j Bp[m][j] Atp[n][j]) for the
 // NF4 weight [out][in] (out % 64 == 0, in % 64 == 0); Bp [out][ldp] and Atp
 // [in][ldp] hold B and A^T zero-padded to rp (a multiple of 16) columns.

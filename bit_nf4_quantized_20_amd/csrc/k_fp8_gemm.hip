@@ -1,0 +1,415 @@
+// k_fp8_gemm.hip -- the 8-bit block-scaled matrix product for gfx950:
+//   C[m][n] = sum_k a_hat[m][k] w_hat[n][k]  +  sum_j act1[m][j] wt1[n][j]
+// a_hat: e4m3 codes with a power-of-two scale per row and 128 columns;
+// w_hat: e4m3 codes with one per 128 x 128 block, read as it is (the forward,
+// n = W's rows) or transposed (dX: n = W's columns, k = its rows).  The second
+// segment is the adapter, as bf16 hi/lo pairs (gemm_tiles / launch_lora_down
+// layouts), added to the same fp32 accumulators before the one rounding.
+//
+// v_mfma_scale_f32_32x32x64_f8f6f4 takes a row scale and a column scale per
+// instruction, so a 128-wide K-step is two matrix instructions with the same
+// scale operands and the scales cost nothing: no per-block rescaling of the
+// accumulators on the vector unit.  The weight tile is the A operand, the
+// activations B, so a lane ends up with four consecutive n of one row m.
+// The matrix cores align an instruction's products before they add them: on
+// normal data that leaves 1.5e-5 of the result's size (measured against 64
+// bits), which does not grow with the number of steps (the accumulators are
+// fp32), against 1.7e-3 for the final rounding to bf16.
+//
+// A 128-column K-step of 8-bit codes is 128 bytes per row, the same tile row
+// that the bf16 kernels use, so tiles are copied straight into LDS with the
+// same swizzle.  Within a K-step the order of k is free as long as both
+// operands agree: a lane takes the 16-byte chunks 4 j + h and 4 j + 2 + h (h =
+// lane / 32) of sub-step j, the conflict-free pattern of the bf16 fragments.
+// The transposed tile is stored as it lies in memory (128 rows of k, BN
+// columns) and its fragments are read with gfx950's transposing LDS loads.
+#include <type_traits>
+
+#include "common.hpp"
+#include "fp8_format.hpp"
+#include "gemm_tiles.hpp"
+#include "nf4_format.hpp"
+
+namespace qlora {
+
+namespace {
+
+constexpr int kStep = kF8Block;           // K codes (and bytes) per step
+constexpr uint32_t kPastEnd = 0x80000000u;
+
+// Weight rows [ROWS] x 128 bytes straight into LDS; the matrix's last K-step
+// may hold only 64 codes per row, whose upper chunks then read as zero.
+template <int ROWS, int NW>
+struct F8Tile {
+  static constexpr int kPerWave = ROWS / 8 / NW;
+  static_assert(kPerWave >= 1 && NW % 2 == 0, "tile rows");
+  __amdgpu_buffer_rsrc_t rs;
+  uint32_t voff[kPerWave];
+  bool upper;  // this lane copies a chunk of columns 64 .. 127
+
+  __device__ __forceinline__ void init(const uint8_t* base, int64_t ld, int64_t row0, int64_t nrows, int wv, int lane) {
+    rs = rows_rsrc(base, ld, row0, nrows, 1);
+#pragma unroll
+    for (int i = 0; i < kPerWave; ++i) {
+      const int row = (i * NW + wv) * 8 + (lane >> 3);
+      voff[i] = static_cast<uint32_t>(row * ld + swz(row, lane & 7) * 16);
+    }
+    upper = swz(wv * 8 + (lane >> 3), lane & 7) >= 4;  // the same for every i (NW is even)
+  }
+  __device__ __forceinline__ void load(uint16_t* lds, int wv, int64_t k0, bool half) const {
+#pragma unroll
+    for (int i = 0; i < kPerWave; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          rs, (__attribute__((address_space(3))) void*)(lds + (i * NW + wv) * 512), 16,
+          half && upper ? kPastEnd : voff[i], static_cast<int>(k0), 0, 0);
+  }
+};
+
+// Transposed weight tile: rows k0 .. k0 + 127 of W, BN of its columns, kept
+// row by row in LDS (BN bytes each).  16-byte chunk c of row k sits at chunk
+// c ^ key(k): a fragment read takes 8 consecutive rows at two adjacent chunks
+// per 32 lanes, and the key spreads those over all 64 banks.
+template <int BN>
+__device__ __forceinline__ int f8t_key(int k) {
+  return BN == 256 ? 2 * (k & 7) : 2 * ((k >> 1) & 3);
+}
+template <int BN, int NW>
+struct F8TileT {
+  static constexpr int kLanesPerRow = BN / 16;
+  static constexpr int kRowsPerCopy = 64 / kLanesPerRow;
+  static constexpr int kPerWave = kStep / kRowsPerCopy / NW;
+  static_assert(BN == 256 || BN == 128, "tile columns");
+  const uint8_t* base;
+  int64_t ld, nrows;
+  uint32_t voff[kPerWave];
+  __device__ __forceinline__ void init(const uint8_t* w, int64_t ldw, int64_t n0, int64_t rows, int wv, int lane) {
+    base = w;
+    ld = ldw;
+    nrows = rows;
+#pragma unroll
+    for (int i = 0; i < kPerWave; ++i) {
+      const int k = (i * NW + wv) * kRowsPerCopy + lane / kLanesPerRow;
+      const int64_t col = n0 + (((lane % kLanesPerRow) ^ f8t_key<BN>(k)) * 16);
+      // columns past the matrix read nothing (their outputs are not stored)
+      voff[i] = col < ldw ? static_cast<uint32_t>(k * ldw + col) : kPastEnd;
+    }
+  }
+  __device__ __forceinline__ void load(uint16_t* lds, int wv, int64_t k0, bool) const {
+    const __amdgpu_buffer_rsrc_t rs = rows_rsrc(base, ld, k0, nrows, 1);  // rows past the last read zero
+#pragma unroll
+    for (int i = 0; i < kPerWave; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          rs, (__attribute__((address_space(3))) void*)(lds + (i * NW + wv) * 512), 16, voff[i], 0, 0, 0);
+  }
+};
+
+__device__ __forceinline__ i32x8 join(u32x4 a, u32x4 b) {
+  return i32x8{static_cast<int>(a[0]), static_cast<int>(a[1]), static_cast<int>(a[2]), static_cast<int>(a[3]),
+               static_cast<int>(b[0]), static_cast<int>(b[1]), static_cast<int>(b[2]), static_cast<int>(b[3])};
+}
+// fragment of row `row` (n or m), sub-step j of an N-row-major tile
+__device__ __forceinline__ i32x8 f8_frag(const uint16_t* lds, int row, int j, int h) {
+  const u32x4 a = *reinterpret_cast<const u32x4*>(lds + row * 64 + swz(row, 4 * j + h) * 8);
+  const u32x4 b = *reinterpret_cast<const u32x4*>(lds + row * 64 + swz(row, 4 * j + 2 + h) * 8);
+  return join(a, b);
+}
+// The same k of columns n0 .. n0 + 31 from a transposed tile.
+// ds_read_b64_tr_b8 hands each group of 16 lanes an 8 x 16 block transposed:
+// lane i of the group supplies the address of row i / 2 at columns 8 (i % 2)
+// .. + 7 and receives column i of the eight rows.
+template <int BN>
+__device__ __forceinline__ i32x8 f8_frag_tr(const uint16_t* lds, int n0, int j) {
+  const int l = threadIdx.x & 63, i = l & 15, G = l >> 4;
+  const int chunk = (n0 >> 4) + (G & 1);
+  i32x8 f;
+#pragma unroll
+  for (int q = 0; q < 2; ++q)     // the two 16-row pieces of this lane's k
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {  // eight rows each
+      const int k = 16 * (4 * j + 2 * q + (G >> 1)) + 8 * s + (i >> 1);
+      const uint8_t* p = reinterpret_cast<const uint8_t*>(lds) + k * BN + ((chunk ^ f8t_key<BN>(k)) << 4) + 8 * (i & 1);
+      const i32x2 v = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+          (__attribute__((address_space(3))) i32x2*)(const_cast<uint8_t*>(p)));
+      f[4 * q + 2 * s] = v[0];
+      f[4 * q + 2 * s + 1] = v[1];
+    }
+  return f;
+}
+
+struct F8Args {
+  int64_t M, N, K;
+  const uint8_t* xq; int64_t ldx;            // activation codes [M][ldx], ldx = K rounded up to 128
+  const uint8_t* xs; int64_t ldxs;           // their scales [M][ldxs], ldxs % 4 == 0
+  const uint8_t* w; int64_t ldw, wrows;      // weight codes [wrows][ldw]
+  const uint8_t* ws; int64_t ws_n, ws_k;     // scale byte of block (n / 128, k / 128): ws[nb ws_n + kb ws_k]
+  int64_t ws_bytes;
+  const uint16_t* act1; int64_t lda1;        // adapter segment (K1 = 0: none)
+  const uint16_t* wt1; int64_t ldw1;
+  int64_t K1;
+  uint16_t* C; int64_t ldc;
+  // split-K: workgroup z takes K-steps [z ks, (z + 1) ks) (ks % 4 == 0), split 0 also the adapter,
+  // and writes fp32 partials part[z][m][n] instead of C
+  float* part; int64_t ks;
+  int64_t gm, gn;                            // output tiles (one flat grid dimension)
+};
+
+}  // namespace
+
+// BM x BN tile, WM x WN waves, K-steps of 128 codes through two LDS stages:
+// step e's copies of step e + 1 are issued first, then the two sub-steps are
+// computed (fragments of the next one read during the current one), then one
+// wait and one barrier.  The scale bytes of four steps sit in one register per
+// activation fragment (op_sel picks the byte) and are fetched four steps ahead.
+template <int BM, int BN, int WM, int WN, bool kTr>
+__global__ __launch_bounds__(64 * WM * WN, 1) void k_fp8_gemm(F8Args p) {
+  constexpr int NW = WM * WN;
+  constexpr int TM = BM / WM, TN = BN / WN, FM = TM / 32, FN = TN / 32;
+  static_assert(TN <= 128 && 128 % TN == 0, "a wave's columns share one scale block");
+  __shared__ __attribute__((aligned(1024))) uint16_t s_act0[BM * 64];
+  __shared__ __attribute__((aligned(1024))) uint16_t s_act1[BM * 64];
+  __shared__ __attribute__((aligned(1024))) uint16_t s_wt0[BN * 64];
+  __shared__ __attribute__((aligned(1024))) uint16_t s_wt1[BN * 64];
+  uint16_t* const s_act[2] = {s_act0, s_act1};
+  uint16_t* const s_wt[2] = {s_wt0, s_wt1};
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wv % WM, wn = wv / WM;
+  int64_t mt, nt;
+  xcd_tile(p.gm, p.gn, mt, nt);
+  const int64_t m0 = mt * BM, n0 = nt * BN;
+  const int r32 = lane & 31, h = lane >> 5;
+
+  f32x16 acc[FN][FM];
+#pragma unroll
+  for (int a = 0; a < FN; ++a)
+#pragma unroll
+    for (int c = 0; c < FM; ++c)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[a][c][e] = 0.f;
+
+  const bool split = p.part != nullptr;
+  const int64_t all = (p.K + kStep - 1) / kStep;
+  const int64_t first = split ? blockIdx.z * p.ks : 0;
+  const int64_t last = split && first + p.ks < all ? first + p.ks : all;  // steps [first, last)
+  const bool odd_tail = p.K % kStep != 0;
+
+  struct Frags { i32x8 w[FN]; i32x8 a[FM]; };
+  auto read_frags = [&](Frags& f, const uint16_t* sw, const uint16_t* sa, int j) {
+#pragma unroll
+    for (int a = 0; a < FN; ++a) {
+      if constexpr (kTr) f.w[a] = f8_frag_tr<BN>(sw, wn * TN + a * 32, j);
+      else f.w[a] = f8_frag(sw, wn * TN + a * 32 + r32, j, h);
+    }
+#pragma unroll
+    for (int c = 0; c < FM; ++c) f.a[c] = f8_frag(sa, wm * TM + c * 32 + r32, j, h);
+  };
+
+  // scales: one dword (four steps) per activation fragment, one byte per step for the weight
+  struct Scales { int a[FM]; int w[4]; };
+  const __amdgpu_buffer_rsrc_t rxs = rows_rsrc(p.xs, p.ldxs, m0, p.M, 1);
+  const __amdgpu_buffer_rsrc_t rws = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<uint8_t*>(p.ws), 0, static_cast<int>(p.ws_bytes < 0x7fffffff ? p.ws_bytes : 0x7fffffff), kBufferWord3);
+  uint32_t xso[FM];
+#pragma unroll
+  for (int c = 0; c < FM; ++c) xso[c] = static_cast<uint32_t>((wm * TM + c * 32 + r32) * p.ldxs);
+  const uint32_t wso = static_cast<uint32_t>((n0 + wn * TN) / kF8Block * p.ws_n);
+  auto load_scales = [&](Scales& s, int64_t e) {  // steps e .. e + 3, e % 4 == 0
+#pragma unroll
+    for (int c = 0; c < FM; ++c)
+      s.a[c] = __builtin_amdgcn_raw_buffer_load_b32(rxs, xso[c] + static_cast<uint32_t>(e), 0, 0);
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      s.w[u] = __builtin_amdgcn_raw_buffer_load_b8(rws, wso + static_cast<uint32_t>((e + u) * p.ws_k), 0, 0);
+  };
+
+  auto mfmas = [&](const Frags& f, const Scales& s, auto uc) {
+    constexpr int U = decltype(uc)::value;
+#pragma unroll
+    for (int a = 0; a < FN; ++a)
+#pragma unroll
+      for (int c = 0; c < FM; ++c)
+        acc[a][c] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(f.w[a], f.a[c], acc[a][c], 0, 0, 0, s.w[U], U,
+                                                                    s.a[c]);
+  };
+
+  if (last > first) {
+    DtlTile<BM, NW> ta;
+    std::conditional_t<kTr, F8TileT<BN, NW>, F8Tile<BN, NW>> tw;
+    ta.init(reinterpret_cast<const uint16_t*>(p.xq), p.ldx / 2, m0, p.M, wv, lane);
+    if constexpr (kTr) tw.init(p.w, p.ldw, n0, p.wrows, wv, lane);
+    else tw.init(p.w, p.ldw, n0, p.wrows, wv, lane);
+    auto copy = [&](int64_t e, uint16_t* sa, uint16_t* sw) {  // steps past the end re-read the last one
+      const int64_t k = (e < last ? e : last - 1);
+      ta.load(sa, wv, k * (kStep / 2));
+      tw.load(sw, wv, k * kStep, odd_tail && k == all - 1);
+    };
+    Scales sc0, sc1;
+    load_scales(sc0, first);
+    copy(first, s_act0, s_wt0);
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();
+    Frags f0, f1;
+    read_frags(f0, s_wt0, s_act0, 0);
+    auto step = [&](int64_t e, const Scales& cur, Scales& nxt, auto uc) {
+      constexpr int U = decltype(uc)::value, B = U & 1;
+      copy(e + 1, s_act[B ^ 1], s_wt[B ^ 1]);
+      if constexpr (U == 0) load_scales(nxt, e + 4);
+      __builtin_amdgcn_s_setprio(1);
+      read_frags(f1, s_wt[B], s_act[B], 1);
+      mfmas(f0, cur, uc);
+      mfmas(f1, cur, uc);
+      __builtin_amdgcn_s_setprio(0);
+      __builtin_amdgcn_s_waitcnt(0);
+      __syncthreads();
+      read_frags(f0, s_wt[B ^ 1], s_act[B ^ 1], 0);
+    };
+    using I0 = std::integral_constant<int, 0>;
+    using I1 = std::integral_constant<int, 1>;
+    using I2 = std::integral_constant<int, 2>;
+    using I3 = std::integral_constant<int, 3>;
+    auto four = [&](int64_t e, const Scales& cur, Scales& nxt) {
+      step(e, cur, nxt, I0{});
+      if (e + 1 < last) step(e + 1, cur, nxt, I1{});
+      if (e + 2 < last) step(e + 2, cur, nxt, I2{});
+      if (e + 3 < last) step(e + 3, cur, nxt, I3{});
+    };
+    for (int64_t e = first; e < last; e += 8) {
+      four(e, sc0, sc1);
+      if (e + 4 < last) four(e + 4, sc1, sc0);
+    }
+  }
+
+  // adapter segment: a few bf16 steps of 64 through stage 0
+  if (p.K1 > 0 && (!split || blockIdx.z == 0)) {
+    DtlTile<BM, NW> ta;
+    DtlTile<BN, NW> tw;
+    ta.init(p.act1, p.lda1, m0, p.M, wv, lane);
+    tw.init(p.wt1, p.ldw1, n0, p.N, wv, lane);
+    for (int64_t e = 0; e < p.K1 / kBK; ++e) {
+      __syncthreads();  // every wave is done reading stage 0
+      ta.load(s_act0, wv, e * kBK);
+      tw.load(s_wt0, wv, e * kBK);
+      __builtin_amdgcn_s_waitcnt(0);
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        bf16x8 fw[FN], fa[FM];
+#pragma unroll
+        for (int a = 0; a < FN; ++a) fw[a] = lds_frag(s_wt0, wn * TN + a * 32 + r32, 2 * j + h);
+#pragma unroll
+        for (int c = 0; c < FM; ++c) fa[c] = lds_frag(s_act0, wm * TM + c * 32 + r32, 2 * j + h);
+#pragma unroll
+        for (int a = 0; a < FN; ++a)
+#pragma unroll
+          for (int c = 0; c < FM; ++c)
+            acc[a][c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fw[a], fa[c], acc[a][c], 0, 0, 0);
+      }
+    }
+  }
+
+  // lane: m = r32 of fragment c, n = 32 a + 8 (e / 4) + 4 h + e % 4
+#pragma unroll
+  for (int c = 0; c < FM; ++c) {
+    const int64_t m = m0 + wm * TM + c * 32 + r32;
+    if (m >= p.M) continue;
+#pragma unroll
+    for (int a = 0; a < FN; ++a)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const int64_t n = n0 + wn * TN + a * 32 + 8 * g + 4 * h;
+        if (n >= p.N) continue;
+        const f32x4 v = {acc[a][c][4 * g], acc[a][c][4 * g + 1], acc[a][c][4 * g + 2], acc[a][c][4 * g + 3]};
+        if (split)
+          *reinterpret_cast<f32x4*>(p.part + (static_cast<int64_t>(blockIdx.z) * p.M + m) * p.N + n) = v;
+        else
+          *reinterpret_cast<u32x2*>(p.C + m * p.ldc + n) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+      }
+  }
+}
+
+template __global__ void k_fp8_gemm<256, 256, 2, 4, false>(F8Args);
+template __global__ void k_fp8_gemm<256, 256, 2, 4, true>(F8Args);
+template __global__ void k_fp8_gemm<128, 128, 2, 2, false>(F8Args);
+template __global__ void k_fp8_gemm<128, 128, 2, 2, true>(F8Args);
+template __global__ void k_fp8_gemm<32, 128, 1, 4, false>(F8Args);
+template __global__ void k_fp8_gemm<32, 128, 1, 4, true>(F8Args);
+
+namespace {
+// rows of a tile: 256 x 256 tiles where they fill the chip, else 128 x 128, 32 x 128 for up to 32 rows
+int f8_tile(int64_t M, int64_t N) {
+  if (M <= 32) return 32;
+  return ceil_div(M, 256) * ceil_div(N, 256) >= 256 ? 256 : 128;
+}
+}  // namespace
+
+// Split-K: grids below two workgroups per CU (of a 256-CU part; the count
+// depends on the shape only) split K into ranges of at least four steps, at
+// most 16, with at most 64 MiB of partials.
+int fp8_splits(int64_t M, int64_t N, int64_t K) {
+  constexpr int64_t kTarget = 512, kMaxSplits = 16, kMaxPartBytes = int64_t(64) << 20;
+  if (M <= 0 || N <= 0) return 1;
+  const int64_t bm = f8_tile(M, N);
+  if (bm == 256) return 1;
+  const int64_t steps = ceil_div(K, kStep);
+  int64_t S = kTarget / (ceil_div(M, bm) * ceil_div(N, 128));
+  if (S > kMaxSplits) S = kMaxSplits;
+  if (S > steps / 4) S = steps / 4;
+  if (S > kMaxPartBytes / (M * N * 4)) S = kMaxPartBytes / (M * N * 4);
+  if (S < 2) return 1;
+  const int64_t ks = round_up(ceil_div(steps, S), 4);
+  return static_cast<int>(ceil_div(steps, ks));
+}
+
+size_t fp8_split_bytes(int64_t M, int64_t N, int64_t K) {
+  const int S = fp8_splits(M, N, K);
+  return S > 1 ? static_cast<size_t>(S) * M * N * 4 : 0;
+}
+
+hipError_t launch_fp8_gemm(const F8Gemm& g, hipStream_t s) {
+  const bool tr = g.transposed;
+  F8Args a{};
+  a.M = g.M;
+  a.N = tr ? g.cols : g.rows;
+  a.K = tr ? g.rows : g.cols;
+  a.xq = g.xq;
+  a.ldx = round_up(a.K, kF8Block);
+  a.xs = g.xs;
+  a.ldxs = g.ldxs;
+  a.w = g.codes;
+  a.ldw = g.cols;
+  a.wrows = g.rows;
+  const int64_t cb = ceil_div(g.cols, kF8Block);
+  a.ws = g.scales;
+  a.ws_n = tr ? 1 : cb;
+  a.ws_k = tr ? cb : 1;
+  a.ws_bytes = cb * ceil_div(g.rows, kF8Block);
+  a.act1 = g.act1; a.lda1 = g.lda1; a.wt1 = g.wt1; a.ldw1 = g.ldw1; a.K1 = g.K1;
+  a.C = g.C;
+  a.ldc = a.N;
+  const int S = fp8_splits(a.M, a.N, a.K);
+  const int bm = f8_tile(a.M, a.N), bn = bm == 256 ? 256 : 128;
+  a.gm = ceil_div(a.M, bm);
+  a.gn = ceil_div(a.N, bn);
+  dim3 grid(static_cast<uint32_t>(a.gm * a.gn), 1, 1);
+  if (S > 1) {
+    a.part = g.part;
+    a.ks = round_up(ceil_div(ceil_div(a.K, kStep), S), 4);
+    grid.z = static_cast<uint32_t>(S);
+  }
+  if (bm == 256) {
+    if (tr) hipLaunchKernelGGL((k_fp8_gemm<256, 256, 2, 4, true>), grid, dim3(512), 0, s, a);
+    else hipLaunchKernelGGL((k_fp8_gemm<256, 256, 2, 4, false>), grid, dim3(512), 0, s, a);
+  } else if (bm == 128) {
+    if (tr) hipLaunchKernelGGL((k_fp8_gemm<128, 128, 2, 2, true>), grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((k_fp8_gemm<128, 128, 2, 2, false>), grid, dim3(256), 0, s, a);
+  } else {
+    if (tr) hipLaunchKernelGGL((k_fp8_gemm<32, 128, 1, 4, true>), grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((k_fp8_gemm<32, 128, 1, 4, false>), grid, dim3(256), 0, s, a);
+  }
+  hipError_t e = hipGetLastError();
+  if (e == hipSuccess && S > 1) e = launch_split_sum(g.part, S, a.M, a.N, a.C, a.N, s);
+  return e;
+}
+
+}  // namespace qlora

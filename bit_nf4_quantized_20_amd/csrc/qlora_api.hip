@@ -800,6 +800,304 @@ int qlora_merge(const qlora_nf4_weight* W, const qlora_bf16* A, const qlora_bf16
   return launched(e);
 }
 
+}  // extern "C"
+
+namespace {
+
+// 8-bit linear: workspace layouts.  The activation codes and scales, then
+// the adapter's parts as in the 4-bit layouts (r > 0), then split-K partials.
+struct Fp8Layout {
+  size_t xq, xs, u_pad, b_pad, ut, vt, b_t, a_t_pad, part, grad, split, total;
+};
+
+int64_t fp8_scale_pitch(int64_t K) { return round_up(ceil_div(K, QLORA_FP8_BLOCK), 4); }
+
+Fp8Layout fp8_layout(int64_t T, int64_t in, int64_t out, int64_t r, bool backward) {
+  Fp8Layout l{};
+  Carve c;
+  const int64_t K = backward ? out : in, N = backward ? in : out;
+  const int64_t rp = padded_rank(r);
+  l.xq = c.take(static_cast<size_t>(T * round_up(K, QLORA_FP8_BLOCK)));
+  l.xs = c.take(static_cast<size_t>(T * fp8_scale_pitch(K)));
+  if (r > 0) {
+    l.u_pad = c.take(static_cast<size_t>(T * rp * 4));  // [T][2rp] bf16: sU, or sV of the backward
+    size_t part = lora_down_part_bytes(T, in, rp);
+    if (backward) {
+      const size_t pv = lora_down_part_bytes(T, out, rp);
+      part = pv > part ? pv : part;
+      l.ut = c.take(static_cast<size_t>(2 * rp * token_pitch(T) * 2));
+      l.vt = c.take(static_cast<size_t>(2 * rp * token_pitch(T) * 2));
+      l.b_t = c.take(static_cast<size_t>(r * out * 2));
+      l.a_t_pad = c.take(static_cast<size_t>(in * rp * 4));
+      l.grad = c.take(grad_part_bytes(T, in, &out, 1, r));
+    } else {
+      l.b_pad = c.take(static_cast<size_t>(out * rp * 4));
+    }
+    l.part = c.take(part);
+  }
+  l.split = c.take(fp8_split_bytes(T, N, K));
+  l.total = c.off;
+  return l;
+}
+
+bool fp8_shapes_ok(int64_t T, int64_t in, int64_t out, int64_t r) {
+  return linear_shapes_ok(T, in, out, r == 0 ? 1 : r) && operands_fit(T, in, out);
+}
+
+int check_fp8_weight(const qlora_fp8_weight* W) {
+  if (W == nullptr) return QLORA_ERR_NULL;
+  if (W->flags != 0) return QLORA_ERR_VALUE;
+  if (!W->codes || !W->scales) return QLORA_ERR_NULL;
+  if (!aligned16(W->codes) || !aligned16(W->scales)) return QLORA_ERR_ALIGN;
+  return QLORA_OK;
+}
+
+bool fp8_matrix_ok(int64_t rows, int64_t cols) {
+  return rows >= 0 && cols >= 0 && rows % 64 == 0 && cols % 64 == 0 && (rows == 0 || cols <= kMaxNumel / rows);
+}
+
+}  // namespace
+
+extern "C" {
+
+int qlora_fp8_storage_bytes(int64_t rows, int64_t cols, size_t* codes_bytes, size_t* scale_bytes) {
+  if (!fp8_matrix_ok(rows, cols)) return QLORA_ERR_SHAPE;
+  if (codes_bytes) *codes_bytes = static_cast<size_t>(rows * cols);
+  if (scale_bytes)
+    *scale_bytes = static_cast<size_t>(ceil_div(rows, QLORA_FP8_BLOCK) * ceil_div(cols, QLORA_FP8_BLOCK));
+  return QLORA_OK;
+}
+
+int qlora_fp8_quantize(const float* w, int64_t rows, int64_t cols, uint8_t* codes, uint8_t* scales,
+                       qlora_stream stream) {
+  if (!fp8_matrix_ok(rows, cols)) return QLORA_ERR_SHAPE;
+  if (rows == 0 || cols == 0) return QLORA_OK;
+  if (!w || !codes || !scales) return QLORA_ERR_NULL;
+  if (!aligned16(w) || !aligned16(codes) || !aligned16(scales)) return QLORA_ERR_ALIGN;
+  if (int st = check_device()) return st;
+  return launched(launch_fp8_quantize(w, rows, cols, codes, scales, static_cast<hipStream_t>(stream)));
+}
+
+int qlora_fp8_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols,
+                         qlora_bf16* w_out, qlora_stream stream) {
+  if (!fp8_matrix_ok(rows, cols)) return QLORA_ERR_SHAPE;
+  if (rows == 0 || cols == 0) return QLORA_OK;
+  if (!codes || !scales || !w_out) return QLORA_ERR_NULL;
+  if (!aligned16(codes) || !aligned16(scales) || !aligned16(w_out)) return QLORA_ERR_ALIGN;
+  if (int st = check_device()) return st;
+  return launched(launch_fp8_dequantize(codes, scales, rows, cols, w_out, static_cast<hipStream_t>(stream)));
+}
+
+size_t qlora_fp8_workspace_bytes(int64_t T, int64_t in_features, int64_t out_features, int64_t r, int backward) {
+  if (!fp8_shapes_ok(T, in_features, out_features, r)) return 0;
+  const size_t need = fp8_layout(T, in_features, out_features, r, backward != 0).total;
+  return need > kMinWorkspace ? need : kMinWorkspace;
+}
+
+int qlora_fp8_linear_fwd(const qlora_fp8_weight* W, const qlora_bf16* X, int64_t T, const qlora_bf16* A,
+                         const qlora_bf16* B, int64_t r, float alpha, qlora_bf16* Y, void* ws, size_t ws_bytes,
+                         qlora_stream stream) {
+  if (int st = check_fp8_weight(W)) return st;
+  const int64_t out = W->rows, in = W->cols;
+  if (!fp8_shapes_ok(T, in, out, r)) return QLORA_ERR_SHAPE;
+  if (r > 0 && (!A || !B)) return QLORA_ERR_NULL;
+  if (r > 0 && (!aligned16(A) || !aligned16(B))) return QLORA_ERR_ALIGN;
+  if (T > 0 && (!X || !Y)) return QLORA_ERR_NULL;
+  if (!aligned16(X) || !aligned16(Y)) return QLORA_ERR_ALIGN;
+  if (r > 0 && !std::isfinite(alpha)) return QLORA_ERR_VALUE;
+  if (T == 0) return QLORA_OK;
+  const Fp8Layout lay = fp8_layout(T, in, out, r, false);
+  if (ws == nullptr || ws_bytes < lay.total) return QLORA_ERR_WORKSPACE;
+  if (!aligned16(ws)) return QLORA_ERR_ALIGN;
+  if (int st = check_device()) return st;
+
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  const int64_t rp = padded_rank(r);
+  F8Gemm g{};
+  hipError_t e = hipSuccess;
+  if (r > 0) {
+    uint16_t* u_pad = reinterpret_cast<uint16_t*>(base + lay.u_pad);
+    uint16_t* b_pad = reinterpret_cast<uint16_t*>(base + lay.b_pad);
+    e = launch_lora_down(X, in, T, in, &A, 1, r, alpha / static_cast<float>(r), u_pad, 2 * rp, nullptr, 0, rp,
+                         reinterpret_cast<float*>(base + lay.part), s);
+    if (e == hipSuccess) e = launch_pad_bf16(B, out, r, false, b_pad, rp, 2 * rp, s);
+    g.act1 = u_pad;
+    g.wt1 = b_pad;
+    g.lda1 = g.ldw1 = g.K1 = 2 * rp;
+  }
+  if (e == hipSuccess)
+    e = launch_fp8_rows(X, in, T, in, base + lay.xq, base + lay.xs, fp8_scale_pitch(in), s);
+  g.M = T;
+  g.codes = W->codes;
+  g.scales = W->scales;
+  g.rows = out;
+  g.cols = in;
+  g.xq = base + lay.xq;
+  g.xs = base + lay.xs;
+  g.ldxs = fp8_scale_pitch(in);
+  g.C = Y;
+  g.part = reinterpret_cast<float*>(base + lay.split);
+  if (e == hipSuccess) e = launch_fp8_gemm(g, s);
+  return launched(e);
+}
+
+int qlora_fp8_linear_bwd(const qlora_fp8_weight* W, const qlora_bf16* X, const qlora_bf16* dY, int64_t T,
+                         const qlora_bf16* A, const qlora_bf16* B, int64_t r, float alpha, qlora_bf16* dX,
+                         float* dA, float* dB, void* ws, size_t ws_bytes, qlora_stream stream) {
+  if (int st = check_fp8_weight(W)) return st;
+  const int64_t out = W->rows, in = W->cols;
+  if (!fp8_shapes_ok(T, in, out, r)) return QLORA_ERR_SHAPE;
+  if (r > 0 && (!A || !B || !dA || !dB)) return QLORA_ERR_NULL;
+  if (r > 0 && (!aligned16(A) || !aligned16(B) || !aligned16(dA) || !aligned16(dB))) return QLORA_ERR_ALIGN;
+  if (T > 0 && (!dY || !dX || (r > 0 && !X))) return QLORA_ERR_NULL;
+  if (!aligned16(dY) || !aligned16(dX) || (r > 0 && !aligned16(X))) return QLORA_ERR_ALIGN;
+  if (r > 0 && !std::isfinite(alpha)) return QLORA_ERR_VALUE;
+  const Fp8Layout lay = fp8_layout(T, in, out, r, true);
+  if (T > 0 && (ws == nullptr || ws_bytes < lay.total)) return QLORA_ERR_WORKSPACE;
+  if (T > 0 && !aligned16(ws)) return QLORA_ERR_ALIGN;
+  if (T == 0 && r == 0) return QLORA_OK;
+  if (int st = check_device()) return st;
+
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (T == 0) {
+    float* dst[2] = {dA, dB};
+    const int64_t n[2] = {r * in, out * r};
+    return launched(launch_fill_many_f32(dst, n, 2, 0.f, s));
+  }
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  const int64_t rp = padded_rank(r), tp = token_pitch(T);
+  F8Gemm g{};
+  hipError_t e = hipSuccess;
+  uint16_t* ut = reinterpret_cast<uint16_t*>(base + lay.ut);
+  uint16_t* vt = reinterpret_cast<uint16_t*>(base + lay.vt);
+  if (r > 0) {
+    const float scale = alpha / static_cast<float>(r);
+    uint16_t* v_pad = reinterpret_cast<uint16_t*>(base + lay.u_pad);
+    uint16_t* b_t = reinterpret_cast<uint16_t*>(base + lay.b_t);
+    uint16_t* a_t_pad = reinterpret_cast<uint16_t*>(base + lay.a_t_pad);
+    float* part = reinterpret_cast<float*>(base + lay.part);
+    const uint16_t* bt = b_t;
+    e = launch_lora_down(X, in, T, in, &A, 1, r, scale, nullptr, 0, ut, tp, rp, part, s);
+    if (e == hipSuccess) e = launch_factor_prep(B, out, r, b_t, A, in, a_t_pad, rp, 2 * rp, s);
+    if (e == hipSuccess) e = launch_lora_down(dY, out, T, out, &bt, 1, r, scale, v_pad, 2 * rp, vt, tp, rp, part, s);
+    g.act1 = v_pad;
+    g.wt1 = a_t_pad;
+    g.lda1 = g.ldw1 = g.K1 = 2 * rp;
+  }
+  if (e == hipSuccess)
+    e = launch_fp8_rows(dY, out, T, out, base + lay.xq, base + lay.xs, fp8_scale_pitch(out), s);
+  g.M = T;
+  g.codes = W->codes;
+  g.scales = W->scales;
+  g.rows = out;
+  g.cols = in;
+  g.transposed = true;
+  g.xq = base + lay.xq;
+  g.xs = base + lay.xs;
+  g.ldxs = fp8_scale_pitch(out);
+  g.C = dX;
+  g.part = reinterpret_cast<float*>(base + lay.split);
+  if (e == hipSuccess) e = launch_fp8_gemm(g, s);
+  if (r > 0) {
+    // token-slice sums of dA and dB, then each added in slice order
+    float* const pa = reinterpret_cast<float*>(base + lay.grad);
+    const int64_t sa = lora_grad_slices(T, in, in), sb = lora_grad_slices(T, out, out);
+    float* const pb = pa + sa * r * in;
+    if (e == hipSuccess) e = launch_lora_grad(vt, T, tp, rp, X, in, in, r, pa, true, s);
+    if (e == hipSuccess) e = launch_lora_grad(ut, T, tp, rp, dY, out, out, r, pb, false, s);
+    const float* src[2] = {pa, pb};
+    const int slices[2] = {static_cast<int>(sa), static_cast<int>(sb)};
+    const int64_t n[2] = {r * in, out * r};
+    float* dst[2] = {dA, dB};
+    if (e == hipSuccess) e = launch_sum_slices(src, slices, n, dst, 2, s);
+  }
+  return launched(e);
+}
+
+}  // extern "C"
+
+namespace {
+
+bool moe_route_shapes_ok(int64_t T, int64_t E, int64_t k) {
+  if (T < 0 || E < 1 || E > QLORA_MOE_MAX_EXPERTS || k < 1 || k > QLORA_MOE_MAX_CHOICES || k > E) return false;
+  return T < (int64_t(1) << 31) / E;
+}
+
+bool moe_shapes_ok(int64_t T, int64_t hidden, int64_t inter, int64_t k) {
+  if (T < 0 || T > QLORA_MOE_MAX_TOKENS || k < 1 || k > QLORA_MOE_MAX_CHOICES || T * k > QLORA_MOE_MAX_PAIRS)
+    return false;
+  constexpr int64_t kMaxSide = int64_t(1) << 20;
+  return hidden >= 64 && hidden < kMaxSide && hidden % 64 == 0 && inter >= 64 && inter < kMaxSide && inter % 64 == 0 &&
+         hidden <= (int64_t(1) << 31) / inter;  // one expert's blocks are counted in 32 bits
+}
+
+static_assert(QLORA_MOE_MAX_EXPERTS == kMoeMaxExperts && QLORA_MOE_MAX_CHOICES == kMoeMaxChoices &&
+              QLORA_MOE_MAX_TOKENS == kMoeMaxTokens && QLORA_MOE_MAX_PAIRS == kMoeMaxPairs);
+
+}  // namespace
+
+extern "C" {
+
+int qlora_moe_route(const float* logits, int64_t T, int64_t E, int64_t k, int renormalize, int32_t* ids,
+                    float* weights, qlora_stream stream) {
+  if (!moe_route_shapes_ok(T, E, k)) return QLORA_ERR_SHAPE;
+  if (T == 0) return QLORA_OK;
+  if (!logits || !ids || !weights) return QLORA_ERR_NULL;
+  if (!aligned16(logits) || !aligned16(ids) || !aligned16(weights)) return QLORA_ERR_ALIGN;
+  if (int st = check_device()) return st;
+  return launched(launch_moe_route(logits, T, static_cast<int>(E), static_cast<int>(k), renormalize != 0, ids, weights,
+                                   static_cast<hipStream_t>(stream)));
+}
+
+int qlora_moe_route_bwd(const float* logits, const int32_t* ids, const float* dweights, int64_t T, int64_t E,
+                        int64_t k, int renormalize, float* dlogits, qlora_stream stream) {
+  if (!moe_route_shapes_ok(T, E, k)) return QLORA_ERR_SHAPE;
+  if (T == 0) return QLORA_OK;
+  if (!logits || !ids || !dweights || !dlogits) return QLORA_ERR_NULL;
+  if (!aligned16(logits) || !aligned16(ids) || !aligned16(dweights) || !aligned16(dlogits)) return QLORA_ERR_ALIGN;
+  if (int st = check_device()) return st;
+  return launched(launch_moe_route_bwd(logits, ids, dweights, T, static_cast<int>(E), static_cast<int>(k),
+                                       renormalize != 0, dlogits, static_cast<hipStream_t>(stream)));
+}
+
+size_t qlora_moe_workspace_bytes(int64_t T, int64_t hidden, int64_t inter, int64_t k) {
+  if (!moe_shapes_ok(T, hidden, inter, k)) return 0;
+  const size_t need = static_cast<size_t>(T * k * inter * 4);  // h of each pair: bf16 hi and lo
+  return need > kMinWorkspace ? need : kMinWorkspace;
+}
+
+int qlora_moe_fwd(const qlora_nf4_weight* gate_up, const qlora_nf4_weight* down, int64_t experts,
+                  const qlora_bf16* X, int64_t T, const int32_t* ids, const float* weights, int64_t k,
+                  qlora_bf16* Y, void* ws, size_t ws_bytes, qlora_stream stream) {
+  if (int st = check_weight(gate_up)) return st;
+  if (int st = check_weight(down)) return st;
+  if (absmax_fp32(*gate_up) || absmax_fp32(*down)) return QLORA_ERR_VALUE;
+  const int64_t hidden = gate_up->cols, inter = down->cols;
+  if (experts < 1 || experts > QLORA_MOE_MAX_EXPERTS || !moe_shapes_ok(T, hidden, inter, k)) return QLORA_ERR_SHAPE;
+  if (gate_up->rows != experts * 2 * inter || down->rows != experts * hidden) return QLORA_ERR_SHAPE;
+  if (T > 0 && (!X || !ids || !weights || !Y)) return QLORA_ERR_NULL;
+  if (!aligned16(X) || !aligned16(ids) || !aligned16(weights) || !aligned16(Y)) return QLORA_ERR_ALIGN;
+  if (T == 0) return QLORA_OK;
+  if (ws == nullptr || ws_bytes < static_cast<size_t>(T * k * inter * 4)) return QLORA_ERR_WORKSPACE;
+  if (!aligned16(ws)) return QLORA_ERR_ALIGN;
+  if (int st = check_device()) return st;
+  MoeArgs a{};
+  a.gate_up = MoeWeight{gate_up->codes, gate_up->absmax_q, gate_up->absmax_scale};
+  a.down = MoeWeight{down->codes, down->absmax_q, down->absmax_scale};
+  a.X = X;
+  a.ids = ids;
+  a.weights = weights;
+  a.h = static_cast<uint16_t*>(ws);
+  a.Y = Y;
+  a.T = static_cast<int>(T);
+  a.E = static_cast<int>(experts);
+  a.k = static_cast<int>(k);
+  a.H = static_cast<int>(hidden);
+  a.I = static_cast<int>(inter);
+  return launched(launch_moe(a, static_cast<hipStream_t>(stream)));
+}
+
 void nf4_codebook(float out[16]) {
   for (int j = 0; j < 16; ++j) out[j] = level(j);
 }

@@ -425,6 +425,158 @@ void nf4_code_buckets(float thr[33], uint32_t base[33]);
 /* Static description of a status code. */
 const char* qlora_status_string(int status);
 
+/*
+ * ---------------------------------------------------------------------------
+ * The 8-bit format: a frozen base in 8 bits beside the 4-bit one, for the
+ * layers of a model that 4 bits cost too much (attention, shared and router
+ * projections of a mixture of experts).
+ * ---------------------------------------------------------------------------
+ * Codes are OCP e4m3 (bias 7, largest finite 448) with one scale per block of
+ * 128 x 128 weights.  Scales are powers of two, stored as biased exponents:
+ * byte b stands for 2^(b - 127).  For a block whose largest magnitude is a,
+ * the scale is 2^e with e the least integer (>= -127) such that a 2^-e <= 448;
+ * an all-zero block has byte 0.
+ *   code = e4m3_rne(w 2^-e);   w_hat = code 2^e
+ * Blocks at the right and lower edge may be smaller; rows and cols are
+ * multiples of 64.  8 + 8 / 16384 bits per weight.
+ *   codes  [rows * cols]                            row-major, one byte each
+ *   scales [ceil(rows / 128) * ceil(cols / 128)]    row-major
+ *   flags  reserved, must be 0 (QLORA_ERR_VALUE otherwise)
+ */
+#define QLORA_FP8_BLOCK 128
+
+typedef struct {
+  const uint8_t* codes;
+  const uint8_t* scales;
+  int64_t rows;
+  int64_t cols;
+  uint32_t flags;
+} qlora_fp8_weight;
+
+/* Sizes in bytes of the two buffers; any output pointer may be NULL.  Host
+ * only.  Errors: SHAPE (negative, or not a multiple of 64). */
+int qlora_fp8_storage_bytes(int64_t rows, int64_t cols, size_t* codes_bytes, size_t* scale_bytes);
+
+/*
+ * qlora_fp8_quantize -- fp32 weight -> codes and scales as defined above.
+ *   w  [rows, cols] fp32, finite (non-finite input: that block's outputs are
+ *   unspecified);  rows, cols >= 0, multiples of 64, rows * cols <= 2^36;
+ *   an empty matrix is a no-op
+ * qlora_fp8_dequantize -- w_out [rows, cols] bf16 = bf16_rne(code 2^e) (exact
+ * unless the value is below bf16's normal range).
+ * Errors: NULL, SHAPE, ALIGN, DEVICE, LAUNCH.
+ */
+int qlora_fp8_quantize(const float* w, int64_t rows, int64_t cols, uint8_t* codes, uint8_t* scales,
+                       qlora_stream stream);
+int qlora_fp8_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols,
+                         qlora_bf16* w_out, qlora_stream stream);
+
+/*
+ * Workspace bytes of the two calls below (0 for invalid shapes, at least 256
+ * otherwise).  Host only.  Scratch only: no initialisation, nothing kept
+ * between calls; calls that overlap in time must not share one.
+ */
+size_t qlora_fp8_workspace_bytes(int64_t T, int64_t in_features, int64_t out_features, int64_t r,
+                                 int backward);
+
+/*
+ * qlora_fp8_linear_fwd -- Y = X_hat W_hat^T + (alpha/r) (X A^T) B^T.
+ * X_hat is X with each row's 128 columns quantized by the rule above (one
+ * power-of-two scale per row and 128 columns, codes e4m3); the base product
+ * is formed of 8-bit codes on the matrix cores, the adapter from the
+ * unquantized X; fp32 accumulation, one rounding of Y to bf16.
+ *   W  8-bit weight [out, in];  X [T, in] bf16;  Y [T, out] bf16 out
+ *   A  [r, in] bf16;  B [out, r] bf16;  0 <= r <= 256 (r = 0: no adapter, A, B
+ *   and alpha are not read and A, B may be NULL);  alpha finite
+ *   ws of ws_bytes >= qlora_fp8_workspace_bytes(T, in, out, r, 0)
+ * A row of X that holds an infinity or a NaN gives a row of Y of NaN.
+ * T = 0 is a no-op.  Size limits as for qlora_linear_fwd.
+ * Errors: NULL, SHAPE, ALIGN, VALUE, WORKSPACE, DEVICE, LAUNCH.
+ */
+int qlora_fp8_linear_fwd(const qlora_fp8_weight* W, const qlora_bf16* X, int64_t T, const qlora_bf16* A,
+                         const qlora_bf16* B, int64_t r, float alpha, qlora_bf16* Y, void* ws, size_t ws_bytes,
+                         qlora_stream stream);
+
+/*
+ * qlora_fp8_linear_bwd -- the gradients of the forward above with the
+ * quantization of X taken as the identity, s = alpha/r:
+ *   dX = dY_hat W_hat + s (dY B) A    [T, in]  bf16 (one rounding)
+ *   dA = s (dY B)^T X                 [r, in]  fp32
+ *   dB = s dY^T (X A^T)               [out, r] fp32
+ * dY_hat is dY quantized per row and 128 columns like X in the forward.  dA
+ * and dB are overwritten and bit-reproducible, as in qlora_linear_bwd; with
+ * r = 0 only dX is written (X, A, B, dA, dB may be NULL).  T = 0 writes zeros
+ * to dA and dB.
+ *   ws of ws_bytes >= qlora_fp8_workspace_bytes(T, in, out, r, 1)
+ * Errors: as the forward.
+ */
+int qlora_fp8_linear_bwd(const qlora_fp8_weight* W, const qlora_bf16* X, const qlora_bf16* dY, int64_t T,
+                         const qlora_bf16* A, const qlora_bf16* B, int64_t r, float alpha, qlora_bf16* dX,
+                         float* dA, float* dB, void* ws, size_t ws_bytes, qlora_stream stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Mixture of experts: the router, and the whole expert layer for a few tokens
+ * over NF4 experts.
+ * ---------------------------------------------------------------------------
+ */
+#define QLORA_MOE_MAX_EXPERTS 1024
+#define QLORA_MOE_MAX_CHOICES 16 /* largest k */
+#define QLORA_MOE_MAX_TOKENS 64  /* largest T of qlora_moe_fwd */
+#define QLORA_MOE_MAX_PAIRS 512  /* largest T * k of qlora_moe_fwd */
+
+/*
+ * qlora_moe_route -- the k largest logits of each row and their weights.
+ *   ids     [T, k] int32: the k largest, largest first; equal logits go to the
+ *           lower index (-0 equals +0; a NaN ranks above every number)
+ *   weights [T, k] fp32: renormalize != 0: the softmax over the k chosen;
+ *           0: their share of the softmax over all E
+ * -inf marks an expert that may not be chosen: its weight is 0 (it is chosen
+ * only when fewer than k others are left); a row of nothing but -inf gets
+ * weights 0.  A row with a NaN or +inf has NaN weights.
+ *   logits  [T, E] fp32;  1 <= E <= 1024;  1 <= k <= min(16, E);  T >= 0
+ *           (0 is a no-op), T * E < 2^31
+ * qlora_moe_route_bwd -- the gradient of the logits for dweights [T, k]: with p
+ * the softmax the weights were taken from (over the chosen, or over all) and
+ * g_e the gradient of e's weight (0 where e was not chosen),
+ *   dlogits [T, E] fp32 = p_e (g_e - sum_i g_i p_i), overwritten; 0 in a row of
+ *   nothing but -inf.  ids as qlora_moe_route wrote them (ids outside [0, E)
+ *   count as no choice).
+ * Both read no memory but their arguments' and need no workspace.
+ * Errors: NULL, SHAPE, ALIGN, DEVICE, LAUNCH.
+ */
+int qlora_moe_route(const float* logits, int64_t T, int64_t E, int64_t k, int renormalize, int32_t* ids,
+                    float* weights, qlora_stream stream);
+int qlora_moe_route_bwd(const float* logits, const int32_t* ids, const float* dweights, int64_t T, int64_t E,
+                        int64_t k, int renormalize, float* dlogits, qlora_stream stream);
+
+/*
+ * qlora_moe_fwd -- the expert layer for a few tokens, in two kernels:
+ *   Y_t = sum_j weights[t, j] Wd_e (silu(Wg_e x_t) * (Wu_e x_t)),  e = ids[t, j]
+ * with silu(g) = g / (1 + exp(-g)).  bf16 inputs, fp32 accumulation, one
+ * rounding of Y to bf16; the hidden values are kept as bf16 hi + lo pairs.
+ * Each expert that is met is read once, whatever the number of its tokens.
+ *   gate_up  double-quantized NF4 weight [experts * 2 * inter, hidden]: expert
+ *            e's rows start at e * 2 * inter, its gate rows before its up rows
+ *   down     double-quantized NF4 weight [experts * hidden, inter]
+ *   X [T, hidden] bf16;  ids [T, k] int32;  weights [T, k] fp32;
+ *   Y [T, hidden] bf16 out;  hidden and inter multiples of 64, below 2^20
+ *   0 <= T <= 64 (0 is a no-op), 1 <= k <= 16, T * k <= 512,
+ *   1 <= experts <= 1024
+ * An id outside [0, experts) is no choice (a padded row, an expert held
+ * elsewhere): it adds nothing, and a row without a choice is written as 0.  An
+ * expert that a row names twice counts twice.
+ *   ws  workspace of ws_bytes >= qlora_moe_workspace_bytes(T, hidden, inter, k)
+ *       (scratch: no initialisation, nothing kept between calls; calls that
+ *       overlap in time must not share one)
+ * The 4.5-bit format (QLORA_NF4_ABSMAX_FP32) is refused (VALUE).
+ * Errors: NULL, SHAPE, ALIGN, VALUE, WORKSPACE, DEVICE, LAUNCH.
+ */
+size_t qlora_moe_workspace_bytes(int64_t T, int64_t hidden, int64_t inter, int64_t k);
+int qlora_moe_fwd(const qlora_nf4_weight* gate_up, const qlora_nf4_weight* down, int64_t experts,
+                  const qlora_bf16* X, int64_t T, const int32_t* ids, const float* weights, int64_t k,
+                  qlora_bf16* Y, void* ws, size_t ws_bytes, qlora_stream stream);
+
 #ifdef __cplusplus
 }
 #endif

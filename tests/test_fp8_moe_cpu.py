@@ -1,0 +1,224 @@
+"""The 8-bit linear layer and the mixture-of-experts operators without a GPU:
+the oracle against its definitions and against differences, and the library's
+and the binding's refusals (every check comes before any HIP call)."""
+
+import ctypes
+import os
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import fp8 as ofp8
+from oracle import moe as omoe
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+LIB = os.environ.get("QLORA_ABI_LIB") or os.path.join(ROOT, "bit_nf4_quantized_20_amd", "libqlora.so")
+F = 0x10000  # 16-byte aligned address that is never dereferenced
+ODD = 0x10008
+NULL, SHAPE, ALIGN, WORKSPACE, VALUE = -1, -2, -3, -4, -7
+
+
+# ------------------------------------------------------------------ oracle
+def test_e4m3_values_match_torch():
+    got = ofp8.e4m3_values()
+    ref = torch.arange(256, dtype=torch.uint8).view(torch.float8_e4m3fn).double().numpy()
+    assert np.array_equal(got, ref, equal_nan=True)
+
+
+def test_encode_is_nearest_even():
+    rng = np.random.Generator(np.random.PCG64(1))
+    mags = ofp8.e4m3_values()[:127]
+    x = np.concatenate([rng.uniform(-448, 448, 4000), rng.normal(0, 0.02, 4000), mags, -mags,
+                        (mags[1:] + mags[:-1]) / 2])  # ties
+    ref = torch.from_numpy(x.astype(np.float32)).to(torch.float8_e4m3fn).view(torch.uint8).numpy()
+    assert np.array_equal(ofp8.encode(x.astype(np.float32).astype(np.float64)), ref)
+
+
+@pytest.mark.parametrize("a,e", [(448.0, 0), (np.nextafter(np.float32(448), np.float32(500)), 1), (224.0, -1),
+                                 (1.0, -8), (1.75, -8), (1.7500001, -7), (0.0, -127), (2.0 ** -149, -127),
+                                 (2.0 ** -119, -127), (3.4e38, 120)])
+def test_scale_exponent(a, e):
+    assert int(ofp8.scale_exponent(a)) == e
+
+
+def test_linear_gradients_match_differences():
+    # d/dX, d/dA, d/dB of sum(Y * G) with the quantization of X taken as the
+    # identity; the product is at most bilinear in each, so central differences
+    # are exact up to rounding
+    rng = np.random.Generator(np.random.PCG64(2))
+    T, n_in, n_out, r, alpha = 3, 64, 64, 4, 8.0
+    Wh = ofp8.dequantize(*ofp8.quantize(rng.normal(0, 0.02, (n_out, n_in))))
+    X, A, B = rng.normal(0, 1, (T, n_in)), rng.normal(0, .1, (r, n_in)), rng.normal(0, .1, (n_out, r))
+    G = ofp8.quantized_rows(rng.normal(0, 1, (T, n_out)))  # its own quantization is then the identity
+    f = lambda X, A, B: float((G * (X @ Wh.T + alpha / r * (X @ A.T) @ B.T)).sum())
+    for which, grad in enumerate(ofp8.linear_bwd(Wh, X, G, A, B, r, alpha)):
+        v = [X, A, B]
+        for _ in range(12):
+            i = tuple(rng.integers(0, n) for n in v[which].shape)
+            up, dn = [a.copy() for a in v], [a.copy() for a in v]
+            up[which][i] += 0.5
+            dn[which][i] -= 0.5
+            assert abs(f(*up) - f(*dn) - grad[i]) <= 1e-9 * (1 + abs(grad[i]))
+
+
+@pytest.mark.parametrize("renorm", [True, False])
+def test_route_gradient_matches_differences(renorm):
+    rng = np.random.Generator(np.random.PCG64(3))
+    l, dw = rng.normal(0, 1, (4, 12)), rng.normal(0, 1, (4, 3))
+    ids, _ = omoe.route(l, 3, renorm)
+    grad = omoe.route_bwd(l, ids, dw, renorm)
+    h = 1e-5
+    for t in range(4):
+        for e in range(12):
+            up, dn = l.copy(), l.copy()
+            up[t, e] += h
+            dn[t, e] -= h
+            iu, wu = omoe.route(up, 3, renorm)
+            idn, wd = omoe.route(dn, 3, renorm)
+            assert np.array_equal(iu, ids) and np.array_equal(idn, ids)  # the choice does not change here
+            # central difference: error h^2 |w'''| / 6 <= 1e-10, rounding 1e-16 / h = 1e-11
+            assert abs(((wu - wd) * dw).sum() / (2 * h) - grad[t, e]) < 1e-8
+
+
+def test_route_oracle_matches_torch_softmax():
+    rng = np.random.Generator(np.random.PCG64(4))
+    l = torch.from_numpy(rng.normal(0, 2, (9, 33))).requires_grad_(True)
+    ids, w = omoe.route(l.detach().numpy(), 5, False)
+    p = torch.softmax(l, 1)
+    top, at = torch.topk(p, 5, dim=1)
+    assert np.array_equal(ids, at.numpy()) and np.allclose(w, top.detach().numpy(), rtol=1e-12)
+    dw = rng.normal(0, 1, (9, 5))
+    (top * torch.from_numpy(dw)).sum().backward()
+    assert np.allclose(omoe.route_bwd(l.detach().numpy(), ids, dw, False), l.grad.numpy(), atol=1e-14)
+
+
+# ------------------------------------------------------------------ the library's refusals
+class _F8(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("rows", ctypes.c_int64),
+                ("cols", ctypes.c_int64), ("flags", ctypes.c_uint32)]
+
+
+class _N4(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("absmax_q", ctypes.c_void_p), ("absmax_scale", ctypes.c_void_p),
+                ("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("flags", ctypes.c_uint32)]
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(LIB):
+        pytest.skip("libqlora.so not built")
+    l = ctypes.CDLL(LIB)
+    p, i64, sz, c = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int
+    f8, n4 = ctypes.POINTER(_F8), ctypes.POINTER(_N4)
+    l.qlora_fp8_storage_bytes.argtypes = [i64, i64, ctypes.POINTER(sz), ctypes.POINTER(sz)]
+    l.qlora_fp8_quantize.argtypes = [p, i64, i64, p, p, p]
+    l.qlora_fp8_dequantize.argtypes = [p, p, i64, i64, p, p]
+    l.qlora_fp8_workspace_bytes.argtypes = [i64, i64, i64, i64, c]
+    l.qlora_fp8_workspace_bytes.restype = sz
+    l.qlora_fp8_linear_fwd.argtypes = [f8, p, i64, p, p, i64, ctypes.c_float, p, p, sz, p]
+    l.qlora_fp8_linear_bwd.argtypes = [f8, p, p, i64, p, p, i64, ctypes.c_float, p, p, p, p, sz, p]
+    l.qlora_moe_route.argtypes = [p, i64, i64, i64, c, p, p, p]
+    l.qlora_moe_route_bwd.argtypes = [p, p, p, i64, i64, i64, c, p, p]
+    l.qlora_moe_workspace_bytes.argtypes = [i64, i64, i64, i64]
+    l.qlora_moe_workspace_bytes.restype = sz
+    l.qlora_moe_fwd.argtypes = [n4, n4, i64, p, i64, p, p, i64, p, p, sz, p]
+    return l
+
+
+def test_fp8_storage(lib):
+    c, s = ctypes.c_size_t(), ctypes.c_size_t()
+    for rows, cols, blocks in ((64, 64, 1), (128, 192, 2), (1088, 4160, 9 * 33), (0, 64, 0)):
+        assert lib.qlora_fp8_storage_bytes(rows, cols, ctypes.byref(c), ctypes.byref(s)) == 0
+        assert (c.value, s.value) == (rows * cols, blocks)
+    assert lib.qlora_fp8_storage_bytes(65, 64, None, None) == SHAPE
+    assert lib.qlora_fp8_storage_bytes(-64, 64, None, None) == SHAPE
+
+
+def test_fp8_quantize_refusals(lib):
+    q, d = lib.qlora_fp8_quantize, lib.qlora_fp8_dequantize
+    assert q(F, 100, 64, F, F, None) == SHAPE and q(F, 64, 100, F, F, None) == SHAPE
+    assert q(F, -64, 64, F, F, None) == SHAPE
+    assert q(F, 1 << 30, 1 << 30, F, F, None) == SHAPE
+    assert q(None, 64, 64, F, F, None) == NULL and q(F, 64, 64, F, None, None) == NULL
+    assert q(ODD, 64, 64, F, F, None) == ALIGN
+    assert q(None, 0, 64, None, None, None) == 0
+    assert d(F, F, 64, 32, F, None) == SHAPE and d(F, None, 64, 64, F, None) == NULL
+    assert d(F, F, 64, 64, ODD, None) == ALIGN and d(None, None, 64, 0, None, None) == 0
+
+
+def test_fp8_linear_refusals(lib):
+    ws = {b: lib.qlora_fp8_workspace_bytes(32, 256, 128, 8, b) for b in (0, 1)}
+    assert ws[0] > 0 and ws[1] > ws[0]
+    assert lib.qlora_fp8_workspace_bytes(0, 256, 128, 0, 0) >= 256
+    for bad in ((-1, 256, 128, 8), (1, 100, 128, 8), (1, 256, 100, 8), (1, 256, 128, 257), (1, 256, 128, -1),
+                (1 << 21, 1024, 128, 8)):
+        assert lib.qlora_fp8_workspace_bytes(*bad, 0) == 0, bad
+    W = _F8(F, F, 128, 256, 0)
+
+    def fwd(W=W, X=F, T=32, A=F, B=F, r=8, alpha=16.0, Y=F, w=F, n=ws[0]):
+        return lib.qlora_fp8_linear_fwd(ctypes.byref(W), X, T, A, B, r, alpha, Y, w, n, None)
+    assert lib.qlora_fp8_linear_fwd(None, F, 32, F, F, 8, 1.0, F, F, ws[0], None) == NULL
+    assert fwd(W=_F8(F, F, 128, 100, 0)) == SHAPE and fwd(W=_F8(F, F, 100, 256, 0)) == SHAPE
+    assert fwd(W=_F8(F, F, 128, 256, 1)) == VALUE and fwd(W=_F8(None, F, 128, 256, 0)) == NULL
+    assert fwd(W=_F8(F, ODD, 128, 256, 0)) == ALIGN
+    assert fwd(r=-1) == SHAPE and fwd(r=257) == SHAPE and fwd(T=-1) == SHAPE
+    assert fwd(A=None) == NULL and fwd(X=None) == NULL and fwd(Y=ODD) == ALIGN
+    assert fwd(alpha=float("nan")) == VALUE
+    assert fwd(w=None) == WORKSPACE and fwd(n=ws[0] - 1) == WORKSPACE and fwd(w=ODD) == ALIGN
+    assert fwd(T=0, X=None, Y=None) == 0
+
+    def bwd(W=W, X=F, dY=F, T=32, A=F, B=F, r=8, alpha=16.0, dX=F, dA=F, dB=F, w=F, n=ws[1]):
+        return lib.qlora_fp8_linear_bwd(ctypes.byref(W), X, dY, T, A, B, r, alpha, dX, dA, dB, w, n, None)
+    assert bwd(dY=None) == NULL and bwd(dA=None) == NULL and bwd(X=None) == NULL and bwd(dX=None) == NULL
+    assert bwd(dB=ODD) == ALIGN and bwd(alpha=float("inf")) == VALUE
+    assert bwd(n=ws[1] - 1) == WORKSPACE and bwd(r=300) == SHAPE
+    assert bwd(T=0, r=0, X=None, dY=None, A=None, B=None, dX=None, dA=None, dB=None, w=None, n=0) == 0
+
+
+def test_moe_refusals(lib):
+    r, b = lib.qlora_moe_route, lib.qlora_moe_route_bwd
+    assert r(F, 4, 8, 9, 1, F, F, None) == SHAPE      # k > E
+    assert r(F, 4, 1025, 2, 1, F, F, None) == SHAPE and r(F, 4, 64, 17, 1, F, F, None) == SHAPE
+    assert r(F, 4, 0, 0, 1, F, F, None) == SHAPE and r(F, -1, 8, 2, 1, F, F, None) == SHAPE
+    assert r(F, 1 << 28, 8, 2, 1, F, F, None) == SHAPE
+    assert r(None, 4, 8, 2, 1, F, F, None) == NULL and r(ODD, 4, 8, 2, 1, F, F, None) == ALIGN
+    assert r(None, 0, 8, 2, 1, None, None, None) == 0
+    assert b(F, F, None, 4, 8, 2, 1, F, None) == NULL and b(F, F, F, 4, 8, 2, 1, ODD, None) == ALIGN
+    assert b(F, F, F, 4, 8, 0, 1, F, None) == SHAPE
+
+    ws = lib.qlora_moe_workspace_bytes(4, 128, 64, 2)
+    assert ws >= 4 * 2 * 64 * 4
+    for bad in ((65, 128, 64, 2), (4, 100, 64, 2), (4, 128, 32, 2), (4, 128, 64, 17), (64, 128, 64, 9),
+                (-1, 128, 64, 2), (4, 1 << 20, 64, 2)):
+        assert lib.qlora_moe_workspace_bytes(*bad) == 0, bad
+    E, H, I = 8, 128, 64
+    gu, dn = _N4(F, F, F, E * 2 * I, H, 0), _N4(F, F, F, E * H, I, 0)
+
+    def moe(gu=gu, dn=dn, E=E, X=F, T=4, ids=F, w=F, k=2, Y=F, wk=F, n=ws):
+        return lib.qlora_moe_fwd(ctypes.byref(gu), ctypes.byref(dn), E, X, T, ids, w, k, Y, wk, n, None)
+    assert moe(gu=_N4(F, F, F, E * 2 * I, H, 1)) == VALUE      # the 4.5-bit format
+    assert moe(gu=_N4(F, F, F, E * I, H, 0)) == SHAPE and moe(dn=_N4(F, F, F, E * H + 64, I, 0)) == SHAPE
+    assert moe(E=7) == SHAPE and moe(E=0) == SHAPE and moe(T=65) == SHAPE and moe(k=0) == SHAPE
+    assert moe(X=None) == NULL and moe(ids=None) == NULL and moe(Y=ODD) == ALIGN
+    assert moe(n=ws - 1) == (WORKSPACE if ws > 256 else 0) and moe(wk=None) == WORKSPACE
+    assert moe(T=0, X=None, ids=None, w=None, Y=None, wk=None) == 0
+
+
+# ------------------------------------------------------------------ the binding's refusals
+def test_binding_refuses_what_the_library_cannot_see():
+    q = pytest.importorskip("bit_nf4_quantized_20_amd")
+    w = torch.zeros(64, 64)
+    with pytest.raises(ValueError, match="GPU"):
+        q.qlora_fp8_quantize(w)                                   # host memory
+    with pytest.raises(ValueError, match="2-D"):
+        q.qlora_fp8_quantize(torch.zeros(64))
+    with pytest.raises(TypeError):
+        q.qlora_moe_route(torch.zeros(4, 8, dtype=torch.float64), 2)
+    with pytest.raises(ValueError, match="GPU"):
+        q.qlora_moe_route(torch.zeros(4, 8), 2)
+    W = q.FP8Weight(torch.zeros(64, 64, dtype=torch.uint8), torch.zeros(1, 1, dtype=torch.uint8), 64, 64)
+    with pytest.raises(ValueError):
+        q.qlora_fp8_linear_fwd(W, torch.zeros(2, 64, dtype=torch.bfloat16), None, None, 0, 0.0)
+    with pytest.raises(TypeError):
+        q.qlora_fp8_linear_bwd(W, None, torch.zeros(2, 64), None, None, 0, 0.0)
