@@ -189,7 +189,12 @@ hipError_t launch_fp8_quantize(const float* w, int64_t rows, int64_t cols, uint8
 hipError_t launch_fp8_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols,
                                  uint16_t* out, hipStream_t s);
 // Activations x [T][ldx] (K columns, K % 8 == 0) -> codes [T][K rounded up to
-// 128, the rest zero], scale bytes [T][ldsc] (one per 128 columns).
+// 128, the rest zero], scale bytes (one per 128 columns) as dwords of four
+// K-blocks [ceil(blocks / 4)][ldsc], row t at column t; ldsc = fp8_row_pitch(T).
+constexpr int64_t fp8_row_pitch(int64_t T) { return round_up(T, 256); }  // whole tiles of rows
+inline size_t fp8_row_scale_bytes(int64_t T, int64_t K) {
+  return static_cast<size_t>(ceil_div(K, 512) * fp8_row_pitch(T) * 4);
+}
 hipError_t launch_fp8_rows(const uint16_t* x, int64_t ldx, int64_t T, int64_t K, uint8_t* codes, uint8_t* scales,
                            int64_t ldsc, hipStream_t s);
 // C [M][N] bf16 = activations (codes, scales as launch_fp8_rows writes them)
@@ -202,7 +207,6 @@ struct F8Gemm {
   int64_t rows, cols;
   bool transposed;
   const uint8_t* xq; const uint8_t* xs;
-  int64_t ldxs;
   const uint16_t* act1; int64_t lda1;
   const uint16_t* wt1; int64_t ldw1;
   int64_t K1;

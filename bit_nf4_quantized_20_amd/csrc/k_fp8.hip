@@ -107,10 +107,11 @@ __global__ __launch_bounds__(256) void k_fp8_dequantize(const uint8_t* __restric
   }
 }
 
-// Activations x [T][ldx] bf16 (columns 0 .. K - 1) -> codes [T][Kp], scales
-// [T][KBp]: 16 lanes hold one row's 128 columns, eight each.  Columns K .. Kp
+// Activations x [T][ldx] bf16 (columns 0 .. K - 1) -> codes [T][Kp], scale
+// bytes in groups of four K-blocks, [ceil(KB / 4)][ldsc] dwords, row t's at
+// column t: 16 lanes hold one row's 128 columns, eight each.  Columns K .. Kp
 // (Kp = K rounded up to 128) become zero codes; scale bytes past the last
-// block are not written.
+// block or row are not written.
 __global__ __launch_bounds__(256) void k_fp8_rows(const uint16_t* __restrict__ x, int64_t ldx, uint32_t K,
                                                   uint32_t KB, uint8_t* __restrict__ codes,
                                                   uint8_t* __restrict__ scales, int64_t ldsc) {
@@ -134,7 +135,7 @@ __global__ __launch_bounds__(256) void k_fp8_rows(const uint16_t* __restrict__ x
     o[d] = f8_pack4(bf16_lo(v[2 * d]) * inv, bf16_hi(v[2 * d]) * inv, bf16_lo(v[2 * d + 1]) * inv,
                     bf16_hi(v[2 * d + 1]) * inv);
   *reinterpret_cast<u32x2*>(codes + (static_cast<int64_t>(row) * KB + kb) * kF8Block + 8 * sub) = o;
-  if (sub == 0) scales[row * ldsc + kb] = static_cast<uint8_t>(b);
+  if (sub == 0) scales[((kb >> 2) * ldsc + row) * 4 + (kb & 3)] = static_cast<uint8_t>(b);
 }
 
 hipError_t launch_fp8_quantize(const float* w, int64_t rows, int64_t cols, uint8_t* codes, uint8_t* scales,

@@ -139,7 +139,7 @@ __device__ __forceinline__ i32x8 f8_frag_tr(const uint16_t* lds, int n0, int j) 
 struct F8Args {
   int64_t M, N, K;
   const uint8_t* xq; int64_t ldx;            // activation codes [M][ldx], ldx = K rounded up to 128
-  const uint8_t* xs; int64_t ldxs;           // their scales [M][ldxs], ldxs % 4 == 0
+  const uint32_t* xs; int64_t ldxs;          // their scales [K / 512][ldxs]: four K-blocks' bytes per row, ldxs >= M in whole tiles
   const uint8_t* w; int64_t ldw, wrows;      // weight codes [wrows][ldw]
   const uint8_t* ws; int64_t ws_n, ws_k;     // scale byte of block (n / 128, k / 128): ws[nb ws_n + kb ws_k]
   int64_t ws_bytes;
@@ -194,43 +194,43 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_fp8_gemm(F8Args p) {
   const int64_t last = split && first + p.ks < all ? first + p.ks : all;  // steps [first, last)
   const bool odd_tail = p.K % kStep != 0;
 
-  struct Frags { i32x8 w[FN]; i32x8 a[FM]; };
-  auto read_frags = [&](Frags& f, const uint16_t* sw, const uint16_t* sa, int j) {
+  // fragments of sub-step j: the weight's for all FN, one of the activations'
+  auto read_w = [&](i32x8 (&f)[FN], const uint16_t* sw, int j) {
 #pragma unroll
     for (int a = 0; a < FN; ++a) {
-      if constexpr (kTr) f.w[a] = f8_frag_tr<BN>(sw, wn * TN + a * 32, j);
-      else f.w[a] = f8_frag(sw, wn * TN + a * 32 + r32, j, h);
+      if constexpr (kTr) f[a] = f8_frag_tr<BN>(sw, wn * TN + a * 32, j);
+      else f[a] = f8_frag(sw, wn * TN + a * 32 + r32, j, h);
     }
-#pragma unroll
-    for (int c = 0; c < FM; ++c) f.a[c] = f8_frag(sa, wm * TM + c * 32 + r32, j, h);
   };
+  auto read_a = [&](const uint16_t* sa, int c, int j) { return f8_frag(sa, wm * TM + c * 32 + r32, j, h); };
 
-  // scales: one dword (four steps) per activation fragment, one byte per step for the weight
-  struct Scales { int a[FM]; int w[4]; };
-  const __amdgpu_buffer_rsrc_t rxs = rows_rsrc(p.xs, p.ldxs, m0, p.M, 1);
+  // scales of four steps: one dword per activation fragment, the weight's four bytes in one
+  struct Scales { int a[FM]; int w; };
+  const uint32_t xso = static_cast<uint32_t>(m0 + wm * TM + r32) * 4;
   const __amdgpu_buffer_rsrc_t rws = __builtin_amdgcn_make_buffer_rsrc(
       const_cast<uint8_t*>(p.ws), 0, static_cast<int>(p.ws_bytes < 0x7fffffff ? p.ws_bytes : 0x7fffffff), kBufferWord3);
-  uint32_t xso[FM];
-#pragma unroll
-  for (int c = 0; c < FM; ++c) xso[c] = static_cast<uint32_t>((wm * TM + c * 32 + r32) * p.ldxs);
   const uint32_t wso = static_cast<uint32_t>((n0 + wn * TN) / kF8Block * p.ws_n);
-  auto load_scales = [&](Scales& s, int64_t e) {  // steps e .. e + 3, e % 4 == 0
+  auto load_xs = [&](Scales& s, int64_t e) {  // steps e .. e + 3, e % 4 == 0 (past the last: any group)
+    const int64_t g = e < all ? e / 4 : 0;
+    const uint8_t* base = reinterpret_cast<const uint8_t*>(p.xs + g * p.ldxs) + xso;
 #pragma unroll
-    for (int c = 0; c < FM; ++c)
-      s.a[c] = __builtin_amdgcn_raw_buffer_load_b32(rxs, xso[c] + static_cast<uint32_t>(e), 0, 0);
+    for (int c = 0; c < FM; ++c) s.a[c] = *reinterpret_cast<const int*>(base + 128 * c);
+  };
+  auto load_ws = [&](int (&raw)[4], int64_t e) {
 #pragma unroll
     for (int u = 0; u < 4; ++u)
-      s.w[u] = __builtin_amdgcn_raw_buffer_load_b8(rws, wso + static_cast<uint32_t>((e + u) * p.ws_k), 0, 0);
+      raw[u] = __builtin_amdgcn_raw_buffer_load_b8(rws, wso + static_cast<uint32_t>((e + u) * p.ws_k), 0, 0);
   };
+  auto pack_ws = [&](Scales& s, const int (&raw)[4]) { s.w = raw[0] | raw[1] << 8 | raw[2] << 16 | raw[3] << 24; };
 
-  auto mfmas = [&](const Frags& f, const Scales& s, auto uc) {
+  auto mfma_col = [&](const i32x8 (&w)[FN], const i32x8& f, int c, const Scales& s, auto uc) {
     constexpr int U = decltype(uc)::value;
+    __builtin_amdgcn_s_setprio(1);  // matrix instructions go ahead of the other wave's loads
 #pragma unroll
     for (int a = 0; a < FN; ++a)
-#pragma unroll
-      for (int c = 0; c < FM; ++c)
-        acc[a][c] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(f.w[a], f.a[c], acc[a][c], 0, 0, 0, s.w[U], U,
-                                                                    s.a[c]);
+      acc[a][c] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w[a], f, acc[a][c], 0, 0, U, s.w, U, s.a[c]);
+    __builtin_amdgcn_s_setprio(0);
+    __builtin_amdgcn_sched_barrier(0);  // the operand registers may be loaded anew from here on
   };
 
   if (last > first) {
@@ -239,45 +239,83 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_fp8_gemm(F8Args p) {
     ta.init(reinterpret_cast<const uint16_t*>(p.xq), p.ldx / 2, m0, p.M, wv, lane);
     if constexpr (kTr) tw.init(p.w, p.ldw, n0, p.wrows, wv, lane);
     else tw.init(p.w, p.ldw, n0, p.wrows, wv, lane);
-    auto copy = [&](int64_t e, uint16_t* sa, uint16_t* sw) {  // steps past the end re-read the last one
-      const int64_t k = (e < last ? e : last - 1);
-      ta.load(sa, wv, k * (kStep / 2));
+    auto copy_act = [&](int64_t e, uint16_t* sa) {  // steps past the end re-read the last one
+      ta.load(sa, wv, (e < last ? e : last - 1) * (kStep / 2));
+    };
+    auto copy_wt = [&](int64_t e, uint16_t* sw) {
+      const int64_t k = e < last ? e : last - 1;
       tw.load(sw, wv, k * kStep, odd_tail && k == all - 1);
     };
-    Scales sc0, sc1;
-    load_scales(sc0, first);
-    copy(first, s_act0, s_wt0);
+    Scales cur, nxt;
+    int raw[4];
+    load_xs(cur, first);
+    load_ws(raw, first);
+    copy_act(first, s_act0);
+    copy_wt(first, s_wt0);
     __builtin_amdgcn_s_waitcnt(0);
+    pack_ws(cur, raw);
     __syncthreads();
-    Frags f0, f1;
-    read_frags(f0, s_wt0, s_act0, 0);
-    auto step = [&](int64_t e, const Scales& cur, Scales& nxt, auto uc) {
+    copy_act(first + 1, s_act1);
+    copy_wt(first + 1, s_wt1);
+    i32x8 w0[FN], w1[FN], fa[FM];
+    read_w(w0, s_wt0, 0);
+#pragma unroll
+    for (int c = 0; c < FM; ++c) fa[c] = read_a(s_act0, c, 0);
+    auto step = [&](int64_t e, auto uc) {
       constexpr int U = decltype(uc)::value, B = U & 1;
-      copy(e + 1, s_act[B ^ 1], s_wt[B ^ 1]);
-      if constexpr (U == 0) load_scales(nxt, e + 4);
-      __builtin_amdgcn_s_setprio(1);
-      read_frags(f1, s_wt[B], s_act[B], 1);
-      mfmas(f0, cur, uc);
-      mfmas(f1, cur, uc);
-      __builtin_amdgcn_s_setprio(0);
+      read_w(w1, s_wt[B], 1);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int c = 0; c < FM; ++c) {
+        mfma_col(w0, fa[c], c, cur, uc);
+        fa[c] = read_a(s_act[B], c, 1);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      mfma_col(w1, fa[0], 0, cur, uc);
+      __builtin_amdgcn_sched_barrier(0);
+      // this wave holds the rest of step e, so stage B is free once every
+      // wave is here; step e + 1's copies, in flight since the last such
+      // point, have landed
       __builtin_amdgcn_s_waitcnt(0);
       __syncthreads();
-      read_frags(f0, s_wt[B ^ 1], s_act[B ^ 1], 0);
+      if constexpr (U == 0) {
+        load_xs(nxt, e + 4);
+        load_ws(raw, e + 4);
+      }
+      if constexpr (U == 1) pack_ws(nxt, raw);
+      read_w(w0, s_wt[B ^ 1], 0);
+      fa[0] = read_a(s_act[B ^ 1], 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int c = 1; c < FM; ++c) {
+        mfma_col(w1, fa[c], c, cur, uc);
+        fa[c] = read_a(s_act[B ^ 1], c, 0);
+        __builtin_amdgcn_sched_barrier(0);
+        // step e + 2 into the free stage, behind the first reads
+        if (c == 1) copy_act(e + 2, s_act[B]);
+        if (c == (FM > 2 ? 2 : 1)) copy_wt(e + 2, s_wt[B]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if constexpr (FM == 1) {
+        copy_act(e + 2, s_act[B]);
+        copy_wt(e + 2, s_wt[B]);
+      }
     };
     using I0 = std::integral_constant<int, 0>;
     using I1 = std::integral_constant<int, 1>;
     using I2 = std::integral_constant<int, 2>;
     using I3 = std::integral_constant<int, 3>;
-    auto four = [&](int64_t e, const Scales& cur, Scales& nxt) {
-      step(e, cur, nxt, I0{});
-      if (e + 1 < last) step(e + 1, cur, nxt, I1{});
-      if (e + 2 < last) step(e + 2, cur, nxt, I2{});
-      if (e + 3 < last) step(e + 3, cur, nxt, I3{});
-    };
-    for (int64_t e = first; e < last; e += 8) {
-      four(e, sc0, sc1);
-      if (e + 4 < last) four(e + 4, sc1, sc0);
+    int64_t e = first;
+    for (; e + 4 <= last; e += 4) {
+      step(e, I0{});
+      step(e + 1, I1{});
+      step(e + 2, I2{});
+      step(e + 3, I3{});
+      cur = nxt;
     }
+    if (e < last) step(e, I0{});
+    if (e + 1 < last) step(e + 1, I1{});
+    if (e + 2 < last) step(e + 2, I2{});
   }
 
   // adapter segment: a few bf16 steps of 64 through stage 0
@@ -308,6 +346,36 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_fp8_gemm(F8Args p) {
     }
   }
 
+  if constexpr (BN == 256) {
+    // never split: each wave parks its TM x TN block in LDS (rows of TN / 8
+    // 16-byte pieces, piece q of row r at q ^ (r % 8)) and stores whole rows
+    // back, 64 pieces per instruction
+    constexpr int kPerArray = NW / 4, kPieces = TN / 8, kRowsPer = 64 / kPieces;
+    static_assert(BM == BN && TM * TN * 2 * kPerArray == BM * 128, "the waves' blocks fill the four stage arrays");
+    __syncthreads();  // every wave is done reading the stages
+    const int array = wv / kPerArray;
+    uint16_t* const s_c = (array == 0 ? s_act0 : array == 1 ? s_act1 : array == 2 ? s_wt0 : s_wt1) + (wv % kPerArray) * (TM * TN);
+#pragma unroll
+    for (int c = 0; c < FM; ++c)
+#pragma unroll
+      for (int a = 0; a < FN; ++a)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const int row = c * 32 + r32, piece = 4 * a + g;
+          *reinterpret_cast<u32x2*>(s_c + row * TN + ((piece ^ (row & 7)) * 8) + 4 * h) =
+              u32x2{pack_bf16x2(acc[a][c][4 * g], acc[a][c][4 * g + 1]),
+                    pack_bf16x2(acc[a][c][4 * g + 2], acc[a][c][4 * g + 3])};
+        }
+    __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): this wave's block is in LDS
+#pragma unroll
+    for (int i = 0; i < TM / kRowsPer; ++i) {
+      const int row = kRowsPer * i + lane / kPieces, piece = lane % kPieces;
+      const int64_t m = m0 + wm * TM + row, n = n0 + wn * TN + 8 * piece;
+      const u32x4 v = *reinterpret_cast<const u32x4*>(s_c + row * TN + ((piece ^ (row & 7)) * 8));
+      if (m < p.M && n < p.N) __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(p.C + m * p.ldc + n));
+    }
+    return;
+  }
   // lane: m = r32 of fragment c, n = 32 a + 8 (e / 4) + 4 h + e % 4
 #pragma unroll
   for (int c = 0; c < FM; ++c) {
@@ -374,8 +442,8 @@ hipError_t launch_fp8_gemm(const F8Gemm& g, hipStream_t s) {
   a.K = tr ? g.rows : g.cols;
   a.xq = g.xq;
   a.ldx = round_up(a.K, kF8Block);
-  a.xs = g.xs;
-  a.ldxs = g.ldxs;
+  a.xs = reinterpret_cast<const uint32_t*>(g.xs);
+  a.ldxs = fp8_row_pitch(g.M);
   a.w = g.codes;
   a.ldw = g.cols;
   a.wrows = g.rows;

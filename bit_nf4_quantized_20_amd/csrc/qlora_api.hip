@@ -810,15 +810,13 @@ struct Fp8Layout {
   size_t xq, xs, u_pad, b_pad, ut, vt, b_t, a_t_pad, part, grad, split, total;
 };
 
-int64_t fp8_scale_pitch(int64_t K) { return round_up(ceil_div(K, QLORA_FP8_BLOCK), 4); }
-
 Fp8Layout fp8_layout(int64_t T, int64_t in, int64_t out, int64_t r, bool backward) {
   Fp8Layout l{};
   Carve c;
   const int64_t K = backward ? out : in, N = backward ? in : out;
   const int64_t rp = padded_rank(r);
   l.xq = c.take(static_cast<size_t>(T * round_up(K, QLORA_FP8_BLOCK)));
-  l.xs = c.take(static_cast<size_t>(T * fp8_scale_pitch(K)));
+  l.xs = c.take(fp8_row_scale_bytes(T, K));
   if (r > 0) {
     l.u_pad = c.take(static_cast<size_t>(T * rp * 4));  // [T][2rp] bf16: sU, or sV of the backward
     size_t part = lora_down_part_bytes(T, in, rp);
@@ -927,7 +925,7 @@ int qlora_fp8_linear_fwd(const qlora_fp8_weight* W, const qlora_bf16* X, int64_t
     g.lda1 = g.ldw1 = g.K1 = 2 * rp;
   }
   if (e == hipSuccess)
-    e = launch_fp8_rows(X, in, T, in, base + lay.xq, base + lay.xs, fp8_scale_pitch(in), s);
+    e = launch_fp8_rows(X, in, T, in, base + lay.xq, base + lay.xs, fp8_row_pitch(T), s);
   g.M = T;
   g.codes = W->codes;
   g.scales = W->scales;
@@ -935,7 +933,6 @@ int qlora_fp8_linear_fwd(const qlora_fp8_weight* W, const qlora_bf16* X, int64_t
   g.cols = in;
   g.xq = base + lay.xq;
   g.xs = base + lay.xs;
-  g.ldxs = fp8_scale_pitch(in);
   g.C = Y;
   g.part = reinterpret_cast<float*>(base + lay.split);
   if (e == hipSuccess) e = launch_fp8_gemm(g, s);
@@ -986,7 +983,7 @@ int qlora_fp8_linear_bwd(const qlora_fp8_weight* W, const qlora_bf16* X, const q
     g.lda1 = g.ldw1 = g.K1 = 2 * rp;
   }
   if (e == hipSuccess)
-    e = launch_fp8_rows(dY, out, T, out, base + lay.xq, base + lay.xs, fp8_scale_pitch(out), s);
+    e = launch_fp8_rows(dY, out, T, out, base + lay.xq, base + lay.xs, fp8_row_pitch(T), s);
   g.M = T;
   g.codes = W->codes;
   g.scales = W->scales;
@@ -995,7 +992,6 @@ int qlora_fp8_linear_bwd(const qlora_fp8_weight* W, const qlora_bf16* X, const q
   g.transposed = true;
   g.xq = base + lay.xq;
   g.xs = base + lay.xs;
-  g.ldxs = fp8_scale_pitch(out);
   g.C = dX;
   g.part = reinterpret_cast<float*>(base + lay.split);
   if (e == hipSuccess) e = launch_fp8_gemm(g, s);
