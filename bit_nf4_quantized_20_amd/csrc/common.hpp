@@ -229,8 +229,9 @@ hipError_t launch_moe_route(const float* logits, int64_t T, int E, int k, bool r
 hipError_t launch_moe_route_bwd(const float* logits, const int* ids, const float* dw, int64_t T, int E, int k,
                                 bool renorm, float* dlogits, hipStream_t s);
 // The expert layer for a few tokens: gate_up [E * 2 I][H] (expert e's gate
-// rows, then its up rows), down [E * H][I], both double-quantized NF4; h is
-// [T k][2][I] bf16 scratch (hi plane, lo plane of each pair).
+// rows, then its up rows), down [E * H][I], both double-quantized NF4.
+// Scratch: h [T k][2][I] bf16 (hi plane, lo plane of each pair), part [T k][H]
+// fp32, each below 2^30 bytes.
 struct MoeWeight {
   const uint8_t* codes; const uint8_t* absmax_q; const float* scale;
 };
@@ -239,9 +240,12 @@ struct MoeArgs {
   const uint16_t* X;
   const int* ids; const float* weights;
   uint16_t* h;
+  float* part;
   uint16_t* Y;
   int T, E, k, H, I;
-  int by_expert;  // set by the launcher
+  // set by the launcher: workgroup slots (experts or pairs), row ranges and
+  // waves that split the reduction, of the two kernels
+  int by_expert, slots, ranges_up, ranges_down, kw_up, kw_down;
 };
 hipError_t launch_moe(MoeArgs a, hipStream_t s);
 

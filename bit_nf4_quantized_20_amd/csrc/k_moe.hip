@@ -159,8 +159,41 @@ __global__ __launch_bounds__(256) void k_moe_route_bwd(const float* __restrict__
 }
 
 // ------------------------------------------------------------- experts
+//
+// Both products are the same panel product: 16-row tiles of an expert's NF4
+// rows against the columns of the pairs (token, choice) that chose it.  A
+// workgroup of eight waves takes one expert and a range of its rows; KW waves
+// share a row group and split the reduction, the others take further row
+// groups.  A wave walks its 64-weight blocks in chunks of four (lane (n = l %
+// 16, g = l / 16): block g of the chunk of row n): the columns' values of the
+// chunk go into registers once and meet RB row tiles, whose codes are
+// dequantized in registers (MFMA A operand) with their loads kDepth tiles
+// ahead.  The vector unit's 3.5 instructions per weight and HBM bound it
+// alike (16 rows x 256 weights: 900 cycles of a SIMD and 2.1 KB), so each
+// expert is read and dequantized once for all its pairs of a column tile.
 namespace {
 constexpr int kPairs = kMoeMaxPairs;
+// Shapes of a workgroup: waves, 16-row tiles per wave (RB) and tiles of codes
+// in flight (kDepth).  Measured at 9 tokens over 8 experts of 4096 x 14336 /
+// 64 tokens over 128 of 2048 x 768, gate and up product: 4 waves, RB 4, depth
+// 1 at four waves per SIMD 118 / 68 us; depth 2 at three 125 / 72; depth 4
+// at two 144 / 86; 8 waves 149 / 86.  Down product: 8 waves, RB 8, depth 2 77 /
+// 37 us; RB 4 89 / 46; 4 waves, RB 8 87 / 36.
+constexpr int kUpWaves = 4, kUpTiles = 4, kUpDepth = 1;
+constexpr int kDownWaves = 8, kDownTiles = 8, kDownDepth = 2;
+constexpr int kFewWaves = 8;  // where there are few workgroups
+constexpr uint32_t kPastEnd = 0x80000000u;  // past every buffer (all < 2^31 bytes)
+constexpr int kBufferWord3 = 0x00020000;
+constexpr int kStreamOnce = 2;              // cache policy nt
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* p, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, static_cast<int>(bytes), kBufferWord3);
+}
+__device__ __forceinline__ u32x4 load16(__amdgpu_buffer_rsrc_t r, uint32_t off, int aux) {
+  // aux has to be a constant of the instruction
+  return __builtin_bit_cast(u32x4, aux ? __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, kStreamOnce)
+                                       : __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+}
 
 // One lane's 64-weight block: 32 code bytes, absmax code, group scale.
 struct Blk {
@@ -169,32 +202,26 @@ struct Blk {
   float sc;
 };
 
-// An expert's rows: pointers to its first code byte and absmax code, the
-// group scales from its first block's group on, and that block's place in it.
-struct Rows {
-  const uint8_t* codes;
-  const uint8_t* q;
-  const float* scale;
+// An expert's rows (rows x nb blocks from block b of the whole weight on):
+// codes, absmax codes, and the group scales from its first block's group on,
+// with that block's place in the group.
+struct ExpertRows {
+  __amdgpu_buffer_rsrc_t rc, rq, rs;
   uint32_t rem;
-  __device__ __forceinline__ Rows(const MoeWeight& w, int64_t row, int64_t nb) {
-    const int64_t b = row * nb;
-    codes = w.codes + b * 32;
-    q = w.absmax_q + b;
-    scale = w.scale + (b >> 8);
+  __device__ __forceinline__ ExpertRows(const MoeWeight& w, int64_t row0, uint32_t rows, uint32_t nb) {
+    const int64_t b = row0 * nb;
+    const uint32_t blocks = rows * nb;
     rem = static_cast<uint32_t>(b & 255);
+    rc = rsrc(w.codes + b * 32, blocks * 32);
+    rq = rsrc(w.absmax_q + b, blocks);
+    rs = rsrc(w.scale + (b >> 8), ((rem + blocks + 255) >> 8) * 4);
   }
-  // block b (counted from the expert's first row)
-  __device__ __forceinline__ void load(Blk& o, uint32_t b, bool live) const {
-    o.c0 = o.c1 = u32x4{0u, 0u, 0u, 0u};
-    o.q = 0;
-    o.sc = 0.f;
-    if (live) {
-      const u32x4* p = reinterpret_cast<const u32x4*>(codes + static_cast<uint64_t>(b) * 32);
-      o.c0 = __builtin_nontemporal_load(p);
-      o.c1 = __builtin_nontemporal_load(p + 1);
-      o.q = q[b];
-      o.sc = scale[(rem + b) >> 8];
-    }
+  // block b (counted from the expert's first row); off = kPastEnd: all zero
+  __device__ __forceinline__ void load(Blk& o, uint32_t b, uint32_t off) const {
+    o.c0 = load16(rc, (b * 32) | off, 1);
+    o.c1 = load16(rc, (b * 32 + 16) | off, 1);
+    o.q = __builtin_amdgcn_raw_buffer_load_b8(rq, b | off, 0, 0);
+    o.sc = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rs, (((rem + b) >> 8) * 4) | off, 0, 0));
   }
 };
 
@@ -202,265 +229,354 @@ __device__ __forceinline__ bf16x8 as_frag(const uint32_t (&w)[4]) {
   return __builtin_bit_cast(bf16x8, u32x4{w[0], w[1], w[2], w[3]});
 }
 
-// the ids of all pairs into LDS (every thread of the workgroup; a barrier follows in the caller)
-__device__ __forceinline__ void stage_ids(int* s_ids, const int* __restrict__ ids, int P, int E, int nthreads) {
-  for (int i = threadIdx.x; i < P; i += nthreads) {
-    const int e = ids[i];
-    s_ids[i] = e >= 0 && e < E ? e : -1;  // -1: no expert
+// The pairs of one expert, found by every workgroup from the ids: a slot is
+// an expert where there are no more experts than pairs, else a pair, whose
+// workgroups work only if it is its expert's first pair.  Returns the expert
+// (-1: nothing to do) and leaves its pairs in ascending order at list.  Up to
+// 64 pairs every wave does this by itself (no barrier before its first weight
+// loads); more are staged in LDS.
+template <int NW>
+struct PairList {
+  int ids[kPairs];
+  uint16_t all[kPairs];
+  uint16_t per_wave[NW][64];
+  int n;
+};
+__device__ __forceinline__ uint64_t lanes_below() { return (uint64_t(1) << (threadIdx.x & 63)) - 1; }
+__device__ __forceinline__ void wave_lds_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+template <int NW>
+__device__ __forceinline__ int find_pairs(PairList<NW>& s, const MoeArgs& a, int slot, const uint16_t*& list, int& nc) {
+  const int tid = threadIdx.x, lane = tid & 63, P = a.T * a.k;
+  if (P <= 64) {
+    const int id = lane < P ? a.ids[lane] : -1;
+    const int e = a.by_expert ? slot : __builtin_amdgcn_readlane(id, slot);
+    if (e < 0 || e >= a.E) return -1;
+    const uint64_t hit = __ballot(id == e);
+    if (hit == 0 || (!a.by_expert && (hit & ((uint64_t(1) << slot) - 1)) != 0)) return -1;
+    uint16_t* mine = s.per_wave[tid >> 6];
+    if (id == e) mine[__popcll(hit & lanes_below())] = static_cast<uint16_t>(lane);
+    wave_lds_sync();
+    list = mine;
+    nc = __popcll(hit);
+    return e;
+  }
+  for (int i = tid; i < P; i += 64 * NW) {
+    const int e = a.ids[i];
+    s.ids[i] = e >= 0 && e < a.E ? e : -1;  // -1: no expert
+  }
+  __syncthreads();
+  const int e = a.by_expert ? slot : s.ids[slot];
+  if (tid < 64) {
+    int n = 0;
+    if (e >= 0)
+      for (int b = 0; b < P; b += 64) {
+        const bool hit = b + lane < P && s.ids[b + lane] == e;
+        const uint64_t m = __ballot(hit);
+        if (hit) s.all[n + __popcll(m & lanes_below())] = static_cast<uint16_t>(b + lane);
+        n += __popcll(m);
+      }
+    if (lane == 0) s.n = n;
+  }
+  __syncthreads();
+  list = s.all;
+  nc = s.n;
+  if (e < 0 || nc == 0 || (!a.by_expert && s.all[0] != slot)) return -1;
+  return e;
+}
+
+// acc[r][t] += rows of tile r (row offsets trow[r], in blocks, of this lane's
+// row) times the columns of tile t, over blocks [b0, b1).  The columns' values
+// lie at colf[t] (byte offsets in rx; kPastEnd: zero column), 128 bytes per
+// block, with kHiLo a second plane lo bytes further that is added in.
+template <int RB, int NT, bool kHiLo, int kDepth>
+__device__ __forceinline__ void panel(f32x4 (&acc)[RB][NT], const ExpertRows& w, const uint32_t (&trow)[RB],
+                                      __amdgpu_buffer_rsrc_t rx, const uint32_t (&colf)[NT], uint32_t lo, int b0,
+                                      int b1) {
+  static_assert(RB % kDepth == 0, "tiles of a chunk use the code registers in turn");
+  const int g = (threadIdx.x & 63) >> 4;
+  const uint32_t none = kPastEnd;
+  Blk buf[kDepth];
+#pragma unroll
+  for (int r = 0; r < kDepth; ++r) w.load(buf[r], trow[r] + b0 + g, b0 + g < b1 ? 0u : none);
+  for (int b = b0; b < b1; b += 4) {
+    const uint32_t off = b + g < b1 ? 0u : none, next = b + 4 + g < b1 ? 0u : none;
+    bf16x8 xh[8][NT], xl[kHiLo ? 8 : 1][NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const uint32_t at = (colf[t] + static_cast<uint32_t>(b + g) * 128) | off;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const u32x4 v = load16(rx, at + 16 * j, 0);
+        const uint32_t vi[4] = {v[0], v[1], v[2], v[3]};
+        uint32_t o[4];
+        to_split_order(vi, o);
+        xh[j][t] = as_frag(o);
+        if constexpr (kHiLo) {
+          const u32x4 u = load16(rx, at + lo + 16 * j, 0);
+          const uint32_t ui[4] = {u[0], u[1], u[2], u[3]};
+          to_split_order(ui, o);
+          xl[j][t] = as_frag(o);
+        }
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < RB; ++r) {
+      const Blk cur = buf[r % kDepth];
+      if (r + kDepth < RB) w.load(buf[r % kDepth], trow[r + kDepth] + b + g, off);
+      else w.load(buf[r % kDepth], trow[(r + kDepth) % RB] + b + 4 + g, next);
+      const Nf4Table tab = make_table(dq_absmax(cur.q, cur.sc));
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        uint32_t o[4];
+        lookup8_split(tab, j < 4 ? cur.c0[j] : cur.c1[j - 4], o);
+        const bf16x8 f = as_frag(o);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          acc[r][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f, xh[j][t], acc[r][t], 0, 0, 0);
+          if constexpr (kHiLo) acc[r][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f, xl[j][t], acc[r][t], 0, 0, 0);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);  // one tile's tables and lookups in registers at a time
+    }
   }
 }
-// the pairs of expert e in ascending order into list (one wave); their count
-__device__ __forceinline__ int list_pairs(const int* s_ids, int P, int e, uint16_t* list) {
-  const int lane = threadIdx.x & 63;
-  int n = 0;
-  for (int b = 0; b < P; b += 64) {
-    const bool hit = b + lane < P && s_ids[b + lane] == e;
-    const uint64_t m = __ballot(hit);
-    if (hit) list[n + __popcll(m & ((uint64_t(1) << lane) - 1))] = static_cast<uint16_t>(b + lane);
-    n += __popcll(m);
+
+// Adds the KW waves' accumulators of a row group in wave order; afterwards
+// the group's first wave holds the sums.  s: room for half of the waves.
+template <int N>
+__device__ __forceinline__ void sum_waves(f32x4 (&acc)[N], f32x4 (*s)[N][64], int wv, int kw) {
+  const int lane = threadIdx.x & 63, z = wv % kw, grp = wv / kw;
+  for (int half = kw / 2; half >= 1; half /= 2) {
+    if (z >= half && z < 2 * half) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) s[grp * (kw / 2) + z - half][i][lane] = acc[i];
+    }
+    __syncthreads();
+    if (z < half) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) acc[i] += s[grp * (kw / 2) + z][i][lane];
+    }
+    __syncthreads();
   }
-  return n;
 }
 }  // namespace
 
-// h[p] = silu(Wg_e x) * (Wu_e x) for every pair p = (token, choice) of expert
-// e.  Workgroup (rb, slot): rows [16 rb, 16 rb + 16) of expert e's gate and up
-// halves.  A slot is an expert where there are no more experts than pairs,
-// else a pair, whose workgroup works only if it is its expert's first pair:
-// either way each expert's weights are read once.  The four waves split the
-// 64-weight blocks of the rows; lane (n = l % 16, g = l / 16) dequantizes block
-// 4 c + g of row n in registers (MFMA A operand) against token columns (B
-// operand: pair n's activations at the same k).
-__global__ __launch_bounds__(256) void k_moe_gate_up(MoeArgs a) {
-  __shared__ int s_ids[kPairs];
-  __shared__ uint16_t s_list[kPairs];
-  __shared__ int s_n;
-  __shared__ f32x4 s_acc[4][2][4][64];
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int P = a.T * a.k;
-  const int blocks = a.I / 16;
-  const int rb = blockIdx.x % blocks, slot = blockIdx.x / blocks;
-  stage_ids(s_ids, a.ids, P, a.E, 256);
-  __syncthreads();
-  const int e = a.by_expert ? slot : s_ids[slot];
+// h[p] = silu(Wg_e x) * (Wu_e x) for every pair p of expert e, as a bf16 pair
+// hi + lo (16 bits of fraction), so that the down product's operand is not
+// rounded to 8 bits before Y's one rounding.  Row group: RB / 2 tiles of the
+// gate half and the same of the up half.  NT column tiles of 16 pairs at a time.
+template <int RB, int NT, int NW, int kDepth>
+__global__ __launch_bounds__(64 * NW, NT == 1 ? (kDepth == 1 ? 4 : 3) : 2) void k_moe_gate_up(MoeArgs a) {
+  __shared__ PairList<NW> s;
+  __shared__ f32x4 s_acc[NW / 2][RB * NT][64];
+  const int lane = threadIdx.x & 63;
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int kw = a.kw_up, range = blockIdx.x % a.ranges_up, slot = blockIdx.x / a.ranges_up;
+  const uint16_t* list;
+  int nc;
+  const int e = find_pairs(s, a, slot, list, nc);
   if (e < 0) return;
-  if (wv == 0) {
-    const int n = list_pairs(s_ids, P, e, s_list);
-    if (lane == 0) s_n = n;
+  const int n = lane & 15;
+  constexpr int kHalf = RB / 2;
+  const uint32_t nb = static_cast<uint32_t>(a.H / 64);
+  const ExpertRows w(a.gate_up, static_cast<int64_t>(e) * 2 * a.I, 2 * static_cast<uint32_t>(a.I), nb);
+  const __amdgpu_buffer_rsrc_t rx = rsrc(a.X, static_cast<uint32_t>(a.T) * a.H * 2);
+  const int tiles = a.I / 16;
+  const int tile0 = (range * (NW / kw) + wv / kw) * kHalf;  // the group's first tile (may lie past the last)
+  uint32_t trow[RB];
+#pragma unroll
+  for (int r = 0; r < RB; ++r) {
+    const int t = tile0 + r % kHalf;
+    trow[r] = ((r >= kHalf ? a.I : 0) + 16 * (t < tiles ? t : tiles - 1) + n) * nb;
   }
-  __syncthreads();
-  const int nc = s_n;
-  if (nc == 0 || (!a.by_expert && s_list[0] != slot)) return;
+  const int z = wv % kw, b0 = tile0 < tiles ? static_cast<int>(nb * z / kw) : 0;
+  const int b1 = tile0 < tiles ? static_cast<int>(nb * (z + 1) / kw) : 0;
 
-  const int n = lane & 15, g = lane >> 4;
-  const int64_t nb64 = a.H / 64;
-  const int nb = static_cast<int>(nb64);
-  const Rows wg(a.gate_up, (static_cast<int64_t>(e) * 2) * a.I + 16 * rb, nb64);
-  const Rows wu(a.gate_up, (static_cast<int64_t>(e) * 2 + 1) * a.I + 16 * rb, nb64);
-  const int b0 = nb * wv / 4, b1 = nb * (wv + 1) / 4;
-
-  auto run = [&](int c0, auto ntc) {
-    constexpr int NT = decltype(ntc)::value;  // column tiles of 16 pairs
-    f32x4 acc[2][NT];
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int t = 0; t < NT; ++t) acc[i][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-    const uint16_t* xp[NT];
-    bool on[NT];
+  for (int c0 = 0; c0 < nc; c0 += 16 * NT) {
+    f32x4 acc[RB][NT];
+    uint32_t colf[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       const int c = c0 + 16 * t + n;
-      on[t] = c < nc;
-      xp[t] = a.X + static_cast<int64_t>(on[t] ? s_list[c] / a.k : 0) * a.H;
+      colf[t] = c < nc ? static_cast<uint32_t>(list[c] / a.k) * a.H * 2 : kPastEnd;
+#pragma unroll
+      for (int r = 0; r < RB; ++r) acc[r][t] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
-    Blk bg, bu, ng, nu;
-    const uint32_t row = static_cast<uint32_t>(n) * nb;
-    wg.load(bg, row + b0 + g, b0 + g < b1);
-    wu.load(bu, row + b0 + g, b0 + g < b1);
-    for (int b = b0; b < b1; b += 4) {
-      const bool live = b + g < b1, next = b + 4 + g < b1;
-      wg.load(ng, row + b + 4 + g, next);
-      wu.load(nu, row + b + 4 + g, next);
-      const Nf4Table tg = make_table(dq_absmax(bg.q, bg.sc));
-      const Nf4Table tu = make_table(dq_absmax(bu.q, bu.sc));
+    panel<RB, NT, false, kDepth>(acc, w, trow, rx, colf, 0, b0, b1);
+    sum_waves<RB * NT>(reinterpret_cast<f32x4(&)[RB * NT]>(acc), s_acc, wv, kw);
+    if (z != 0) continue;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        u32x4 x[NT];
+    for (int r = 0; r < kHalf; ++r)
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          x[t] = u32x4{0u, 0u, 0u, 0u};
-          if (live && on[t]) x[t] = *reinterpret_cast<const u32x4*>(xp[t] + (b + g) * 64 + 8 * j);
+      for (int t = 0; t < NT; ++t) {
+        const int c = c0 + 16 * t + n;
+        if (tile0 + r >= tiles || c >= nc) continue;
+        float hv[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float gv = acc[r][t][q];
+          hv[q] = gv / (1.0f + __expf(-gv)) * acc[r + kHalf][t][q];
         }
-        uint32_t w[4];
-        lookup8(tg, j < 4 ? bg.c0[j] : bg.c1[j - 4], w);
-        const bf16x8 fg = as_frag(w);
-        lookup8(tu, j < 4 ? bu.c0[j] : bu.c1[j - 4], w);
-        const bf16x8 fu = as_frag(w);
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          const bf16x8 fx = __builtin_bit_cast(bf16x8, x[t]);
-          acc[0][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fg, fx, acc[0][t], 0, 0, 0);
-          acc[1][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fu, fx, acc[1][t], 0, 0, 0);
-        }
+        const uint32_t h0 = pack_bf16x2(hv[0], hv[1]), h1 = pack_bf16x2(hv[2], hv[3]);
+        const uint32_t l0 = pack_bf16x2(hv[0] - bf16_lo(h0), hv[1] - bf16_hi(h0));
+        const uint32_t l1 = pack_bf16x2(hv[2] - bf16_lo(h1), hv[3] - bf16_hi(h1));
+        uint16_t* dst = a.h + static_cast<int64_t>(list[c]) * 2 * a.I + 16 * (tile0 + r) + 4 * (lane >> 4);
+        *reinterpret_cast<u32x2*>(dst) = u32x2{h0, h1};
+        *reinterpret_cast<u32x2*>(dst + a.I) = u32x2{l0, l1};
       }
-      bg = ng;
-      bu = nu;
-    }
-    // the waves' partial sums meet in LDS, added in wave order; h as a bf16
-    // pair hi + lo (16 bits of fraction), so the down product's operand is not
-    // rounded to 8 bits a second time before Y's one rounding
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int t = 0; t < NT; ++t) s_acc[wv][i][t][lane] = acc[i][t];
-    __syncthreads();
-    for (int v = tid; v < 64 * NT; v += 256) {
-      const int t = v >> 6, l = v & 63;
-      const int c = c0 + 16 * t + (l & 15);
-      if (c >= nc) continue;
-      f32x4 gs = s_acc[0][0][t][l], us = s_acc[0][1][t][l];
-#pragma unroll
-      for (int w = 1; w < 4; ++w) {
-        gs += s_acc[w][0][t][l];
-        us += s_acc[w][1][t][l];
-      }
-      float hv[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) hv[q] = gs[q] / (1.0f + __expf(-gs[q])) * us[q];
-      const uint32_t h0 = pack_bf16x2(hv[0], hv[1]), h1 = pack_bf16x2(hv[2], hv[3]);
-      const uint32_t l0 = pack_bf16x2(hv[0] - bf16_lo(h0), hv[1] - bf16_hi(h0));
-      const uint32_t l1 = pack_bf16x2(hv[2] - bf16_lo(h1), hv[3] - bf16_hi(h1));
-      uint16_t* dst = a.h + static_cast<int64_t>(s_list[c]) * 2 * a.I + 16 * rb + 4 * (l >> 4);
-      *reinterpret_cast<u32x2*>(dst) = u32x2{h0, h1};
-      *reinterpret_cast<u32x2*>(dst + a.I) = u32x2{l0, l1};
-    }
-  };
-  if (nc <= 16) run(0, std::integral_constant<int, 1>{});
-  else if (nc <= 32) run(0, std::integral_constant<int, 2>{});
-  else
-    for (int c = 0; c < nc; c += 64) run(c, std::integral_constant<int, 4>{});
+  }
 }
 
-// Y_t = sum_j w_tj Wd_e h_tj.  Workgroup b owns rows [16 b, 16 b + 16) of Y's
-// columns for every token: its waves take (expert, range of I) units in
-// turn, each leaving its pairs' 16 sums in LDS, and the workgroup then adds
-// them per token in the order of the choices: no partial sums cross
-// workgroups and the order of additions is fixed.
-constexpr int kDownWaves = 8;
-constexpr int kDownSums = 1024;  // (range, pair) sums of 16 rows held in LDS: 64 KiB
-__global__ __launch_bounds__(64 * kDownWaves) void k_moe_down(MoeArgs a) {
-  __shared__ int s_ids[kPairs];
-  __shared__ int s_first[kMoeMaxExperts];
-  __shared__ uint16_t s_lead[kPairs];
-  __shared__ int s_leads;
-  __shared__ uint16_t s_list[kDownWaves][kPairs];
-  __shared__ float s_sum[kDownSums][16];
+// part[p] = Wd_e h[p] in fp32 for every pair p of expert e.  Row group: RB
+// tiles.  (Adding the experts inside the kernel, by the last workgroup of a
+// row range to arrive, cost a release fence per workgroup: 156 us against 11 at
+// one token.)
+template <int RB, int NT, int NW, int kDepth>
+__global__ __launch_bounds__(64 * NW, 2) void k_moe_down(MoeArgs a) {
+  __shared__ PairList<NW> s;
+  __shared__ f32x4 s_acc[NW / 2][RB * NT][64];
+  const int lane = threadIdx.x & 63;
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int kw = a.kw_down, range = blockIdx.x % a.ranges_down, slot = blockIdx.x / a.ranges_down;
+  const uint16_t* list;
+  int nc;
+  const int e = find_pairs(s, a, slot, list, nc);
+  if (e < 0) return;
+  const int n = lane & 15, tiles = a.H / 16;
+  const uint32_t nb = static_cast<uint32_t>(a.I / 64);
+  const ExpertRows w(a.down, static_cast<int64_t>(e) * a.H, static_cast<uint32_t>(a.H), nb);
+  const __amdgpu_buffer_rsrc_t rx = rsrc(a.h, static_cast<uint32_t>(a.T) * a.k * a.I * 4);
+  const int tile0 = (range * (NW / kw) + wv / kw) * RB;
+  uint32_t trow[RB];
+#pragma unroll
+  for (int r = 0; r < RB; ++r) trow[r] = (16 * (tile0 + r < tiles ? tile0 + r : tiles - 1) + n) * nb;
+  const int z = wv % kw, b0 = tile0 < tiles ? static_cast<int>(nb * z / kw) : 0;
+  const int b1 = tile0 < tiles ? static_cast<int>(nb * (z + 1) / kw) : 0;
+  for (int c0 = 0; c0 < nc; c0 += 16 * NT) {
+    f32x4 acc[RB][NT];
+    uint32_t colf[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const int c = c0 + 16 * t + n;
+      colf[t] = c < nc ? static_cast<uint32_t>(list[c]) * a.I * 4 : kPastEnd;
+#pragma unroll
+      for (int r = 0; r < RB; ++r) acc[r][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+    panel<RB, NT, true, kDepth>(acc, w, trow, rx, colf, a.I * 2, b0, b1);
+    sum_waves<RB * NT>(reinterpret_cast<f32x4(&)[RB * NT]>(acc), s_acc, wv, kw);
+    if (z != 0) continue;
+#pragma unroll
+    for (int r = 0; r < RB; ++r)
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const int c = c0 + 16 * t + n;
+        if (tile0 + r < tiles && c < nc)
+          *reinterpret_cast<f32x4*>(a.part + static_cast<int64_t>(list[c]) * a.H + 16 * (tile0 + r) +
+                                    4 * (lane >> 4)) = acc[r][t];
+      }
+  }
+}
+
+// Y_t = sum_j w_tj part[t k + j], the choices added in order; a thread takes
+// four columns of one token.
+__global__ __launch_bounds__(256) void k_moe_sum(MoeArgs a) {
+  const int v = blockIdx.x * 256 + threadIdx.x, quads = a.H / 4;
+  if (v >= a.T * quads) return;
+  const int t = v / quads, r = v % quads * 4;
+  f32x4 y = {0.f, 0.f, 0.f, 0.f};
+  const float* src = a.part + static_cast<int64_t>(t) * a.k * a.H + r;
+  for (int j0 = 0; j0 < a.k; j0 += 8) {
+    // eight choices' loads in flight; a place that is no choice was not
+    // written and does not count, whatever it holds
+    f32x4 d[8];
+    float w[8];
+    bool on[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int j = j0 + i < a.k ? j0 + i : a.k - 1;
+      d[i] = *reinterpret_cast<const f32x4*>(src + static_cast<int64_t>(j) * a.H);
+      w[i] = a.weights[t * a.k + j];
+      const int e = a.ids[t * a.k + j];
+      on[i] = j0 + i < a.k && e >= 0 && e < a.E;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) y[q] = on[i] ? __builtin_fmaf(w[i], d[i][q], y[q]) : y[q];
+  }
+  *reinterpret_cast<u32x2*>(a.Y + static_cast<int64_t>(t) * a.H + r) =
+      u32x2{pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3])};
+}
+
+// The down product of at most 64 pairs in one launch: a workgroup owns one
+// 16-row tile of Y's columns for every token; its waves take (expert, range of
+// I) units in turn, leave each pair's 16 sums in LDS, and the workgroup adds
+// them per token in the order of the choices.
+__global__ __launch_bounds__(64 * kFewWaves) void k_moe_down_few(MoeArgs a) {
+  constexpr int kMost = 64;
+  __shared__ int s_ids[kMost];
+  __shared__ int s_lead[kMost];
+  __shared__ uint16_t s_list[kFewWaves][kMost];
+  __shared__ f32x4 s_sum[kFewWaves][kMost][4];  // [range][pair]
   const int tid = threadIdx.x, lane = tid & 63;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int P = a.T * a.k;
-  const int64_t r0 = static_cast<int64_t>(blockIdx.x) * 16;
-  stage_ids(s_ids, a.ids, P, a.E, 64 * kDownWaves);
-  for (int i = tid; i < a.E; i += 64 * kDownWaves) s_first[i] = P;
-  __syncthreads();
-  for (int p = tid; p < P; p += 64 * kDownWaves)
-    if (s_ids[p] >= 0) atomicMin(&s_first[s_ids[p]], p);
-  __syncthreads();
-  // the experts met, by their first pair
+  // every wave finds the experts met, in the order of their first pairs
+  int id = lane < P ? a.ids[lane] : -1;
+  if (id < 0 || id >= a.E) id = -1;
+  bool first = id >= 0;
+  for (int j = 0; j + 1 < P; ++j)
+    if (lane > j && __builtin_amdgcn_readlane(id, j) == id) first = false;
+  const uint64_t lm = __ballot(first);
+  const int leads = __popcll(lm);
   if (wv == 0) {
-    int m = 0;
-    for (int b = 0; b < P; b += 64) {
-      const int p = b + lane;
-      const bool hit = p < P && s_ids[p] >= 0 && s_first[s_ids[p]] == p;
-      const uint64_t mask = __ballot(hit);
-      if (hit) s_lead[m + __popcll(mask & ((uint64_t(1) << lane) - 1))] = static_cast<uint16_t>(s_ids[p]);
-      m += __popcll(mask);
-    }
-    if (lane == 0) s_leads = m;
+    s_ids[lane] = id;
+    if (first) s_lead[__popcll(lm & lanes_below())] = id;
   }
   __syncthreads();
-  const int leads = s_leads;
-  const int nb = a.I / 64;
+  const uint32_t nb = static_cast<uint32_t>(a.I / 64);
   // ranges of I per expert: more than one where there are fewer experts than waves
-  int ks = leads > 0 ? kDownWaves / leads : 1;
-  ks = ks > kDownSums / P ? kDownSums / P : ks;
-  ks = ks > nb / 4 ? nb / 4 : ks;
+  int ks = leads > 0 ? kFewWaves / leads : 1;
+  ks = ks > static_cast<int>(nb) ? static_cast<int>(nb) : ks;
   ks = ks < 1 ? 1 : ks;
-
-  const int n = lane & 15, g = lane >> 4;
-  for (int u = wv; u < leads * ks; u += kDownWaves) {
-    const int e = s_lead[u / ks], z = u % ks;
-    uint16_t* list = s_list[wv];
-    const int nc = list_pairs(s_ids, P, e, list);
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  const int n = lane & 15;
+  const __amdgpu_buffer_rsrc_t rx = rsrc(a.h, static_cast<uint32_t>(P) * a.I * 4);
+  const uint32_t trow[1] = {(16 * blockIdx.x + n) * nb};
+  for (int u = wv; u < leads * ks; u += kFewWaves) {
+    const int e = __builtin_amdgcn_readfirstlane(s_lead[u / ks]), z = u % ks;
+    const uint64_t hit = __ballot(id == e);
+    const int nc = __popcll(hit);
+    if (id == e) s_list[wv][__popcll(hit & lanes_below())] = static_cast<uint16_t>(lane);
+    wave_lds_sync();
+    const ExpertRows w(a.down, static_cast<int64_t>(e) * a.H, static_cast<uint32_t>(a.H), nb);
+    for (int c0 = 0; c0 < nc; c0 += 16) {
+      const int p = c0 + n < nc ? s_list[wv][c0 + n] : -1;
+      const uint32_t colf[1] = {p >= 0 ? static_cast<uint32_t>(p) * a.I * 4 : kPastEnd};
+      f32x4 acc[1][1] = {{f32x4{0.f, 0.f, 0.f, 0.f}}};
+      panel<1, 1, true, 1>(acc, w, trow, rx, colf, a.I * 2, static_cast<int>(nb * z / ks),
+                        static_cast<int>(nb * (z + 1) / ks));
+      if (p >= 0) s_sum[z][p][lane >> 4] = acc[0][0];
+    }
     __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-    const Rows wd(a.down, static_cast<int64_t>(e) * a.H + r0, nb);
-    const int b0 = nb * z / ks, b1 = nb * (z + 1) / ks;
-    const uint32_t row = static_cast<uint32_t>(n) * nb;
-    auto run = [&](int c0, auto ntc) {
-      constexpr int NT = decltype(ntc)::value;
-      f32x4 acc[NT];
-      const uint16_t* hp[NT];
-      bool on[NT];
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-        const int c = c0 + 16 * t + n;
-        on[t] = c < nc;
-        hp[t] = a.h + static_cast<int64_t>(on[t] ? list[c] : 0) * 2 * a.I;
-      }
-      Blk cur, nxt;
-      wd.load(cur, row + b0 + g, b0 + g < b1);
-      for (int b = b0; b < b1; b += 4) {
-        const bool live = b + g < b1;
-        wd.load(nxt, row + b + 4 + g, b + 4 + g < b1);
-        const Nf4Table tab = make_table(dq_absmax(cur.q, cur.sc));
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          uint32_t w[4];
-          lookup8(tab, j < 4 ? cur.c0[j] : cur.c1[j - 4], w);
-          const bf16x8 fw = as_frag(w);
-#pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            u32x4 hi = u32x4{0u, 0u, 0u, 0u}, lo = hi;
-            if (live && on[t]) {
-              hi = *reinterpret_cast<const u32x4*>(hp[t] + (b + g) * 64 + 8 * j);
-              lo = *reinterpret_cast<const u32x4*>(hp[t] + a.I + (b + g) * 64 + 8 * j);
-            }
-            acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fw, __builtin_bit_cast(bf16x8, hi), acc[t], 0, 0, 0);
-            acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fw, __builtin_bit_cast(bf16x8, lo), acc[t], 0, 0, 0);
-          }
-        }
-        cur = nxt;
-      }
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-        if (on[t])
-          *reinterpret_cast<f32x4*>(&s_sum[z * P + list[c0 + 16 * t + n]][4 * g]) = acc[t];
-    };
-    if (nc <= 16) run(0, std::integral_constant<int, 1>{});
-    else if (nc <= 32) run(0, std::integral_constant<int, 2>{});
-    else
-      for (int c = 0; c < nc; c += 64) run(c, std::integral_constant<int, 4>{});
   }
   __syncthreads();
-  // token t, rows r0 + 4 q .. + 3
-  for (int v = tid; v < a.T * 4; v += 64 * kDownWaves) {
+  for (int v = tid; v < a.T * 4; v += 64 * kFewWaves) {
     const int t = v >> 2, q = v & 3;
     f32x4 y = {0.f, 0.f, 0.f, 0.f};
     for (int j = 0; j < a.k; ++j) {
       const int p = t * a.k + j;
       if (s_ids[p] < 0) continue;
-      f32x4 s = {0.f, 0.f, 0.f, 0.f};
-      for (int z = 0; z < ks; ++z) s += *reinterpret_cast<const f32x4*>(&s_sum[z * P + p][4 * q]);
+      f32x4 d = s_sum[0][p][q];
+      for (int z = 1; z < ks; ++z) d += s_sum[z][p][q];
       const float w = a.weights[p];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) y[i] = __builtin_fmaf(w, s[i], y[i]);
+      for (int i = 0; i < 4; ++i) y[i] = __builtin_fmaf(w, d[i], y[i]);
     }
-    *reinterpret_cast<u32x2*>(a.Y + static_cast<int64_t>(t) * a.H + r0 + 4 * q) =
+    *reinterpret_cast<u32x2*>(a.Y + static_cast<int64_t>(t) * a.H + 16 * blockIdx.x + 4 * q) =
         u32x2{pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3])};
   }
 }
@@ -501,14 +617,53 @@ hipError_t launch_moe_route_bwd(const float* logits, const int* ids, const float
   return hipGetLastError();
 }
 
+namespace {
+// Waves that split a reduction of nb 64-weight blocks: as many of the eight as
+// keep the lanes at least 7/8 busy (a chunk is four blocks), with few
+// workgroups as many as have a block at all.
+int moe_split_waves(int nb, int waves, bool few) {
+  int kw = waves;
+  if (few) {
+    while (kw > 1 && kw > nb) kw /= 2;
+    return kw;
+  }
+  while (kw > 1 && kw * round_up(ceil_div(nb, kw), 4) * 7 > nb * 8) kw /= 2;
+  return kw;
+}
+}  // namespace
+
 hipError_t launch_moe(MoeArgs a, hipStream_t s) {
   const int P = a.T * a.k;
   a.by_expert = a.E <= P ? 1 : 0;
-  const int64_t slots = a.by_expert ? a.E : P;
-  hipLaunchKernelGGL(k_moe_gate_up, dim3(static_cast<uint32_t>(a.I / 16 * slots)), dim3(256), 0, s, a);
+  a.slots = a.by_expert ? a.E : P;
+  // wide row groups (four 16-row tiles a wave) where those still fill the chip
+  // twice, else the narrowest
+  const bool few_up = int64_t(a.slots) * a.I / 32 < 1024;
+  const bool few_down = P <= 64 && int64_t(a.slots) * a.H / 64 < 512;
+  // pairs per expert on average: above half a column tile, two of them at a time
+  const bool two = P > 8 * a.E;
+  const int tiles_down = two ? 4 : kDownTiles;
+  const int waves_up = few_up ? kFewWaves : kUpWaves, tiles_up = few_up ? 1 : kUpTiles / 2;
+  a.kw_up = moe_split_waves(a.H / 64, waves_up, few_up);
+  a.kw_down = moe_split_waves(a.I / 64, kDownWaves, false);
+  a.ranges_up = static_cast<int>(ceil_div(a.I, 16 * tiles_up * (waves_up / a.kw_up)));
+  a.ranges_down = static_cast<int>(ceil_div(a.H, 16 * tiles_down * (kDownWaves / a.kw_down)));
+  const dim3 block_up(64 * kUpWaves), block_down(64 * kDownWaves), few(64 * kFewWaves), up(static_cast<uint32_t>(a.ranges_up * a.slots));
+  if (few_up) hipLaunchKernelGGL((k_moe_gate_up<2, 1, kFewWaves, 2>), up, few, 0, s, a);
+  else if (!two) hipLaunchKernelGGL((k_moe_gate_up<kUpTiles, 1, kUpWaves, kUpDepth>), up, block_up, 0, s, a);
+  else hipLaunchKernelGGL((k_moe_gate_up<kUpTiles, 2, kUpWaves, 2>), up, block_up, 0, s, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(k_moe_down, dim3(static_cast<uint32_t>(a.H / 16)), dim3(64 * kDownWaves), 0, s, a);
+  if (few_down) {
+    hipLaunchKernelGGL(k_moe_down_few, dim3(static_cast<uint32_t>(a.H / 16)), few, 0, s, a);
+    return hipGetLastError();
+  }
+  const dim3 down(static_cast<uint32_t>(a.ranges_down * a.slots));
+  if (!two) hipLaunchKernelGGL((k_moe_down<kDownTiles, 1, kDownWaves, kDownDepth>), down, block_down, 0, s, a);
+  else hipLaunchKernelGGL((k_moe_down<4, 2, kDownWaves, kDownDepth>), down, block_down, 0, s, a);
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(k_moe_sum, dim3(static_cast<uint32_t>(ceil_div(int64_t(a.T) * a.H / 4, 256))), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 

@@ -1024,8 +1024,26 @@ bool moe_shapes_ok(int64_t T, int64_t hidden, int64_t inter, int64_t k) {
   if (T < 0 || T > QLORA_MOE_MAX_TOKENS || k < 1 || k > QLORA_MOE_MAX_CHOICES || T * k > QLORA_MOE_MAX_PAIRS)
     return false;
   constexpr int64_t kMaxSide = int64_t(1) << 20;
-  return hidden >= 64 && hidden < kMaxSide && hidden % 64 == 0 && inter >= 64 && inter < kMaxSide && inter % 64 == 0 &&
-         hidden <= (int64_t(1) << 31) / inter;  // one expert's blocks are counted in 32 bits
+  if (hidden < 64 || hidden >= kMaxSide || hidden % 64 != 0 || inter < 64 || inter >= kMaxSide || inter % 64 != 0)
+    return false;
+  // one expert's codes (hidden * inter bytes of gate and up) and the pairs'
+  // scratch planes are addressed with 32-bit offsets (bit 31 marks an offset
+  // past the end, so a plane's offsets plus one row stay below it)
+  constexpr int64_t kMax = int64_t(1) << 31;
+  const int64_t pairs = T * k > 0 ? T * k : 1;
+  return hidden < kMax / inter && hidden < kMax / 8 / pairs && inter < kMax / 8 / pairs;
+}
+
+struct MoeLayout {
+  size_t h, part, total;
+};
+MoeLayout moe_layout(int64_t T, int64_t hidden, int64_t inter, int64_t k) {
+  MoeLayout l{};
+  Carve c;
+  l.h = c.take(static_cast<size_t>(T * k * inter * 4));      // bf16 hi and lo of each pair's hidden values
+  l.part = c.take(static_cast<size_t>(T * k * hidden * 4));  // each pair's down product, fp32
+  l.total = c.off;
+  return l;
 }
 
 static_assert(QLORA_MOE_MAX_EXPERTS == kMoeMaxExperts && QLORA_MOE_MAX_CHOICES == kMoeMaxChoices &&
@@ -1059,7 +1077,7 @@ int qlora_moe_route_bwd(const float* logits, const int32_t* ids, const float* dw
 
 size_t qlora_moe_workspace_bytes(int64_t T, int64_t hidden, int64_t inter, int64_t k) {
   if (!moe_shapes_ok(T, hidden, inter, k)) return 0;
-  const size_t need = static_cast<size_t>(T * k * inter * 4);  // h of each pair: bf16 hi and lo
+  const size_t need = moe_layout(T, hidden, inter, k).total;
   return need > kMinWorkspace ? need : kMinWorkspace;
 }
 
@@ -1075,16 +1093,19 @@ int qlora_moe_fwd(const qlora_nf4_weight* gate_up, const qlora_nf4_weight* down,
   if (T > 0 && (!X || !ids || !weights || !Y)) return QLORA_ERR_NULL;
   if (!aligned16(X) || !aligned16(ids) || !aligned16(weights) || !aligned16(Y)) return QLORA_ERR_ALIGN;
   if (T == 0) return QLORA_OK;
-  if (ws == nullptr || ws_bytes < static_cast<size_t>(T * k * inter * 4)) return QLORA_ERR_WORKSPACE;
+  const MoeLayout lay = moe_layout(T, hidden, inter, k);
+  if (ws == nullptr || ws_bytes < lay.total) return QLORA_ERR_WORKSPACE;
   if (!aligned16(ws)) return QLORA_ERR_ALIGN;
   if (int st = check_device()) return st;
+  uint8_t* base = static_cast<uint8_t*>(ws);
   MoeArgs a{};
   a.gate_up = MoeWeight{gate_up->codes, gate_up->absmax_q, gate_up->absmax_scale};
   a.down = MoeWeight{down->codes, down->absmax_q, down->absmax_scale};
   a.X = X;
   a.ids = ids;
   a.weights = weights;
-  a.h = static_cast<uint16_t*>(ws);
+  a.h = reinterpret_cast<uint16_t*>(base + lay.h);
+  a.part = reinterpret_cast<float*>(base + lay.part);
   a.Y = Y;
   a.T = static_cast<int>(T);
   a.E = static_cast<int>(experts);
