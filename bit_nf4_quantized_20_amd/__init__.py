@@ -575,19 +575,19 @@ class FP8Weight:
 
 
 def _arg(t, dtype, shape, name: str, dev):
-    """A contiguous tensor of this type, device and number of elements
-    (shape: its sizes, or its element count)."""
+    """A contiguous tensor of this type, device and size (shape: its sizes, or
+    its element count).  One chain of tests for the call that is right; what
+    is wrong is found out afterwards."""
+    if (t.dtype is dtype and t.device == dev and t.is_contiguous() and dev.type == "cuda"
+            and (t.numel() == shape if type(shape) is int else t.shape == shape)):
+        return
     if t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if t.device != dev or dev.type != "cuda":
         raise ValueError(f"{name}: on {t.device}, the call runs on {dev} (a GPU is needed)")
     if not t.is_contiguous():
         raise ValueError(f"{name}: must be contiguous")
-    if isinstance(shape, int):
-        if t.numel() != shape:
-            raise ValueError(f"{name}: expected {shape} elements, got {t.numel()}")
-    elif tuple(t.shape) != shape:
-        raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
+    raise ValueError(f"{name}: expected {shape} elements, got {tuple(t.shape)}")
 
 
 def _matrix(t, name: str):
@@ -597,13 +597,20 @@ def _matrix(t, name: str):
     return t.shape
 
 
+# the current stream's handle by device index (the public query builds a
+# Stream object, 1.9 us against 0.1 of a call's 8)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _on(dev, fn, where: str, *args):
     """Calls fn(*args, stream) with dev current, on dev's current stream."""
-    if torch.cuda.current_device() == dev.index:
-        st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    index = dev.index
+    if torch.cuda.current_device() == index:
+        st = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(dev):
-            st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+            st = fn(*args, _raw_stream(index))
     if st != QLORA_OK:
         raise QloraError(st, where)
 
@@ -611,25 +618,23 @@ def _on(dev, fn, where: str, *args):
 _SCRATCH = {}
 
 
-def _scratch(ws, need: int, where: str, dev):
-    """The caller's workspace, or one kept per (device, stream).  Under graph
-    capture it is a new allocation of the graph's own pool: a replay then
-    shares no scratch with eager calls or with other graphs."""
-    if ws is not None:
-        if ws.device != dev:
-            raise ValueError(f"ws: on {ws.device}, the call runs on {dev}")
-        if not ws.is_contiguous():
-            raise ValueError("ws: must be contiguous")
-        return ws
-    if need == 0:  # refused shapes: the library says why
-        return make_workspace(256, dev)
-    if torch.cuda.is_current_stream_capturing():
-        return make_workspace(need, dev)
-    key = (dev.index, torch.cuda.current_stream(dev).cuda_stream)
-    ws = _SCRATCH.get(key)
-    if ws is None or ws.numel() < need:
-        ws = make_workspace(need, dev)
-        _SCRATCH[key] = ws
+def _scratch(ws, need: int, dev):
+    """The caller's workspace, or one kept per (device, stream): its address
+    and size.  Under graph capture it is a new allocation of the graph's own
+    pool: a replay then shares no scratch with eager calls or with other
+    graphs."""
+    if ws is None:
+        if torch.cuda.is_current_stream_capturing():
+            ws = make_workspace(need, dev)
+        else:
+            key = (dev.index, _raw_stream(dev.index))
+            ws = _SCRATCH.get(key)
+            if ws is None or ws.numel() < need:
+                _SCRATCH[key] = ws = make_workspace(need, dev)
+    elif ws.device != dev:
+        raise ValueError(f"ws: on {ws.device}, the call runs on {dev}")
+    elif not ws.is_contiguous():
+        raise ValueError("ws: must be contiguous")
     return ws
 
 
@@ -702,7 +707,7 @@ def qlora_fp8_linear_fwd(W: FP8Weight, X, A, B, r: int, alpha: float, Y=None, ws
     if Y is None:
         Y = torch.empty(T, W.rows, dtype=torch.bfloat16, device=dev)
     _arg(Y, torch.bfloat16, T * W.rows, "Y", dev)
-    ws = _scratch(ws, qlora_fp8_workspace_bytes(T, W.cols, W.rows, r, False), "qlora_fp8_linear_fwd", dev)
+    ws = _scratch(ws, qlora_fp8_workspace_bytes(T, W.cols, W.rows, r, False), dev)
     _on(dev, _lib.qlora_fp8_linear_fwd, "qlora_fp8_linear_fwd", ctypes.byref(W._c()), X.data_ptr(), T,
         A.data_ptr() if r > 0 else None, B.data_ptr() if r > 0 else None, r, float(alpha), Y.data_ptr(),
         ws.data_ptr(), ws.numel() * ws.element_size())
@@ -730,7 +735,7 @@ def qlora_fp8_linear_bwd(W: FP8Weight, X, dY, A, B, r: int, alpha: float, dX=Non
         _arg(dB, torch.float32, W.rows * r, "dB", dev)
     else:
         X = A = B = dA = dB = None
-    ws = _scratch(ws, qlora_fp8_workspace_bytes(T, W.cols, W.rows, r, True), "qlora_fp8_linear_bwd", dev)
+    ws = _scratch(ws, qlora_fp8_workspace_bytes(T, W.cols, W.rows, r, True), dev)
     ptr = (lambda t: t.data_ptr() if t is not None else None)
     _on(dev, _lib.qlora_fp8_linear_bwd, "qlora_fp8_linear_bwd", ctypes.byref(W._c()), ptr(X), dY.data_ptr(), T,
         ptr(A), ptr(B), r, float(alpha), dX.data_ptr(), ptr(dA), ptr(dB), ws.data_ptr(),
@@ -802,7 +807,7 @@ def qlora_moe_fwd(gate_up: NF4Weight, down: NF4Weight, experts: int, X, ids, wei
     if Y is None:
         Y = torch.empty(T, hidden, dtype=torch.bfloat16, device=dev)
     _arg(Y, torch.bfloat16, T * hidden, "Y", dev)
-    ws = _scratch(ws, qlora_moe_workspace_bytes(T, hidden, inter, k), "qlora_moe_fwd", dev)
+    ws = _scratch(ws, qlora_moe_workspace_bytes(T, hidden, inter, k), dev)
     _on(dev, _lib.qlora_moe_fwd, "qlora_moe_fwd", ctypes.byref(gate_up._c()), ctypes.byref(down._c()), experts,
         X.data_ptr(), T, ids.data_ptr(), weights.data_ptr(), k, Y.data_ptr(), ws.data_ptr(),
         ws.numel() * ws.element_size())

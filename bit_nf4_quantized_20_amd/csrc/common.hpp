@@ -249,6 +249,15 @@ struct MoeArgs {
 };
 hipError_t launch_moe(MoeArgs a, hipStream_t s);
 
+// Small-token forward of an 8-bit weight (fp8_decode_fits, r <= 256): Y = X_hat
+// W_hat^T + s U B^T.  U = X A^T is formed inside the kernel (u null) where
+// fp8_decode_fuses(out, in, r), else taken from u [T][r] fp32.
+bool fp8_decode_fits(int64_t T, int64_t in);
+bool fp8_decode_fuses(int64_t out, int64_t in, int64_t r);
+hipError_t launch_fp8_decode(const uint8_t* codes, const uint8_t* scales, int64_t out, int64_t in, const uint16_t* X,
+                             int64_t T, const uint16_t* A, const uint16_t* B, int64_t r, float s, const float* u,
+                             uint16_t* Y, hipStream_t st);
+
 // W_merged[m][n] = bf16(W_hat[m][n] + s * sum_j Bp[m][j] Atp[n][j]) for the
 // NF4 weight [out][in] (out % 64 == 0, in % 64 == 0); Bp [out][ldp] and Atp
 // [in][ldp] hold B and A^T zero-padded to rp (a multiple of 16) columns.
@@ -312,6 +321,9 @@ struct BwdSmallDev {
 // dxp_bytes: the space at dxp (caps the row splits)
 hipError_t launch_bwd_small(BwdSmallDev a, size_t dxp_bytes, bool absmax_fp32, hipStream_t s);
 size_t bwd_small_uv_bytes(int64_t T, int64_t in, const int64_t* outs, int n, int64_t r);
+// The same for one 8-bit weight (n = 1, proj[0]: codes, absmax_q = the scale
+// bytes); r = 0: no adapter, two launches.
+hipError_t launch_fp8_bwd_small(BwdSmallDev a, size_t dxp_bytes, hipStream_t s);
 
 struct DecodeProj {
   const uint8_t* codes; const uint8_t* absmax_q; const float* scale;

@@ -7,7 +7,9 @@
 //                              base, dX = (W_hat + s B A)^T dY; dA, dB by the
 //                              chain rule, no gradient for W_hat)
 //
-// over n projections stacked along the rows of W (q|k|v: dY's columns
+// (for an 8-bit base dX = dY_hat W_hat + (s V) A with dY_hat = dY quantized
+// per token and 128 rows, see fp8_format.hpp), over n projections stacked
+// along the rows of W (q|k|v: dY's columns
 // [row0_i, row0_i + out_i) belong to projection i).  The weight is read once
 // as codes; W_hat exists only in LDS, one 64 x 64 tile per wave at a time.
 //
@@ -33,6 +35,7 @@
 //  * dA_i[j][k] = sum_t sV_i[t][j] X[t][k] and dB_i[m][j] = sum_t dY[t][m]
 //    sU_i[t][j], each element once (no atomics: written, reproducible).
 #include "common.hpp"
+#include "fp8_format.hpp"
 #include "nf4_format.hpp"
 
 namespace qlora {
@@ -150,12 +153,112 @@ __device__ __forceinline__ void uv_part(const BwdSmallDev& a, int q, uint16_t* l
 }
 }  // namespace
 
+// The weight's format: NF4 with double-quantized or fp32 absmax, or 8 bits.
+constexpr int kSmallNf4 = 0, kSmallNf4Fp32 = 1, kSmallFp8 = 2;
+
+namespace {
+// dX row split of an 8-bit weight: acc[nt] lane (t = i16, g): columns n0 + 16
+// nt + 4 g .. + 3.  A wave takes 128-row chunks (one scale per chunk and
+// column block) in turn, the next one's codes and dY in registers meanwhile.
+// The codes go into the wave's LDS tile as they lie in memory (64 bytes per
+// row) and come back transposed as the A operand of v_mfma_scale
+// (16 columns x 128 rows, lane group g: rows 32 g .. + 31); a token's 128 dY
+// values meet in the four lanes that hold them for their scale, and are the B
+// operand.  16-byte chunk c of row k sits at c ^ key(k), which spreads the
+// 16 x 8-row pieces that 32 lanes read over all banks.
+__device__ __forceinline__ int f8s_key(int k) { return ((k >> 2) & 1) | ((k >> 4) & 2); }
+
+__device__ __forceinline__ void fp8_split(const BwdSmallDev& a, int64_t n0, int c0, int c1, uint16_t* tile16,
+                                          f32x4 (&acc)[4]) {
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+  const int i16 = lane & 15, g = lane >> 4;
+  const int64_t in = a.in, N = a.N;
+  uint8_t* const tile = reinterpret_cast<uint8_t*>(tile16);
+  const uint8_t* const w = a.set.proj[0].codes;
+  const uint8_t* const scales = a.set.proj[0].absmax_q;
+  const int64_t cb = ceil_div(in, kF8Block);
+  struct Stage {
+    u32x4 w[8], y[4];
+    uint32_t sw;
+  };
+  auto load = [&](Stage& st, int c) {  // chunk c's codes, dY and scale; rows past the last are zero
+    const int64_t k0 = static_cast<int64_t>(c) * kF8Block;
+    const bool live = c < c1;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int64_t k = k0 + 16 * i + (lane >> 2);
+      st.w[i] = u32x4{0u, 0u, 0u, 0u};
+      if (live && k < N)
+        st.w[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(w + k * in + n0 + 16 * (lane & 3)));
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t k = k0 + 32 * g + 8 * i;
+      st.y[i] = u32x4{0u, 0u, 0u, 0u};
+      if (live && i16 < a.T && k < N) st.y[i] = *reinterpret_cast<const u32x4*>(a.dY + i16 * N + k);
+    }
+    st.sw = live ? scales[static_cast<int64_t>(c) * cb + n0 / kF8Block] : 0;
+  };
+  auto sync = [] {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+  };
+  Stage cur;
+  load(cur, c0 + wv);
+  for (int c = c0 + wv; c < c1; c += 4) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int k = 16 * i + (lane >> 2);
+      *reinterpret_cast<u32x4*>(tile + k * 64 + (((lane & 3) ^ f8s_key(k)) << 4)) = cur.w[i];
+    }
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int d = 0; d < 4; ++d)
+        m = max(m, max((cur.y[i][d] << 16) & 0x7fffffffu, cur.y[i][d] & 0x7fff0000u));
+    m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), 16)));
+    m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), 32)));
+    const uint32_t sb = f8_scale_byte(m);
+    const float inv = f8_inv_scale(sb);
+    i32x8 fy;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int d = 0; d < 2; ++d)
+        fy[2 * i + d] = static_cast<int>(f8_pack4(bf16_lo(cur.y[i][2 * d]) * inv, bf16_hi(cur.y[i][2 * d]) * inv,
+                                                  bf16_lo(cur.y[i][2 * d + 1]) * inv, bf16_hi(cur.y[i][2 * d + 1]) * inv));
+    const int sw = static_cast<int>(cur.sw);
+    load(cur, c + 4);
+    sync();
+#pragma unroll
+    for (int nt = 0; nt < 4; ++nt) {
+      i32x8 fw;
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        // lane i16 of group g supplies row 32 g + 8 s + i16 / 2 at columns 8
+        // (i16 % 2) .. + 7 and receives column i16 of the eight rows
+        const int k = 32 * g + 8 * s + (i16 >> 1);
+        const i32x2 v = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+            (__attribute__((address_space(3))) i32x2*)(tile + k * 64 + ((nt ^ f8s_key(k)) << 4) + 8 * (i16 & 1)));
+        fw[2 * s] = v[0];
+        fw[2 * s + 1] = v[1];
+      }
+      acc[nt] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fw, fy, acc[nt], 0, 0, 0, sw, 0, static_cast<int>(sb));
+    }
+    sync();  // the tile is read before the next chunk overwrites it
+  }
+}
+}  // namespace
+
 // Launch 1: workgroups [0, a.uvw) the U and V chunks (first, so that they
 // run beside the dX row splits instead of after them; the count is padded to
 // a multiple of 8, the padding exits at once, so the splits keep their XCD
 // order), then [a.uvw, a.uvw + gp) the dX row splits.
-template <bool kFp32>
+template <int kFormat>
 __global__ __launch_bounds__(256) void k_bwd_small_part(BwdSmallDev a) {
+  constexpr bool kFp32 = kFormat == kSmallNf4Fp32;
   __shared__ __attribute__((aligned(16))) uint16_t s_w[4][64 * kDxPitch];
   __shared__ f32x4 s_acc[4][4][64];
   const int L0 = static_cast<int>(blockIdx.x);
@@ -174,7 +277,7 @@ __global__ __launch_bounds__(256) void k_bwd_small_part(BwdSmallDev a) {
   int strip, split;
   dx_strip_split(L, static_cast<int>(in / 64), static_cast<int>(in / 64) * nsplits, strip, split);
   const int64_t n0 = static_cast<int64_t>(strip) * 64;
-  const int nchunks = static_cast<int>(N / 64);
+  const int nchunks = static_cast<int>(kFormat == kSmallFp8 ? (N + kF8Block - 1) / kF8Block : N / 64);
   const int c0 = split * chunks_per_split;
   const int c1 = min(c0 + chunks_per_split, nchunks);
 
@@ -191,6 +294,8 @@ __global__ __launch_bounds__(256) void k_bwd_small_part(BwdSmallDev a) {
   for (int nt = 0; nt < 4; ++nt) acc[nt] = f32x4{0.f, 0.f, 0.f, 0.f};
   uint16_t* tile = s_w[wv];
 
+  if constexpr (kFormat == kSmallFp8) fp8_split(a, n0, c0, c1, tile, acc);
+  else
   for (int c = c0 + wv; c < c1; c += 4) {
     const int64_t R0 = static_cast<int64_t>(c) * 64;  // the chunk's first row of the stack
     int pj = 0;
@@ -397,9 +502,11 @@ int dx_small_splits(int64_t N, int64_t in, int T, size_t part_bytes) {
   return splits < 1 ? 1 : splits;
 }
 
-hipError_t launch_bwd_small(BwdSmallDev a, size_t dxp_bytes, bool absmax_fp32, hipStream_t s) {
+namespace {
+template <int kFormat>
+hipError_t launch_bwd_small_as(BwdSmallDev a, size_t dxp_bytes, hipStream_t s) {
   const int strips = static_cast<int>(a.in / 64);
-  const int nchunks = static_cast<int>(a.N / 64);
+  const int nchunks = static_cast<int>(kFormat == kSmallFp8 ? ceil_div(a.N, kF8Block) : a.N / 64);
   const int splits = dx_small_splits(a.N, a.in, a.T, dxp_bytes);
   a.per = (nchunks + splits - 1) / splits;
   a.splits = (nchunks + a.per - 1) / a.per;  // splits that get chunks
@@ -407,18 +514,32 @@ hipError_t launch_bwd_small(BwdSmallDev a, size_t dxp_bytes, bool absmax_fp32, h
   a.nu = static_cast<int>(ceil_div(a.in, kUvChunk));
   a.vc0[0] = 0;
   for (int i = 0; i < a.n; ++i) a.vc0[i + 1] = a.vc0[i] + static_cast<int>(ceil_div(a.out[i], kUvChunk));
-  a.uvw = static_cast<int>(round_up(a.nu + a.vc0[a.n], 8));
+  a.uvw = a.r > 0 ? static_cast<int>(round_up(a.nu + a.vc0[a.n], 8)) : 0;
   const uint32_t g1 = static_cast<uint32_t>(a.uvw + a.gp);
-  if (absmax_fp32) hipLaunchKernelGGL(k_bwd_small_part<true>, dim3(g1), dim3(256), 0, s, a);
-  else hipLaunchKernelGGL(k_bwd_small_part<false>, dim3(g1), dim3(256), 0, s, a);
+  hipLaunchKernelGGL(k_bwd_small_part<kFormat>, dim3(g1), dim3(256), 0, s, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
+  const uint32_t dx_wgs = static_cast<uint32_t>(strips * ((a.T + 3) / 4));
+  if (a.r == 0) {  // no adapter: only dX's row splits are left to add
+    hipLaunchKernelGGL(k_bwd_small_fin, dim3(dx_wgs), dim3(256), 0, s, a);
+    return hipGetLastError();
+  }
   hipLaunchKernelGGL(k_bwd_small_uv, dim3(static_cast<uint32_t>(a.n * ((a.T * a.r + 63) / 64))), dim3(256), 0, s, a);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const uint32_t g3 = static_cast<uint32_t>(strips * ((a.T + 3) / 4) + a.n * strips + nchunks);
+  const uint32_t g3 = dx_wgs + static_cast<uint32_t>(a.n * strips + a.N / 64);
   hipLaunchKernelGGL(k_bwd_small_fin, dim3(g3), dim3(256), 0, s, a);
   return hipGetLastError();
+}
+}  // namespace
+
+hipError_t launch_bwd_small(BwdSmallDev a, size_t dxp_bytes, bool absmax_fp32, hipStream_t s) {
+  return absmax_fp32 ? launch_bwd_small_as<kSmallNf4Fp32>(a, dxp_bytes, s)
+                     : launch_bwd_small_as<kSmallNf4>(a, dxp_bytes, s);
+}
+
+hipError_t launch_fp8_bwd_small(BwdSmallDev a, size_t dxp_bytes, hipStream_t s) {
+  return launch_bwd_small_as<kSmallFp8>(a, dxp_bytes, s);
 }
 
 size_t bwd_small_uv_bytes(int64_t T, int64_t in, const int64_t* outs, int n, int64_t r) {

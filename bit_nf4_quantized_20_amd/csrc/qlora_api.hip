@@ -808,13 +808,32 @@ namespace {
 // the adapter's parts as in the 4-bit layouts (r > 0), then split-K partials.
 struct Fp8Layout {
   size_t xq, xs, u_pad, b_pad, ut, vt, b_t, a_t_pad, part, grad, split, total;
+  size_t uvp, suv;  // small-token backward (dX row splits at split)
 };
+
+// Up to 16 tokens both calls stream the weight once (k_fp8_decode, the small
+// backward of k_dx_small.hip) and quantize the activations on the way; rows
+// too long for the forward's registers take the GEMM.
+bool fp8_small(int64_t T, int64_t in, bool backward) { return backward ? T <= kDxSmallMaxT : fp8_decode_fits(T, in); }
 
 Fp8Layout fp8_layout(int64_t T, int64_t in, int64_t out, int64_t r, bool backward) {
   Fp8Layout l{};
   Carve c;
   const int64_t K = backward ? out : in, N = backward ? in : out;
   const int64_t rp = padded_rank(r);
+  if (fp8_small(T, in, backward)) {
+    if (backward) {
+      l.split = c.take(static_cast<size_t>(dx_small_max_splits(out, in) * T * in * 4));
+      if (r > 0) {
+        l.uvp = c.take(bwd_small_uv_bytes(T, in, &out, 1, r));
+        l.suv = c.take(static_cast<size_t>(2 * T * r * 4));
+      }
+    } else if (r > 0 && !fp8_decode_fuses(out, in, r)) {
+      l.u_pad = c.take(decode_u_bytes(1, T, r));  // U [T][r] fp32
+    }
+    l.total = c.off;
+    return l;
+  }
   l.xq = c.take(static_cast<size_t>(T * round_up(K, QLORA_FP8_BLOCK)));
   l.xs = c.take(fp8_row_scale_bytes(T, K));
   if (r > 0) {
@@ -905,15 +924,29 @@ int qlora_fp8_linear_fwd(const qlora_fp8_weight* W, const qlora_bf16* X, int64_t
   if (r > 0 && !std::isfinite(alpha)) return QLORA_ERR_VALUE;
   if (T == 0) return QLORA_OK;
   const Fp8Layout lay = fp8_layout(T, in, out, r, false);
-  if (ws == nullptr || ws_bytes < lay.total) return QLORA_ERR_WORKSPACE;
+  if (lay.total > 0 && (ws == nullptr || ws_bytes < lay.total)) return QLORA_ERR_WORKSPACE;
   if (!aligned16(ws)) return QLORA_ERR_ALIGN;
   if (int st = check_device()) return st;
 
   hipStream_t s = static_cast<hipStream_t>(stream);
   uint8_t* base = static_cast<uint8_t*>(ws);
   const int64_t rp = padded_rank(r);
-  F8Gemm g{};
   hipError_t e = hipSuccess;
+  if (fp8_small(T, in, false)) {
+    float* u = nullptr;
+    if (r > 0 && !fp8_decode_fuses(out, in, r)) {
+      DecodeSet set{};
+      set.n = 1;
+      set.proj[0].A = A;
+      u = reinterpret_cast<float*>(base + lay.u_pad);
+      e = launch_decode_u(set, in, X, T, r, u, s);
+    }
+    if (e == hipSuccess)
+      e = launch_fp8_decode(W->codes, W->scales, out, in, X, T, A, B, r, r > 0 ? alpha / static_cast<float>(r) : 0.f,
+                            u, Y, s);
+    return launched(e);
+  }
+  F8Gemm g{};
   if (r > 0) {
     uint16_t* u_pad = reinterpret_cast<uint16_t*>(base + lay.u_pad);
     uint16_t* b_pad = reinterpret_cast<uint16_t*>(base + lay.b_pad);
@@ -963,6 +996,30 @@ int qlora_fp8_linear_bwd(const qlora_fp8_weight* W, const qlora_bf16* X, const q
     return launched(launch_fill_many_f32(dst, n, 2, 0.f, s));
   }
   uint8_t* base = static_cast<uint8_t*>(ws);
+  if (fp8_small(T, in, true)) {
+    BwdSmallDev a{};
+    a.set.n = a.n = 1;
+    a.set.proj[0] = DxProj{W->codes, W->scales, nullptr, 0};
+    a.A.p[0] = A;
+    a.B.p[0] = B;
+    a.out[0] = a.N = out;
+    a.dA[0] = dA;
+    a.dB[0] = dB;
+    a.T = static_cast<int>(T);
+    a.r = static_cast<int>(r);
+    a.in = in;
+    a.X = X;
+    a.dY = dY;
+    a.dxp = reinterpret_cast<float*>(base + lay.split);
+    if (r > 0) {
+      a.uvp = reinterpret_cast<float*>(base + lay.uvp);
+      a.su = reinterpret_cast<float*>(base + lay.suv);
+      a.sv = a.su + T * r;
+      a.s = alpha / static_cast<float>(r);
+    }
+    a.dX = dX;
+    return launched(launch_fp8_bwd_small(a, static_cast<size_t>(dx_small_max_splits(out, in) * T * in * 4), s));
+  }
   const int64_t rp = padded_rank(r), tp = token_pitch(T);
   F8Gemm g{};
   hipError_t e = hipSuccess;
