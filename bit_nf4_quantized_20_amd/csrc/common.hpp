@@ -323,7 +323,9 @@ hipError_t launch_bwd_small(BwdSmallDev a, size_t dxp_bytes, bool absmax_fp32, h
 size_t bwd_small_uv_bytes(int64_t T, int64_t in, const int64_t* outs, int n, int64_t r);
 // The same for one 8-bit weight (n = 1, proj[0]: codes, absmax_q = the scale
 // bytes); r = 0: no adapter, two launches.
-hipError_t launch_fp8_bwd_small(BwdSmallDev a, size_t dxp_bytes, hipStream_t s);
+// dxp: fp8_bwd_small_splits(out, in) partials of [T][in] fp32.
+int fp8_bwd_small_splits(int64_t out, int64_t in);
+hipError_t launch_fp8_bwd_small(BwdSmallDev a, hipStream_t s);
 
 struct DecodeProj {
   const uint8_t* codes; const uint8_t* absmax_q; const float* scale;

@@ -153,43 +153,42 @@ __device__ __forceinline__ void uv_part(const BwdSmallDev& a, int q, uint16_t* l
 }
 }  // namespace
 
-// The weight's format: NF4 with double-quantized or fp32 absmax, or 8 bits.
-constexpr int kSmallNf4 = 0, kSmallNf4Fp32 = 1, kSmallFp8 = 2;
-
 namespace {
-// dX row split of an 8-bit weight: acc[nt] lane (t = i16, g): columns n0 + 16
-// nt + 4 g .. + 3.  A wave takes 128-row chunks (one scale per chunk and
-// column block) in turn, the next one's codes and dY in registers meanwhile.
-// The codes go into the wave's LDS tile as they lie in memory (64 bytes per
-// row) and come back transposed as the A operand of v_mfma_scale
-// (16 columns x 128 rows, lane group g: rows 32 g .. + 31); a token's 128 dY
-// values meet in the four lanes that hold them for their scale, and are the B
-// operand.  16-byte chunk c of row k sits at c ^ key(k), which spreads the
-// 16 x 8-row pieces that 32 lanes read over all banks.
-__device__ __forceinline__ int f8s_key(int k) { return ((k >> 2) & 1) | ((k >> 4) & 2); }
+constexpr int kF8Strip = 128;  // columns of an 8-bit row split
 
-__device__ __forceinline__ void fp8_split(const BwdSmallDev& a, int64_t n0, int c0, int c1, uint16_t* tile16,
-                                          f32x4 (&acc)[4]) {
-  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+// dX row split of an 8-bit weight: columns n0 .. n0 + 127 of W over the 128-row
+// chunks [c0, c1).  The workgroup copies a chunk's tile (128 rows x 128 bytes:
+// whole lines) through registers into LDS, the next one's loads in flight
+// meanwhile; 16-byte piece k of row m sits at k ^ key(m), which spreads the 16
+// rows that 32 lanes read transposed over all banks.  Wave v takes columns 32 v
+// .. + 31 as two A operands of v_mfma_scale_f32_16x16x128 (16 columns x 128 rows,
+// lane group g: rows 32 g .. + 31); a token's 128 dY values meet in the four
+// lanes that hold them for their scale and are the B operand.
+__device__ __forceinline__ int f8s_key(int m) { return ((m >> 1) & 3) | ((m >> 3) & 4); }
+
+__device__ __forceinline__ void fp8_split(const BwdSmallDev& a, int64_t n0, int split, uint8_t* tile, float* part) {
+  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
   const int i16 = lane & 15, g = lane >> 4;
   const int64_t in = a.in, N = a.N;
-  uint8_t* const tile = reinterpret_cast<uint8_t*>(tile16);
-  const uint8_t* const w = a.set.proj[0].codes;
-  const uint8_t* const scales = a.set.proj[0].absmax_q;
+  const int chunks = static_cast<int>((N + kF8Block - 1) / kF8Block);
+  const int c0 = split * a.per, c1 = min(c0 + a.per, chunks);
+  const uint8_t* const w = a.set.proj[0].codes + n0;
+  const uint8_t* const scales = a.set.proj[0].absmax_q + n0 / kF8Block;
   const int64_t cb = ceil_div(in, kF8Block);
+  const bool cols = n0 + 16 * (tid & 7) < in;  // the last strip may hold 64 columns
   struct Stage {
-    u32x4 w[8], y[4];
+    u32x4 w[4], y[4];
     uint32_t sw;
   };
   auto load = [&](Stage& st, int c) {  // chunk c's codes, dY and scale; rows past the last are zero
     const int64_t k0 = static_cast<int64_t>(c) * kF8Block;
     const bool live = c < c1;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int64_t k = k0 + 16 * i + (lane >> 2);
+    for (int i = 0; i < 4; ++i) {
+      const int64_t k = k0 + 32 * i + (tid >> 3);
       st.w[i] = u32x4{0u, 0u, 0u, 0u};
-      if (live && k < N)
-        st.w[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(w + k * in + n0 + 16 * (lane & 3)));
+      if (live && cols && k < N)
+        st.w[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(w + k * in + 16 * (tid & 7)));
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -197,20 +196,17 @@ __device__ __forceinline__ void fp8_split(const BwdSmallDev& a, int64_t n0, int 
       st.y[i] = u32x4{0u, 0u, 0u, 0u};
       if (live && i16 < a.T && k < N) st.y[i] = *reinterpret_cast<const u32x4*>(a.dY + i16 * N + k);
     }
-    st.sw = live ? scales[static_cast<int64_t>(c) * cb + n0 / kF8Block] : 0;
+    st.sw = live ? scales[c * cb] : 0;
   };
-  auto sync = [] {
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-  };
+  f32x4 acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
   Stage cur;
-  load(cur, c0 + wv);
-  for (int c = c0 + wv; c < c1; c += 4) {
+  load(cur, c0);
+  for (int c = c0; c < c1; ++c) {
+    uint8_t* const t = tile + ((c - c0) & 1) * (kF8Block * kF8Strip);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int k = 16 * i + (lane >> 2);
-      *reinterpret_cast<u32x4*>(tile + k * 64 + (((lane & 3) ^ f8s_key(k)) << 4)) = cur.w[i];
+    for (int i = 0; i < 4; ++i) {
+      const int k = 32 * i + (tid >> 3);
+      *reinterpret_cast<u32x4*>(t + k * kF8Strip + (((tid & 7) ^ f8s_key(k)) << 4)) = cur.w[i];
     }
     uint32_t m = 0;
 #pragma unroll
@@ -230,10 +226,10 @@ __device__ __forceinline__ void fp8_split(const BwdSmallDev& a, int64_t n0, int 
         fy[2 * i + d] = static_cast<int>(f8_pack4(bf16_lo(cur.y[i][2 * d]) * inv, bf16_hi(cur.y[i][2 * d]) * inv,
                                                   bf16_lo(cur.y[i][2 * d + 1]) * inv, bf16_hi(cur.y[i][2 * d + 1]) * inv));
     const int sw = static_cast<int>(cur.sw);
-    load(cur, c + 4);
-    sync();
+    load(cur, c + 1);
+    __syncthreads();  // the tile is in LDS (and every wave is done with the other one)
 #pragma unroll
-    for (int nt = 0; nt < 4; ++nt) {
+    for (int nt = 0; nt < 2; ++nt) {
       i32x8 fw;
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
@@ -241,24 +237,94 @@ __device__ __forceinline__ void fp8_split(const BwdSmallDev& a, int64_t n0, int 
         // (i16 % 2) .. + 7 and receives column i16 of the eight rows
         const int k = 32 * g + 8 * s + (i16 >> 1);
         const i32x2 v = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
-            (__attribute__((address_space(3))) i32x2*)(tile + k * 64 + ((nt ^ f8s_key(k)) << 4) + 8 * (i16 & 1)));
+            (__attribute__((address_space(3))) i32x2*)(t + k * kF8Strip + (((2 * wv + nt) ^ f8s_key(k)) << 4) +
+                                                       8 * (i16 & 1)));
         fw[2 * s] = v[0];
         fw[2 * s + 1] = v[1];
       }
       acc[nt] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fw, fy, acc[nt], 0, 0, 0, sw, 0, static_cast<int>(sb));
     }
-    sync();  // the tile is read before the next chunk overwrites it
+  }
+  // lane: columns 32 wv + 16 nt + 4 g .. + 3 of token i16
+  if (i16 < a.T) {
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt) {
+      const int64_t col = n0 + 32 * wv + 16 * nt + 4 * g;
+      if (col < in) *reinterpret_cast<f32x4*>(part + (static_cast<int64_t>(split) * a.T + i16) * in + col) = acc[nt];
+    }
+  }
+}
+
+// One wave: chunk q of U = X A^T (q < nu: columns 128 q .. of X and A) or of V
+// = dY B (the chunk's 128 rows of dY's columns and of B), in the layout of
+// uv_part but on the matrix cores: bf16 products and fp32 sums of 128 (16 ranks
+// x 16 tokens x 32 positions an instruction).
+__device__ __forceinline__ void uv_part_mfma(const BwdSmallDev& a, int q) {
+  const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
+  const int T = a.T, r = a.r;
+  const bool is_u = q < a.nu;
+  const int c = is_u ? q : q - a.nu;
+  const int64_t k0 = static_cast<int64_t>(c) * kUvChunk, K = is_u ? a.in : a.N;
+  const uint16_t* const act = is_u ? a.X : a.dY;
+  float* const out = a.uvp + static_cast<int64_t>(q) * T * r;  // V's chunks follow U's
+  bf16x8 x[4];
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    const int64_t k = k0 + 32 * s + 8 * g;
+    u32x4 v = {0u, 0u, 0u, 0u};
+    if (n < T && k < K) v = *reinterpret_cast<const u32x4*>(act + n * K + k);
+    x[s] = dx_bf16x8(v);
+  }
+  for (int j0 = 0; j0 < r; j0 += 16) {
+    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+    u32x4 f[4];
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      const int64_t k = k0 + 32 * s + 8 * g;
+      f[s] = u32x4{0u, 0u, 0u, 0u};
+      if (j0 + n < r && k < K) {
+        if (is_u) {
+          f[s] = *reinterpret_cast<const u32x4*>(a.A.p[0] + (j0 + n) * K + k);
+        } else {
+          const uint16_t* b = a.B.p[0] + k * r + j0 + n;  // lanes n: consecutive ranks of a row
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            f[s][e] = static_cast<uint32_t>(b[2 * e * r]) | (static_cast<uint32_t>(b[(2 * e + 1) * r]) << 16);
+        }
+      }
+    }
+#pragma unroll
+    for (int s = 0; s < 4; ++s) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(dx_bf16x8(f[s]), x[s], acc, 0, 0, 0);
+    // lane: ranks j0 + 4 g .. + 3 of token n
+    if (n < T) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (j0 + 4 * g + e < r) out[n * r + j0 + 4 * g + e] = acc[e];
+    }
   }
 }
 }  // namespace
+
+// Launch 1 for an 8-bit weight: workgroups [0, a.uvw) U and V chunks, one per
+// wave, then the row splits (neighbouring strips on one XCD share no lines).
+__global__ __launch_bounds__(256) void k_fp8_bwd_small_part(BwdSmallDev a) {
+  __shared__ __attribute__((aligned(16))) uint8_t s_tile[2 * kF8Block * kF8Strip];
+  const int L = static_cast<int>(blockIdx.x);
+  if (L < a.uvw) {
+    const int q = 4 * L + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if (q < a.nu + a.vc0[1]) uv_part_mfma(a, q);
+    return;
+  }
+  const int strips = static_cast<int>((a.in + kF8Strip - 1) / kF8Strip);
+  fp8_split(a, static_cast<int64_t>((L - a.uvw) % strips) * kF8Strip, (L - a.uvw) / strips, s_tile, a.dxp);
+}
 
 // Launch 1: workgroups [0, a.uvw) the U and V chunks (first, so that they
 // run beside the dX row splits instead of after them; the count is padded to
 // a multiple of 8, the padding exits at once, so the splits keep their XCD
 // order), then [a.uvw, a.uvw + gp) the dX row splits.
-template <int kFormat>
+template <bool kFp32>
 __global__ __launch_bounds__(256) void k_bwd_small_part(BwdSmallDev a) {
-  constexpr bool kFp32 = kFormat == kSmallNf4Fp32;
   __shared__ __attribute__((aligned(16))) uint16_t s_w[4][64 * kDxPitch];
   __shared__ f32x4 s_acc[4][4][64];
   const int L0 = static_cast<int>(blockIdx.x);
@@ -277,7 +343,7 @@ __global__ __launch_bounds__(256) void k_bwd_small_part(BwdSmallDev a) {
   int strip, split;
   dx_strip_split(L, static_cast<int>(in / 64), static_cast<int>(in / 64) * nsplits, strip, split);
   const int64_t n0 = static_cast<int64_t>(strip) * 64;
-  const int nchunks = static_cast<int>(kFormat == kSmallFp8 ? (N + kF8Block - 1) / kF8Block : N / 64);
+  const int nchunks = static_cast<int>(N / 64);
   const int c0 = split * chunks_per_split;
   const int c1 = min(c0 + chunks_per_split, nchunks);
 
@@ -294,8 +360,6 @@ __global__ __launch_bounds__(256) void k_bwd_small_part(BwdSmallDev a) {
   for (int nt = 0; nt < 4; ++nt) acc[nt] = f32x4{0.f, 0.f, 0.f, 0.f};
   uint16_t* tile = s_w[wv];
 
-  if constexpr (kFormat == kSmallFp8) fp8_split(a, n0, c0, c1, tile, acc);
-  else
   for (int c = c0 + wv; c < c1; c += 4) {
     const int64_t R0 = static_cast<int64_t>(c) * 64;  // the chunk's first row of the stack
     int pj = 0;
@@ -394,9 +458,11 @@ __global__ __launch_bounds__(256) void k_bwd_small_uv(BwdSmallDev a) {
   }
 }
 
-// Launch 3: workgroups [0, gx) dX (64 columns x 4 tokens each), then
-// [gx, gx + n in / 64) dA (one projection's 64 columns each), then N / 64
-// for dB (64 stacked rows each).
+// Launch 3: workgroups [0, gx) dX (64 columns x 4 tokens each), then n (in /
+// 64) ceil(r / 16) for dA (one projection's 64 columns and 16 ranks each), then
+// N / 16 for dB (16 stacked rows each).  (With all ranks of 64 columns / 64 rows
+// to a workgroup the longest ones took 9 of this launch's 13 us at 13 tokens,
+// 4096 x 4096, r = 16: a thread's chain of LDS reads, not the memory.)
 __global__ __launch_bounds__(256) void k_bwd_small_fin(BwdSmallDev a) {
   __shared__ float s_a[64][65];   // dX: [rank][column]
   __shared__ float s_t[16][65];   // dX: sV [token][rank]; dA: X [token][column]; dB: dY [token][row]
@@ -404,7 +470,8 @@ __global__ __launch_bounds__(256) void k_bwd_small_fin(BwdSmallDev a) {
   const int tid = threadIdx.x, T = a.T, r = a.r;
   const int64_t in = a.in;
   const int strips = static_cast<int>(in / 64);
-  const int gx = strips * ((T + 3) / 4), ga = a.n * strips;
+  const int rank_groups = (r + 15) / 16;
+  const int gx = strips * ((T + 3) / 4), ga = a.n * strips * rank_groups;
   const int L = static_cast<int>(blockIdx.x);
   if (L < gx) {
     // dX[t][n] = bf16(sum_s dxp[s][t][n] + sum_i sum_j sV_i[t][j] A_i[j][n])
@@ -441,41 +508,41 @@ __global__ __launch_bounds__(256) void k_bwd_small_fin(BwdSmallDev a) {
   }
   if (L < gx + ga) {
     // dA_i[j][k0 + c] = sum_t sV_i[t][j] X[t][k0 + c]
-    const int q = L - gx, i = q / strips;
+    const int q = (L - gx) / rank_groups, j0 = 16 * ((L - gx) % rank_groups), i = q / strips;
     const int64_t k0 = static_cast<int64_t>(q % strips) * 64;
     for (int idx = tid; idx < T * 64; idx += 256)
       s_t[idx >> 6][idx & 63] = __builtin_bit_cast(float, static_cast<uint32_t>(a.X[(idx >> 6) * in + k0 + (idx & 63)]) << 16);
-    for (int idx = tid; idx < T * r; idx += 256) s_r[idx / r][idx % r] = a.sv[static_cast<int64_t>(i) * T * r + idx];
+    for (int idx = tid; idx < T * 16; idx += 256) {
+      const int tt = idx >> 4, j = j0 + (idx & 15);
+      s_r[tt][idx & 15] = j < r ? a.sv[(static_cast<int64_t>(i) * T + tt) * r + j] : 0.f;
+    }
     __syncthreads();
     const int c = tid & 63;
     float* __restrict__ dA = a.dA[i];
-    for (int j = tid >> 6; j < r; j += 4) {
+    for (int j = tid >> 6; j < 16 && j0 + j < r; j += 4) {
       float d = 0.f;
       for (int tt = 0; tt < T; ++tt) d = __builtin_fmaf(s_r[tt][j], s_t[tt][c], d);
-      dA[static_cast<int64_t>(j) * in + k0 + c] = d;
+      dA[static_cast<int64_t>(j0 + j) * in + k0 + c] = d;
     }
     return;
   }
-  // dB_i[m0 + m][j] = sum_t dY[t][row] sU_i[t][j] for the 64 stacked rows
-  // row = 64 (L - gx - ga) + m
-  const int64_t R0 = static_cast<int64_t>(L - gx - ga) * 64;
+  // dB_i[m0 + m][j] = sum_t dY[t][row] sU_i[t][j] for the 16 stacked rows
+  // row = 16 (L - gx - ga) + m
+  const int64_t R0 = static_cast<int64_t>(L - gx - ga) * 16;
   int i = 0;
   for (int k = 1; k < a.n; ++k)
     if (R0 >= a.set.proj[k].row0) i = k;
   const int64_t m0 = R0 - a.set.proj[i].row0;
-  for (int idx = tid; idx < T * 64; idx += 256)
-    s_t[idx >> 6][idx & 63] = __builtin_bit_cast(float, static_cast<uint32_t>(a.dY[(idx >> 6) * a.N + R0 + (idx & 63)]) << 16);
+  for (int idx = tid; idx < T * 16; idx += 256)
+    s_t[idx >> 4][idx & 15] = __builtin_bit_cast(float, static_cast<uint32_t>(a.dY[(idx >> 4) * a.N + R0 + (idx & 15)]) << 16);
   for (int idx = tid; idx < T * r; idx += 256) s_r[idx / r][idx % r] = a.su[static_cast<int64_t>(i) * T * r + idx];
   __syncthreads();
-  float* __restrict__ dB = a.dB[i];
-  for (int j0 = 0; j0 < r; j0 += 64) {
-    const int j = j0 + (tid & 63);
-    if (j < r)
-      for (int m = tid >> 6; m < 64; m += 4) {
-        float d = 0.f;
-        for (int tt = 0; tt < T; ++tt) d = __builtin_fmaf(s_t[tt][m], s_r[tt][j], d);
-        dB[(m0 + m) * r + j] = d;
-      }
+  float* __restrict__ dB = a.dB[i] + m0 * r;  // (16 whole rows: one contiguous piece)
+  for (int idx = tid; idx < 16 * r; idx += 256) {
+    const int m = idx / r, j = idx % r;
+    float d = 0.f;
+    for (int tt = 0; tt < T; ++tt) d = __builtin_fmaf(s_t[tt][m], s_r[tt][j], d);
+    dB[idx] = d;
   }
 }
 
@@ -503,10 +570,26 @@ int dx_small_splits(int64_t N, int64_t in, int T, size_t part_bytes) {
 }
 
 namespace {
-template <int kFormat>
-hipError_t launch_bwd_small_as(BwdSmallDev a, size_t dxp_bytes, hipStream_t s) {
+// launches 2 and 3
+hipError_t launch_bwd_small_rest(const BwdSmallDev& a, hipStream_t s) {
   const int strips = static_cast<int>(a.in / 64);
-  const int nchunks = static_cast<int>(kFormat == kSmallFp8 ? ceil_div(a.N, kF8Block) : a.N / 64);
+  const uint32_t dx_wgs = static_cast<uint32_t>(strips * ((a.T + 3) / 4));
+  if (a.r == 0) {  // no adapter: only dX's row splits are left to add
+    hipLaunchKernelGGL(k_bwd_small_fin, dim3(dx_wgs), dim3(256), 0, s, a);
+    return hipGetLastError();
+  }
+  hipLaunchKernelGGL(k_bwd_small_uv, dim3(static_cast<uint32_t>(a.n * ((a.T * a.r + 63) / 64))), dim3(256), 0, s, a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const uint32_t g3 = dx_wgs + static_cast<uint32_t>(a.n * strips * ceil_div(a.r, 16) + a.N / 16);
+  hipLaunchKernelGGL(k_bwd_small_fin, dim3(g3), dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+}  // namespace
+
+hipError_t launch_bwd_small(BwdSmallDev a, size_t dxp_bytes, bool absmax_fp32, hipStream_t s) {
+  const int strips = static_cast<int>(a.in / 64);
+  const int nchunks = static_cast<int>(a.N / 64);
   const int splits = dx_small_splits(a.N, a.in, a.T, dxp_bytes);
   a.per = (nchunks + splits - 1) / splits;
   a.splits = (nchunks + a.per - 1) / a.per;  // splits that get chunks
@@ -514,32 +597,34 @@ hipError_t launch_bwd_small_as(BwdSmallDev a, size_t dxp_bytes, hipStream_t s) {
   a.nu = static_cast<int>(ceil_div(a.in, kUvChunk));
   a.vc0[0] = 0;
   for (int i = 0; i < a.n; ++i) a.vc0[i + 1] = a.vc0[i] + static_cast<int>(ceil_div(a.out[i], kUvChunk));
-  a.uvw = a.r > 0 ? static_cast<int>(round_up(a.nu + a.vc0[a.n], 8)) : 0;
+  a.uvw = static_cast<int>(round_up(a.nu + a.vc0[a.n], 8));
   const uint32_t g1 = static_cast<uint32_t>(a.uvw + a.gp);
-  hipLaunchKernelGGL(k_bwd_small_part<kFormat>, dim3(g1), dim3(256), 0, s, a);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  const uint32_t dx_wgs = static_cast<uint32_t>(strips * ((a.T + 3) / 4));
-  if (a.r == 0) {  // no adapter: only dX's row splits are left to add
-    hipLaunchKernelGGL(k_bwd_small_fin, dim3(dx_wgs), dim3(256), 0, s, a);
-    return hipGetLastError();
-  }
-  hipLaunchKernelGGL(k_bwd_small_uv, dim3(static_cast<uint32_t>(a.n * ((a.T * a.r + 63) / 64))), dim3(256), 0, s, a);
-  e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  const uint32_t g3 = dx_wgs + static_cast<uint32_t>(a.n * strips + a.N / 64);
-  hipLaunchKernelGGL(k_bwd_small_fin, dim3(g3), dim3(256), 0, s, a);
-  return hipGetLastError();
-}
-}  // namespace
-
-hipError_t launch_bwd_small(BwdSmallDev a, size_t dxp_bytes, bool absmax_fp32, hipStream_t s) {
-  return absmax_fp32 ? launch_bwd_small_as<kSmallNf4Fp32>(a, dxp_bytes, s)
-                     : launch_bwd_small_as<kSmallNf4>(a, dxp_bytes, s);
+  if (absmax_fp32) hipLaunchKernelGGL(k_bwd_small_part<true>, dim3(g1), dim3(256), 0, s, a);
+  else hipLaunchKernelGGL(k_bwd_small_part<false>, dim3(g1), dim3(256), 0, s, a);
+  const hipError_t e = hipGetLastError();
+  return e == hipSuccess ? launch_bwd_small_rest(a, s) : e;
 }
 
-hipError_t launch_fp8_bwd_small(BwdSmallDev a, size_t dxp_bytes, hipStream_t s) {
-  return launch_bwd_small_as<kSmallFp8>(a, dxp_bytes, s);
+// about two workgroups per CU (of a 256-CU part), at most one chunk each
+int fp8_bwd_small_splits(int64_t out, int64_t in) {
+  const int64_t strips = ceil_div(in, kF8Strip), chunks = ceil_div(out, kF8Block);
+  const int64_t splits = ceil_div(kDxSmallTargetWgs, strips);
+  return static_cast<int>(splits < chunks ? splits : chunks);
+}
+
+hipError_t launch_fp8_bwd_small(BwdSmallDev a, hipStream_t s) {
+  const int strips = static_cast<int>(ceil_div(a.in, kF8Strip)), chunks = static_cast<int>(ceil_div(a.N, kF8Block));
+  const int splits = fp8_bwd_small_splits(a.N, a.in);
+  a.per = (chunks + splits - 1) / splits;
+  a.splits = (chunks + a.per - 1) / a.per;
+  a.gp = strips * a.splits;
+  a.nu = a.r > 0 ? static_cast<int>(ceil_div(a.in, kUvChunk)) : 0;
+  a.vc0[0] = 0;
+  a.vc0[1] = a.r > 0 ? static_cast<int>(ceil_div(a.N, kUvChunk)) : 0;
+  a.uvw = (a.nu + a.vc0[1] + 3) / 4;
+  hipLaunchKernelGGL(k_fp8_bwd_small_part, dim3(static_cast<uint32_t>(a.uvw + a.gp)), dim3(256), 0, s, a);
+  const hipError_t e = hipGetLastError();
+  return e == hipSuccess ? launch_bwd_small_rest(a, s) : e;
 }
 
 size_t bwd_small_uv_bytes(int64_t T, int64_t in, const int64_t* outs, int n, int64_t r) {

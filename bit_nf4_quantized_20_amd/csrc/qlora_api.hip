@@ -823,7 +823,7 @@ Fp8Layout fp8_layout(int64_t T, int64_t in, int64_t out, int64_t r, bool backwar
   const int64_t rp = padded_rank(r);
   if (fp8_small(T, in, backward)) {
     if (backward) {
-      l.split = c.take(static_cast<size_t>(dx_small_max_splits(out, in) * T * in * 4));
+      l.split = c.take(static_cast<size_t>(fp8_bwd_small_splits(out, in) * T * in * 4));
       if (r > 0) {
         l.uvp = c.take(bwd_small_uv_bytes(T, in, &out, 1, r));
         l.suv = c.take(static_cast<size_t>(2 * T * r * 4));
@@ -1018,7 +1018,7 @@ int qlora_fp8_linear_bwd(const qlora_fp8_weight* W, const qlora_bf16* X, const q
       a.s = alpha / static_cast<float>(r);
     }
     a.dX = dX;
-    return launched(launch_fp8_bwd_small(a, static_cast<size_t>(dx_small_max_splits(out, in) * T * in * 4), s));
+    return launched(launch_fp8_bwd_small(a, s));
   }
   const int64_t rp = padded_rank(r), tp = token_pitch(T);
   F8Gemm g{};
