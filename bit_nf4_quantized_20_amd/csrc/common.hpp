@@ -76,7 +76,9 @@ size_t lora_down_part_bytes(int64_t T, int64_t K, int64_t nprp);
 hipError_t launch_lora_down(const uint16_t* in, int64_t ldin, int64_t T, int64_t K,
                             const uint16_t* const* P, int nP, int64_t r, float scale, uint16_t* pad,
                             int64_t ldpad, uint16_t* hilo_t, int64_t ldt, int64_t rp, float* part,
-                            hipStream_t s, const uint8_t* keep = nullptr, int64_t ldk = 0);
+                            hipStream_t s, const uint8_t* keep = nullptr, int64_t ldk = 0, int planes = 2);
+// planes = 3: hilo_t is [nP][3 rp][ldt], the third plane (rows [2 rp, 3 rp)) what
+// hi + lo leaves of the fp32 value; lora_grad then adds all three.
 // out(j, c) = sum_t (Pt[j'][t] + Pt[rp + j'][t]) Q[t][c] for j < r, c < C (C % 64
 // == 0), laid out as out[j * C + c] (out_jc) or out[c * r + j], where rank j is
 // rank j' = j % rproj of the projection j / rproj of Pt (projections stacked,
@@ -90,7 +92,7 @@ int64_t lora_grad_slices(int64_t T, int64_t C, int64_t ldq);
 hipError_t launch_lora_grad(const uint16_t* Pt, int64_t T, int64_t ldt, int64_t rp, const uint16_t* Q,
                             int64_t C, int64_t ldq, int64_t r, float* part, bool out_jc, hipStream_t s,
                             const uint8_t* keep = nullptr, int64_t ldk = 0, float oscale = 1.f,
-                            int64_t rproj = 0);
+                            int64_t rproj = 0, int planes = 2);
 // dst[c][r] = src[r][c] for src [R][C]
 hipError_t launch_transpose_bf16(const uint16_t* src, int64_t R, int64_t C, uint16_t* dst,
                                  hipStream_t s);

@@ -215,12 +215,16 @@ __global__ __launch_bounds__(256) void k_lora_down_part(const uint16_t* __restri
 // both stores are coalesced.  Ranks r .. rp - 1 are written as zeros without
 // reading the partials (k_lora_down_part leaves them unwritten).
 constexpr int kDownMaxKC = 16;
+// NP = 3: the transposed layout has a third plane, what hi + lo leaves of the
+// fp32 value (rows [2 rp, 3 rp) of each projection).
+template <int NP>
 __global__ __launch_bounds__(256) void k_lora_down_fin(const float* __restrict__ part, int64_t T, int KC,
                                                        int nP, int r, int rp, float scale,
                                                        uint16_t* __restrict__ pad,
                                                        int64_t ldpad, uint16_t* __restrict__ hilo_t,
                                                        int64_t ldt) {
   __shared__ uint32_t s_t[64][17];  // [rank][token] hi | lo << 16
+  __shared__ uint16_t s_t3[NP == 3 ? 64 : 1][18];
   const int tid = threadIdx.x;
   const int64_t tb = static_cast<int64_t>(blockIdx.x) * 16;
   const int jb = static_cast<int>(blockIdx.y) * 64;
@@ -252,6 +256,8 @@ __global__ __launch_bounds__(256) void k_lora_down_fin(const float* __restrict__
       row[rp] = static_cast<uint16_t>(lb);
     }
     s_t[jl][tl] = hb | (lb << 16);  // tokens >= T hold zero
+    if constexpr (NP == 3)
+      s_t3[jl][tl] = static_cast<uint16_t>(pack_bf16x2(v - hi - __builtin_bit_cast(float, lb << 16), 0.f) & 0xffffu);
   }
   if (hilo_t == nullptr) return;
   __syncthreads();
@@ -263,9 +269,10 @@ __global__ __launch_bounds__(256) void k_lora_down_fin(const float* __restrict__
   for (int i = 0; i < 4; ++i) {
     const int j = (tid >> 4) + 16 * i;
     const uint32_t v = s_t[j][tl];
-    uint16_t* blk = hilo_t + static_cast<int64_t>(pj) * 2 * rp * ldt;  // projection pj's [2 rp][ldt]
+    uint16_t* blk = hilo_t + static_cast<int64_t>(pj) * NP * rp * ldt;  // projection pj's [NP rp][ldt]
     blk[static_cast<int64_t>(jj + j) * ldt + t] = static_cast<uint16_t>(v & 0xffffu);
     blk[static_cast<int64_t>(rp + jj + j) * ldt + t] = static_cast<uint16_t>(v >> 16);
+    if constexpr (NP == 3) blk[static_cast<int64_t>(2 * rp + jj + j) * ldt + t] = s_t3[j][tl];
   }
 }
 
@@ -292,7 +299,7 @@ size_t lora_down_part_bytes(int64_t T, int64_t K, int64_t nprp) {
 hipError_t launch_lora_down(const uint16_t* in, int64_t ldin, int64_t T, int64_t K,
                             const uint16_t* const* P, int nP, int64_t r, float scale, uint16_t* pad,
                             int64_t ldpad, uint16_t* hilo_t, int64_t ldt, int64_t rp, float* part,
-                            hipStream_t s, const uint8_t* keep, int64_t ldk) {
+                            hipStream_t s, const uint8_t* keep, int64_t ldk, int planes) {
   if (T <= 0) return hipSuccess;
   if (nP < 1 || nP > kMaxProj) return hipErrorInvalidValue;
   // 32-bit buffer offsets: one tile's rows of `in` and P stay under 2^31 bytes
@@ -316,8 +323,12 @@ hipError_t launch_lora_down(const uint16_t* in, int64_t ldin, int64_t T, int64_t
   if (e != hipSuccess) return e;
   const int64_t tt = hilo_t != nullptr ? (ldt > T ? ldt : T) : T;
   const dim3 fgrid(static_cast<uint32_t>(ceil_div(tt, 16)), static_cast<uint32_t>(nP * rp / 64));
-  hipLaunchKernelGGL(k_lora_down_fin, fgrid, dim3(256), 0, s, part, T, static_cast<int>(KC), nP,
-                     static_cast<int>(r), static_cast<int>(rp), scale, pad, ldpad, hilo_t, ldt);
+  if (planes == 3)
+    hipLaunchKernelGGL(k_lora_down_fin<3>, fgrid, dim3(256), 0, s, part, T, static_cast<int>(KC), nP,
+                       static_cast<int>(r), static_cast<int>(rp), scale, pad, ldpad, hilo_t, ldt);
+  else
+    hipLaunchKernelGGL(k_lora_down_fin<2>, fgrid, dim3(256), 0, s, part, T, static_cast<int>(KC), nP,
+                       static_cast<int>(r), static_cast<int>(rp), scale, pad, ldpad, hilo_t, ldt);
   return hipGetLastError();
 }
 
@@ -355,14 +366,16 @@ __device__ __forceinline__ int grad_qslot(int c, int w) { return kGradPitch * c 
 // The workgroup of token slice y writes its sums (times oscale) to slice y of
 // `part` ([slices][r * C] floats, each element written once per slice); a
 // second launch adds the slices in order (k_sum_slices).
-template <int JT, bool kJC, bool kMask>
+// NP: planes of Pt (2: hi and lo; 3: and what they leave, for fp32 sums of fp32
+// factors instead of 16-bit ones).
+template <int JT, bool kJC, bool kMask, int NP = 2>
 __global__ __launch_bounds__(256) void k_lora_grad(const uint16_t* __restrict__ Pt, int64_t T,
                                                    int64_t ldt, int rp, const uint16_t* __restrict__ Q,
                                                    int64_t C, int64_t ldq, int r, int j0, int rproj,
                                                    float* __restrict__ part, int64_t TS,
                                                    const uint8_t* __restrict__ keep, int64_t ldk,
                                                    float oscale) {
-  constexpr int kPRows = 64 * JT;  // hi rows [0, 32JT), lo rows [32JT, 64JT)
+  constexpr int kPRows = 32 * NP * JT;  // hi rows [0, 32JT), lo rows [32JT, 64JT), ...
   __shared__ uint32_t s_q[2][kGradCT * kGradPitch];
   __shared__ uint32_t s_p[2][kPRows * kGradPitch];
   const int tid = threadIdx.x, lane = tid & 63;
@@ -379,20 +392,20 @@ __global__ __launch_bounds__(256) void k_lora_grad(const uint16_t* __restrict__ 
   const __amdgpu_buffer_rsrc_t rs_q = __builtin_amdgcn_make_buffer_rsrc(
       const_cast<uint16_t*>(Q + ts * ldq), 0, static_cast<int>(q_bytes < 0x7fffffffu ? q_bytes : 0x7fffffffu),
       kBufferWord3);
-  // Pt holds ceil(r / rproj) stacked projections of 2 rp rows each
+  // Pt holds ceil(r / rproj) stacked projections of NP rp rows each
   const int nproj = (r + rproj - 1) / rproj;
   const __amdgpu_buffer_rsrc_t rs_p = __builtin_amdgcn_make_buffer_rsrc(
-      const_cast<uint16_t*>(Pt), 0, static_cast<int>(static_cast<uint64_t>(nproj) * 2 * rp * ldt * 2),
+      const_cast<uint16_t*>(Pt), 0, static_cast<int>(static_cast<uint64_t>(nproj) * NP * rp * ldt * 2),
       kBufferWord3);
   // Rank J of the call is rank J % rproj of projection J / rproj, whose hi and
   // lo rows are i 2rp + J % rproj and i 2rp + rp + J % rproj; ranks past r read zeros.
-  int64_t prow_base[2 * JT];
+  int64_t prow_base[NP * JT];
 #pragma unroll
-  for (int i = 0; i < 2 * JT; ++i) {
+  for (int i = 0; i < NP * JT; ++i) {
     const int prow = (tid + 256 * i) >> 3;
-    const int J = j0 + (prow < 32 * JT ? prow : prow - 32 * JT);
+    const int plane = prow / (32 * JT), J = j0 + prow % (32 * JT);
     const int pi = J / rproj, jl = J - pi * rproj;
-    prow_base[i] = J < r ? static_cast<int64_t>(pi) * 2 * rp + jl + (prow < 32 * JT ? 0 : rp) : -1;
+    prow_base[i] = J < r ? static_cast<int64_t>(pi) * NP * rp + jl + plane * rp : -1;
   }
 
   // Q staging items: column group cg (8 columns), token pairs tp and tp + 16
@@ -402,7 +415,7 @@ __global__ __launch_bounds__(256) void k_lora_grad(const uint16_t* __restrict__ 
   // loads are in flight while a third is computed
   u32x4 qv[2][4];
   uint32_t kb[2][4];
-  u32x4 pv[2][2 * JT];
+  u32x4 pv[2][NP * JT];
   const uint64_t kbytes = kMask ? static_cast<uint64_t>(T - ts) * ldk : 0;
   const __amdgpu_buffer_rsrc_t rs_k = __builtin_amdgcn_make_buffer_rsrc(
       const_cast<uint8_t*>(kMask ? keep + ts * ldk : keep), 0,
@@ -424,7 +437,7 @@ __global__ __launch_bounds__(256) void k_lora_grad(const uint16_t* __restrict__ 
       }
     }
 #pragma unroll
-    for (int i = 0; i < 2 * JT; ++i) {
+    for (int i = 0; i < NP * JT; ++i) {
       const int id = tid + 256 * i, q = id & 7;
       const int64_t grow = prow_base[i];
       const int64_t tk = t0 + 8 * q;  // tokens in [T, ldt) are zero in Pt
@@ -449,7 +462,7 @@ __global__ __launch_bounds__(256) void k_lora_grad(const uint16_t* __restrict__ 
       }
     }
 #pragma unroll
-    for (int i = 0; i < 2 * JT; ++i) {
+    for (int i = 0; i < NP * JT; ++i) {
       const int id = tid + 256 * i, prow = id >> 3, q = id & 7;
       *reinterpret_cast<u32x4*>(&s_p[buf][kGradPitch * prow + 4 * q]) = pv[S][i];
     }
@@ -480,6 +493,9 @@ __global__ __launch_bounds__(256) void k_lora_grad(const uint16_t* __restrict__ 
     for (int s4 = 0; s4 < 4; ++s4) {
       const int w0 = 8 * s4 + 4 * h;
       const u32x4 qf = *reinterpret_cast<const u32x4*>(&s_q[buf][grad_qslot(c, w0)]);
+      auto third = [&](int jt) {
+        return *reinterpret_cast<const u32x4*>(&s_p[buf][kGradPitch * (64 * JT + 32 * jt + r32) + w0]);
+      };
 #pragma unroll
       for (int jt = 0; jt < JT; ++jt) {
         const u32x4 ph = *reinterpret_cast<const u32x4*>(&s_p[buf][kGradPitch * (32 * jt + r32) + w0]);
@@ -487,9 +503,11 @@ __global__ __launch_bounds__(256) void k_lora_grad(const uint16_t* __restrict__ 
         if constexpr (kJC) {  // D[j][c]
           acc[jt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(ph), as_bf16x8(qf), acc[jt], 0, 0, 0);
           acc[jt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(pl), as_bf16x8(qf), acc[jt], 0, 0, 0);
+          if constexpr (NP == 3) acc[jt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(third(jt)), as_bf16x8(qf), acc[jt], 0, 0, 0);
         } else {  // D[c][j]
           acc[jt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(qf), as_bf16x8(ph), acc[jt], 0, 0, 0);
           acc[jt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(qf), as_bf16x8(pl), acc[jt], 0, 0, 0);
+          if constexpr (NP == 3) acc[jt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(qf), as_bf16x8(third(jt)), acc[jt], 0, 0, 0);
         }
       }
     }
@@ -552,10 +570,10 @@ int64_t lora_grad_slices(int64_t T, int64_t C, int64_t ldq) {
 
 hipError_t launch_lora_grad(const uint16_t* Pt, int64_t T, int64_t ldt, int64_t rp, const uint16_t* Q,
                             int64_t C, int64_t ldq, int64_t r, float* part, bool out_jc, hipStream_t s,
-                            const uint8_t* keep, int64_t ldk, float oscale, int64_t rproj) {
+                            const uint8_t* keep, int64_t ldk, float oscale, int64_t rproj, int planes) {
   if (T <= 0) return hipSuccess;
   if (rproj <= 0) rproj = r;
-  if (ceil_div(r, rproj) * 2 * rp * ldt * 2 >= (int64_t(1) << 31)) return hipErrorInvalidValue;  // Pt under 2^31 bytes
+  if (ceil_div(r, rproj) * planes * rp * ldt * 2 >= (int64_t(1) << 31)) return hipErrorInvalidValue;  // Pt under 2^31 bytes
   if (keep != nullptr && T * ldk >= (int64_t(1) << 31)) return hipErrorInvalidValue;
   const int64_t TS = grad_slice_tokens(T, C, ldq);
   const int64_t slices = ceil_div(T, TS);
@@ -566,13 +584,23 @@ hipError_t launch_lora_grad(const uint16_t* Pt, int64_t T, int64_t ldt, int64_t 
     const int64_t left = r - j0;
     const int jt = static_cast<int>(ceil_div(left < 32 * kGradMaxJT ? left : 32 * kGradMaxJT, 32));
     const int ij0 = static_cast<int>(j0);
-#define QLORA_GRAD(JTV, JC, MK)                                                                      \
-  hipLaunchKernelGGL((k_lora_grad<JTV, JC, MK>), grid, dim3(256), 0, s, Pt, T, ldt, irp, Q, C, ldq, ir, ij0, \
-                     static_cast<int>(rproj), part, TS, keep, ldk, oscale)
+#define QLORA_GRAD(JTV, JC, MK, ...)                                                                           \
+  hipLaunchKernelGGL((k_lora_grad<JTV, JC, MK __VA_OPT__(,) __VA_ARGS__>), grid, dim3(256), 0, s, Pt, T, ldt, irp, Q, C, \
+                     ldq, ir, ij0, static_cast<int>(rproj), part, TS, keep, ldk, oscale)
     if (keep != nullptr) {  // the masked operand is X: dA, out_jc
       if (jt <= 1) QLORA_GRAD(1, true, true);
       else if (jt <= 2) QLORA_GRAD(2, true, true);
       else QLORA_GRAD(4, true, true);
+    } else if (planes == 3) {
+      if (out_jc) {
+        if (jt <= 1) QLORA_GRAD(1, true, false, 3);
+        else if (jt <= 2) QLORA_GRAD(2, true, false, 3);
+        else QLORA_GRAD(4, true, false, 3);
+      } else {
+        if (jt <= 1) QLORA_GRAD(1, false, false, 3);
+        else if (jt <= 2) QLORA_GRAD(2, false, false, 3);
+        else QLORA_GRAD(4, false, false, 3);
+      }
     } else if (out_jc) {
       if (jt <= 1) QLORA_GRAD(1, true, false);
       else if (jt <= 2) QLORA_GRAD(2, true, false);

@@ -806,6 +806,11 @@ namespace {
 
 // 8-bit linear: workspace layouts.  The activation codes and scales, then
 // the adapter's parts as in the 4-bit layouts (r > 0), then split-K partials.
+// dA and dB are held to fp32: sU and sV meet the matrix cores as three bf16
+// planes (2^-25 left; hi + lo alone leave 2^-17, 2.4e-6 of the gradients
+// against 1.2e-6 for fp32 products in the reference's order)
+constexpr int kFp8Planes = 3;
+
 struct Fp8Layout {
   size_t xq, xs, u_pad, b_pad, ut, vt, b_t, a_t_pad, part, grad, split, total;
   size_t uvp, suv;  // small-token backward (dX row splits at split)
@@ -842,8 +847,8 @@ Fp8Layout fp8_layout(int64_t T, int64_t in, int64_t out, int64_t r, bool backwar
     if (backward) {
       const size_t pv = lora_down_part_bytes(T, out, rp);
       part = pv > part ? pv : part;
-      l.ut = c.take(static_cast<size_t>(2 * rp * token_pitch(T) * 2));
-      l.vt = c.take(static_cast<size_t>(2 * rp * token_pitch(T) * 2));
+      l.ut = c.take(static_cast<size_t>(kFp8Planes * rp * token_pitch(T) * 2));
+      l.vt = c.take(static_cast<size_t>(kFp8Planes * rp * token_pitch(T) * 2));
       l.b_t = c.take(static_cast<size_t>(r * out * 2));
       l.a_t_pad = c.take(static_cast<size_t>(in * rp * 4));
       l.grad = c.take(grad_part_bytes(T, in, &out, 1, r));
@@ -858,7 +863,12 @@ Fp8Layout fp8_layout(int64_t T, int64_t in, int64_t out, int64_t r, bool backwar
 }
 
 bool fp8_shapes_ok(int64_t T, int64_t in, int64_t out, int64_t r) {
-  return linear_shapes_ok(T, in, out, r == 0 ? 1 : r) && operands_fit(T, in, out);
+  if (!linear_shapes_ok(T, in, out, r == 0 ? 1 : r) || !operands_fit(T, in, out)) return false;
+  // the rank-r products address a tile's rows of X, dY, A, B and the planes of
+  // sU, sV with 32-bit offsets
+  constexpr int64_t kRowMost = int64_t(1) << 23;
+  return r == 0 || T <= kDecodeMaxT ||
+         (in < kRowMost && out < kRowMost && kFp8Planes * 2 * padded_rank(r) * token_pitch(T) <= kMaxOperandBytes);
 }
 
 int check_fp8_weight(const qlora_fp8_weight* W) {
@@ -1032,9 +1042,10 @@ int qlora_fp8_linear_bwd(const qlora_fp8_weight* W, const qlora_bf16* X, const q
     uint16_t* a_t_pad = reinterpret_cast<uint16_t*>(base + lay.a_t_pad);
     float* part = reinterpret_cast<float*>(base + lay.part);
     const uint16_t* bt = b_t;
-    e = launch_lora_down(X, in, T, in, &A, 1, r, scale, nullptr, 0, ut, tp, rp, part, s);
+    e = launch_lora_down(X, in, T, in, &A, 1, r, scale, nullptr, 0, ut, tp, rp, part, s, nullptr, 0, kFp8Planes);
     if (e == hipSuccess) e = launch_factor_prep(B, out, r, b_t, A, in, a_t_pad, rp, 2 * rp, s);
-    if (e == hipSuccess) e = launch_lora_down(dY, out, T, out, &bt, 1, r, scale, v_pad, 2 * rp, vt, tp, rp, part, s);
+    if (e == hipSuccess)
+      e = launch_lora_down(dY, out, T, out, &bt, 1, r, scale, v_pad, 2 * rp, vt, tp, rp, part, s, nullptr, 0, kFp8Planes);
     g.act1 = v_pad;
     g.wt1 = a_t_pad;
     g.lda1 = g.ldw1 = g.K1 = 2 * rp;
@@ -1057,8 +1068,8 @@ int qlora_fp8_linear_bwd(const qlora_fp8_weight* W, const qlora_bf16* X, const q
     float* const pa = reinterpret_cast<float*>(base + lay.grad);
     const int64_t sa = lora_grad_slices(T, in, in), sb = lora_grad_slices(T, out, out);
     float* const pb = pa + sa * r * in;
-    if (e == hipSuccess) e = launch_lora_grad(vt, T, tp, rp, X, in, in, r, pa, true, s);
-    if (e == hipSuccess) e = launch_lora_grad(ut, T, tp, rp, dY, out, out, r, pb, false, s);
+    if (e == hipSuccess) e = launch_lora_grad(vt, T, tp, rp, X, in, in, r, pa, true, s, nullptr, 0, 1.f, 0, kFp8Planes);
+    if (e == hipSuccess) e = launch_lora_grad(ut, T, tp, rp, dY, out, out, r, pb, false, s, nullptr, 0, 1.f, 0, kFp8Planes);
     const float* src[2] = {pa, pb};
     const int slices[2] = {static_cast<int>(sa), static_cast<int>(sb)};
     const int64_t n[2] = {r * in, out * r};
