@@ -638,6 +638,7 @@ def _scratch(ws, need: int, dev):
     return ws
 
 
+@functools.lru_cache(maxsize=4096)
 def qlora_fp8_storage_bytes(rows: int, cols: int):
     c, s = _sz(), _sz()
     _check(_lib.qlora_fp8_storage_bytes(rows, cols, ctypes.byref(c), ctypes.byref(s)), "qlora_fp8_storage_bytes")
@@ -654,10 +655,12 @@ def qlora_fp8_quantize(w: torch.Tensor, codes=None, scales=None):
     grid = (-(-rows // 128), -(-cols // 128))
     if codes is None:
         codes = torch.empty(rows, cols, dtype=torch.uint8, device=dev)
+    else:
+        _arg(codes, torch.uint8, rows * cols, "codes", dev)
     if scales is None:
         scales = torch.empty(grid, dtype=torch.uint8, device=dev)
-    _arg(codes, torch.uint8, rows * cols, "codes", dev)
-    _arg(scales, torch.uint8, grid[0] * grid[1], "scales", dev)
+    else:
+        _arg(scales, torch.uint8, grid[0] * grid[1], "scales", dev)
     _on(dev, _lib.qlora_fp8_quantize, "qlora_fp8_quantize", w.data_ptr(), rows, cols, codes.data_ptr(),
         scales.data_ptr())
     return codes, scales
@@ -677,7 +680,8 @@ def qlora_fp8_dequantize(codes, scales, rows: int, cols: int, out=None):
     _arg(scales, torch.uint8, sb, "scales", dev)
     if out is None:
         out = torch.empty(rows, cols, dtype=torch.bfloat16, device=dev)
-    _arg(out, torch.bfloat16, rows * cols, "out", dev)
+    else:
+        _arg(out, torch.bfloat16, rows * cols, "out", dev)
     _on(dev, _lib.qlora_fp8_dequantize, "qlora_fp8_dequantize", codes.data_ptr(), scales.data_ptr(), rows, cols,
         out.data_ptr())
     return out
@@ -706,7 +710,8 @@ def qlora_fp8_linear_fwd(W: FP8Weight, X, A, B, r: int, alpha: float, Y=None, ws
     _fp8_args(W, X, A, B, r, dev, T)
     if Y is None:
         Y = torch.empty(T, W.rows, dtype=torch.bfloat16, device=dev)
-    _arg(Y, torch.bfloat16, T * W.rows, "Y", dev)
+    else:
+        _arg(Y, torch.bfloat16, T * W.rows, "Y", dev)
     ws = _scratch(ws, qlora_fp8_workspace_bytes(T, W.cols, W.rows, r, False), dev)
     _on(dev, _lib.qlora_fp8_linear_fwd, "qlora_fp8_linear_fwd", ctypes.byref(W._c()), X.data_ptr(), T,
         A.data_ptr() if r > 0 else None, B.data_ptr() if r > 0 else None, r, float(alpha), Y.data_ptr(),
@@ -725,14 +730,17 @@ def qlora_fp8_linear_bwd(W: FP8Weight, X, dY, A, B, r: int, alpha: float, dX=Non
     _fp8_args(W, X, A, B, r, dev, T)
     if dX is None:
         dX = torch.empty(T, W.cols, dtype=torch.bfloat16, device=dev)
-    _arg(dX, torch.bfloat16, T * W.cols, "dX", dev)
+    else:
+        _arg(dX, torch.bfloat16, T * W.cols, "dX", dev)
     if r > 0:
         if dA is None:
             dA = torch.empty(r, W.cols, dtype=torch.float32, device=dev)
+        else:
+            _arg(dA, torch.float32, r * W.cols, "dA", dev)
         if dB is None:
             dB = torch.empty(W.rows, r, dtype=torch.float32, device=dev)
-        _arg(dA, torch.float32, r * W.cols, "dA", dev)
-        _arg(dB, torch.float32, W.rows * r, "dB", dev)
+        else:
+            _arg(dB, torch.float32, W.rows * r, "dB", dev)
     else:
         X = A = B = dA = dB = None
     ws = _scratch(ws, qlora_fp8_workspace_bytes(T, W.cols, W.rows, r, True), dev)
@@ -752,10 +760,12 @@ def qlora_moe_route(logits, k: int, renormalize: bool = True, ids=None, weights=
     _arg(logits, torch.float32, T * E, "logits", dev)
     if ids is None:
         ids = torch.empty(T, max(k, 0), dtype=torch.int32, device=dev)
+    else:
+        _arg(ids, torch.int32, T * k, "ids", dev)
     if weights is None:
         weights = torch.empty(T, max(k, 0), dtype=torch.float32, device=dev)
-    _arg(ids, torch.int32, T * k, "ids", dev)
-    _arg(weights, torch.float32, T * k, "weights", dev)
+    else:
+        _arg(weights, torch.float32, T * k, "weights", dev)
     _on(dev, _lib.qlora_moe_route, "qlora_moe_route", logits.data_ptr(), T, E, k, 1 if renormalize else 0,
         ids.data_ptr(), weights.data_ptr())
     return ids, weights
@@ -771,7 +781,8 @@ def qlora_moe_route_bwd(logits, ids, dweights, renormalize: bool = True, dlogits
     _arg(dweights, torch.float32, (T, k), "dweights", dev)
     if dlogits is None:
         dlogits = torch.empty(T, E, dtype=torch.float32, device=dev)
-    _arg(dlogits, torch.float32, T * E, "dlogits", dev)
+    else:
+        _arg(dlogits, torch.float32, T * E, "dlogits", dev)
     _on(dev, _lib.qlora_moe_route_bwd, "qlora_moe_route_bwd", logits.data_ptr(), ids.data_ptr(),
         dweights.data_ptr(), T, E, k, 1 if renormalize else 0, dlogits.data_ptr())
     return dlogits
@@ -806,7 +817,8 @@ def qlora_moe_fwd(gate_up: NF4Weight, down: NF4Weight, experts: int, X, ids, wei
     _nf4_arg(down, "down", dev)
     if Y is None:
         Y = torch.empty(T, hidden, dtype=torch.bfloat16, device=dev)
-    _arg(Y, torch.bfloat16, T * hidden, "Y", dev)
+    else:
+        _arg(Y, torch.bfloat16, T * hidden, "Y", dev)
     ws = _scratch(ws, qlora_moe_workspace_bytes(T, hidden, inter, k), dev)
     _on(dev, _lib.qlora_moe_fwd, "qlora_moe_fwd", ctypes.byref(gate_up._c()), ctypes.byref(down._c()), experts,
         X.data_ptr(), T, ids.data_ptr(), weights.data_ptr(), k, Y.data_ptr(), ws.data_ptr(),

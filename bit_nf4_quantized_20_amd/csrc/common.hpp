@@ -88,7 +88,7 @@ hipError_t launch_lora_down(const uint16_t* in, int64_t ldin, int64_t T, int64_t
 // launch_sum_slices.  (Q rows have stride ldq elements, ldq >= C.)  keep
 // (optional, LoRA dropout, out_jc only): Q[t][c] counts only where bit c % 8 of
 // keep[t * ldk + c / 8] is set; every sum is multiplied by oscale.
-int64_t lora_grad_slices(int64_t T, int64_t C, int64_t ldq);
+int64_t lora_grad_slices(int64_t T, int64_t C, int64_t ldq, int planes = 2);
 hipError_t launch_lora_grad(const uint16_t* Pt, int64_t T, int64_t ldt, int64_t rp, const uint16_t* Q,
                             int64_t C, int64_t ldq, int64_t r, float* part, bool out_jc, hipStream_t s,
                             const uint8_t* keep = nullptr, int64_t ldk = 0, float oscale = 1.f,

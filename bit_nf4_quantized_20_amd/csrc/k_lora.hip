@@ -548,12 +548,14 @@ __global__ __launch_bounds__(256) void k_lora_grad(const uint16_t* __restrict__ 
 // Token slices (multiples of 64 tokens) for about one workgroup per CU: more
 // slices shorten each workgroup's stream but add partial sums (measured on
 // the 8B-MLP shapes: 256-450 workgroups are fastest, 560 were 35% slower for
-// 14336 columns, 512 were 30% slower for 4096).  The count depends on the
-// shape only.
+// 14336 columns, 512 were 30% slower for 4096).  Three planes leave LDS for one
+// workgroup per CU, so their grid stays within one round of 256 (4096 tokens,
+// 14336 columns, rank 64: 224 workgroups 40 us, 336 54 us).  The count depends
+// on the shape only.
 namespace {
-int64_t grad_slice_tokens(int64_t T, int64_t C, int64_t ldq) {
+int64_t grad_slice_tokens(int64_t T, int64_t C, int64_t ldq, int planes) {
   const int64_t ctiles = ceil_div(C, kGradCT);
-  int64_t slices = ceil_div(256, ctiles);
+  int64_t slices = planes == 3 ? 256 / ctiles : ceil_div(256, ctiles);
   const int64_t max_slices = ceil_div(T, 64);
   if (slices > max_slices) slices = max_slices;
   if (slices < 1) slices = 1;
@@ -564,8 +566,8 @@ int64_t grad_slice_tokens(int64_t T, int64_t C, int64_t ldq) {
 }
 }  // namespace
 
-int64_t lora_grad_slices(int64_t T, int64_t C, int64_t ldq) {
-  return T > 0 ? ceil_div(T, grad_slice_tokens(T, C, ldq)) : 0;
+int64_t lora_grad_slices(int64_t T, int64_t C, int64_t ldq, int planes) {
+  return T > 0 ? ceil_div(T, grad_slice_tokens(T, C, ldq, planes)) : 0;
 }
 
 hipError_t launch_lora_grad(const uint16_t* Pt, int64_t T, int64_t ldt, int64_t rp, const uint16_t* Q,
@@ -575,7 +577,7 @@ hipError_t launch_lora_grad(const uint16_t* Pt, int64_t T, int64_t ldt, int64_t 
   if (rproj <= 0) rproj = r;
   if (ceil_div(r, rproj) * planes * rp * ldt * 2 >= (int64_t(1) << 31)) return hipErrorInvalidValue;  // Pt under 2^31 bytes
   if (keep != nullptr && T * ldk >= (int64_t(1) << 31)) return hipErrorInvalidValue;
-  const int64_t TS = grad_slice_tokens(T, C, ldq);
+  const int64_t TS = grad_slice_tokens(T, C, ldq, planes);
   const int64_t slices = ceil_div(T, TS);
   const int64_t ctiles = ceil_div(C, kGradCT);
   const dim3 grid(static_cast<uint32_t>(ctiles), static_cast<uint32_t>(slices));

@@ -851,7 +851,8 @@ Fp8Layout fp8_layout(int64_t T, int64_t in, int64_t out, int64_t r, bool backwar
       l.vt = c.take(static_cast<size_t>(kFp8Planes * rp * token_pitch(T) * 2));
       l.b_t = c.take(static_cast<size_t>(r * out * 2));
       l.a_t_pad = c.take(static_cast<size_t>(in * rp * 4));
-      l.grad = c.take(grad_part_bytes(T, in, &out, 1, r));
+      l.grad = c.take(static_cast<size_t>((lora_grad_slices(T, in, in, kFp8Planes) * in +
+                                           lora_grad_slices(T, out, out, kFp8Planes) * out) * r * 4));
     } else {
       l.b_pad = c.take(static_cast<size_t>(out * rp * 4));
     }
@@ -1066,7 +1067,7 @@ int qlora_fp8_linear_bwd(const qlora_fp8_weight* W, const qlora_bf16* X, const q
   if (r > 0) {
     // token-slice sums of dA and dB, then each added in slice order
     float* const pa = reinterpret_cast<float*>(base + lay.grad);
-    const int64_t sa = lora_grad_slices(T, in, in), sb = lora_grad_slices(T, out, out);
+    const int64_t sa = lora_grad_slices(T, in, in, kFp8Planes), sb = lora_grad_slices(T, out, out, kFp8Planes);
     float* const pb = pa + sa * r * in;
     if (e == hipSuccess) e = launch_lora_grad(vt, T, tp, rp, X, in, in, r, pa, true, s, nullptr, 0, 1.f, 0, kFp8Planes);
     if (e == hipSuccess) e = launch_lora_grad(ut, T, tp, rp, dY, out, out, r, pb, false, s, nullptr, 0, 1.f, 0, kFp8Planes);
