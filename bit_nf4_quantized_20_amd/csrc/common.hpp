@@ -76,9 +76,10 @@ size_t lora_down_part_bytes(int64_t T, int64_t K, int64_t nprp);
 hipError_t launch_lora_down(const uint16_t* in, int64_t ldin, int64_t T, int64_t K,
                             const uint16_t* const* P, int nP, int64_t r, float scale, uint16_t* pad,
                             int64_t ldpad, uint16_t* hilo_t, int64_t ldt, int64_t rp, float* part,
-                            hipStream_t s, const uint8_t* keep = nullptr, int64_t ldk = 0, int planes = 2);
-// planes = 3: hilo_t is [nP][3 rp][ldt], the third plane (rows [2 rp, 3 rp)) what
-// hi + lo leaves of the fp32 value; lora_grad then adds all three.
+                            hipStream_t s, const uint8_t* keep = nullptr, int64_t ldk = 0);
+// the second half of launch_lora_down alone
+hipError_t launch_lora_down_fin(const float* part, int64_t T, int64_t K, int nP, int64_t r, float scale, uint16_t* pad,
+                                int64_t ldpad, uint16_t* hilo_t, int64_t ldt, int64_t rp, hipStream_t s);
 // out(j, c) = sum_t (Pt[j'][t] + Pt[rp + j'][t]) Q[t][c] for j < r, c < C (C % 64
 // == 0), laid out as out[j * C + c] (out_jc) or out[c * r + j], where rank j is
 // rank j' = j % rproj of the projection j / rproj of Pt (projections stacked,
@@ -92,7 +93,7 @@ int64_t lora_grad_slices(int64_t T, int64_t C, int64_t ldq, int planes = 2);
 hipError_t launch_lora_grad(const uint16_t* Pt, int64_t T, int64_t ldt, int64_t rp, const uint16_t* Q,
                             int64_t C, int64_t ldq, int64_t r, float* part, bool out_jc, hipStream_t s,
                             const uint8_t* keep = nullptr, int64_t ldk = 0, float oscale = 1.f,
-                            int64_t rproj = 0, int planes = 2);
+                            int64_t rproj = 0);
 // dst[c][r] = src[r][c] for src [R][C]
 hipError_t launch_transpose_bf16(const uint16_t* src, int64_t R, int64_t C, uint16_t* dst,
                                  hipStream_t s);
@@ -197,8 +198,44 @@ constexpr int64_t fp8_row_pitch(int64_t T) { return round_up(T, 256); }  // whol
 inline size_t fp8_row_scale_bytes(int64_t T, int64_t K) {
   return static_cast<size_t>(ceil_div(K, 512) * fp8_row_pitch(T) * 4);
 }
-hipError_t launch_fp8_rows(const uint16_t* x, int64_t ldx, int64_t T, int64_t K, uint8_t* codes, uint8_t* scales,
-                           int64_t ldsc, hipStream_t s);
+struct Fp8Rows {
+  const uint16_t* x;
+  int64_t T, ldx, ldsc;
+  uint32_t K, KB;  // columns, blocks of 128 columns
+  uint8_t *codes, *scales;
+};
+hipError_t launch_fp8_rows(const Fp8Rows& a, hipStream_t s);
+// The 8-bit layer's rank products (k_lora.hip), pieces that share a launch:
+// part = the K-chunks of in P^T (in [T][K], P [r][K]; lora_down_part_bytes(T, K,
+// rp) bytes); rows quantized (rows.T = 0: none); bt [r][out] = B^T (out = 0:
+// none); dst = src [R][r] (transpose: src [r][R]) zero-padded to rp columns and
+// written twice, row stride ldd (R = 0: none).
+struct LoraFront {
+  const uint16_t* in; const uint16_t* P;
+  int64_t T, K, r, rp;
+  float* part;
+  Fp8Rows rows;
+  const uint16_t* B; uint16_t* bt;
+  int64_t out;
+  const uint16_t* src; uint16_t* dst;
+  int64_t R, ldd;
+  bool transpose;
+};
+hipError_t launch_lora_front(const LoraFront& f, hipStream_t s);
+// s times the sums of two K-chunk lists (lengths K[0], K[1]): three bf16 planes
+// of each into hilo_t[i] [3 rp][ldt] as launch_lora_down lays them out, hi and
+// lo of the second into pad too.
+hipError_t launch_lora_fin_two(const float* const* part, const int64_t* K, int64_t T, int64_t r, int64_t rp,
+                               float scale, uint16_t* pad, int64_t ldpad, uint16_t* const* hilo_t, int64_t ldt,
+                               hipStream_t s);
+// The token-slice sums of dA (Pt[0], Q[0] [T][C[0]]; out_jc) and dB (Pt[1],
+// Q[1]; not) as launch_lora_grad writes them with three planes.
+hipError_t launch_lora_grad_two(const uint16_t* const* Pt, int64_t T, int64_t ldt, int64_t rp,
+                                const uint16_t* const* Q, const int64_t* C, int64_t r, float* const* part,
+                                hipStream_t s);
+// launch_sum_slices over count jobs (may be 0) and, where S > 1, launch_split_sum
+hipError_t launch_grad_sums(const float* const* part, const int* slices, const int64_t* n, float* const* out, int count,
+                            const float* split, int S, int64_t M, int64_t N, uint16_t* C, hipStream_t s);
 // C [M][N] bf16 = activations (codes, scales as launch_fp8_rows writes them)
 // times the 8-bit weight (not transposed: N = rows, K = cols; transposed: N =
 // cols, K = rows) plus the adapter segment (K1 = 0: none; as in
@@ -214,6 +251,7 @@ struct F8Gemm {
   int64_t K1;
   uint16_t* C;
   float* part;
+  bool keep_parts;  // K splits stay in part: the caller adds them
 };
 int fp8_splits(int64_t M, int64_t N, int64_t K);
 size_t fp8_split_bytes(int64_t M, int64_t N, int64_t K);

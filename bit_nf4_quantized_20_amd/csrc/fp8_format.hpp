@@ -16,6 +16,7 @@
 #pragma once
 
 #include "common.hpp"
+#include "nf4_format.hpp"
 
 namespace qlora {
 
@@ -44,6 +45,62 @@ __device__ __forceinline__ uint32_t f8_pack4(float a, float b, float c, float d)
   int v = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
   v = __builtin_amdgcn_cvt_pk_fp8_f32(c, d, v, true);
   return static_cast<uint32_t>(v);
+}
+
+template <int kCtrl>
+__device__ __forceinline__ uint32_t dpp_max_u32(uint32_t v) {
+  return max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), kCtrl, 0xf, 0xf, false)));
+}
+// max over each aligned group of 16 lanes
+__device__ __forceinline__ uint32_t max16_u32(uint32_t v) {
+  v = dpp_max_u32<kDppQuadXor1>(v);
+  v = dpp_max_u32<kDppQuadXor2>(v);
+  v = dpp_max_u32<kDppRowHalfMirror>(v);
+  return dpp_max_u32<kDppRowMirror>(v);
+}
+
+// Activations x [T][ldx] bf16 (columns 0 .. K - 1) -> codes [T][Kp], scale
+// bytes in groups of four K-blocks, [ceil(KB / 4)][ldsc] dwords, row t's at
+// column t: 16 lanes hold one row's 128 columns, eight each.  Columns K .. Kp
+// (Kp = K rounded up to 128) become zero codes; scale bytes past the last
+// block or row are not written.  A workgroup of 256 threads takes kF8RowsPer
+// rows of 16 blocks, all loads before the first use: that keeps enough bytes
+// in flight where few workgroups fit a CU (k_lora_front).
+constexpr int kF8RowsPer = 4;
+inline int64_t fp8_rows_blocks(const Fp8Rows& a) {
+  return ceil_div(a.T, kF8RowsPer) * ceil_div(static_cast<int64_t>(a.KB), int64_t(16));
+}
+__device__ __forceinline__ void fp8_rows_tile(const Fp8Rows& a, uint32_t blk) {
+  const uint32_t pieces = (a.KB + 15) / 16;
+  const int64_t row = static_cast<int64_t>(blk / pieces) * kF8RowsPer;
+  const uint32_t kb = blk % pieces * 16 + (threadIdx.x >> 4);
+  const int sub = threadIdx.x & 15;
+  const uint32_t col = kb * kF8Block + 8 * sub;
+  u32x4 v[kF8RowsPer];
+#pragma unroll
+  for (int i = 0; i < kF8RowsPer; ++i) {
+    v[i] = u32x4{0u, 0u, 0u, 0u};
+    if (col < a.K && row + i < a.T) v[i] = *reinterpret_cast<const u32x4*>(a.x + (row + i) * a.ldx + col);
+  }
+  if (kb >= a.KB) return;
+#pragma unroll
+  for (int i = 0; i < kF8RowsPer; ++i) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int d = 0; d < 4; ++d) m = max(m, max((v[i][d] << 16) & 0x7fffffffu, v[i][d] & 0x7fff0000u));
+    m = max16_u32(m);
+    const uint32_t b = f8_scale_byte(m);
+    const float inv = f8_inv_scale(b);
+    u32x2 o;
+#pragma unroll
+    for (int d = 0; d < 2; ++d)
+      o[d] = f8_pack4(bf16_lo(v[i][2 * d]) * inv, bf16_hi(v[i][2 * d]) * inv, bf16_lo(v[i][2 * d + 1]) * inv,
+                      bf16_hi(v[i][2 * d + 1]) * inv);
+    if (row + i < a.T) {
+      *reinterpret_cast<u32x2*>(a.codes + ((row + i) * a.KB + kb) * kF8Block + 8 * sub) = o;
+      if (sub == 0) a.scales[((kb >> 2) * a.ldsc + row + i) * 4 + (kb & 3)] = static_cast<uint8_t>(b);
+    }
+  }
 }
 
 }  // namespace qlora

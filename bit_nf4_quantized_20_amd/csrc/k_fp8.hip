@@ -10,18 +10,6 @@ namespace qlora {
 
 namespace {
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __builtin_bit_cast(uint32_t, v) & 0x7fffffffu; }
-
-template <int kCtrl>
-__device__ __forceinline__ uint32_t dpp_max_u32(uint32_t v) {
-  return max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), kCtrl, 0xf, 0xf, false)));
-}
-// max over each aligned group of 16 lanes
-__device__ __forceinline__ uint32_t max16_u32(uint32_t v) {
-  v = dpp_max_u32<kDppQuadXor1>(v);
-  v = dpp_max_u32<kDppQuadXor2>(v);
-  v = dpp_max_u32<kDppRowHalfMirror>(v);
-  return dpp_max_u32<kDppRowMirror>(v);
-}
 }  // namespace
 
 // One workgroup of 256 threads per 128 x 128 block: thread t holds four
@@ -107,36 +95,8 @@ __global__ __launch_bounds__(256) void k_fp8_dequantize(const uint8_t* __restric
   }
 }
 
-// Activations x [T][ldx] bf16 (columns 0 .. K - 1) -> codes [T][Kp], scale
-// bytes in groups of four K-blocks, [ceil(KB / 4)][ldsc] dwords, row t's at
-// column t: 16 lanes hold one row's 128 columns, eight each.  Columns K .. Kp
-// (Kp = K rounded up to 128) become zero codes; scale bytes past the last
-// block or row are not written.
-__global__ __launch_bounds__(256) void k_fp8_rows(const uint16_t* __restrict__ x, int64_t ldx, uint32_t K,
-                                                  uint32_t KB, uint8_t* __restrict__ codes,
-                                                  uint8_t* __restrict__ scales, int64_t ldsc) {
-  const uint32_t pieces = (KB + 15) / 16;  // workgroups per row
-  const uint32_t row = blockIdx.x / pieces;
-  const uint32_t kb = blockIdx.x % pieces * 16 + (threadIdx.x >> 4);
-  const int sub = threadIdx.x & 15;
-  const uint32_t col = kb * kF8Block + 8 * sub;
-  u32x4 v = u32x4{0u, 0u, 0u, 0u};
-  if (col < K) v = *reinterpret_cast<const u32x4*>(x + static_cast<int64_t>(row) * ldx + col);
-  uint32_t m = 0;
-#pragma unroll
-  for (int d = 0; d < 4; ++d) m = max(m, max((v[d] << 16) & 0x7fffffffu, v[d] & 0x7fff0000u));
-  m = max16_u32(m);
-  const uint32_t b = f8_scale_byte(m);
-  const float inv = f8_inv_scale(b);
-  if (kb >= KB) return;
-  u32x2 o;
-#pragma unroll
-  for (int d = 0; d < 2; ++d)
-    o[d] = f8_pack4(bf16_lo(v[2 * d]) * inv, bf16_hi(v[2 * d]) * inv, bf16_lo(v[2 * d + 1]) * inv,
-                    bf16_hi(v[2 * d + 1]) * inv);
-  *reinterpret_cast<u32x2*>(codes + (static_cast<int64_t>(row) * KB + kb) * kF8Block + 8 * sub) = o;
-  if (sub == 0) scales[((kb >> 2) * ldsc + row) * 4 + (kb & 3)] = static_cast<uint8_t>(b);
-}
+// (fp8_rows_tile: rows of 128 columns held by 16 lanes)
+__global__ __launch_bounds__(256) void k_fp8_rows(Fp8Rows a) { fp8_rows_tile(a, blockIdx.x); }
 
 hipError_t launch_fp8_quantize(const float* w, int64_t rows, int64_t cols, uint8_t* codes, uint8_t* scales,
                                hipStream_t s) {
@@ -154,11 +114,8 @@ hipError_t launch_fp8_dequantize(const uint8_t* codes, const uint8_t* scales, in
   return hipGetLastError();
 }
 
-hipError_t launch_fp8_rows(const uint16_t* x, int64_t ldx, int64_t T, int64_t K, uint8_t* codes, uint8_t* scales,
-                           int64_t ldsc, hipStream_t s) {
-  const int64_t KB = ceil_div(K, kF8Block);
-  hipLaunchKernelGGL(k_fp8_rows, dim3(static_cast<uint32_t>(T * ceil_div(KB, 16))), dim3(256), 0, s, x, ldx,
-                     static_cast<uint32_t>(K), static_cast<uint32_t>(KB), codes, scales, ldsc);
+hipError_t launch_fp8_rows(const Fp8Rows& a, hipStream_t s) {
+  hipLaunchKernelGGL(k_fp8_rows, dim3(static_cast<uint32_t>(fp8_rows_blocks(a))), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 

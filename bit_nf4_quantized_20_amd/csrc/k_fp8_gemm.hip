@@ -476,7 +476,7 @@ hipError_t launch_fp8_gemm(const F8Gemm& g, hipStream_t s) {
     else hipLaunchKernelGGL((k_fp8_gemm<32, 128, 1, 4, false>), grid, dim3(256), 0, s, a);
   }
   hipError_t e = hipGetLastError();
-  if (e == hipSuccess && S > 1) e = launch_split_sum(g.part, S, a.M, a.N, a.C, a.N, s);
+  if (e == hipSuccess && S > 1 && !g.keep_parts) e = launch_split_sum(g.part, S, a.M, a.N, a.C, a.N, s);
   return e;
 }
 

@@ -5,10 +5,12 @@
 // sU and sV are kept as bf16 pairs hi + lo (hi = bf16(v), lo = bf16(v - hi)),
 // so products with them carry ~16 bits of the fp32 value; all accumulation is
 // fp32.  Also the zero-padding / transposition of the small LoRA matrices
-// into the layouts the GEMM's extra K-steps read.
+// into the layouts the GEMM's extra K-steps read, and the sums over token slices
+// and K splits.
 #include <type_traits>
 
 #include "common.hpp"
+#include "fp8_format.hpp"
 #include "nf4_format.hpp"
 
 namespace qlora {
@@ -68,23 +70,27 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t down_rsrc(const uint16_t* base
 // part[kc][t][p rp + j] (fp32, [KC][T][nP rp]) = sum over chunk kc of
 // in[t][k] P_p[j][k], for the nP rank factors P_p (one per projection).
 // kMask: in[t][k] counts only where bit k % 8 of keep[t * ldk + k / 8] is set.
+// Workgroup (bx, kc, bz) of the grid, npr = nP rp.
+struct DownStage {
+  uint16_t x[2][kDownTok * 64];
+  uint16_t p[2][kDownRanks * 64];
+};
+namespace {
 template <bool kMask>
-__global__ __launch_bounds__(256) void k_lora_down_part(const uint16_t* __restrict__ in, int64_t ldin,
-                                                        int64_t T, int64_t K, DownFactors P,
-                                                        int r, int rp, int64_t kch,
-                                                        float* __restrict__ part,
-                                                        const uint8_t* __restrict__ keep, int64_t ldk) {
-  __shared__ __attribute__((aligned(16))) uint16_t s_x[2][kDownTok * 64];
-  __shared__ __attribute__((aligned(16))) uint16_t s_p[2][kDownRanks * 64];
+__device__ __forceinline__ void down_part_tile(DownStage& stage, const uint16_t* __restrict__ in, int64_t ldin,
+                                               int64_t T, int64_t K, const DownFactors& P, int r, int rp,
+                                               int64_t kch, float* __restrict__ part,
+                                               const uint8_t* __restrict__ keep, int64_t ldk, int64_t bx, int64_t kc,
+                                               int bz, int npr) {
+  auto& s_x = stage.x;
+  auto& s_p = stage.p;
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
   const int wm = wv & 1, wn = wv >> 1;
   const int r32 = lane & 31, h = lane >> 5;
-  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kDownTok;
-  const int64_t kc = blockIdx.y;
+  const int64_t t0 = bx * kDownTok;
   const int tiles_per_p = rp / kDownRanks;
-  const int pj = static_cast<int>(blockIdx.z) / tiles_per_p;           // projection
-  const int j0 = (static_cast<int>(blockIdx.z) % tiles_per_p) * kDownRanks;
-  const int npr = static_cast<int>(gridDim.z) * kDownRanks;            // nP * rp
+  const int pj = bz / tiles_per_p;           // projection
+  const int j0 = (bz % tiles_per_p) * kDownRanks;
   const int64_t kbeg = kc * kch;
   const int64_t kend = kbeg + kch < K ? kbeg + kch : K;
   const int nsteps = static_cast<int>((kend - kbeg) / 64);
@@ -205,6 +211,18 @@ __global__ __launch_bounds__(256) void k_lora_down_part(const uint16_t* __restri
             f32x4v{acc[c][4 * g], acc[c][4 * g + 1], acc[c][4 * g + 2], acc[c][4 * g + 3]};
   }
 }
+}  // namespace
+
+template <bool kMask>
+__global__ __launch_bounds__(256) void k_lora_down_part(const uint16_t* __restrict__ in, int64_t ldin,
+                                                        int64_t T, int64_t K, DownFactors P,
+                                                        int r, int rp, int64_t kch,
+                                                        float* __restrict__ part,
+                                                        const uint8_t* __restrict__ keep, int64_t ldk) {
+  __shared__ __attribute__((aligned(16))) DownStage stage;
+  down_part_tile<kMask>(stage, in, ldin, T, K, P, r, rp, kch, part, keep, ldk, blockIdx.x, blockIdx.y,
+                        static_cast<int>(blockIdx.z), static_cast<int>(gridDim.z) * kDownRanks);
+}
 
 // Sums the KC (<= kDownMaxKC) partials in order, scales and writes sU as
 // bf16 hi/lo pairs:
@@ -218,13 +236,17 @@ constexpr int kDownMaxKC = 16;
 // NP = 3: the transposed layout has a third plane, what hi + lo leaves of the
 // fp32 value (rows [2 rp, 3 rp) of each projection).
 template <int NP>
-__global__ __launch_bounds__(256) void k_lora_down_fin(const float* __restrict__ part, int64_t T, int KC,
-                                                       int nP, int r, int rp, float scale,
-                                                       uint16_t* __restrict__ pad,
-                                                       int64_t ldpad, uint16_t* __restrict__ hilo_t,
-                                                       int64_t ldt) {
-  __shared__ uint32_t s_t[64][17];  // [rank][token] hi | lo << 16
-  __shared__ uint16_t s_t3[NP == 3 ? 64 : 1][18];
+struct FinStage {
+  uint32_t t[64][17];  // [rank][token] hi | lo << 16
+  uint16_t t3[NP == 3 ? 64 : 1][18];
+};
+namespace {
+template <int NP>
+__device__ __forceinline__ void down_fin_tile(FinStage<NP>& stage, const float* __restrict__ part, int64_t T, int KC,
+                                              int nP, int r, int rp, float scale, uint16_t* __restrict__ pad,
+                                              int64_t ldpad, uint16_t* __restrict__ hilo_t, int64_t ldt) {
+  auto& s_t = stage.t;
+  auto& s_t3 = stage.t3;
   const int tid = threadIdx.x;
   const int64_t tb = static_cast<int64_t>(blockIdx.x) * 16;
   const int jb = static_cast<int>(blockIdx.y) * 64;
@@ -275,6 +297,16 @@ __global__ __launch_bounds__(256) void k_lora_down_fin(const float* __restrict__
     if constexpr (NP == 3) blk[static_cast<int64_t>(2 * rp + jj + j) * ldt + t] = s_t3[j][tl];
   }
 }
+}  // namespace
+
+__global__ __launch_bounds__(256) void k_lora_down_fin(const float* __restrict__ part, int64_t T, int KC,
+                                                       int nP, int r, int rp, float scale,
+                                                       uint16_t* __restrict__ pad,
+                                                       int64_t ldpad, uint16_t* __restrict__ hilo_t,
+                                                       int64_t ldt) {
+  __shared__ FinStage<2> stage;
+  down_fin_tile<2>(stage, part, T, KC, nP, r, rp, scale, pad, ldpad, hilo_t, ldt);
+}
 
 namespace {
 // K-chunk length (a multiple of 64) for about 256 partial workgroups (at
@@ -299,7 +331,7 @@ size_t lora_down_part_bytes(int64_t T, int64_t K, int64_t nprp) {
 hipError_t launch_lora_down(const uint16_t* in, int64_t ldin, int64_t T, int64_t K,
                             const uint16_t* const* P, int nP, int64_t r, float scale, uint16_t* pad,
                             int64_t ldpad, uint16_t* hilo_t, int64_t ldt, int64_t rp, float* part,
-                            hipStream_t s, const uint8_t* keep, int64_t ldk, int planes) {
+                            hipStream_t s, const uint8_t* keep, int64_t ldk) {
   if (T <= 0) return hipSuccess;
   if (nP < 1 || nP > kMaxProj) return hipErrorInvalidValue;
   // 32-bit buffer offsets: one tile's rows of `in` and P stay under 2^31 bytes
@@ -319,16 +351,19 @@ hipError_t launch_lora_down(const uint16_t* in, int64_t ldin, int64_t T, int64_t
     hipLaunchKernelGGL(k_lora_down_part<false>, grid, dim3(256), 0, s, in, ldin, T, K, f,
                        static_cast<int>(r), static_cast<int>(rp), kch, part, keep, ldk);
   }
-  hipError_t e = hipGetLastError();
+  const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
+  return launch_lora_down_fin(part, T, K, nP, r, scale, pad, ldpad, hilo_t, ldt, rp, s);
+}
+
+hipError_t launch_lora_down_fin(const float* part, int64_t T, int64_t K, int nP, int64_t r, float scale, uint16_t* pad,
+                                int64_t ldpad, uint16_t* hilo_t, int64_t ldt, int64_t rp, hipStream_t s) {
+  if (T <= 0) return hipSuccess;
+  const int64_t KC = ceil_div(K, down_chunk(T, K, nP * rp));
   const int64_t tt = hilo_t != nullptr ? (ldt > T ? ldt : T) : T;
-  const dim3 fgrid(static_cast<uint32_t>(ceil_div(tt, 16)), static_cast<uint32_t>(nP * rp / 64));
-  if (planes == 3)
-    hipLaunchKernelGGL(k_lora_down_fin<3>, fgrid, dim3(256), 0, s, part, T, static_cast<int>(KC), nP,
-                       static_cast<int>(r), static_cast<int>(rp), scale, pad, ldpad, hilo_t, ldt);
-  else
-    hipLaunchKernelGGL(k_lora_down_fin<2>, fgrid, dim3(256), 0, s, part, T, static_cast<int>(KC), nP,
-                       static_cast<int>(r), static_cast<int>(rp), scale, pad, ldpad, hilo_t, ldt);
+  hipLaunchKernelGGL(k_lora_down_fin, dim3(static_cast<uint32_t>(ceil_div(tt, 16)), static_cast<uint32_t>(nP * rp / 64)),
+                     dim3(256), 0, s, part, T, static_cast<int>(KC), nP, static_cast<int>(r), static_cast<int>(rp),
+                     scale, pad, ldpad, hilo_t, ldt);
   return hipGetLastError();
 }
 
@@ -368,21 +403,25 @@ __device__ __forceinline__ int grad_qslot(int c, int w) { return kGradPitch * c 
 // second launch adds the slices in order (k_sum_slices).
 // NP: planes of Pt (2: hi and lo; 3: and what they leave, for fp32 sums of fp32
 // factors instead of 16-bit ones).
-template <int JT, bool kJC, bool kMask, int NP = 2>
-__global__ __launch_bounds__(256) void k_lora_grad(const uint16_t* __restrict__ Pt, int64_t T,
-                                                   int64_t ldt, int rp, const uint16_t* __restrict__ Q,
-                                                   int64_t C, int64_t ldq, int r, int j0, int rproj,
-                                                   float* __restrict__ part, int64_t TS,
-                                                   const uint8_t* __restrict__ keep, int64_t ldk,
-                                                   float oscale) {
-  constexpr int kPRows = 32 * NP * JT;  // hi rows [0, 32JT), lo rows [32JT, 64JT), ...
-  __shared__ uint32_t s_q[2][kGradCT * kGradPitch];
-  __shared__ uint32_t s_p[2][kPRows * kGradPitch];
+template <int JT, int NP>
+struct GradStage {
+  uint32_t q[2][kGradCT * kGradPitch];
+  uint32_t p[2][32 * NP * JT * kGradPitch];  // hi rows [0, 32JT), lo rows [32JT, 64JT), ...
+};
+namespace {
+template <int JT, bool kJC, bool kMask, int NP>
+__device__ __forceinline__ void grad_tile(GradStage<JT, NP>& stage, const uint16_t* __restrict__ Pt, int64_t T,
+                                          int64_t ldt, int rp, const uint16_t* __restrict__ Q, int64_t C, int64_t ldq,
+                                          int r, int j0, int rproj, float* __restrict__ part, int64_t TS,
+                                          const uint8_t* __restrict__ keep, int64_t ldk, float oscale, int64_t bx,
+                                          int64_t by) {
+  auto& s_q = stage.q;
+  auto& s_p = stage.p;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r32 = lane & 31, h = lane >> 5;
-  const int64_t c0 = static_cast<int64_t>(blockIdx.x) * kGradCT;
-  const int64_t ts = static_cast<int64_t>(blockIdx.y) * TS;
+  const int64_t c0 = bx * kGradCT;
+  const int64_t ts = by * TS;
   const int64_t te = ts + TS < T ? ts + TS : T;
   const int nsteps = static_cast<int>((te - ts + 63) / 64);
 
@@ -518,7 +557,7 @@ __global__ __launch_bounds__(256) void k_lora_grad(const uint16_t* __restrict__ 
     body(step, I0{});
     body(step + 1, I1{});
   }
-  float* const out = part + static_cast<int64_t>(blockIdx.y) * r * C;  // this slice's sums
+  float* const out = part + by * r * C;  // this slice's sums
   if constexpr (kJC) {
     // D[j][c]: lane holds column c, rows j = 8*(e/4) + 4*h + e%4
     const int64_t cc = c0 + c;
@@ -543,6 +582,19 @@ __global__ __launch_bounds__(256) void k_lora_grad(const uint16_t* __restrict__ 
       }
     }
   }
+}
+}  // namespace
+
+template <int JT, bool kJC, bool kMask>
+__global__ __launch_bounds__(256) void k_lora_grad(const uint16_t* __restrict__ Pt, int64_t T,
+                                                   int64_t ldt, int rp, const uint16_t* __restrict__ Q,
+                                                   int64_t C, int64_t ldq, int r, int j0, int rproj,
+                                                   float* __restrict__ part, int64_t TS,
+                                                   const uint8_t* __restrict__ keep, int64_t ldk,
+                                                   float oscale) {
+  __shared__ __attribute__((aligned(16))) GradStage<JT, 2> stage;
+  grad_tile<JT, kJC, kMask, 2>(stage, Pt, T, ldt, rp, Q, C, ldq, r, j0, rproj, part, TS, keep, ldk, oscale,
+                                blockIdx.x, blockIdx.y);
 }
 
 // Token slices (multiples of 64 tokens) for about one workgroup per CU: more
@@ -572,12 +624,12 @@ int64_t lora_grad_slices(int64_t T, int64_t C, int64_t ldq, int planes) {
 
 hipError_t launch_lora_grad(const uint16_t* Pt, int64_t T, int64_t ldt, int64_t rp, const uint16_t* Q,
                             int64_t C, int64_t ldq, int64_t r, float* part, bool out_jc, hipStream_t s,
-                            const uint8_t* keep, int64_t ldk, float oscale, int64_t rproj, int planes) {
+                            const uint8_t* keep, int64_t ldk, float oscale, int64_t rproj) {
   if (T <= 0) return hipSuccess;
   if (rproj <= 0) rproj = r;
-  if (ceil_div(r, rproj) * planes * rp * ldt * 2 >= (int64_t(1) << 31)) return hipErrorInvalidValue;  // Pt under 2^31 bytes
+  if (ceil_div(r, rproj) * 2 * rp * ldt * 2 >= (int64_t(1) << 31)) return hipErrorInvalidValue;  // Pt under 2^31 bytes
   if (keep != nullptr && T * ldk >= (int64_t(1) << 31)) return hipErrorInvalidValue;
-  const int64_t TS = grad_slice_tokens(T, C, ldq, planes);
+  const int64_t TS = grad_slice_tokens(T, C, ldq, 2);
   const int64_t slices = ceil_div(T, TS);
   const int64_t ctiles = ceil_div(C, kGradCT);
   const dim3 grid(static_cast<uint32_t>(ctiles), static_cast<uint32_t>(slices));
@@ -586,23 +638,13 @@ hipError_t launch_lora_grad(const uint16_t* Pt, int64_t T, int64_t ldt, int64_t 
     const int64_t left = r - j0;
     const int jt = static_cast<int>(ceil_div(left < 32 * kGradMaxJT ? left : 32 * kGradMaxJT, 32));
     const int ij0 = static_cast<int>(j0);
-#define QLORA_GRAD(JTV, JC, MK, ...)                                                                           \
-  hipLaunchKernelGGL((k_lora_grad<JTV, JC, MK __VA_OPT__(,) __VA_ARGS__>), grid, dim3(256), 0, s, Pt, T, ldt, irp, Q, C, \
+#define QLORA_GRAD(JTV, JC, MK)                                                                           \
+  hipLaunchKernelGGL((k_lora_grad<JTV, JC, MK>), grid, dim3(256), 0, s, Pt, T, ldt, irp, Q, C, \
                      ldq, ir, ij0, static_cast<int>(rproj), part, TS, keep, ldk, oscale)
     if (keep != nullptr) {  // the masked operand is X: dA, out_jc
       if (jt <= 1) QLORA_GRAD(1, true, true);
       else if (jt <= 2) QLORA_GRAD(2, true, true);
       else QLORA_GRAD(4, true, true);
-    } else if (planes == 3) {
-      if (out_jc) {
-        if (jt <= 1) QLORA_GRAD(1, true, false, 3);
-        else if (jt <= 2) QLORA_GRAD(2, true, false, 3);
-        else QLORA_GRAD(4, true, false, 3);
-      } else {
-        if (jt <= 1) QLORA_GRAD(1, false, false, 3);
-        else if (jt <= 2) QLORA_GRAD(2, false, false, 3);
-        else QLORA_GRAD(4, false, false, 3);
-      }
     } else if (out_jc) {
       if (jt <= 1) QLORA_GRAD(1, true, false);
       else if (jt <= 2) QLORA_GRAD(2, true, false);
@@ -787,8 +829,8 @@ struct SumList {
   int count;
 };
 
-__global__ __launch_bounds__(256) void k_sum_slices(SumList L) {
-  const int64_t wg = blockIdx.x;
+namespace {
+__device__ __forceinline__ void sum_slices_tile(SumList L, int64_t wg) {
   int b = 0;
 #pragma unroll
   for (int i = 1; i < kMaxFill; ++i)
@@ -818,6 +860,48 @@ __global__ __launch_bounds__(256) void k_sum_slices(SumList L) {
   *reinterpret_cast<f32x4*>(out + idx) = acc;
 }
 
+// C[m][n] = bf16(sum over z = 0, 1, ... of part[z][m][n]), the splits added
+// in order (bit-reproducible), one rounding.  Thread: 8 consecutive columns
+// of one row; N % 8 == 0.
+__device__ __forceinline__ void split_sum_tile(const float* part, int S, int64_t M, int64_t N, int64_t ldp, uint16_t* C,
+                                               int64_t ldc, int64_t wg) {
+  const int64_t groups = N / 8;
+  const int64_t id = wg * 256 + threadIdx.x;
+  if (id >= M * groups) return;
+  const int64_t m = id / groups, n = (id % groups) * 8;
+  float acc[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+  for (int z = 0; z < S; ++z) {
+    const float* src = part + (static_cast<int64_t>(z) * M + m) * ldp + n;
+    const f32x4 u = *reinterpret_cast<const f32x4*>(src);
+    const f32x4 v = *reinterpret_cast<const f32x4*>(src + 4);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      acc[e] += u[e];
+      acc[4 + e] += v[e];
+    }
+  }
+  *reinterpret_cast<u32x4*>(C + m * ldc + n) =
+      u32x4{pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]), pack_bf16x2(acc[4], acc[5]),
+            pack_bf16x2(acc[6], acc[7])};
+}
+}  // namespace
+
+__global__ __launch_bounds__(256) void k_split_sum(const float* part, int S, int64_t M, int64_t N,
+                                                   int64_t ldp, uint16_t* C, int64_t ldc) {
+  split_sum_tile(part, S, M, N, ldp, C, ldc, blockIdx.x);
+}
+
+hipError_t launch_split_sum(const float* part, int S, int64_t M, int64_t N, uint16_t* C, int64_t ldc,
+                            hipStream_t s) {
+  hipLaunchKernelGGL(k_split_sum, dim3(static_cast<uint32_t>(ceil_div(M * (N / 8), 256))), dim3(256), 0, s, part, S,
+                     M, N, N, C, ldc);
+  return hipGetLastError();
+}
+
+__global__ __launch_bounds__(256) void k_sum_slices(SumList L) { sum_slices_tile(L, blockIdx.x); }
+
 hipError_t launch_sum_slices(const float* const* part, const int* slices, const int64_t* n, float* const* out,
                              int count, hipStream_t s, const int64_t* stride) {
   if (count < 1 || count > kMaxFill) return hipErrorInvalidValue;
@@ -838,6 +922,186 @@ hipError_t launch_sum_slices(const float* const* part, const int* slices, const 
   L.first[count] = wgs;
   if (wgs == 0) return hipSuccess;
   hipLaunchKernelGGL(k_sum_slices, dim3(static_cast<uint32_t>(wgs)), dim3(256), 0, s, L);
+  return hipGetLastError();
+}
+
+// ---------------------------------------------------------------------------
+// The 8-bit layer's rank products: the same work as above in fewer launches.
+// At these sizes (a few hundred tokens and less) a launch costs more than what
+// it computes, so pieces that do not depend on each other share one, by ranges
+// of the workgroup index:
+//   k_lora_front     X A^T by K-chunks | the activations' codes | factor copies
+//   k_lora_fin_two   sU and sV from their K-chunks
+//   k_lora_grad_two  dA and dB by token slices
+//   k_grad_sums      the slices of dA and dB | the K splits of dX
+// Every piece is the same code and adds in the same order as on its own.
+// ---------------------------------------------------------------------------
+namespace {
+struct FrontArgs {
+  const uint16_t* in;
+  int64_t ldin, T, K, kch;
+  DownFactors P;
+  float* part;
+  int r, rp, gx, kc;                   // grid of the down product: gx tokens, kc K-chunks, rp / 64 rank tiles
+  Fp8Rows rows;
+  const uint16_t* B; uint16_t* bt;     // bt [r][out] = B^T (out = 0: none)
+  int64_t out;
+  const uint16_t* src; uint16_t* dst;  // dst: src padded (pad_elem)
+  int64_t R, ldd;
+  int transpose;
+  int64_t rows0, bt0, pad0;            // first workgroup of the later ranges
+};
+}  // namespace
+
+__global__ __launch_bounds__(256) void k_lora_front(FrontArgs a) {
+  __shared__ __attribute__((aligned(16))) DownStage stage;
+  const int64_t wg = blockIdx.x;
+  if (wg < a.rows0) {
+    const uint32_t w = static_cast<uint32_t>(wg), gx = static_cast<uint32_t>(a.gx), kc = static_cast<uint32_t>(a.kc);
+    down_part_tile<false>(stage, a.in, a.ldin, a.T, a.K, a.P, a.r, a.rp, a.kch, a.part, nullptr, 0, w % gx,
+                          w / gx % kc, static_cast<int>(w / gx / kc), a.rp);
+  } else if (wg < a.bt0) {
+    fp8_rows_tile(a.rows, static_cast<uint32_t>(wg - a.rows0));
+  } else if (wg < a.pad0) {
+    transpose_elem((wg - a.bt0) * 256 + threadIdx.x, a.B, a.out, a.r, a.bt);
+  } else {
+    pad_elem((wg - a.pad0) * 256 + threadIdx.x, a.src, a.R, a.r, a.transpose, a.dst, a.rp, a.ldd);
+  }
+}
+
+hipError_t launch_lora_front(const LoraFront& f, hipStream_t s) {
+  if (f.T <= 0) return hipSuccess;
+  if (kDownTok * f.K * 2 >= (int64_t(1) << 31)) return hipErrorInvalidValue;  // 32-bit buffer offsets
+  FrontArgs a{};
+  a.in = f.in; a.ldin = a.K = f.K; a.T = f.T;
+  a.P.p[0] = f.P;
+  a.part = f.part;
+  a.r = static_cast<int>(f.r);
+  a.rp = static_cast<int>(f.rp);
+  a.kch = down_chunk(f.T, f.K, f.rp);
+  a.gx = static_cast<int>(ceil_div(f.T, kDownTok));
+  a.kc = static_cast<int>(ceil_div(f.K, a.kch));
+  a.rows = f.rows;
+  a.B = f.B; a.bt = f.bt; a.out = f.out;
+  a.src = f.src; a.dst = f.dst; a.R = f.R; a.ldd = f.ldd; a.transpose = f.transpose ? 1 : 0;
+  a.rows0 = int64_t(a.gx) * a.kc * (f.rp / kDownRanks);
+  a.bt0 = a.rows0 + (f.rows.T > 0 ? fp8_rows_blocks(f.rows) : 0);
+  a.pad0 = a.bt0 + ceil_div(f.out * f.r, 256);
+  const int64_t wgs = a.pad0 + ceil_div(f.R * f.rp, 256);
+  if (wgs >= (int64_t(1) << 31)) return hipErrorInvalidValue;
+  hipLaunchKernelGGL(k_lora_front, dim3(static_cast<uint32_t>(wgs)), dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
+namespace {
+struct FinTwo {
+  const float* part[2];
+  uint16_t* pad[2];
+  uint16_t* hilo_t[2];
+  int kc[2];
+};
+}  // namespace
+
+__global__ __launch_bounds__(256) void k_lora_fin_two(FinTwo f, int64_t T, int r, int rp, float scale, int64_t ldpad,
+                                                      int64_t ldt) {
+  __shared__ FinStage<3> stage;
+  const bool b = blockIdx.z != 0;
+  down_fin_tile<3>(stage, b ? f.part[1] : f.part[0], T, b ? f.kc[1] : f.kc[0], 1, r, rp, scale,
+                   b ? f.pad[1] : f.pad[0], ldpad, b ? f.hilo_t[1] : f.hilo_t[0], ldt);
+}
+
+hipError_t launch_lora_fin_two(const float* const* part, const int64_t* K, int64_t T, int64_t r, int64_t rp,
+                               float scale, uint16_t* pad, int64_t ldpad, uint16_t* const* hilo_t, int64_t ldt,
+                               hipStream_t s) {
+  if (T <= 0) return hipSuccess;
+  FinTwo f{};
+  for (int i = 0; i < 2; ++i) {
+    f.part[i] = part[i];
+    f.hilo_t[i] = hilo_t[i];
+    f.kc[i] = static_cast<int>(ceil_div(K[i], down_chunk(T, K[i], rp)));
+  }
+  f.pad[1] = pad;
+  hipLaunchKernelGGL(k_lora_fin_two,
+                     dim3(static_cast<uint32_t>(ceil_div(ldt > T ? ldt : T, 16)), static_cast<uint32_t>(rp / 64), 2),
+                     dim3(256), 0, s, f, T, static_cast<int>(r), static_cast<int>(rp), scale, ldpad, ldt);
+  return hipGetLastError();
+}
+
+namespace {
+struct GradJob {
+  const uint16_t* Pt;
+  const uint16_t* Q;
+  int64_t C, TS;
+  float* part;
+};
+}  // namespace
+
+// workgroups [0, first): dA (job 0) with ca columns tiles, the rest: dB (job 1)
+template <int JT>
+__global__ __launch_bounds__(256) void k_lora_grad_two(GradJob ja, GradJob jb, uint32_t first, uint32_t ca,
+                                                       uint32_t cb, int64_t T, int64_t ldt, int rp, int r, int j0) {
+  __shared__ __attribute__((aligned(16))) GradStage<JT, 3> stage;
+  if (blockIdx.x < first)
+    grad_tile<JT, true, false, 3>(stage, ja.Pt, T, ldt, rp, ja.Q, ja.C, ja.C, r, j0, r, ja.part, ja.TS, nullptr, 0,
+                                  1.f, blockIdx.x % ca, blockIdx.x / ca);
+  else
+    grad_tile<JT, false, false, 3>(stage, jb.Pt, T, ldt, rp, jb.Q, jb.C, jb.C, r, j0, r, jb.part, jb.TS, nullptr, 0,
+                                   1.f, (blockIdx.x - first) % cb, (blockIdx.x - first) / cb);
+}
+
+hipError_t launch_lora_grad_two(const uint16_t* const* Pt, int64_t T, int64_t ldt, int64_t rp,
+                                const uint16_t* const* Q, const int64_t* C, int64_t r, float* const* part,
+                                hipStream_t s) {
+  if (T <= 0) return hipSuccess;
+  if (3 * rp * ldt * 2 >= (int64_t(1) << 31)) return hipErrorInvalidValue;  // Pt under 2^31 bytes
+  GradJob j[2];
+  uint32_t ct[2], wgs[2];
+  for (int i = 0; i < 2; ++i) {
+    const int64_t TS = grad_slice_tokens(T, C[i], C[i], 3);
+    j[i] = GradJob{Pt[i], Q[i], C[i], TS, part[i]};
+    ct[i] = static_cast<uint32_t>(ceil_div(C[i], kGradCT));
+    wgs[i] = ct[i] * static_cast<uint32_t>(ceil_div(T, TS));
+  }
+  for (int64_t j0 = 0; j0 < r; j0 += 32 * kGradMaxJT) {
+    const int jt = static_cast<int>(ceil_div(r - j0 < 32 * kGradMaxJT ? r - j0 : 32 * kGradMaxJT, 32));
+    const dim3 grid(wgs[0] + wgs[1]);
+    const int irp = static_cast<int>(rp), ir = static_cast<int>(r), ij0 = static_cast<int>(j0);
+    if (jt <= 1) hipLaunchKernelGGL(k_lora_grad_two<1>, grid, dim3(256), 0, s, j[0], j[1], wgs[0], ct[0], ct[1], T, ldt, irp, ir, ij0);
+    else if (jt <= 2) hipLaunchKernelGGL(k_lora_grad_two<2>, grid, dim3(256), 0, s, j[0], j[1], wgs[0], ct[0], ct[1], T, ldt, irp, ir, ij0);
+    else hipLaunchKernelGGL(k_lora_grad_two<4>, grid, dim3(256), 0, s, j[0], j[1], wgs[0], ct[0], ct[1], T, ldt, irp, ir, ij0);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+__global__ __launch_bounds__(256) void k_grad_sums(SumList L, const float* part, int S, int64_t M, int64_t N,
+                                                   uint16_t* C) {
+  const int64_t wg = blockIdx.x, first = L.first[L.count];
+  if (wg < first) sum_slices_tile(L, wg);
+  else split_sum_tile(part, S, M, N, N, C, N, wg - first);
+}
+
+hipError_t launch_grad_sums(const float* const* part, const int* slices, const int64_t* n, float* const* out, int count,
+                            const float* split, int S, int64_t M, int64_t N, uint16_t* C, hipStream_t s) {
+  if (count < 0 || count > kMaxFill) return hipErrorInvalidValue;
+  SumList L{};
+  L.count = count;
+  int64_t wgs = 0;
+  for (int i = 0; i < count; ++i) {
+    if (n[i] % 4 != 0 || slices[i] < 1) return hipErrorInvalidValue;
+    L.part[i] = part[i];
+    L.out[i] = out[i];
+    L.n[i] = L.stride[i] = n[i];
+    L.slices[i] = slices[i];
+    L.first[i] = wgs;
+    wgs += ceil_div(n[i], 1024);
+  }
+  L.first[count] = wgs;
+  if (S > 1) wgs += ceil_div(M * (N / 8), 256);
+  if (wgs == 0) return hipSuccess;
+  if (wgs >= (int64_t(1) << 31)) return hipErrorInvalidValue;
+  hipLaunchKernelGGL(k_grad_sums, dim3(static_cast<uint32_t>(wgs)), dim3(256), 0, s, L, split, S, M, N, C);
   return hipGetLastError();
 }
 

@@ -812,7 +812,7 @@ namespace {
 constexpr int kFp8Planes = 3;
 
 struct Fp8Layout {
-  size_t xq, xs, u_pad, b_pad, ut, vt, b_t, a_t_pad, part, grad, split, total;
+  size_t xq, xs, u_pad, b_pad, ut, vt, b_t, a_t_pad, part, part_v, grad, split, total;
   size_t uvp, suv;  // small-token backward (dX row splits at split)
 };
 
@@ -843,10 +843,9 @@ Fp8Layout fp8_layout(int64_t T, int64_t in, int64_t out, int64_t r, bool backwar
   l.xs = c.take(fp8_row_scale_bytes(T, K));
   if (r > 0) {
     l.u_pad = c.take(static_cast<size_t>(T * rp * 4));  // [T][2rp] bf16: sU, or sV of the backward
-    size_t part = lora_down_part_bytes(T, in, rp);
+    l.part = c.take(lora_down_part_bytes(T, in, rp));
     if (backward) {
-      const size_t pv = lora_down_part_bytes(T, out, rp);
-      part = pv > part ? pv : part;
+      l.part_v = c.take(lora_down_part_bytes(T, out, rp));
       l.ut = c.take(static_cast<size_t>(kFp8Planes * rp * token_pitch(T) * 2));
       l.vt = c.take(static_cast<size_t>(kFp8Planes * rp * token_pitch(T) * 2));
       l.b_t = c.take(static_cast<size_t>(r * out * 2));
@@ -856,11 +855,15 @@ Fp8Layout fp8_layout(int64_t T, int64_t in, int64_t out, int64_t r, bool backwar
     } else {
       l.b_pad = c.take(static_cast<size_t>(out * rp * 4));
     }
-    l.part = c.take(part);
   }
   l.split = c.take(fp8_split_bytes(T, N, K));
   l.total = c.off;
   return l;
+}
+
+Fp8Rows fp8_rows(const uint16_t* x, int64_t T, int64_t K, uint8_t* codes, uint8_t* scales) {
+  return Fp8Rows{x, T, K, fp8_row_pitch(T), static_cast<uint32_t>(K),
+                 static_cast<uint32_t>(ceil_div(K, QLORA_FP8_BLOCK)), codes, scales};
 }
 
 bool fp8_shapes_ok(int64_t T, int64_t in, int64_t out, int64_t r) {
@@ -958,18 +961,24 @@ int qlora_fp8_linear_fwd(const qlora_fp8_weight* W, const qlora_bf16* X, int64_t
     return launched(e);
   }
   F8Gemm g{};
+  const Fp8Rows rows = fp8_rows(X, T, in, base + lay.xq, base + lay.xs);
   if (r > 0) {
     uint16_t* u_pad = reinterpret_cast<uint16_t*>(base + lay.u_pad);
     uint16_t* b_pad = reinterpret_cast<uint16_t*>(base + lay.b_pad);
-    e = launch_lora_down(X, in, T, in, &A, 1, r, alpha / static_cast<float>(r), u_pad, 2 * rp, nullptr, 0, rp,
-                         reinterpret_cast<float*>(base + lay.part), s);
-    if (e == hipSuccess) e = launch_pad_bf16(B, out, r, false, b_pad, rp, 2 * rp, s);
+    LoraFront f{};
+    f.in = X; f.P = A; f.T = T; f.K = in; f.r = r; f.rp = rp;
+    f.part = reinterpret_cast<float*>(base + lay.part);
+    f.rows = rows;
+    f.src = B; f.dst = b_pad; f.R = out; f.ldd = 2 * rp;
+    e = launch_lora_front(f, s);
+    if (e == hipSuccess)
+      e = launch_lora_down_fin(f.part, T, in, 1, r, alpha / static_cast<float>(r), u_pad, 2 * rp, nullptr, 0, rp, s);
     g.act1 = u_pad;
     g.wt1 = b_pad;
     g.lda1 = g.ldw1 = g.K1 = 2 * rp;
+  } else {
+    e = launch_fp8_rows(rows, s);
   }
-  if (e == hipSuccess)
-    e = launch_fp8_rows(X, in, T, in, base + lay.xq, base + lay.xs, fp8_row_pitch(T), s);
   g.M = T;
   g.codes = W->codes;
   g.scales = W->scales;
@@ -1036,23 +1045,35 @@ int qlora_fp8_linear_bwd(const qlora_fp8_weight* W, const qlora_bf16* X, const q
   hipError_t e = hipSuccess;
   uint16_t* ut = reinterpret_cast<uint16_t*>(base + lay.ut);
   uint16_t* vt = reinterpret_cast<uint16_t*>(base + lay.vt);
+  const Fp8Rows rows = fp8_rows(dY, T, out, base + lay.xq, base + lay.xs);
   if (r > 0) {
-    const float scale = alpha / static_cast<float>(r);
     uint16_t* v_pad = reinterpret_cast<uint16_t*>(base + lay.u_pad);
     uint16_t* b_t = reinterpret_cast<uint16_t*>(base + lay.b_t);
     uint16_t* a_t_pad = reinterpret_cast<uint16_t*>(base + lay.a_t_pad);
-    float* part = reinterpret_cast<float*>(base + lay.part);
-    const uint16_t* bt = b_t;
-    e = launch_lora_down(X, in, T, in, &A, 1, r, scale, nullptr, 0, ut, tp, rp, part, s, nullptr, 0, kFp8Planes);
-    if (e == hipSuccess) e = launch_factor_prep(B, out, r, b_t, A, in, a_t_pad, rp, 2 * rp, s);
+    float* part_u = reinterpret_cast<float*>(base + lay.part);
+    float* part_v = reinterpret_cast<float*>(base + lay.part_v);
+    LoraFront f{};
+    f.in = X; f.P = A; f.T = T; f.K = in; f.r = r; f.rp = rp;
+    f.part = part_u;
+    f.rows = rows;
+    f.B = B; f.bt = b_t; f.out = out;
+    f.src = A; f.dst = a_t_pad; f.R = in; f.ldd = 2 * rp; f.transpose = true;
+    e = launch_lora_front(f, s);
+    LoraFront v{};
+    v.in = dY; v.P = b_t; v.T = T; v.K = out; v.r = r; v.rp = rp;
+    v.part = part_v;
+    if (e == hipSuccess) e = launch_lora_front(v, s);
+    const float* parts[2] = {part_u, part_v};
+    const int64_t K[2] = {in, out};
+    uint16_t* planes[2] = {ut, vt};
     if (e == hipSuccess)
-      e = launch_lora_down(dY, out, T, out, &bt, 1, r, scale, v_pad, 2 * rp, vt, tp, rp, part, s, nullptr, 0, kFp8Planes);
+      e = launch_lora_fin_two(parts, K, T, r, rp, alpha / static_cast<float>(r), v_pad, 2 * rp, planes, tp, s);
     g.act1 = v_pad;
     g.wt1 = a_t_pad;
     g.lda1 = g.ldw1 = g.K1 = 2 * rp;
+  } else {
+    e = launch_fp8_rows(rows, s);
   }
-  if (e == hipSuccess)
-    e = launch_fp8_rows(dY, out, T, out, base + lay.xq, base + lay.xs, fp8_row_pitch(T), s);
   g.M = T;
   g.codes = W->codes;
   g.scales = W->scales;
@@ -1063,19 +1084,34 @@ int qlora_fp8_linear_bwd(const qlora_fp8_weight* W, const qlora_bf16* X, const q
   g.xs = base + lay.xs;
   g.C = dX;
   g.part = reinterpret_cast<float*>(base + lay.split);
+  g.keep_parts = r > 0;
   if (e == hipSuccess) e = launch_fp8_gemm(g, s);
   if (r > 0) {
-    // token-slice sums of dA and dB, then each added in slice order
-    float* const pa = reinterpret_cast<float*>(base + lay.grad);
-    const int64_t sa = lora_grad_slices(T, in, in, kFp8Planes), sb = lora_grad_slices(T, out, out, kFp8Planes);
-    float* const pb = pa + sa * r * in;
-    if (e == hipSuccess) e = launch_lora_grad(vt, T, tp, rp, X, in, in, r, pa, true, s, nullptr, 0, 1.f, 0, kFp8Planes);
-    if (e == hipSuccess) e = launch_lora_grad(ut, T, tp, rp, dY, out, out, r, pb, false, s, nullptr, 0, 1.f, 0, kFp8Planes);
-    const float* src[2] = {pa, pb};
-    const int slices[2] = {static_cast<int>(sa), static_cast<int>(sb)};
-    const int64_t n[2] = {r * in, out * r};
-    float* dst[2] = {dA, dB};
-    if (e == hipSuccess) e = launch_sum_slices(src, slices, n, dst, 2, s);
+    // token-slice sums of dA and dB, each added in slice order (one slice is the
+    // sum already), with the K splits of dX
+    float* pt = reinterpret_cast<float*>(base + lay.grad);
+    const int64_t C[2] = {in, out};
+    float* const dst[2] = {dA, dB};
+    float* part[2];
+    const float* src[2];
+    float* sum[2];
+    int slices[2], jobs = 0;
+    int64_t n[2];
+    for (int i = 0; i < 2; ++i) {
+      const int64_t S = lora_grad_slices(T, C[i], C[i], kFp8Planes);
+      part[i] = dst[i];
+      if (S == 1) continue;
+      src[jobs] = part[i] = pt;
+      slices[jobs] = static_cast<int>(S);
+      n[jobs] = r * C[i];
+      sum[jobs++] = dst[i];
+      pt += S * r * C[i];
+    }
+    const uint16_t* planes[2] = {vt, ut};
+    const uint16_t* Q[2] = {X, dY};
+    if (e == hipSuccess) e = launch_lora_grad_two(planes, T, tp, rp, Q, C, r, part, s);
+    if (e == hipSuccess)
+      e = launch_grad_sums(src, slices, n, sum, jobs, g.part, fp8_splits(T, in, out), T, in, dX, s);
   }
   return launched(e);
 }
