@@ -181,10 +181,6 @@ hipError_t launch_gemm_nf4t(int64_t M, int64_t N, int nproj, const Nf4Proj* proj
                             const uint8_t* keep = nullptr, int64_t ldk = 0, float keep_scale = 1.f,
                             float* part = nullptr, size_t part_bytes = 0);
 
-// C[m][n] = bf16(sum over z < S of part[z][m][n]), added in order (N % 8 == 0)
-hipError_t launch_split_sum(const float* part, int S, int64_t M, int64_t N, uint16_t* C, int64_t ldc,
-                            hipStream_t s);
-
 // The 8-bit format (fp8_format.hpp).  Weights: codes [rows][cols], scale
 // bytes [ceil(rows / 128)][ceil(cols / 128)].
 hipError_t launch_fp8_quantize(const float* w, int64_t rows, int64_t cols, uint8_t* codes, uint8_t* scales,
@@ -233,13 +229,15 @@ hipError_t launch_lora_fin_two(const float* const* part, const int64_t* K, int64
 hipError_t launch_lora_grad_two(const uint16_t* const* Pt, int64_t T, int64_t ldt, int64_t rp,
                                 const uint16_t* const* Q, const int64_t* C, int64_t r, float* const* part,
                                 hipStream_t s);
-// launch_sum_slices over count jobs (may be 0) and, where S > 1, launch_split_sum
+// launch_sum_slices over count jobs (may be 0) and, where S > 1, the splits of
+// an 8-bit product that were kept in `split`
 hipError_t launch_grad_sums(const float* const* part, const int* slices, const int64_t* n, float* const* out, int count,
                             const float* split, int S, int64_t M, int64_t N, uint16_t* C, hipStream_t s);
 // C [M][N] bf16 = activations (codes, scales as launch_fp8_rows writes them)
 // times the 8-bit weight (not transposed: N = rows, K = cols; transposed: N =
 // cols, K = rows) plus the adapter segment (K1 = 0: none; as in
-// launch_gemm_nt), rounded once.  part: fp8_split_bytes(M, N, K) bytes.
+// launch_gemm_nt), rounded once.  part: fp8_split_bytes(M, N, K) bytes, the
+// splits as fp8_sum_tile (fp8_format.hpp) reads them.
 struct F8Gemm {
   int64_t M;
   const uint8_t* codes; const uint8_t* scales;

@@ -103,4 +103,48 @@ __device__ __forceinline__ void fp8_rows_tile(const Fp8Rows& a, uint32_t blk) {
   }
 }
 
+// The K splits of a product [M][N], N % 32 == 0: fragment (m / 32, n / 32) of
+// split z is 4 KB of fp32, laid out as the matrix cores leave it: piece g = 0 ..
+// 3 of lane l (16 bytes) holds row l % 32, columns 8 g + 4 (l / 32) .. + 3.  A
+// store instruction then writes 1 KB in one piece; by rows it would touch 32
+// rows of 32 bytes (301 x 4096 outputs of 4096 codes in four splits: 17.9 us by
+// rows, 15.4 us this way).
+__device__ __forceinline__ f32x4* fp8_part_frag(float* part, int64_t z, int64_t mf, int64_t nf, int64_t M, int64_t N) {
+  return reinterpret_cast<f32x4*>(part) + ((z * ceil_div(M, 32) + mf) * (N / 32) + nf) * 256;
+}
+// C = bf16(splits added in order): a wave adds two pieces of a fragment, eight
+// splits in flight; its halves swap one piece so that a lane stores 16 bytes.
+inline int64_t fp8_sum_blocks(int64_t M, int64_t N) { return ceil_div(ceil_div(M, 32) * (N / 32), 2); }
+__device__ __forceinline__ void fp8_sum_tile(const float* part, int S, int64_t M, int64_t N, uint16_t* C, int64_t wg) {
+  const int lane = threadIdx.x & 63, h = lane >> 5, wv = threadIdx.x >> 6, j = wv & 1;
+  const int64_t id = wg * 2 + (wv >> 1), nfs = N / 32, mf = id / nfs, nf = id % nfs;
+  if (mf * 32 >= M) return;
+  f32x4 acc[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
+  const f32x4* src = fp8_part_frag(const_cast<float*>(part), 0, mf, nf, M, N) + 128 * j + lane;
+  const int64_t stride = ceil_div(M, 32) * nfs * 256;
+  for (int z0 = 0; z0 < S; z0 += 8) {
+    f32x4 v[8][2];
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+#pragma unroll
+      for (int g = 0; g < 2; ++g) v[u][g] = z0 + u < S ? src[(z0 + u) * stride + 64 * g] : f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (z0 + u < S)
+#pragma unroll
+        for (int g = 0; g < 2; ++g) acc[g] += v[u][g];
+  }
+  // half h keeps piece 2 j + h and gives the other away
+  u32x2 p[2];
+#pragma unroll
+  for (int g = 0; g < 2; ++g) p[g] = u32x2{pack_bf16x2(acc[g][0], acc[g][1]), pack_bf16x2(acc[g][2], acc[g][3])};
+  const u32x2 mine = h == 0 ? p[0] : p[1], away = h == 0 ? p[1] : p[0];
+  u32x2 got;
+#pragma unroll
+  for (int d = 0; d < 2; ++d) got[d] = static_cast<uint32_t>(__shfl_xor(static_cast<int>(away[d]), 32));
+  const u32x2 lo = h == 0 ? mine : got, hi = h == 0 ? got : mine;
+  const int64_t m = mf * 32 + (lane & 31);
+  if (m < M) *reinterpret_cast<u32x4*>(C + m * N + nf * 32 + 16 * j + 8 * h) = u32x4{lo[0], lo[1], hi[0], hi[1]};
+}
+
 }  // namespace qlora

@@ -148,7 +148,7 @@ struct F8Args {
   int64_t K1;
   uint16_t* C; int64_t ldc;
   // split-K: workgroup z takes K-steps [z ks, (z + 1) ks) (ks % 4 == 0), split 0 also the adapter,
-  // and writes fp32 partials part[z][m][n] instead of C
+  // and writes fp32 partials (fp8_part_frag) instead of C
   float* part; int64_t ks;
   int64_t gm, gn;                            // output tiles (one flat grid dimension)
 };
@@ -346,54 +346,53 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_fp8_gemm(F8Args p) {
     }
   }
 
-  if constexpr (BN == 256) {
-    // never split: each wave parks its TM x TN block in LDS (rows of TN / 8
-    // 16-byte pieces, piece q of row r at q ^ (r % 8)) and stores whole rows
-    // back, 64 pieces per instruction
-    constexpr int kPerArray = NW / 4, kPieces = TN / 8, kRowsPer = 64 / kPieces;
-    static_assert(BM == BN && TM * TN * 2 * kPerArray == BM * 128, "the waves' blocks fill the four stage arrays");
-    __syncthreads();  // every wave is done reading the stages
-    const int array = wv / kPerArray;
-    uint16_t* const s_c = (array == 0 ? s_act0 : array == 1 ? s_act1 : array == 2 ? s_wt0 : s_wt1) + (wv % kPerArray) * (TM * TN);
+  if (BN != 256 && split) {  // 256 x 256 tiles are never split
 #pragma unroll
     for (int c = 0; c < FM; ++c)
 #pragma unroll
-      for (int a = 0; a < FN; ++a)
+      for (int a = 0; a < FN; ++a) {
+        const int64_t m = m0 + wm * TM + c * 32, n = n0 + wn * TN + a * 32;
+        if (m >= p.M || n >= p.N) continue;
+        f32x4* dst = fp8_part_frag(p.part, blockIdx.z, m / 32, n / 32, p.M, p.N) + lane;
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const int row = c * 32 + r32, piece = 4 * a + g;
-          *reinterpret_cast<u32x2*>(s_c + row * TN + ((piece ^ (row & 7)) * 8) + 4 * h) =
-              u32x2{pack_bf16x2(acc[a][c][4 * g], acc[a][c][4 * g + 1]),
-                    pack_bf16x2(acc[a][c][4 * g + 2], acc[a][c][4 * g + 3])};
-        }
-    __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): this wave's block is in LDS
-#pragma unroll
-    for (int i = 0; i < TM / kRowsPer; ++i) {
-      const int row = kRowsPer * i + lane / kPieces, piece = lane % kPieces;
-      const int64_t m = m0 + wm * TM + row, n = n0 + wn * TN + 8 * piece;
-      const u32x4 v = *reinterpret_cast<const u32x4*>(s_c + row * TN + ((piece ^ (row & 7)) * 8));
-      if (m < p.M && n < p.N) __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(p.C + m * p.ldc + n));
-    }
+        for (int g = 0; g < 4; ++g)
+          dst[64 * g] = f32x4{acc[a][c][4 * g], acc[a][c][4 * g + 1], acc[a][c][4 * g + 2], acc[a][c][4 * g + 3]};
+      }
     return;
   }
-  // lane: m = r32 of fragment c, n = 32 a + 8 (e / 4) + 4 h + e % 4
+  // each wave parks its TM x TN block in LDS (rows of TN / 8 16-byte pieces,
+  // piece q of row r at q ^ (r % 8)) and stores whole rows back, 64 pieces per
+  // instruction; lane: m = r32 of fragment c, n = 32 a + 8 g + 4 h + 0 .. 3
+  constexpr int kArrays = BM == BN ? 4 : 2, kPerArray = NW / kArrays, kPieces = TN / 8, kRowsPer = 64 / kPieces;
+  constexpr int kKey = (kPieces < 8 ? kPieces : 8) - 1;
+  static_assert(TM * TN * kPerArray <= BN * 64, "the waves' blocks fit the stage arrays");
+  __builtin_amdgcn_s_waitcnt(0);  // the copies behind the last step have landed
+  __syncthreads();                // every wave is done reading the stages
+  const int array = wv / kPerArray;
+  uint16_t* const s_c = (array == 0 ? s_wt0 : array == 1 ? s_wt1 : array == 2 ? s_act0 : s_act1) + (wv % kPerArray) * (TM * TN);
 #pragma unroll
-  for (int c = 0; c < FM; ++c) {
-    const int64_t m = m0 + wm * TM + c * 32 + r32;
-    if (m >= p.M) continue;
+  for (int c = 0; c < FM; ++c)
 #pragma unroll
     for (int a = 0; a < FN; ++a)
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
-        const int64_t n = n0 + wn * TN + a * 32 + 8 * g + 4 * h;
-        if (n >= p.N) continue;
-        const f32x4 v = {acc[a][c][4 * g], acc[a][c][4 * g + 1], acc[a][c][4 * g + 2], acc[a][c][4 * g + 3]};
-        if (split)
-          *reinterpret_cast<f32x4*>(p.part + (static_cast<int64_t>(blockIdx.z) * p.M + m) * p.N + n) = v;
-        else
-          *reinterpret_cast<u32x2*>(p.C + m * p.ldc + n) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+        const int row = c * 32 + r32, piece = 4 * a + g;
+        *reinterpret_cast<u32x2*>(s_c + row * TN + ((piece ^ (row & kKey)) * 8) + 4 * h) =
+            u32x2{pack_bf16x2(acc[a][c][4 * g], acc[a][c][4 * g + 1]),
+                  pack_bf16x2(acc[a][c][4 * g + 2], acc[a][c][4 * g + 3])};
       }
+  __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): this wave's block is in LDS
+#pragma unroll
+  for (int i = 0; i < TM / kRowsPer; ++i) {
+    const int row = kRowsPer * i + lane / kPieces, piece = lane % kPieces;
+    const int64_t m = m0 + wm * TM + row, n = n0 + wn * TN + 8 * piece;
+    const u32x4 v = *reinterpret_cast<const u32x4*>(s_c + row * TN + ((piece ^ (row & kKey)) * 8));
+    if (m < p.M && n < p.N) __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(p.C + m * p.ldc + n));
   }
+}
+
+__global__ __launch_bounds__(256) void k_fp8_split_sum(const float* part, int S, int64_t M, int64_t N, uint16_t* C) {
+  fp8_sum_tile(part, S, M, N, C, blockIdx.x);
 }
 
 template __global__ void k_fp8_gemm<256, 256, 2, 4, false>(F8Args);
@@ -412,7 +411,7 @@ int f8_tile(int64_t M, int64_t N) {
 }  // namespace
 
 // Split-K: grids below two workgroups per CU (of a 256-CU part; the count
-// depends on the shape only) split K into ranges of at least four steps, at
+// depends on the shape only) split K into ranges of at least eight steps, at
 // most 16, with at most 64 MiB of partials.
 int fp8_splits(int64_t M, int64_t N, int64_t K) {
   constexpr int64_t kTarget = 512, kMaxSplits = 16, kMaxPartBytes = int64_t(64) << 20;
@@ -422,16 +421,16 @@ int fp8_splits(int64_t M, int64_t N, int64_t K) {
   const int64_t steps = ceil_div(K, kStep);
   int64_t S = kTarget / (ceil_div(M, bm) * ceil_div(N, 128));
   if (S > kMaxSplits) S = kMaxSplits;
-  if (S > steps / 4) S = steps / 4;
+  if (S > ceil_div(steps, 8)) S = ceil_div(steps, 8);
   if (S > kMaxPartBytes / (M * N * 4)) S = kMaxPartBytes / (M * N * 4);
-  if (S < 2) return 1;
+  if (S < 2 || steps < 16) return 1;  // a short K: the sum's launch costs more than the steps it saves
   const int64_t ks = round_up(ceil_div(steps, S), 4);
   return static_cast<int>(ceil_div(steps, ks));
 }
 
 size_t fp8_split_bytes(int64_t M, int64_t N, int64_t K) {
   const int S = fp8_splits(M, N, K);
-  return S > 1 ? static_cast<size_t>(S) * M * N * 4 : 0;
+  return S > 1 ? static_cast<size_t>(S) * round_up(M, 32) * N * 4 : 0;
 }
 
 hipError_t launch_fp8_gemm(const F8Gemm& g, hipStream_t s) {
@@ -476,7 +475,11 @@ hipError_t launch_fp8_gemm(const F8Gemm& g, hipStream_t s) {
     else hipLaunchKernelGGL((k_fp8_gemm<32, 128, 1, 4, false>), grid, dim3(256), 0, s, a);
   }
   hipError_t e = hipGetLastError();
-  if (e == hipSuccess && S > 1 && !g.keep_parts) e = launch_split_sum(g.part, S, a.M, a.N, a.C, a.N, s);
+  if (e == hipSuccess && S > 1 && !g.keep_parts) {
+    hipLaunchKernelGGL(k_fp8_split_sum, dim3(static_cast<uint32_t>(fp8_sum_blocks(a.M, a.N))), dim3(256), 0, s,
+                       static_cast<const float*>(g.part), S, a.M, a.N, a.C);
+    e = hipGetLastError();
+  }
   return e;
 }
 

@@ -547,6 +547,33 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N) void k_gemm(GemmArgs p) {
   }
 }
 
+// C[m][n] = bf16(sum over z = 0, 1, ... of part[z][m][n]), the splits added
+// in order (bit-reproducible), one rounding.  Thread: 8 consecutive columns
+// of one row; N % 8 == 0.
+__global__ __launch_bounds__(256) void k_split_sum(const float* part, int S, int64_t M, int64_t N,
+                                                   int64_t ldp, uint16_t* C, int64_t ldc) {
+  const int64_t groups = N / 8;
+  const int64_t id = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (id >= M * groups) return;
+  const int64_t m = id / groups, n = (id % groups) * 8;
+  float acc[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+  for (int z = 0; z < S; ++z) {
+    const float* src = part + (static_cast<int64_t>(z) * M + m) * ldp + n;
+    const f32x4 u = *reinterpret_cast<const f32x4*>(src);
+    const f32x4 v = *reinterpret_cast<const f32x4*>(src + 4);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      acc[e] += u[e];
+      acc[4 + e] += v[e];
+    }
+  }
+  *reinterpret_cast<u32x4*>(C + m * ldc + n) =
+      u32x4{pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]), pack_bf16x2(acc[4], acc[5]),
+            pack_bf16x2(acc[6], acc[7])};
+}
+
 // BM x 256 tiles (BM = 256 or 128), 8 waves (see the file comment).
 // Launch: 512 threads.
 template <int kW, int BM>
@@ -864,8 +891,10 @@ hipError_t launch_tiles(const GemmArgs& a0, hipStream_t s, float* part = nullptr
     dim3 grid(static_cast<uint32_t>(ceil_div(a.M, 128)), static_cast<uint32_t>(ceil_div(a.N, 128)),
               static_cast<uint32_t>(Sr));
     hipLaunchKernelGGL((k_gemm<128, 128, 2, 2, kW>), grid, dim3(256), 0, s, a);
-    const hipError_t e = hipGetLastError();
-    return e == hipSuccess ? launch_split_sum(part, Sr, a.M, a.N, a.C, a.ldc, s) : e;
+    const int64_t threads = a.M * (a.N / 8);
+    hipLaunchKernelGGL(k_split_sum, dim3(static_cast<uint32_t>(ceil_div(threads, 256))), dim3(256), 0, s,
+                       static_cast<const float*>(part), Sr, a.M, a.N, a.N, a.C, a.ldc);
+    return hipGetLastError();
   }
   a.part = nullptr;
   if (tc.bn == 256) {

@@ -5,8 +5,7 @@
 // sU and sV are kept as bf16 pairs hi + lo (hi = bf16(v), lo = bf16(v - hi)),
 // so products with them carry ~16 bits of the fp32 value; all accumulation is
 // fp32.  Also the zero-padding / transposition of the small LoRA matrices
-// into the layouts the GEMM's extra K-steps read, and the sums over token slices
-// and K splits.
+// into the layouts the GEMM's extra K-steps read.
 #include <type_traits>
 
 #include "common.hpp"
@@ -256,18 +255,25 @@ __device__ __forceinline__ void down_fin_tile(FinStage<NP>& stage, const float* 
   // rank columns of this workgroup: projection pj, ranks jj .. jj + 63 (rp % 64 == 0)
   const int pj = jb / rp, jj = jb % rp;
   const bool live_rank = jj + jl < r;
+  // every load of the workgroup's values before the first use: the partials
+  // come from other XCDs, 2 us a round trip (four rounds of 16 loads: 7.2 us
+  // against 4 for 64 tokens of rank 16).  Places that do not count read one that exists.
+  float pv[4][kDownMaxKC];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t t = tb + (tid >> 6) + 4 * i;
+    const float* src = part + (t < T ? t : T - 1) * npr + jb + (live_rank ? jl : 0);
+#pragma unroll
+    for (int q = 0; q < kDownMaxKC; ++q) pv[i][q] = src[static_cast<int64_t>(q < KC ? q : KC - 1) * T * npr];
+  }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int tl = (tid >> 6) + 4 * i;
     const int64_t t = tb + tl;
     const bool ok = t < T;
-    float pv[kDownMaxKC];
-#pragma unroll
-    for (int q = 0; q < kDownMaxKC; ++q)
-      pv[q] = (ok && live_rank && q < KC) ? part[(static_cast<int64_t>(q) * T + t) * npr + jb + jl] : 0.f;
     float v = 0.f;
 #pragma unroll
-    for (int q = 0; q < kDownMaxKC; ++q) v += pv[q];
+    for (int q = 0; q < kDownMaxKC; ++q) v += ok && live_rank && q < KC ? pv[i][q] : 0.f;
     v *= scale;
     const uint32_t hb = pack_bf16x2(v, 0.f) & 0xffffu;
     const float hi = __builtin_bit_cast(float, hb << 16);
@@ -860,45 +866,7 @@ __device__ __forceinline__ void sum_slices_tile(SumList L, int64_t wg) {
   *reinterpret_cast<f32x4*>(out + idx) = acc;
 }
 
-// C[m][n] = bf16(sum over z = 0, 1, ... of part[z][m][n]), the splits added
-// in order (bit-reproducible), one rounding.  Thread: 8 consecutive columns
-// of one row; N % 8 == 0.
-__device__ __forceinline__ void split_sum_tile(const float* part, int S, int64_t M, int64_t N, int64_t ldp, uint16_t* C,
-                                               int64_t ldc, int64_t wg) {
-  const int64_t groups = N / 8;
-  const int64_t id = wg * 256 + threadIdx.x;
-  if (id >= M * groups) return;
-  const int64_t m = id / groups, n = (id % groups) * 8;
-  float acc[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) acc[e] = 0.f;
-  for (int z = 0; z < S; ++z) {
-    const float* src = part + (static_cast<int64_t>(z) * M + m) * ldp + n;
-    const f32x4 u = *reinterpret_cast<const f32x4*>(src);
-    const f32x4 v = *reinterpret_cast<const f32x4*>(src + 4);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      acc[e] += u[e];
-      acc[4 + e] += v[e];
-    }
-  }
-  *reinterpret_cast<u32x4*>(C + m * ldc + n) =
-      u32x4{pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]), pack_bf16x2(acc[4], acc[5]),
-            pack_bf16x2(acc[6], acc[7])};
-}
 }  // namespace
-
-__global__ __launch_bounds__(256) void k_split_sum(const float* part, int S, int64_t M, int64_t N,
-                                                   int64_t ldp, uint16_t* C, int64_t ldc) {
-  split_sum_tile(part, S, M, N, ldp, C, ldc, blockIdx.x);
-}
-
-hipError_t launch_split_sum(const float* part, int S, int64_t M, int64_t N, uint16_t* C, int64_t ldc,
-                            hipStream_t s) {
-  hipLaunchKernelGGL(k_split_sum, dim3(static_cast<uint32_t>(ceil_div(M * (N / 8), 256))), dim3(256), 0, s, part, S,
-                     M, N, N, C, ldc);
-  return hipGetLastError();
-}
 
 __global__ __launch_bounds__(256) void k_sum_slices(SumList L) { sum_slices_tile(L, blockIdx.x); }
 
@@ -1079,7 +1047,7 @@ __global__ __launch_bounds__(256) void k_grad_sums(SumList L, const float* part,
                                                    uint16_t* C) {
   const int64_t wg = blockIdx.x, first = L.first[L.count];
   if (wg < first) sum_slices_tile(L, wg);
-  else split_sum_tile(part, S, M, N, N, C, N, wg - first);
+  else fp8_sum_tile(part, S, M, N, C, wg - first);
 }
 
 hipError_t launch_grad_sums(const float* const* part, const int* slices, const int64_t* n, float* const* out, int count,
@@ -1098,7 +1066,7 @@ hipError_t launch_grad_sums(const float* const* part, const int* slices, const i
     wgs += ceil_div(n[i], 1024);
   }
   L.first[count] = wgs;
-  if (S > 1) wgs += ceil_div(M * (N / 8), 256);
+  if (S > 1) wgs += fp8_sum_blocks(M, N);
   if (wgs == 0) return hipSuccess;
   if (wgs >= (int64_t(1) << 31)) return hipErrorInvalidValue;
   hipLaunchKernelGGL(k_grad_sums, dim3(static_cast<uint32_t>(wgs)), dim3(256), 0, s, L, split, S, M, N, C);
