@@ -871,7 +871,7 @@ bool fp8_shapes_ok(int64_t T, int64_t in, int64_t out, int64_t r) {
   // the rank-r products address a tile's rows of X, dY, A, B and the planes of
   // sU, sV with 32-bit offsets
   constexpr int64_t kRowMost = int64_t(1) << 23;
-  return r == 0 || T <= kDecodeMaxT ||
+  return r == 0 || fp8_decode_fits(T, in) ||
          (in < kRowMost && out < kRowMost && kFp8Planes * 2 * padded_rank(r) * token_pitch(T) <= kMaxOperandBytes);
 }
 
