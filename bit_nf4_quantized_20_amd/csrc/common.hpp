@@ -281,9 +281,10 @@ struct MoeArgs {
   float* part;
   uint16_t* Y;
   int T, E, k, H, I;
-  // set by the launcher: workgroup slots (experts or pairs), row ranges and
-  // waves that split the reduction, of the two kernels
-  int by_expert, slots, ranges_up, ranges_down, kw_up, kw_down;
+  // set by the launcher: workgroup slots (experts or pairs) and, per launch,
+  // the waves that split the reduction, the row ranges, and the workgroups that
+  // share a range's column tiles
+  int by_expert, slots, kw, ranges, cols;
 };
 hipError_t launch_moe(MoeArgs a, hipStream_t s);
 

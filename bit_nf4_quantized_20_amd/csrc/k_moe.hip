@@ -162,9 +162,8 @@ __global__ __launch_bounds__(256) void k_moe_route_bwd(const float* __restrict__
 //
 // Both products are the same panel product: 16-row tiles of an expert's NF4
 // rows against the columns of the pairs (token, choice) that chose it.  A
-// workgroup of eight waves takes one expert and a range of its rows; KW waves
-// share a row group and split the reduction, the others take further row
-// groups.  A wave walks its 64-weight blocks in chunks of four (lane (n = l %
+// workgroup takes one expert and a range of its rows; kw of its waves share a
+// row group and split the reduction, the others take further row groups.  A wave walks its 64-weight blocks in chunks of four (lane (n = l %
 // 16, g = l / 16): block g of the chunk of row n): the columns' values of the
 // chunk go into registers once and meet RB row tiles, whose codes are
 // dequantized in registers (MFMA A operand) with their loads kDepth tiles
@@ -288,6 +287,17 @@ __device__ __forceinline__ int find_pairs(PairList<NW>& s, const MoeArgs& a, int
   return e;
 }
 
+// Workgroup -> slot, row range, and which of the range's column workgroups;
+// those are eight apart, on one XCD, so that they share the weights in its L2.
+// False: past the last.
+__device__ __forceinline__ bool place(const MoeArgs& a, int& slot, int& range, int& col) {
+  const int lin = blockIdx.x, w = lin / (8 * a.cols) * 8 + lin % 8;
+  col = lin / 8 % a.cols;
+  range = w % a.ranges;
+  slot = w / a.ranges;
+  return slot < a.slots;
+}
+
 // acc[r][t] += rows of tile r (row offsets trow[r], in blocks, of this lane's
 // row) times the columns of tile t, over blocks [b0, b1).  The columns' values
 // lie at colf[t] (byte offsets in rx; kPastEnd: zero column), 128 bytes per
@@ -375,7 +385,9 @@ __global__ __launch_bounds__(64 * NW, NT == 1 ? (kDepth == 1 ? 4 : 3) : 2) void 
   __shared__ f32x4 s_acc[NW / 2][RB * NT][64];
   const int lane = threadIdx.x & 63;
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int kw = a.kw_up, range = blockIdx.x % a.ranges_up, slot = blockIdx.x / a.ranges_up;
+  const int kw = a.kw;
+  int slot, range, col;
+  if (!place(a, slot, range, col)) return;
   const uint16_t* list;
   int nc;
   const int e = find_pairs(s, a, slot, list, nc);
@@ -396,7 +408,7 @@ __global__ __launch_bounds__(64 * NW, NT == 1 ? (kDepth == 1 ? 4 : 3) : 2) void 
   const int z = wv % kw, b0 = tile0 < tiles ? static_cast<int>(nb * z / kw) : 0;
   const int b1 = tile0 < tiles ? static_cast<int>(nb * (z + 1) / kw) : 0;
 
-  for (int c0 = 0; c0 < nc; c0 += 16 * NT) {
+  for (int c0 = 16 * NT * col; c0 < nc; c0 += 16 * NT * a.cols) {
     f32x4 acc[RB][NT];
     uint32_t colf[NT];
 #pragma unroll
@@ -441,7 +453,9 @@ __global__ __launch_bounds__(64 * NW, 2) void k_moe_down(MoeArgs a) {
   __shared__ f32x4 s_acc[NW / 2][RB * NT][64];
   const int lane = threadIdx.x & 63;
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int kw = a.kw_down, range = blockIdx.x % a.ranges_down, slot = blockIdx.x / a.ranges_down;
+  const int kw = a.kw;
+  int slot, range, col;
+  if (!place(a, slot, range, col)) return;
   const uint16_t* list;
   int nc;
   const int e = find_pairs(s, a, slot, list, nc);
@@ -456,7 +470,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_moe_down(MoeArgs a) {
   for (int r = 0; r < RB; ++r) trow[r] = (16 * (tile0 + r < tiles ? tile0 + r : tiles - 1) + n) * nb;
   const int z = wv % kw, b0 = tile0 < tiles ? static_cast<int>(nb * z / kw) : 0;
   const int b1 = tile0 < tiles ? static_cast<int>(nb * (z + 1) / kw) : 0;
-  for (int c0 = 0; c0 < nc; c0 += 16 * NT) {
+  for (int c0 = 16 * NT * col; c0 < nc; c0 += 16 * NT * a.cols) {
     f32x4 acc[RB][NT];
     uint32_t colf[NT];
 #pragma unroll
@@ -618,17 +632,20 @@ hipError_t launch_moe_route_bwd(const float* logits, const int* ids, const float
 }
 
 namespace {
-// Waves that split a reduction of nb 64-weight blocks: as many of the eight as
-// keep the lanes at least 7/8 busy (a chunk is four blocks), with few
-// workgroups as many as have a block at all.
-int moe_split_waves(int nb, int waves, bool few) {
-  int kw = waves;
-  if (few) {
-    while (kw > 1 && kw > nb) kw /= 2;
-    return kw;
-  }
-  while (kw > 1 && kw * round_up(ceil_div(nb, kw), 4) * 7 > nb * 8) kw /= 2;
-  return kw;
+constexpr int kLeast = 512;
+
+// Row ranges of one expert's `rows` rows, of which a wave takes rows_wave, and
+// the waves that split a reduction of nb 64-weight blocks: as many as keep the
+// lanes at least 7/8 busy (a chunk is four blocks), and where that leaves fewer
+// than `least` workgroups as many more as have a block at all.  (Short row
+// groups, 52 tokens x 4 over 60 experts of 512 x 448: one block per wave 46.5 us,
+// this way 38.8; 3 x 4 over 8 of 640 x 3776 44.6 and 33.3.)
+void moe_ranges(MoeArgs& a, int rows, int rows_wave, int nb, int waves, int least) {
+  auto ranges = [&](int kw) { return static_cast<int>(ceil_div(rows, rows_wave * (waves / kw))); };
+  a.kw = waves;
+  while (a.kw > 1 && a.kw * round_up(ceil_div(nb, a.kw), 4) * 7 > nb * 8) a.kw /= 2;
+  while (a.kw < waves && 2 * a.kw <= nb && int64_t(a.slots) * ranges(a.kw) < least) a.kw *= 2;
+  a.ranges = ranges(a.kw);
 }
 }  // namespace
 
@@ -636,30 +653,48 @@ hipError_t launch_moe(MoeArgs a, hipStream_t s) {
   const int P = a.T * a.k;
   a.by_expert = a.E <= P ? 1 : 0;
   a.slots = a.by_expert ? a.E : P;
-  // wide row groups (four 16-row tiles a wave) where those still fill the chip
-  // twice, else the narrowest
-  const bool few_up = int64_t(a.slots) * a.I / 32 < 1024;
-  const bool few_down = P <= 64 && int64_t(a.slots) * a.H / 64 < 512;
   // pairs per expert on average: above half a column tile, two of them at a time
   const bool two = P > 8 * a.E;
-  const int tiles_down = two ? 4 : kDownTiles;
-  const int waves_up = few_up ? kFewWaves : kUpWaves, tiles_up = few_up ? 1 : kUpTiles / 2;
-  a.kw_up = moe_split_waves(a.H / 64, waves_up, few_up);
-  a.kw_down = moe_split_waves(a.I / 64, kDownWaves, false);
-  a.ranges_up = static_cast<int>(ceil_div(a.I, 16 * tiles_up * (waves_up / a.kw_up)));
-  a.ranges_down = static_cast<int>(ceil_div(a.H, 16 * tiles_down * (kDownWaves / a.kw_down)));
-  const dim3 block_up(64 * kUpWaves), block_down(64 * kDownWaves), few(64 * kFewWaves), up(static_cast<uint32_t>(a.ranges_up * a.slots));
-  if (few_up) hipLaunchKernelGGL((k_moe_gate_up<2, 1, kFewWaves, 2>), up, few, 0, s, a);
+  // Column tiles of an expert, shared by several workgroups where there are few
+  // (61 tokens x 4 over 4 experts of 576 x 2304: 76.8 -> 62.6 us).
+  const int col_tiles = static_cast<int>(ceil_div(P, 32 * a.E));
+  auto grid = [&]() {
+    const int64_t wgs = int64_t(a.slots) * a.ranges;
+    a.cols = two && wgs < kLeast ? col_tiles : 1;
+    return dim3(static_cast<uint32_t>(round_up(wgs, 8) * a.cols));
+  };
+  // Tall row groups where those fill the chip, else short ones with the reduction
+  // split further: the tall ones dequantize as much for fewer reads of the
+  // columns.  Gate and up, tall / short: 7 tokens x 8 over 60 experts of 3392 x
+  // 448 (784 units of 32 rows) 72.7 / 61.5 us the layer; with two column tiles 40
+  // x 7 over 16 of 512 x 1664 (832) 32.3 / 66.6.
+  const bool few_up = int64_t(a.slots) * a.I / 32 < (two ? 512 : 1024);
+  if (few_up) moe_ranges(a, a.I, 16, a.H / 64, kFewWaves, kLeast);
+  else moe_ranges(a, a.I, 16 * kUpTiles / 2, a.H / 64, kUpWaves, 0);
+  const dim3 up = grid(), block_up(64 * (few_up ? kFewWaves : kUpWaves));
+  if (few_up && !two) hipLaunchKernelGGL((k_moe_gate_up<2, 1, kFewWaves, 2>), up, block_up, 0, s, a);
+  else if (few_up) hipLaunchKernelGGL((k_moe_gate_up<2, 2, kFewWaves, 2>), up, block_up, 0, s, a);
   else if (!two) hipLaunchKernelGGL((k_moe_gate_up<kUpTiles, 1, kUpWaves, kUpDepth>), up, block_up, 0, s, a);
   else hipLaunchKernelGGL((k_moe_gate_up<kUpTiles, 2, kUpWaves, 2>), up, block_up, 0, s, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  if (few_down) {
-    hipLaunchKernelGGL(k_moe_down_few, dim3(static_cast<uint32_t>(a.H / 16)), few, 0, s, a);
+  // One launch where the few workgroups of 16 rows have little to do each: 7 pairs
+  // of 2496 x 576 22.2 us the layer against 33.2 with two; 42 pairs of 640 x 5504
+  // the other way 344 against 111.
+  if (P <= 64 && int64_t(P) * a.I <= 16384) {
+    hipLaunchKernelGGL(k_moe_down_few, dim3(static_cast<uint32_t>(a.H / 16)), dim3(64 * kFewWaves), 0, s, a);
     return hipGetLastError();
   }
-  const dim3 down(static_cast<uint32_t>(a.ranges_down * a.slots));
-  if (!two) hipLaunchKernelGGL((k_moe_down<kDownTiles, 1, kDownWaves, kDownDepth>), down, block_down, 0, s, a);
+  moe_ranges(a, a.H, 16 * (two ? 4 : kDownTiles), a.I / 64, kDownWaves, 0);
+  // as above: short groups below 256 workgroups (15 tokens x 2 over 60 of 704 x
+  // 4480, 240 of them, 179 -> 77 us the layer; 5 x 5 over 32 of 1984 x 5440, 400,
+  // 96.6 tall, 113.5 short)
+  const bool few_down = int64_t(a.slots) * a.ranges < 256;
+  if (few_down) moe_ranges(a, a.H, 32, a.I / 64, kDownWaves, kLeast);
+  const dim3 down = grid(), block_down(64 * kDownWaves);
+  if (few_down && !two) hipLaunchKernelGGL((k_moe_down<2, 1, kDownWaves, kDownDepth>), down, block_down, 0, s, a);
+  else if (few_down) hipLaunchKernelGGL((k_moe_down<2, 2, kDownWaves, kDownDepth>), down, block_down, 0, s, a);
+  else if (!two) hipLaunchKernelGGL((k_moe_down<kDownTiles, 1, kDownWaves, kDownDepth>), down, block_down, 0, s, a);
   else hipLaunchKernelGGL((k_moe_down<4, 2, kDownWaves, kDownDepth>), down, block_down, 0, s, a);
   e = hipGetLastError();
   if (e != hipSuccess) return e;

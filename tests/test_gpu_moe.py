@@ -139,6 +139,35 @@ def test_experts_match_oracle(T, E, k, H, I):
     _check(host_bits(Y), *omoe.experts(vg, vd, odense.widen(X), ids, w))
 
 
+@pytest.mark.parametrize("T,E,k,H,I", [
+    (16, 64, 4, 1600, 512),   # tall row groups in both products
+    (64, 16, 3, 2048, 1024),  # the same with two column tiles at a time
+    (64, 2, 2, 256, 512),     # column tiles shared by several workgroups
+    (4, 128, 8, 128, 1024),   # tall, then short; fewer pairs than experts
+    (16, 32, 4, 256, 256), (16, 32, 4, 256, 320), (64, 8, 8, 512, 64), (61, 4, 4, 576, 256),
+])
+def test_experts_where_the_kernels_change(T, E, k, H, I):
+    """Sizes that reach every kernel of the layer; the experts repeat five."""
+    q = require_gpu()
+    banner(f"moe borders T={T} E={E} k={k} H={H} I={I}")
+    base = 5
+    assert H * I % 16384 == 0  # an expert ends with a group of scales
+    gu, dn, vg, vd = _experts(q, 65, base, H, I)
+    which = torch.arange(E, device="cuda") % base
+
+    def repeat(W):
+        def pick(t):
+            return t.view(base, -1)[which].reshape(-1).contiguous()
+        return q.NF4Weight(pick(W.codes), pick(W.absmax_q), pick(W.absmax_scale), W.rows // base * E, W.cols)
+    rng = np.random.Generator(np.random.PCG64(T * E + k))
+    ids = np.stack([rng.permutation(E)[:k] for _ in range(T)]).astype(np.int32)
+    ids[T // 2, 0] = -1
+    w = rng.normal(0, 1, (T, k)).astype(np.float32)
+    X = synth.bf16_bits(synth.normal_f32(66, (T, H), 1.0))
+    Y = q.qlora_moe_fwd(repeat(gu), repeat(dn), E, dev_bf16(X), torch.from_numpy(ids).cuda(), dev_f32(w))
+    _check(host_bits(Y), *omoe.experts(vg, vd, odense.widen(X), np.where(ids >= 0, ids % base, -1), w))
+
+
 def test_experts_special_ids():
     q = require_gpu()
     banner("moe special ids")
