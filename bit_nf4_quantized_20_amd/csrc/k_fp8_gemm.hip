@@ -155,11 +155,18 @@ struct F8Args {
 
 }  // namespace
 
-// BM x BN tile, WM x WN waves, K-steps of 128 codes through two LDS stages:
-// step e's copies of step e + 1 are issued first, then the two sub-steps are
-// computed (fragments of the next one read during the current one), then one
-// wait and one barrier.  The scale bytes of four steps sit in one register per
-// activation fragment (op_sel picks the byte) and are fetched four steps ahead.
+// BM x BN tile, WM x WN waves, K-steps of 128 codes through two LDS stages.
+// Within a step the matrix instructions of the first 64 codes and the first
+// fragment's of the second run, then comes the step's one wait and barrier:
+// every wave holds the rest of the step in registers, so the stage takes the
+// copies of step e + 2 while the second half is computed, and step e + 1's have
+// had a whole step in flight.  The activation fragments are single (each is
+// read anew behind its last use).  The scale bytes of four steps sit in one
+// register per activation fragment (op_sel picks the byte) and are fetched four
+// steps ahead.  4096 x 4096 -> 14336: 262 us with the barrier at the step's end
+// and both operands' fragments doubled, 230 this way (2.1 PF/s; without copies
+// and LDS reads the matrix instructions alone took 183, at the 2.0 GHz that the
+// power limit leaves them); 4 waves of 128 x 128 took 252.
 template <int BM, int BN, int WM, int WN, bool kTr>
 __global__ __launch_bounds__(64 * WM * WN, 1) void k_fp8_gemm(F8Args p) {
   constexpr int NW = WM * WN;
@@ -403,7 +410,11 @@ template __global__ void k_fp8_gemm<32, 128, 1, 4, false>(F8Args);
 template __global__ void k_fp8_gemm<32, 128, 1, 4, true>(F8Args);
 
 namespace {
-// rows of a tile: 256 x 256 tiles where they fill the chip, else 128 x 128, 32 x 128 for up to 32 rows
+// Rows of a tile: 256 x 256 tiles where they give every CU one (2048 tokens,
+// 14336 columns: 109 us, 4096 tokens 2.1 PF/s), else 128 x 128, which hold two
+// workgroups per CU (1024 tokens 71 us, 2048 tokens by 4096 columns 46 us for
+// 4096 codes), and 32 x 128 for up to 32 rows, whose other tiles would be mostly
+// empty (17 tokens 4096 x 4096 12.4 us, 33 tokens in a 128-row tile 15.3).
 int f8_tile(int64_t M, int64_t N) {
   if (M <= 32) return 32;
   return ceil_div(M, 256) * ceil_div(N, 256) >= 256 ? 256 : 128;
@@ -412,7 +423,10 @@ int f8_tile(int64_t M, int64_t N) {
 
 // Split-K: grids below two workgroups per CU (of a 256-CU part; the count
 // depends on the shape only) split K into ranges of at least eight steps, at
-// most 16, with at most 64 MiB of partials.
+// most 16, with at most 64 MiB of partials.  Ranges of four steps (eight): 64
+// tokens 4096 x 4096 17.9 us (16.2); K = 1088 in two ranges (unsplit): 301 tokens
+// 19.5 us (14.5).  One workgroup per CU (two): 301 tokens 4096 x 14336 50.7 us
+// (40.5); four per CU 50.1.
 int fp8_splits(int64_t M, int64_t N, int64_t K) {
   constexpr int64_t kTarget = 512, kMaxSplits = 16, kMaxPartBytes = int64_t(64) << 20;
   if (M <= 0 || N <= 0) return 1;

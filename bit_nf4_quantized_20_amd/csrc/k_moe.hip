@@ -37,7 +37,8 @@ __device__ __forceinline__ float max_group(float v) {
 // e < PER.  k rounds of an arg max over the group: the key of a logit joined
 // with its complemented index, so equal logits go to the lower index.  A
 // chosen logit's key becomes 0 (no logit has key 0: the smallest, -inf, is
-// 0x007fffff).
+// 0x007fffff).  Bound by the rounds' shuffles, not by memory: 16384 x 128, k = 8,
+// 11 us for 9.4 MB; a call from the binding takes 8 us of the host.
 template <int G, int PER>
 __global__ __launch_bounds__(256) void k_moe_route(const float* __restrict__ logits, int64_t T, int E, int k,
                                                    int renorm, int* __restrict__ ids, float* __restrict__ weights) {
@@ -102,7 +103,8 @@ __global__ __launch_bounds__(256) void k_moe_route(const float* __restrict__ log
 
 // Gradient of the logits: with p the softmax over the chosen logits (renorm)
 // or over all, dl_e = p_e (g_e - sum g p), g_e the gradient of e's weight (0
-// where e was not chosen).  Ids outside [0, E) count as no choice.
+// where e was not chosen).  Ids outside [0, E) count as no choice.  16384 x 128:
+// 7.6 us for 17.8 MB.
 template <int G, int PER>
 __global__ __launch_bounds__(256) void k_moe_route_bwd(const float* __restrict__ logits, const int* __restrict__ ids,
                                                        const float* __restrict__ dw, int64_t T, int E, int k,
@@ -653,8 +655,10 @@ hipError_t launch_moe(MoeArgs a, hipStream_t s) {
   const int P = a.T * a.k;
   a.by_expert = a.E <= P ? 1 : 0;
   a.slots = a.by_expert ? a.E : P;
-  // pairs per expert on average: above half a column tile, two of them at a time
-  const bool two = P > 8 * a.E;
+  // Two column tiles of 16 at a time above ten pairs per expert on average (many
+  // experts then have more than 16): 8 experts of 1216 x 6720, nine each 84.7 us
+  // with one, 98.9 with two; fourteen 133 and 111.
+  const bool two = P > 10 * a.E;
   // Column tiles of an expert, shared by several workgroups where there are few
   // (61 tokens x 4 over 4 experts of 576 x 2304: 76.8 -> 62.6 us).
   const int col_tiles = static_cast<int>(ceil_div(P, 32 * a.E));

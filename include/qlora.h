@@ -474,7 +474,9 @@ int qlora_fp8_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t ro
 /*
  * Workspace bytes of the two calls below (0 for invalid shapes, at least 256
  * otherwise).  Host only.  Scratch only: no initialisation, nothing kept
- * between calls; calls that overlap in time must not share one.
+ * between calls; calls that overlap in time must not share one.  The forward
+ * of up to 16 tokens with in <= 8192 needs none, and ws may be NULL, without
+ * an adapter or with r <= 16 and out, in <= 4096.
  */
 size_t qlora_fp8_workspace_bytes(int64_t T, int64_t in_features, int64_t out_features, int64_t r,
                                  int backward);
@@ -490,7 +492,9 @@ size_t qlora_fp8_workspace_bytes(int64_t T, int64_t in_features, int64_t out_fea
  *   and alpha are not read and A, B may be NULL);  alpha finite
  *   ws of ws_bytes >= qlora_fp8_workspace_bytes(T, in, out, r, 0)
  * A row of X that holds an infinity or a NaN gives a row of Y of NaN.
- * T = 0 is a no-op.  Size limits as for qlora_linear_fwd.
+ * T = 0 is a no-op.  Size limits as for qlora_linear_fwd; with r > 0, above 16
+ * tokens or 8192 columns also in, out < 2^23 and 6 rp tp < 2^31, rp being r
+ * rounded up to 64 and tp T rounded up to 8 (both calls).
  * Errors: NULL, SHAPE, ALIGN, VALUE, WORKSPACE, DEVICE, LAUNCH.
  */
 int qlora_fp8_linear_fwd(const qlora_fp8_weight* W, const qlora_bf16* X, int64_t T, const qlora_bf16* A,
@@ -551,16 +555,17 @@ int qlora_moe_route_bwd(const float* logits, const int32_t* ids, const float* dw
                         int64_t k, int renormalize, float* dlogits, qlora_stream stream);
 
 /*
- * qlora_moe_fwd -- the expert layer for a few tokens, in two kernels:
+ * qlora_moe_fwd -- the expert layer for a few tokens, in two or three launches:
  *   Y_t = sum_j weights[t, j] Wd_e (silu(Wg_e x_t) * (Wu_e x_t)),  e = ids[t, j]
  * with silu(g) = g / (1 + exp(-g)).  bf16 inputs, fp32 accumulation, one
  * rounding of Y to bf16; the hidden values are kept as bf16 hi + lo pairs.
- * Each expert that is met is read once, whatever the number of its tokens.
+ * Each expert that is met is dequantized once per 16 or 32 of its tokens.
  *   gate_up  double-quantized NF4 weight [experts * 2 * inter, hidden]: expert
  *            e's rows start at e * 2 * inter, its gate rows before its up rows
  *   down     double-quantized NF4 weight [experts * hidden, inter]
  *   X [T, hidden] bf16;  ids [T, k] int32;  weights [T, k] fp32;
- *   Y [T, hidden] bf16 out;  hidden and inter multiples of 64, below 2^20
+ *   Y [T, hidden] bf16 out;  hidden and inter multiples of 64, below 2^20,
+ *   hidden * inter < 2^31, T * k * max(hidden, inter) < 2^28
  *   0 <= T <= 64 (0 is a no-op), 1 <= k <= 16, T * k <= 512,
  *   1 <= experts <= 1024
  * An id outside [0, experts) is no choice (a padded row, an expert held

@@ -154,6 +154,16 @@ def test_fp8_linear_refusals(lib):
     for bad in ((-1, 256, 128, 8), (1, 100, 128, 8), (1, 256, 100, 8), (1, 256, 128, 257), (1, 256, 128, -1),
                 (1 << 21, 1024, 128, 8)):
         assert lib.qlora_fp8_workspace_bytes(*bad, 0) == 0, bad
+    # with an adapter the rank-r products' 32-bit offsets bound the sizes
+    for ok, bad in (((32, (1 << 23) - 64, 64, 8), (32, 1 << 23, 64, 8)), ((32, 64, (1 << 23) - 64, 8), (32, 64, 1 << 23, 8)),
+                    ((1398096, 64, 64, 256), (1398104, 64, 64, 256)), ((16, 8192, 64, 8), (16, 1 << 23, 64, 8))):
+        for b in (0, 1):
+            assert lib.qlora_fp8_workspace_bytes(*ok, b) > 0, ok
+            assert lib.qlora_fp8_workspace_bytes(*bad, b) == 0, bad
+            assert lib.qlora_fp8_workspace_bytes(*bad[:3], 0, b) > 0, bad
+    big = _F8(F, F, 64, 1 << 23, 0)
+    assert lib.qlora_fp8_linear_fwd(ctypes.byref(big), F, 32, F, F, 8, 1.0, F, F, 1 << 40, None) == SHAPE
+    assert lib.qlora_fp8_linear_bwd(ctypes.byref(big), F, F, 32, F, F, 8, 1.0, F, F, F, F, 1 << 40, None) == SHAPE
     W = _F8(F, F, 128, 256, 0)
 
     def fwd(W=W, X=F, T=32, A=F, B=F, r=8, alpha=16.0, Y=F, w=F, n=ws[0]):
@@ -189,8 +199,11 @@ def test_moe_refusals(lib):
 
     ws = lib.qlora_moe_workspace_bytes(4, 128, 64, 2)
     assert ws >= 4 * 2 * 64 * 4
+    assert lib.qlora_moe_workspace_bytes(64, (1 << 19) - 64, 64, 8) > 0
+    assert lib.qlora_moe_workspace_bytes(1, 1 << 15, (1 << 16) - 64, 1) > 0
     for bad in ((65, 128, 64, 2), (4, 100, 64, 2), (4, 128, 32, 2), (4, 128, 64, 17), (64, 128, 64, 9),
-                (-1, 128, 64, 2), (4, 1 << 20, 64, 2)):
+                (-1, 128, 64, 2), (4, 1 << 20, 64, 2), (64, 1 << 19, 64, 8), (64, 64, 1 << 19, 8),
+                (1, 1 << 15, 1 << 16, 1)):
         assert lib.qlora_moe_workspace_bytes(*bad) == 0, bad
     E, H, I = 8, 128, 64
     gu, dn = _N4(F, F, F, E * 2 * I, H, 0), _N4(F, F, F, E * H, I, 0)

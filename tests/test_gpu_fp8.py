@@ -250,3 +250,69 @@ def test_repeated_streams_and_graphs(T):
             g.replay()
             torch.cuda.synchronize()
             assert all(torch.equal(a, b) for a, b in zip(out, want)), turn
+
+
+def test_binding_refuses_wrong_tensors():
+    q = require_gpu()
+    banner("fp8 binding refusals")
+    W = q.qlora_fp8_quantize_weight(dev_f32(synth.normal_f32(57, (128, 192), synth.W_STD)))
+    A, B = dev_bf16(_bf16(58, (8, 192))), dev_bf16(_bf16(59, (128, 8)))
+    X, dY = dev_bf16(_bf16(60, (40, 192))), dev_bf16(_bf16(61, (40, 128)))
+    ok = q.qlora_fp8_linear_fwd(W, X, A, B, 8, 16.0)
+
+    def refused(error, fn, *args, **kw):
+        with pytest.raises(error):
+            fn(*args, **kw)
+    fwd, bwd = q.qlora_fp8_linear_fwd, q.qlora_fp8_linear_bwd
+    refused(ValueError, fwd, W, dY, A, B, 8, 16.0)                                 # another width
+    refused(ValueError, fwd, W, dev_bf16(_bf16(60, (192, 40))).t(), A, B, 8, 16.0)  # strided
+    refused(ValueError, fwd, W, X.cpu(), A, B, 8, 16.0)                            # another device
+    refused(ValueError, fwd, W, X, A[:4], B, 8, 16.0)                              # another rank
+    refused(TypeError, fwd, W, X.half(), A, B, 8, 16.0)
+    refused(TypeError, fwd, W, X, A, B, 8, 16.0, Y=torch.empty(40, 128, device="cuda"))
+    refused(ValueError, fwd, W, X, A, B, 8, 16.0, Y=torch.empty(39, 128, dtype=torch.bfloat16, device="cuda"))
+    refused(ValueError, bwd, W, X[:39], dY, A, B, 8, 16.0)
+    refused(TypeError, bwd, W, X, dY, A, B, 8, 16.0, dA=torch.empty(8, 192, dtype=torch.bfloat16, device="cuda"))
+    refused(q.QloraError, fwd, W, X, A, B, 8, float("nan"))
+    small = torch.empty(256, dtype=torch.uint8, device="cuda")
+    refused(q.QloraError, fwd, W, X, A, B, 8, 16.0, ws=small)
+    refused(q.QloraError, bwd, W, X, dY, A, B, 8, 16.0, ws=small)
+    refused(ValueError, fwd, W, X, A, B, 8, 16.0, ws=small.cpu())
+    # views are at home as long as they are whole rows, 16-byte aligned
+    big = torch.cat([X, X])
+    assert torch.equal(fwd(W, big[40:], A, B, 8, 16.0), ok)
+    odd = torch.empty(40 * 192 + 1, dtype=torch.bfloat16, device="cuda")[1:].view(40, 192)
+    refused(q.QloraError, fwd, W, odd, A, B, 8, 16.0)
+    assert torch.equal(fwd(W, X, A, B, 8, 16.0), ok)
+
+
+@pytest.mark.parametrize("T", [13, 300])
+def test_gradients_are_the_differences_of_the_forward(T):
+    """dA and dB against central differences of sum(dY * Y) over the kernel's
+    own forward.  Y is linear in A and in B, so the only errors are Y's
+    rounding (at most 2^-8 of each value, independent of one another: their
+    sum's standard deviation is at most that times the norm) over the step, and
+    the gradients' own."""
+    q = require_gpu()
+    banner(f"fp8 differences T={T}")
+    n_in, n_out, r, alpha = 320, 192, 8, 16.0
+    W = q.qlora_fp8_quantize_weight(dev_f32(synth.normal_f32(62, (n_out, n_in), synth.W_STD)))
+    A, B = dev_bf16(_bf16(63, (r, n_in), 0.5)), dev_bf16(_bf16(64, (n_out, r), 0.5))
+    X, dY = dev_bf16(_bf16(65, (T, n_in))), dev_bf16(_bf16(66, (T, n_out)))
+    _, dA, dB = q.qlora_fp8_linear_bwd(W, X, dY, A, B, r, alpha)
+
+    def loss(A, B):
+        Y = q.qlora_fp8_linear_fwd(W, X, A, B, r, alpha)
+        return (Y.double() * dY.double()).sum().item(), (Y.double() * dY.double()).norm().item()
+    step = 0.5  # a power of two: A +- step is exact for |A| in [2^-2, 2)
+    for P, grad, which in ((A, dA, 0), (B, dB, 1)):
+        at = [(i, j) for i, j in ((0, 0), (P.shape[0] - 1, P.shape[1] - 1), (P.shape[0] // 2, 3))]
+        for i, j in at:
+            P0 = P.clone()
+            P0[i, j] = 1.0  # Y is linear in this value, the gradient does not depend on it
+            up, down = P0.clone(), P0.clone()
+            up[i, j], down[i, j] = 1.0 + step, 1.0 - step
+            (lu, nu), (ld, nd) = (loss(up, B), loss(down, B)) if which == 0 else (loss(A, up), loss(A, down))
+            g = q.qlora_fp8_linear_bwd(W, X, dY, *((P0, B) if which == 0 else (A, P0)), r, alpha)[1 + which][i, j].item()
+            bound = 5 * 2.0 ** -8 * (nu + nd) / (2 * step) + 1e-4 * abs(g)
+            assert abs((lu - ld) / (2 * step) - g) <= bound, (which, i, j, (lu - ld) / (2 * step), g, bound)

@@ -211,6 +211,37 @@ def test_experts_rows_stay_their_own():
     assert torch.equal(Y[keep], clean[keep]) and bool(torch.isnan(Y[4]).all())
 
 
+def test_binding_refuses_wrong_tensors():
+    q = require_gpu()
+    banner("moe binding refusals")
+    T, E, k, H, I = 6, 4, 2, 128, 192
+    gu, dn, _, _ = _experts(q, 83, E, H, I)
+    X = dev_bf16(synth.bf16_bits(synth.normal_f32(84, (T, H), 1.0)))
+    l = dev_f32(synth.normal_f32(85, (T, E), 1.0))
+    ids, w = q.qlora_moe_route(l, k)
+    ok = q.qlora_moe_fwd(gu, dn, E, X, ids, w)
+
+    def refused(error, fn, *args, **kw):
+        with pytest.raises(error):
+            fn(*args, **kw)
+    refused(q.QloraError, q.qlora_moe_route, l, 5)                                # k above the experts
+    refused(q.QloraError, q.qlora_moe_route, l, 0)
+    refused(ValueError, q.qlora_moe_route, dev_f32(synth.normal_f32(85, (E, T), 1.0)).t(), k)
+    refused(TypeError, q.qlora_moe_route, l, k, ids=torch.empty(T, k, dtype=torch.int64, device="cuda"))
+    refused(ValueError, q.qlora_moe_route_bwd, l, ids[:3], w)
+    refused(TypeError, q.qlora_moe_route_bwd, l, ids.long(), w)
+    refused(ValueError, q.qlora_moe_fwd, gu, dn, E, X[:, :64].contiguous(), ids, w)
+    refused(ValueError, q.qlora_moe_fwd, gu, dn, E, X, ids[:3], w)
+    refused(TypeError, q.qlora_moe_fwd, gu, dn, E, X, ids.long(), w)
+    refused(q.QloraError, q.qlora_moe_fwd, gu, dn, E + 1, X, ids, w)              # not the weights' experts
+    refused(ValueError, q.qlora_moe_fwd, dn, gu, E, X, ids, w)                    # the weights exchanged
+    refused(ValueError, q.qlora_moe_fwd, gu, dn, E, X, ids, w, ws=torch.empty(1 << 20, dtype=torch.uint8))
+    refused(q.QloraError, q.qlora_moe_fwd, gu, dn, E, X, ids, w, ws=torch.empty(256, dtype=torch.uint8, device="cuda"))
+    many = X.repeat(11, 1)
+    refused(q.QloraError, q.qlora_moe_fwd, gu, dn, E, many, ids.repeat(11, 1), w.repeat(11, 1))  # 66 tokens
+    assert torch.equal(q.qlora_moe_fwd(gu, dn, E, X, ids, w), ok)
+
+
 # ------------------------------------------------------------------ together
 @pytest.mark.parametrize("T", [1, 6, 48])
 def test_a_decode_block_eager_streams_and_graphs(T):
