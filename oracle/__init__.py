@@ -27,6 +27,8 @@ Modules:
     dense     -- fp64 forward/backward of the QLoRA linear
     storage   -- bits/param and storage closed forms
     native    -- ctypes loader for the plain-C brute-force nearest-level search
+    fp8       -- the 8-bit block format (e4m3, power-of-two scales) and its linear layer
+    moe       -- the router with its gradient, and the expert layer
 
 Pins (what each part is checked against) live in tests/test_oracle_*.py.
 Parity unpinned: none of the functions here; the page figures that need
