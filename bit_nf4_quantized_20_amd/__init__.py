@@ -21,6 +21,7 @@ Names and semantics follow include/qlora.h:
 import ctypes
 import functools
 import os
+import threading
 from dataclasses import dataclass
 
 import torch
@@ -615,22 +616,23 @@ def _on(dev, fn, where: str, *args):
         raise QloraError(st, where)
 
 
-_SCRATCH = {}
+_SCRATCH = threading.local()
 
 
 def _scratch(ws, need: int, dev):
-    """The caller's workspace, or one kept per (device, stream): its address
-    and size.  Under graph capture it is a new allocation of the graph's own
-    pool: a replay then shares no scratch with eager calls or with other
-    graphs."""
+    """The caller's workspace, or one kept per host thread, device and stream
+    (the launches of two threads' calls may interleave on one stream).  Under
+    graph capture it is a new allocation of the graph's own pool: a replay then
+    shares no scratch with eager calls or with other graphs."""
     if ws is None:
         if torch.cuda.is_current_stream_capturing():
             ws = make_workspace(need, dev)
         else:
+            kept = _SCRATCH.__dict__
             key = (dev.index, _raw_stream(dev.index))
-            ws = _SCRATCH.get(key)
+            ws = kept.get(key)
             if ws is None or ws.numel() < need:
-                _SCRATCH[key] = ws = make_workspace(need, dev)
+                kept[key] = ws = make_workspace(need, dev)
     elif ws.device != dev:
         raise ValueError(f"ws: on {ws.device}, the call runs on {dev}")
     elif not ws.is_contiguous():

@@ -613,24 +613,39 @@ void route_shape(int E, int k, F&& f) {
 }
 }  // namespace
 
+namespace {
+// rows of one launch: below 2^32 lanes
+constexpr int64_t kRouteRows = int64_t(1) << 25;
+}  // namespace
+
 hipError_t launch_moe_route(const float* logits, int64_t T, int E, int k, bool renorm, int* ids, float* weights,
                             hipStream_t s) {
-  route_shape(E, k, [&](auto gc, auto pc) {
-    constexpr int G = decltype(gc)::value, PER = decltype(pc)::value;
-    hipLaunchKernelGGL((k_moe_route<G, PER>), dim3(static_cast<uint32_t>(ceil_div(T * G, 256))), dim3(256), 0, s,
-                       logits, T, E, k, renorm ? 1 : 0, ids, weights);
-  });
-  return hipGetLastError();
+  for (int64_t t = 0; t < T; t += kRouteRows) {
+    const int64_t n = T - t < kRouteRows ? T - t : kRouteRows;
+    route_shape(E, k, [&](auto gc, auto pc) {
+      constexpr int G = decltype(gc)::value, PER = decltype(pc)::value;
+      hipLaunchKernelGGL((k_moe_route<G, PER>), dim3(static_cast<uint32_t>(ceil_div(n * G, 256))), dim3(256), 0, s,
+                         logits + t * E, n, E, k, renorm ? 1 : 0, ids + t * k, weights + t * k);
+    });
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 hipError_t launch_moe_route_bwd(const float* logits, const int* ids, const float* dw, int64_t T, int E, int k,
                                 bool renorm, float* dlogits, hipStream_t s) {
-  route_shape(E, k, [&](auto gc, auto pc) {
-    constexpr int G = decltype(gc)::value, PER = decltype(pc)::value;
-    hipLaunchKernelGGL((k_moe_route_bwd<G, PER>), dim3(static_cast<uint32_t>(ceil_div(T * G, 256))), dim3(256), 0, s,
-                       logits, ids, dw, T, E, k, renorm ? 1 : 0, dlogits);
-  });
-  return hipGetLastError();
+  for (int64_t t = 0; t < T; t += kRouteRows) {
+    const int64_t n = T - t < kRouteRows ? T - t : kRouteRows;
+    route_shape(E, k, [&](auto gc, auto pc) {
+      constexpr int G = decltype(gc)::value, PER = decltype(pc)::value;
+      hipLaunchKernelGGL((k_moe_route_bwd<G, PER>), dim3(static_cast<uint32_t>(ceil_div(n * G, 256))), dim3(256), 0, s,
+                         logits + t * E, ids + t * k, dw + t * k, n, E, k, renorm ? 1 : 0, dlogits + t * E);
+    });
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 namespace {

@@ -9,6 +9,8 @@ rest is a handful of products).  The expert layer: relative Frobenius <= 2e-3
 1024 terms, 2^-14 each at the very worst; the hidden values as hi + lo pairs,
 2^-17, and the exponential, 2^-20, are below that)."""
 
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -240,6 +242,56 @@ def test_binding_refuses_wrong_tensors():
     many = X.repeat(11, 1)
     refused(q.QloraError, q.qlora_moe_fwd, gu, dn, E, many, ids.repeat(11, 1), w.repeat(11, 1))  # 66 tokens
     assert torch.equal(q.qlora_moe_fwd(gu, dn, E, X, ids, w), ok)
+
+
+def test_two_threads_on_one_stream():
+    """Calls of two host threads whose launches interleave on the same stream."""
+    q = require_gpu()
+    banner("moe and fp8 from two threads")
+    E, k, H, I, r, T = 8, 4, 256, 512, 16, 40
+    gu, dn, _, _ = _experts(q, 86, E, H, I)
+    W = q.qlora_fp8_quantize_weight(dev_f32(synth.normal_f32(87, (H, H), 1.0 / H ** 0.5)))
+    A = dev_bf16(synth.bf16_bits(synth.normal_f32(88, (r, H), 0.05)))
+    B = dev_bf16(synth.bf16_bits(synth.normal_f32(89, (H, r), 0.05)))
+    logits = dev_f32(synth.normal_f32(90, (T, E), 1.0))
+    inputs = [dev_bf16(synth.bf16_bits(synth.normal_f32(91 + i, (T, H), 1.0))) for i in range(2)]
+
+    def work(X):
+        ids, w = q.qlora_moe_route(logits, k)
+        return (*q.qlora_fp8_linear_bwd(W, X, X, A, B, r, 16.0), q.qlora_fp8_linear_fwd(W, X, A, B, r, 16.0),
+                q.qlora_moe_fwd(gu, dn, E, X, ids, w))
+    want = [work(X) for X in inputs]
+    torch.cuda.synchronize()
+    got = [[], []]
+
+    def run(i):
+        for _ in range(50):
+            got[i].append(work(inputs[i]))
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert len(got[i]) == 50
+        assert all(torch.equal(a, b) for out in got[i] for a, b in zip(out, want[i]))
+
+
+def test_route_most_rows():
+    """More rows than one launch takes (2^32 lanes)."""
+    q = require_gpu()
+    banner("route 2^29 rows")
+    T = (1 << 29) + 7
+    if torch.cuda.mem_get_info()[0] < 12 << 30:
+        pytest.skip("needs 12 GiB of GPU memory")
+    l = torch.zeros(T, 1, device="cuda")
+    l[-1] = float("-inf")
+    ids, w = q.qlora_moe_route(l, 1)
+    assert not bool(ids.any()) and bool((w[:-1] == 1).all()) and w[-1].item() == 0
+    l[-1] = 2.0
+    w.fill_(3.0)
+    assert not bool(q.qlora_moe_route_bwd(l, ids, w).any())
 
 
 # ------------------------------------------------------------------ together
