@@ -579,9 +579,11 @@ def _arg(t, dtype, shape, name: str, dev):
     """A contiguous tensor of this type, device and size (shape: its sizes, or
     its element count).  One chain of tests for the call that is right; what
     is wrong is found out afterwards."""
-    if (t.dtype is dtype and t.device == dev and t.is_contiguous() and dev.type == "cuda"
+    if (t is not None and t.dtype is dtype and t.device == dev and t.is_contiguous() and dev.type == "cuda"
             and (t.numel() == shape if type(shape) is int else t.shape == shape)):
         return
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a tensor, got {type(t).__name__}")
     if t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if t.device != dev or dev.type != "cuda":
@@ -593,6 +595,8 @@ def _arg(t, dtype, shape, name: str, dev):
 
 def _matrix(t, name: str):
     """(rows, cols) of a 2-D tensor."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a tensor, got {type(t).__name__}")
     if t.dim() != 2:
         raise ValueError(f"{name}: must be 2-D, got {t.dim()}-D")
     return t.shape

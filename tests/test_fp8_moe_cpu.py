@@ -169,6 +169,7 @@ def test_fp8_linear_refusals(lib):
     def fwd(W=W, X=F, T=32, A=F, B=F, r=8, alpha=16.0, Y=F, w=F, n=ws[0]):
         return lib.qlora_fp8_linear_fwd(ctypes.byref(W), X, T, A, B, r, alpha, Y, w, n, None)
     assert lib.qlora_fp8_linear_fwd(None, F, 32, F, F, 8, 1.0, F, F, ws[0], None) == NULL
+    assert fwd(W=_F8(F, F, 128, 0, 0)) == SHAPE and fwd(W=_F8(F, F, 0, 256, 0)) == SHAPE
     assert fwd(W=_F8(F, F, 128, 100, 0)) == SHAPE and fwd(W=_F8(F, F, 100, 256, 0)) == SHAPE
     assert fwd(W=_F8(F, F, 128, 256, 1)) == VALUE and fwd(W=_F8(None, F, 128, 256, 0)) == NULL
     assert fwd(W=_F8(F, ODD, 128, 256, 0)) == ALIGN
@@ -235,3 +236,9 @@ def test_binding_refuses_what_the_library_cannot_see():
         q.qlora_fp8_linear_fwd(W, torch.zeros(2, 64, dtype=torch.bfloat16), None, None, 0, 0.0)
     with pytest.raises(TypeError):
         q.qlora_fp8_linear_bwd(W, None, torch.zeros(2, 64), None, None, 0, 0.0)
+    with pytest.raises(TypeError, match="X: expected a tensor"):
+        q.qlora_fp8_linear_fwd(W, None, None, None, 0, 0.0)
+    with pytest.raises(TypeError, match="ids: expected a tensor"):
+        q.qlora_moe_route_bwd(torch.zeros(4, 8), None, torch.zeros(4, 2))
+    with pytest.raises(TypeError, match="A: expected a tensor"):
+        q._arg(None, torch.bfloat16, 4, "A", torch.device("cuda", 0))
