@@ -89,7 +89,7 @@ hipError_t launch_lora_down_fin(const float* part, int64_t T, int64_t K, int nP,
 // launch_sum_slices.  (Q rows have stride ldq elements, ldq >= C.)  keep
 // (optional, LoRA dropout, out_jc only): Q[t][c] counts only where bit c % 8 of
 // keep[t * ldk + c / 8] is set; every sum is multiplied by oscale.
-int64_t lora_grad_slices(int64_t T, int64_t C, int64_t ldq, int planes = 2);
+int64_t lora_grad_slices(int64_t T, int64_t C, int64_t ldq);
 hipError_t launch_lora_grad(const uint16_t* Pt, int64_t T, int64_t ldt, int64_t rp, const uint16_t* Q,
                             int64_t C, int64_t ldq, int64_t r, float* part, bool out_jc, hipStream_t s,
                             const uint8_t* keep = nullptr, int64_t ldk = 0, float oscale = 1.f,
@@ -225,7 +225,9 @@ hipError_t launch_lora_fin_two(const float* const* part, const int64_t* K, int64
                                float scale, uint16_t* pad, int64_t ldpad, uint16_t* const* hilo_t, int64_t ldt,
                                hipStream_t s);
 // The token-slice sums of dA (Pt[0], Q[0] [T][C[0]]; out_jc) and dB (Pt[1],
-// Q[1]; not) as launch_lora_grad writes them with three planes.
+// Q[1]; not) as launch_lora_grad writes them, with three planes, in
+// lora_grad_two_slices(T, C[0], C[1], r) slices each.
+int64_t lora_grad_two_slices(int64_t T, int64_t C0, int64_t C1, int64_t r);
 hipError_t launch_lora_grad_two(const uint16_t* const* Pt, int64_t T, int64_t ldt, int64_t rp,
                                 const uint16_t* const* Q, const int64_t* C, int64_t r, float* const* part,
                                 hipStream_t s);

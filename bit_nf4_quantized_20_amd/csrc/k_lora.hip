@@ -606,14 +606,12 @@ __global__ __launch_bounds__(256) void k_lora_grad(const uint16_t* __restrict__ 
 // Token slices (multiples of 64 tokens) for about one workgroup per CU: more
 // slices shorten each workgroup's stream but add partial sums (measured on
 // the 8B-MLP shapes: 256-450 workgroups are fastest, 560 were 35% slower for
-// 14336 columns, 512 were 30% slower for 4096).  Three planes leave LDS for one
-// workgroup per CU, so their grid stays within one round of 256 (4096 tokens,
-// 14336 columns, rank 64: 224 workgroups 40 us, 336 54 us).  The count depends
-// on the shape only.
+// 14336 columns, 512 were 30% slower for 4096).  The count depends on the
+// shape only.
 namespace {
-int64_t grad_slice_tokens(int64_t T, int64_t C, int64_t ldq, int planes) {
+int64_t grad_slice_tokens(int64_t T, int64_t C, int64_t ldq) {
   const int64_t ctiles = ceil_div(C, kGradCT);
-  int64_t slices = planes == 3 ? 256 / ctiles : ceil_div(256, ctiles);
+  int64_t slices = ceil_div(256, ctiles);
   const int64_t max_slices = ceil_div(T, 64);
   if (slices > max_slices) slices = max_slices;
   if (slices < 1) slices = 1;
@@ -624,8 +622,8 @@ int64_t grad_slice_tokens(int64_t T, int64_t C, int64_t ldq, int planes) {
 }
 }  // namespace
 
-int64_t lora_grad_slices(int64_t T, int64_t C, int64_t ldq, int planes) {
-  return T > 0 ? ceil_div(T, grad_slice_tokens(T, C, ldq, planes)) : 0;
+int64_t lora_grad_slices(int64_t T, int64_t C, int64_t ldq) {
+  return T > 0 ? ceil_div(T, grad_slice_tokens(T, C, ldq)) : 0;
 }
 
 hipError_t launch_lora_grad(const uint16_t* Pt, int64_t T, int64_t ldt, int64_t rp, const uint16_t* Q,
@@ -635,7 +633,7 @@ hipError_t launch_lora_grad(const uint16_t* Pt, int64_t T, int64_t ldt, int64_t 
   if (rproj <= 0) rproj = r;
   if (ceil_div(r, rproj) * 2 * rp * ldt * 2 >= (int64_t(1) << 31)) return hipErrorInvalidValue;  // Pt under 2^31 bytes
   if (keep != nullptr && T * ldk >= (int64_t(1) << 31)) return hipErrorInvalidValue;
-  const int64_t TS = grad_slice_tokens(T, C, ldq, 2);
+  const int64_t TS = grad_slice_tokens(T, C, ldq);
   const int64_t slices = ceil_div(T, TS);
   const int64_t ctiles = ceil_div(C, kGradCT);
   const dim3 grid(static_cast<uint32_t>(ctiles), static_cast<uint32_t>(slices));
@@ -1019,6 +1017,39 @@ __global__ __launch_bounds__(256) void k_lora_grad_two(GradJob ja, GradJob jb, u
                                    1.f, (blockIdx.x - first) % cb, (blockIdx.x - first) / cb);
 }
 
+namespace {
+// Tokens of a slice (steps of 64), the same for dA and dB, for the fewest steps
+// of the longest CU: rounds of workgroups (one per CU above 32 ranks, whose
+// three planes leave LDS for no more, else two) times a slice's steps and about
+// four steps' worth of start and stores, and what the slices' sums read again.
+// Rank 64, the whole backward, against up to 256 workgroups for dA and for dB
+// each: 4096 x 4096, 301 tokens 50.9 -> 45.0 us, 4096 tokens 129 -> 122; 4096 ->
+// 14336, 301 tokens 78.6 -> 69.9, 4096 tokens 301 -> 305.  Eight waves by 256
+// columns took 50 us instead of 55 at 4096 x 14336 -> 4096, but twice the slices.
+int64_t grad_two_tokens(int64_t T, int64_t C0, int64_t C1, int64_t r) {
+  const int64_t ct = ceil_div(C0, kGradCT) + ceil_div(C1, kGradCT), most = C0 > C1 ? C0 : C1;
+  const int64_t steps = ceil_div(T, 64), room = r > 32 ? 256 : 512;
+  // 32-bit buffer offsets: a slice of Q stays under 2^30 bytes
+  int64_t best = 1;
+  double least = -1.0;
+  for (int64_t S = ceil_div(T * most * 2, int64_t(1) << 30); S <= 64; ++S) {
+    const int64_t ts = round_up(ceil_div(steps, S), steps > S ? 2 : 1), slices = ceil_div(steps, ts);  // an odd step runs as two
+    const double cost = static_cast<double>(ceil_div(ct * slices, room) * (ts + 4)) +
+                        (slices > 1 ? 1.2e-4 * static_cast<double>(slices * ct * (r < 128 ? r : 128)) : 0.0);
+    if (least < 0.0 || cost < least) {
+      least = cost;
+      best = ts;
+    }
+    if (ts <= 1) break;
+  }
+  return 64 * best;
+}
+}  // namespace
+
+int64_t lora_grad_two_slices(int64_t T, int64_t C0, int64_t C1, int64_t r) {
+  return T > 0 ? ceil_div(T, grad_two_tokens(T, C0, C1, r)) : 0;
+}
+
 hipError_t launch_lora_grad_two(const uint16_t* const* Pt, int64_t T, int64_t ldt, int64_t rp,
                                 const uint16_t* const* Q, const int64_t* C, int64_t r, float* const* part,
                                 hipStream_t s) {
@@ -1026,8 +1057,8 @@ hipError_t launch_lora_grad_two(const uint16_t* const* Pt, int64_t T, int64_t ld
   if (3 * rp * ldt * 2 >= (int64_t(1) << 31)) return hipErrorInvalidValue;  // Pt under 2^31 bytes
   GradJob j[2];
   uint32_t ct[2], wgs[2];
+  const int64_t TS = grad_two_tokens(T, C[0], C[1], r);
   for (int i = 0; i < 2; ++i) {
-    const int64_t TS = grad_slice_tokens(T, C[i], C[i], 3);
     j[i] = GradJob{Pt[i], Q[i], C[i], TS, part[i]};
     ct[i] = static_cast<uint32_t>(ceil_div(C[i], kGradCT));
     wgs[i] = ct[i] * static_cast<uint32_t>(ceil_div(T, TS));

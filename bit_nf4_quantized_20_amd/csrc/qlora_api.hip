@@ -850,8 +850,8 @@ Fp8Layout fp8_layout(int64_t T, int64_t in, int64_t out, int64_t r, bool backwar
       l.vt = c.take(static_cast<size_t>(kFp8Planes * rp * token_pitch(T) * 2));
       l.b_t = c.take(static_cast<size_t>(r * out * 2));
       l.a_t_pad = c.take(static_cast<size_t>(in * rp * 4));
-      l.grad = c.take(static_cast<size_t>((lora_grad_slices(T, in, in, kFp8Planes) * in +
-                                           lora_grad_slices(T, out, out, kFp8Planes) * out) * r * 4));
+      const int64_t slices = lora_grad_two_slices(T, in, out, r);
+      l.grad = c.take(slices > 1 ? static_cast<size_t>(slices * (in + out) * r * 4) : 0);  // one slice: no partials
     } else {
       l.b_pad = c.take(static_cast<size_t>(out * rp * 4));
     }
@@ -1089,29 +1089,18 @@ int qlora_fp8_linear_bwd(const qlora_fp8_weight* W, const qlora_bf16* X, const q
   if (r > 0) {
     // token-slice sums of dA and dB, each added in slice order (one slice is the
     // sum already), with the K splits of dX
-    float* pt = reinterpret_cast<float*>(base + lay.grad);
-    const int64_t C[2] = {in, out};
+    const int64_t C[2] = {in, out}, n[2] = {r * in, out * r};
     float* const dst[2] = {dA, dB};
-    float* part[2];
-    const float* src[2];
-    float* sum[2];
-    int slices[2], jobs = 0;
-    int64_t n[2];
-    for (int i = 0; i < 2; ++i) {
-      const int64_t S = lora_grad_slices(T, C[i], C[i], kFp8Planes);
-      part[i] = dst[i];
-      if (S == 1) continue;
-      src[jobs] = part[i] = pt;
-      slices[jobs] = static_cast<int>(S);
-      n[jobs] = r * C[i];
-      sum[jobs++] = dst[i];
-      pt += S * r * C[i];
-    }
+    const int64_t S = lora_grad_two_slices(T, in, out, r);
+    float* const pa = reinterpret_cast<float*>(base + lay.grad);
+    float* const part[2] = {S > 1 ? pa : dA, S > 1 ? pa + S * n[0] : dB};
+    const float* src[2] = {part[0], part[1]};
+    const int slices[2] = {static_cast<int>(S), static_cast<int>(S)};
     const uint16_t* planes[2] = {vt, ut};
     const uint16_t* Q[2] = {X, dY};
     if (e == hipSuccess) e = launch_lora_grad_two(planes, T, tp, rp, Q, C, r, part, s);
     if (e == hipSuccess)
-      e = launch_grad_sums(src, slices, n, sum, jobs, g.part, fp8_splits(T, in, out), T, in, dX, s);
+      e = launch_grad_sums(src, slices, n, dst, S > 1 ? 2 : 0, g.part, fp8_splits(T, in, out), T, in, dX, s);
   }
   return launched(e);
 }
