@@ -406,6 +406,8 @@ template __global__ void k_fp8_gemm<256, 256, 2, 4, false>(F8Args);
 template __global__ void k_fp8_gemm<256, 256, 2, 4, true>(F8Args);
 template __global__ void k_fp8_gemm<128, 128, 2, 2, false>(F8Args);
 template __global__ void k_fp8_gemm<128, 128, 2, 2, true>(F8Args);
+template __global__ void k_fp8_gemm<64, 128, 2, 2, false>(F8Args);
+template __global__ void k_fp8_gemm<64, 128, 2, 2, true>(F8Args);
 template __global__ void k_fp8_gemm<32, 128, 1, 4, false>(F8Args);
 template __global__ void k_fp8_gemm<32, 128, 1, 4, true>(F8Args);
 
@@ -413,10 +415,13 @@ namespace {
 // Rows of a tile: 256 x 256 tiles where they give every CU one (2048 tokens,
 // 14336 columns: 109 us, 4096 tokens 2.1 PF/s), else 128 x 128, which hold two
 // workgroups per CU (1024 tokens 71 us, 2048 tokens by 4096 columns 46 us for
-// 4096 codes), and 32 x 128 for up to 32 rows, whose other tiles would be mostly
-// empty (17 tokens 4096 x 4096 12.4 us, 33 tokens in a 128-row tile 15.3).
+// 4096 codes).  Below, the grid is filled by splitting K and lower tiles waste
+// fewer rows of matrix instructions and partial sums; 4096 -> 14336, 32 / 64 /
+// 128 rows: 33 tokens 19.6 / 21.0 / 21.8 us, 64 tokens 20.4 / 21.4 / 21.8, 128
+// tokens 24.1 / 23.6 / 26.1, 256 tokens 36.6 / 26.8 / 31.3, 512 tokens - / 52.0 / 36.3.
 int f8_tile(int64_t M, int64_t N) {
-  if (M <= 32) return 32;
+  if (M <= 64) return 32;
+  if (M <= 256) return 64;
   return ceil_div(M, 256) * ceil_div(N, 256) >= 256 ? 256 : 128;
 }
 }  // namespace
@@ -484,6 +489,9 @@ hipError_t launch_fp8_gemm(const F8Gemm& g, hipStream_t s) {
   } else if (bm == 128) {
     if (tr) hipLaunchKernelGGL((k_fp8_gemm<128, 128, 2, 2, true>), grid, dim3(256), 0, s, a);
     else hipLaunchKernelGGL((k_fp8_gemm<128, 128, 2, 2, false>), grid, dim3(256), 0, s, a);
+  } else if (bm == 64) {
+    if (tr) hipLaunchKernelGGL((k_fp8_gemm<64, 128, 2, 2, true>), grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((k_fp8_gemm<64, 128, 2, 2, false>), grid, dim3(256), 0, s, a);
   } else {
     if (tr) hipLaunchKernelGGL((k_fp8_gemm<32, 128, 1, 4, true>), grid, dim3(256), 0, s, a);
     else hipLaunchKernelGGL((k_fp8_gemm<32, 128, 1, 4, false>), grid, dim3(256), 0, s, a);

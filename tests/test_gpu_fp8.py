@@ -174,6 +174,7 @@ def test_linear_matches_oracle(T, n_in, n_out, r, alpha):
     (3, 8192, 64, 16, 32.0), (16, 8256, 192, 0, 0.0), (1, 14336, 128, 16, 32.0), (9, 8256, 64, 100, 50.0),
     (2, 4160, 4224, 256, 16.0), (13, 64, 8192, 100, 20.0), (16, 8192, 8256, 12, 24.0), (65, 2048, 192, 16, 32.0),
     (40, 14336, 64, 130, 65.0), (600, 2048, 4160, 0, 0.0), (1030, 1984, 2112, 100, 50.0), (96, 1920, 320, 256, 16.0),
+    (64, 4096, 320, 16, 32.0), (192, 2048, 576, 8, 16.0), (256, 1024, 4160, 0, 0.0), (257, 1024, 448, 24, 48.0),
 ])
 def test_linear_where_the_kernels_change(T, n_in, n_out, r, alpha):
     """Sizes next to which another kernel, tile or K split takes over."""
