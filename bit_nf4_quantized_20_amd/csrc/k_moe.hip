@@ -147,13 +147,15 @@ __global__ __launch_bounds__(256) void k_moe_route_bwd(const float* __restrict__
   float total = 0.f, dot = 0.f;
 #pragma unroll
   for (int e = 0; e < PER; ++e) {
-    x[e] = top == kNegInf ? 0.f : (sub + G * e < E ? expf(x[e] - top) : 0.f);
+    x[e] = x[e] == kNegInf ? 0.f : expf(x[e] - top);
     total += x[e];
     dot += x[e] * g[e];
   }
   total = sum_group<G>(total);
   dot = sum_group<G>(dot);
-  const float inv = top == kNegInf ? 0.f : 1.0f / total;
+  // a row of nothing but -inf adds up to 0; the largest of NaNs is -inf too
+  // (fmaxf passes them over), but their total is NaN
+  const float inv = total == 0.f ? 0.f : 1.0f / total;
   dot *= inv;
 #pragma unroll
   for (int e = 0; e < PER; ++e)
