@@ -141,6 +141,7 @@ __global__ __launch_bounds__(256) void k_moe_route_bwd(const float* __restrict__
 #pragma unroll
   for (int e = 0; e < PER; ++e) {
     if (renorm && !((chosen >> e) & 1u)) x[e] = kNegInf;
+    if (x[e] == kNegInf) g[e] = 0.f;  // a masked choice: no weight, so no infinity or NaN of its gradient either
     top = fmaxf(top, x[e]);
   }
   top = max_group<G>(top);

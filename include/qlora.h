@@ -544,7 +544,8 @@ int qlora_fp8_linear_bwd(const qlora_fp8_weight* W, const qlora_bf16* X, const q
  * the softmax the weights were taken from (over the chosen, or over all) and
  * g_e the gradient of e's weight (0 where e was not chosen),
  *   dlogits [T, E] fp32 = p_e (g_e - sum_i g_i p_i), overwritten; 0 in a row of
- *   nothing but -inf, NaN where the row's weights are NaN.  ids as
+ *   nothing but -inf, NaN where the row's weights are NaN.  A chosen expert
+ *   whose logit is -inf counts for nothing, whatever its dweights hold.  ids as
  *   qlora_moe_route wrote them (ids outside [0, E) count as no choice).
  * Both read no memory but their arguments' and need no workspace.
  * Errors: NULL, SHAPE, ALIGN, DEVICE, LAUNCH.
