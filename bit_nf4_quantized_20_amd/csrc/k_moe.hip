@@ -438,9 +438,9 @@ __global__ __launch_bounds__(64 * NW, NT == 1 ? (kDepth == 1 ? 4 : 3) : 2) void 
           const float gv = acc[r][t][q];
           hv[q] = gv / (1.0f + __expf(-gv)) * acc[r + kHalf][t][q];
         }
-        const uint32_t h0 = pack_bf16x2(hv[0], hv[1]), h1 = pack_bf16x2(hv[2], hv[3]);
-        const uint32_t l0 = pack_bf16x2(hv[0] - bf16_lo(h0), hv[1] - bf16_hi(h0));
-        const uint32_t l1 = pack_bf16x2(hv[2] - bf16_lo(h1), hv[3] - bf16_hi(h1));
+        uint32_t h0, h1, l0, l1;
+        split_bf16x2(hv[0], hv[1], h0, l0);
+        split_bf16x2(hv[2], hv[3], h1, l1);
         uint16_t* dst = a.h + static_cast<int64_t>(list[c]) * 2 * a.I + 16 * (tile0 + r) + 4 * (lane >> 4);
         *reinterpret_cast<u32x2*>(dst) = u32x2{h0, h1};
         *reinterpret_cast<u32x2*>(dst + a.I) = u32x2{l0, l1};

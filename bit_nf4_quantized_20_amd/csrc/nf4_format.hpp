@@ -166,6 +166,17 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
 __device__ __forceinline__ float bf16_lo(uint32_t p) { return __builtin_bit_cast(float, p << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t p) { return __builtin_bit_cast(float, p & 0xffff0000u); }
 
+// Two fp32 values as bf16 pairs hi + lo (16 bits of fraction).  A finite value
+// that would round past bf16's largest takes that as its hi, so that lo holds
+// the rest; an infinite one has no rest (inf - inf is NaN).
+__device__ __forceinline__ bool is_finite(float v) { return __builtin_fabsf(v) < __builtin_inff(); }
+__device__ __forceinline__ void split_bf16x2(float a, float b, uint32_t& hi, uint32_t& lo) {
+  constexpr float kMost = 0x1.fep127f;
+  const bool fa = is_finite(a), fb = is_finite(b);
+  hi = pack_bf16x2(fa ? __builtin_amdgcn_fmed3f(a, -kMost, kMost) : a, fb ? __builtin_amdgcn_fmed3f(b, -kMost, kMost) : b);
+  lo = pack_bf16x2(fa ? a - bf16_lo(hi) : 0.f, fb ? b - bf16_hi(hi) : 0.f);
+}
+
 // ---------------------------------------------------------------------------
 // Double-quantized absmax: a_hat = fl32(fl32(q / 255) * s).
 // fl32(q / 255) without a division: r0 = fl32(q * c) with c = fl32(1/255),

@@ -559,7 +559,8 @@ int qlora_moe_route_bwd(const float* logits, const int32_t* ids, const float* dw
  * qlora_moe_fwd -- the expert layer for a few tokens, in two or three launches:
  *   Y_t = sum_j weights[t, j] Wd_e (silu(Wg_e x_t) * (Wu_e x_t)),  e = ids[t, j]
  * with silu(g) = g / (1 + exp(-g)).  bf16 inputs, fp32 accumulation, one
- * rounding of Y to bf16; the hidden values are kept as bf16 hi + lo pairs.
+ * rounding of Y to bf16; the hidden values are kept as bf16 hi + lo pairs (an
+ * infinite one stays infinite; one that is finite in fp32 stays finite).
  * Each expert that is met is dequantized once per 16 or 32 of its tokens.
  *   gate_up  double-quantized NF4 weight [experts * 2 * inter, hidden]: expert
  *            e's rows start at e * 2 * inter, its gate rows before its up rows

@@ -8,8 +8,9 @@ import torch
 
 import synth
 from oracle import moe as omoe
+from oracle import nf4 as onf4
 
-from gpu_util import banner, dev_f32, host, require_gpu
+from gpu_util import banner, dev_bf16, dev_f32, host, host_bits, require_gpu
 
 pytestmark = pytest.mark.gpu
 
@@ -75,3 +76,55 @@ def test_route_gradient_of_masked_choices_counts_for_nothing(E, bad, renorm):
     assert not dl[1].any()
     assert np.array_equal(dl, _grad(q, l, ids, clean, renorm))
     assert np.abs(dl - omoe.route_bwd(l, ids, clean, renorm)).max() <= FP32 * 2 * np.abs(clean).max()
+
+
+@pytest.mark.parametrize("T,E,k,H,I", [
+    (4, 2, 1, 64, 64),        # the down product in one launch
+    (40, 2, 2, 64, 128),      # in two, two column tiles at a time
+    (5, 60, 4, 256, 1024),    # one
+    (64, 60, 8, 128, 512),    # more than 64 pairs
+])
+def test_experts_hidden_values_past_bf16(T, E, k, H, I):
+    """Hidden values are kept as bf16 pairs hi + lo.  One between bf16's largest
+    and fp32's has to stay the finite number it is, an infinite one infinite
+    with its sign: the lo of an infinite hi must not be inf - inf.
+
+    All weights of the gate and up products are c = 181/128 (its block's
+    absmax and its group's: exact in the 4-bit format), all of the down
+    product 2^-10.  x has one value, 181/128 2^63: g = u = 1.99957 2^63, exact, h
+    = 1.99915 2^127, above bf16's largest (1.99219 2^127) by more than the half
+    step that still rounds to it; silu(g) = g, since exp(-g) is 0."""
+    q = require_gpu()
+    banner(f"moe hidden values past bf16 T={T} E={E} k={k} H={H} I={I}")
+    c, d = 181 / 128, 2.0 ** -10
+    gu = q.nf4_quantize_weight(torch.full((E * 2 * I, H), c, device="cuda"))
+    dn = q.nf4_quantize_weight(torch.full((E * H, I), d, device="cuda"))
+    x = np.zeros((T, H), dtype=np.float64)
+    x[0, H // 2] = c * 2.0 ** 63                 # h in (bf16's largest, fp32's largest)
+    x[1, 3] = 2.0 ** 100                         # h infinite
+    x[2:] = synth.normal_f32(205, (T - 2, H), 1.0)
+    x[3] = 0.0
+    bits = synth.bf16_bits(x.astype(np.float32))
+    x = onf4.bf16_bits_to_f32(bits).astype(np.float64)
+    ids = np.tile(np.arange(k, dtype=np.int32), (T, 1))
+    w = np.abs(synth.normal_f32(206, (T, k), 0.25)) + 0.125
+    w /= 16 * k                                  # Y of row 0 stays finite
+    sign = np.ones(T, np.float32)
+    sign[1] = -1.0
+    w = (w * sign[:, None]).astype(np.float32)
+    Y = onf4.bf16_bits_to_f32(host_bits(q.qlora_moe_fwd(gu, dn, E, dev_bf16(bits), torch.from_numpy(ids).cuda(),
+                                                        dev_f32(w)))).astype(np.float64)
+    g = c * x.sum(1)                             # the same in every gate, up and down row
+    with np.errstate(over="ignore"):
+        h = g / (1 + np.exp(-g)) * g
+    assert (2 - 2.0 ** -8) * 2.0 ** 127 < h[0] < np.finfo(np.float32).max < h[1]
+    ref = w.astype(np.float64).sum(1) * I * d * h
+    assert np.isneginf(Y[1]).all()
+    fine = np.arange(T) != 1
+    # row 0 and the others: the final rounding, 2^-8, and 2^-13 of the terms' magnitudes
+    # as for any row; x of the others adds up H terms of both signs in fp32, at most
+    # H 2^-24 of their magnitudes, twice, in g and u
+    mag = np.abs(w).sum(1) * I * d * np.abs(h)
+    drift = np.abs(w).sum(1) * I * d * 4 * np.abs(g) * c * np.abs(x).sum(1) * H * 2.0 ** -24
+    bound = 2.0 ** -8 * np.abs(ref) + 2.0 ** -13 * mag + drift + 1e-37
+    assert (np.abs(Y - ref[:, None]) <= bound[:, None])[fine].all()
