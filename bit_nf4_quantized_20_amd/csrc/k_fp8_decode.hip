@@ -217,10 +217,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void k_fp8_decode(DecodeF8 p) {
   }
   uint32_t uh[4], ul[4];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    uh[e] = pack_bf16x2(u8[2 * e], u8[2 * e + 1]);
-    ul[e] = pack_bf16x2(u8[2 * e] - bf16_lo(uh[e]), u8[2 * e + 1] - bf16_hi(uh[e]));
-  }
+  for (int e = 0; e < 4; ++e) split_bf16x2(u8[2 * e], u8[2 * e + 1], uh[e], ul[e]);
   const bf16x8 fuh = frag(u32x4{uh[0], uh[1], uh[2], uh[3]}), ful = frag(u32x4{ul[0], ul[1], ul[2], ul[3]});
   const bool adapter = 32 * wv < r;  // (uniform)
   auto load_b = [&](int t) {         // row n of tile t, ranks 8 g .. + 7 of the wave's; zero past the last rank

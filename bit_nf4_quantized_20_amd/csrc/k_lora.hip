@@ -275,9 +275,8 @@ __device__ __forceinline__ void down_fin_tile(FinStage<NP>& stage, const float* 
 #pragma unroll
     for (int q = 0; q < kDownMaxKC; ++q) v += ok && live_rank && q < KC ? pv[i][q] : 0.f;
     v *= scale;
-    const uint32_t hb = pack_bf16x2(v, 0.f) & 0xffffu;
-    const float hi = __builtin_bit_cast(float, hb << 16);
-    const uint32_t lb = pack_bf16x2(v - hi, 0.f) & 0xffffu;
+    uint32_t hb, lb;  // (upper halves 0)
+    split_bf16x2(v, 0.f, hb, lb);
     if (ok && pad != nullptr) {
       uint16_t* row = pad + t * ldpad + pj * 2 * rp + jj + jl;
       row[0] = static_cast<uint16_t>(hb);
@@ -285,7 +284,7 @@ __device__ __forceinline__ void down_fin_tile(FinStage<NP>& stage, const float* 
     }
     s_t[jl][tl] = hb | (lb << 16);  // tokens >= T hold zero
     if constexpr (NP == 3)
-      s_t3[jl][tl] = static_cast<uint16_t>(pack_bf16x2(v - hi - __builtin_bit_cast(float, lb << 16), 0.f) & 0xffffu);
+      s_t3[jl][tl] = static_cast<uint16_t>(pack_bf16x2(is_finite(v) ? v - bf16_lo(hb) - bf16_lo(lb) : 0.f, 0.f));
   }
   if (hilo_t == nullptr) return;
   __syncthreads();
