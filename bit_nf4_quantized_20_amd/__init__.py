@@ -582,6 +582,24 @@ def _arg(t, dtype, shape, name: str, dev):
     if (t is not None and t.dtype is dtype and t.device == dev and t.is_contiguous() and dev.type == "cuda"
             and (t.numel() == shape if type(shape) is int else t.shape == shape)):
         return
+    _arg_rest(t, dtype, name, dev)
+    raise ValueError(f"{name}: expected {shape} elements, got {tuple(t.shape)}")
+
+
+def _rows_arg(t, dtype, rows: int, cols: int, name: str, dev):
+    """As _arg for a row-major matrix: [rows, cols], the same rows under more
+    axes, or flat.  A transposed one has the right number of elements and would
+    be read or written in the wrong order."""
+    if (t is not None and t.dtype is dtype and t.device == dev and t.is_contiguous() and dev.type == "cuda"
+            and (t.shape == (rows, cols)
+                 or t.numel() == rows * cols and t.dim() > 0 and (t.dim() == 1 or t.shape[-1] == cols))):
+        return
+    _arg_rest(t, dtype, name, dev)
+    raise ValueError(f"{name}: expected ({rows}, {cols}), got {tuple(t.shape)}")
+
+
+def _arg_rest(t, dtype, name: str, dev):
+    """Raises for what is wrong besides the size."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a tensor, got {type(t).__name__}")
     if t.dtype != dtype:
@@ -590,7 +608,6 @@ def _arg(t, dtype, shape, name: str, dev):
         raise ValueError(f"{name}: on {t.device}, the call runs on {dev} (a GPU is needed)")
     if not t.is_contiguous():
         raise ValueError(f"{name}: must be contiguous")
-    raise ValueError(f"{name}: expected {shape} elements, got {tuple(t.shape)}")
 
 
 def _matrix(t, name: str):
@@ -662,11 +679,11 @@ def qlora_fp8_quantize(w: torch.Tensor, codes=None, scales=None):
     if codes is None:
         codes = torch.empty(rows, cols, dtype=torch.uint8, device=dev)
     else:
-        _arg(codes, torch.uint8, rows * cols, "codes", dev)
+        _rows_arg(codes, torch.uint8, rows, cols, "codes", dev)
     if scales is None:
         scales = torch.empty(grid, dtype=torch.uint8, device=dev)
     else:
-        _arg(scales, torch.uint8, grid[0] * grid[1], "scales", dev)
+        _rows_arg(scales, torch.uint8, *grid, "scales", dev)
     _on(dev, _lib.qlora_fp8_quantize, "qlora_fp8_quantize", w.data_ptr(), rows, cols, codes.data_ptr(),
         scales.data_ptr())
     return codes, scales
@@ -681,13 +698,13 @@ def qlora_fp8_quantize_weight(w: torch.Tensor) -> FP8Weight:
 def qlora_fp8_dequantize(codes, scales, rows: int, cols: int, out=None):
     """-> bf16 device tensor [rows, cols]."""
     dev = codes.device
-    _, sb = qlora_fp8_storage_bytes(rows, cols)
-    _arg(codes, torch.uint8, rows * cols, "codes", dev)
-    _arg(scales, torch.uint8, sb, "scales", dev)
+    qlora_fp8_storage_bytes(rows, cols)  # refuses other sizes
+    _rows_arg(codes, torch.uint8, rows, cols, "codes", dev)
+    _rows_arg(scales, torch.uint8, -(-rows // 128), -(-cols // 128), "scales", dev)
     if out is None:
         out = torch.empty(rows, cols, dtype=torch.bfloat16, device=dev)
     else:
-        _arg(out, torch.bfloat16, rows * cols, "out", dev)
+        _rows_arg(out, torch.bfloat16, rows, cols, "out", dev)
     _on(dev, _lib.qlora_fp8_dequantize, "qlora_fp8_dequantize", codes.data_ptr(), scales.data_ptr(), rows, cols,
         out.data_ptr())
     return out
@@ -698,13 +715,12 @@ def qlora_fp8_workspace_bytes(T: int, in_features: int, out_features: int, r: in
     return int(_lib.qlora_fp8_workspace_bytes(T, in_features, out_features, r, 1 if backward else 0))
 
 
-def _fp8_args(W, X, A, B, r, dev, T):
-    blocks = -(-W.rows // 128) * -(-W.cols // 128)
-    _arg(W.codes, torch.uint8, W.rows * W.cols, "W.codes", dev)
-    _arg(W.scales, torch.uint8, blocks, "W.scales", dev)
+def _fp8_args(W, A, B, r, dev):
+    _rows_arg(W.codes, torch.uint8, W.rows, W.cols, "W.codes", dev)
+    _rows_arg(W.scales, torch.uint8, -(-W.rows // 128), -(-W.cols // 128), "W.scales", dev)
     if r > 0:
-        _arg(A, torch.bfloat16, r * W.cols, "A", dev)
-        _arg(B, torch.bfloat16, W.rows * r, "B", dev)
+        _rows_arg(A, torch.bfloat16, r, W.cols, "A", dev)
+        _rows_arg(B, torch.bfloat16, W.rows, r, "B", dev)
 
 
 def qlora_fp8_linear_fwd(W: FP8Weight, X, A, B, r: int, alpha: float, Y=None, ws=None):
@@ -713,11 +729,11 @@ def qlora_fp8_linear_fwd(W: FP8Weight, X, A, B, r: int, alpha: float, Y=None, ws
     T, _ = _matrix(X, "X")
     dev = X.device
     _arg(X, torch.bfloat16, (T, W.cols), "X", dev)
-    _fp8_args(W, X, A, B, r, dev, T)
+    _fp8_args(W, A, B, r, dev)
     if Y is None:
         Y = torch.empty(T, W.rows, dtype=torch.bfloat16, device=dev)
     else:
-        _arg(Y, torch.bfloat16, T * W.rows, "Y", dev)
+        _rows_arg(Y, torch.bfloat16, T, W.rows, "Y", dev)
     ws = _scratch(ws, qlora_fp8_workspace_bytes(T, W.cols, W.rows, r, False), dev)
     _on(dev, _lib.qlora_fp8_linear_fwd, "qlora_fp8_linear_fwd", ctypes.byref(W._c()), X.data_ptr(), T,
         A.data_ptr() if r > 0 else None, B.data_ptr() if r > 0 else None, r, float(alpha), Y.data_ptr(),
@@ -733,20 +749,20 @@ def qlora_fp8_linear_bwd(W: FP8Weight, X, dY, A, B, r: int, alpha: float, dX=Non
     _arg(dY, torch.bfloat16, (T, W.rows), "dY", dev)
     if r > 0:
         _arg(X, torch.bfloat16, (T, W.cols), "X", dev)
-    _fp8_args(W, X, A, B, r, dev, T)
+    _fp8_args(W, A, B, r, dev)
     if dX is None:
         dX = torch.empty(T, W.cols, dtype=torch.bfloat16, device=dev)
     else:
-        _arg(dX, torch.bfloat16, T * W.cols, "dX", dev)
+        _rows_arg(dX, torch.bfloat16, T, W.cols, "dX", dev)
     if r > 0:
         if dA is None:
             dA = torch.empty(r, W.cols, dtype=torch.float32, device=dev)
         else:
-            _arg(dA, torch.float32, r * W.cols, "dA", dev)
+            _rows_arg(dA, torch.float32, r, W.cols, "dA", dev)
         if dB is None:
             dB = torch.empty(W.rows, r, dtype=torch.float32, device=dev)
         else:
-            _arg(dB, torch.float32, W.rows * r, "dB", dev)
+            _rows_arg(dB, torch.float32, W.rows, r, "dB", dev)
     else:
         X = A = B = dA = dB = None
     ws = _scratch(ws, qlora_fp8_workspace_bytes(T, W.cols, W.rows, r, True), dev)
@@ -767,11 +783,11 @@ def qlora_moe_route(logits, k: int, renormalize: bool = True, ids=None, weights=
     if ids is None:
         ids = torch.empty(T, max(k, 0), dtype=torch.int32, device=dev)
     else:
-        _arg(ids, torch.int32, T * k, "ids", dev)
+        _rows_arg(ids, torch.int32, T, k, "ids", dev)
     if weights is None:
         weights = torch.empty(T, max(k, 0), dtype=torch.float32, device=dev)
     else:
-        _arg(weights, torch.float32, T * k, "weights", dev)
+        _rows_arg(weights, torch.float32, T, k, "weights", dev)
     _on(dev, _lib.qlora_moe_route, "qlora_moe_route", logits.data_ptr(), T, E, k, 1 if renormalize else 0,
         ids.data_ptr(), weights.data_ptr())
     return ids, weights
@@ -788,7 +804,7 @@ def qlora_moe_route_bwd(logits, ids, dweights, renormalize: bool = True, dlogits
     if dlogits is None:
         dlogits = torch.empty(T, E, dtype=torch.float32, device=dev)
     else:
-        _arg(dlogits, torch.float32, T * E, "dlogits", dev)
+        _rows_arg(dlogits, torch.float32, T, E, "dlogits", dev)
     _on(dev, _lib.qlora_moe_route_bwd, "qlora_moe_route_bwd", logits.data_ptr(), ids.data_ptr(),
         dweights.data_ptr(), T, E, k, 1 if renormalize else 0, dlogits.data_ptr())
     return dlogits
@@ -824,7 +840,7 @@ def qlora_moe_fwd(gate_up: NF4Weight, down: NF4Weight, experts: int, X, ids, wei
     if Y is None:
         Y = torch.empty(T, hidden, dtype=torch.bfloat16, device=dev)
     else:
-        _arg(Y, torch.bfloat16, T * hidden, "Y", dev)
+        _rows_arg(Y, torch.bfloat16, T, hidden, "Y", dev)
     ws = _scratch(ws, qlora_moe_workspace_bytes(T, hidden, inter, k), dev)
     _on(dev, _lib.qlora_moe_fwd, "qlora_moe_fwd", ctypes.byref(gate_up._c()), ctypes.byref(down._c()), experts,
         X.data_ptr(), T, ids.data_ptr(), weights.data_ptr(), k, Y.data_ptr(), ws.data_ptr(),

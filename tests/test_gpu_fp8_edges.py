@@ -88,3 +88,30 @@ def test_adapter_products_past_bf16(T, n_in, n_out, r):
     dX, dA, _ = q.qlora_fp8_linear_bwd(W, X, dY, A, B, r, float(r))
     assert np.isposinf(_wide(dX)[1]).all() and not _wide(dX)[2:].any()
     assert np.isneginf(host(dA)[0]).all() and not host(dA)[1:].any()
+
+
+def test_transposed_tensors_are_refused():
+    """Contiguous tensors of the right element count in the other order; other
+    views of the same rows stay at home."""
+    q = require_gpu()
+    banner("fp8 transposed tensors")
+    T, n_in, n_out, r = 40, 192, 128, 8
+    W = q.qlora_fp8_quantize_weight(dev_f32(synth.normal_f32(301, (n_out, n_in), synth.W_STD)))
+    X, dY = dev_bf16(_bf16(302, (T, n_in))), dev_bf16(_bf16(303, (T, n_out)))
+    A, B = dev_bf16(_bf16(304, (r, n_in))), dev_bf16(_bf16(305, (n_out, r)))
+    Y = q.qlora_fp8_linear_fwd(W, X, A, B, r, 16.0)
+    grads = q.qlora_fp8_linear_bwd(W, X, dY, A, B, r, 16.0)
+    At, Bt = A.t().contiguous(), B.t().contiguous()
+    turned = q.FP8Weight(W.codes.t().contiguous(), W.scales, n_out, n_in)
+    for a, b, w in ((At, B, W), (A, Bt, W), (At, Bt, W), (A, B, turned)):
+        with pytest.raises(ValueError):
+            q.qlora_fp8_linear_fwd(w, X, a, b, r, 16.0)
+        with pytest.raises(ValueError):
+            q.qlora_fp8_linear_bwd(w, X, dY, a, b, r, 16.0)
+    with pytest.raises(ValueError):
+        q.qlora_fp8_linear_fwd(W, X, A, B, r, 16.0, Y=torch.empty(n_out, T, dtype=torch.bfloat16, device="cuda"))
+    flat = q.FP8Weight(W.codes.view(-1), W.scales.view(-1), n_out, n_in)
+    deep = torch.empty(5, 8, n_out, dtype=torch.bfloat16, device="cuda")
+    assert q.qlora_fp8_linear_fwd(flat, X, A[None], B.view(-1), r, 16.0, Y=deep) is deep
+    assert torch.equal(deep.view(T, n_out), Y)
+    assert all(torch.equal(a, b) for a, b in zip(q.qlora_fp8_linear_bwd(flat, X, dY, A[None], B.view(-1), r, 16.0), grads))
