@@ -640,13 +640,22 @@ def _on(dev, fn, where: str, *args):
 _SCRATCH = threading.local()
 
 
+def _capturing(dev) -> bool:
+    """Whether dev's current stream is being captured (torch asks about the
+    current GPU's)."""
+    if torch.cuda.current_device() == dev.index:
+        return torch.cuda.is_current_stream_capturing()
+    with torch.cuda.device(dev):
+        return torch.cuda.is_current_stream_capturing()
+
+
 def _scratch(ws, need: int, dev):
     """The caller's workspace, or one kept per host thread, device and stream
     (the launches of two threads' calls may interleave on one stream).  Under
     graph capture it is a new allocation of the graph's own pool: a replay then
     shares no scratch with eager calls or with other graphs."""
     if ws is None:
-        if torch.cuda.is_current_stream_capturing():
+        if _capturing(dev):
             ws = make_workspace(need, dev)
         else:
             kept = _SCRATCH.__dict__

@@ -106,3 +106,51 @@ def test_transposed_tensors_are_refused_elsewhere(q):
                      lambda: q.qlora_moe_route_bwd(l, ids, wt, dlogits=l)):
             with pytest.raises(_Accepted):
                 call()
+
+
+# ------------------------------------------------------------------ workspaces
+class _Gpus:
+    """torch.cuda as far as the workspaces ask it: which GPU is current and
+    whether each one's current stream is being captured."""
+
+    def __init__(self, monkeypatch, q, current, capturing):
+        self.current, self.capturing = current, capturing
+        gpus = self
+
+        class Guard:
+            def __init__(self, dev):
+                self.to = dev if isinstance(dev, int) else dev.index
+
+            def __enter__(self):
+                self.back, gpus.current = gpus.current, self.to
+
+            def __exit__(self, *_):
+                gpus.current = self.back
+        monkeypatch.setattr(torch.cuda, "current_device", lambda: gpus.current)
+        monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: gpus.capturing[gpus.current])
+        monkeypatch.setattr(torch.cuda, "device", Guard)
+        monkeypatch.setattr(q, "_raw_stream", lambda index: 100 + index)
+        self.made = []
+
+        def make(nbytes, dev):
+            self.made.append((nbytes, dev.index))
+            return torch.empty(nbytes, dtype=torch.uint8)
+        monkeypatch.setattr(q, "make_workspace", make)
+        monkeypatch.setattr(q, "_SCRATCH", type(q._SCRATCH)())
+
+
+@pytest.mark.parametrize("current", [0, 1])
+def test_capture_is_asked_of_the_tensors_gpu(monkeypatch, current):
+    """A capture on the GPU of the call's tensors gets workspaces of its own,
+    whichever GPU is current when the call is made, and one on the current GPU
+    does not concern a call on another."""
+    q = pytest.importorskip("bit_nf4_quantized_20_amd")
+    dev = torch.device("cuda", 0)
+    gpus = _Gpus(monkeypatch, q, current, {0: True, 1: False})
+    captured = [q._scratch(None, 512, dev) for _ in range(2)]
+    assert captured[0].data_ptr() != captured[1].data_ptr() and gpus.current == current
+    gpus.capturing = {0: False, 1: True}
+    kept = [q._scratch(None, 512, dev) for _ in range(2)]
+    assert kept[0] is kept[1] and all(kept[0] is not c for c in captured)
+    gpus.capturing = {0: True, 1: True}
+    assert q._scratch(None, 512, dev) is not kept[0]
