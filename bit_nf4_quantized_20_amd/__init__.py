@@ -649,13 +649,19 @@ def _capturing(dev) -> bool:
         return torch.cuda.is_current_stream_capturing()
 
 
+# the most bytes of a workspace that is kept: a larger one comes from torch's
+# allocator and goes back to it (1.3 us, where such a call's kernels take 20 and
+# more)
+_KEEP_MOST = 32 << 20
+
+
 def _scratch(ws, need: int, dev):
     """The caller's workspace, or one kept per host thread, device and stream
     (the launches of two threads' calls may interleave on one stream).  Under
     graph capture it is a new allocation of the graph's own pool: a replay then
     shares no scratch with eager calls or with other graphs."""
     if ws is None:
-        if _capturing(dev):
+        if need > _KEEP_MOST or _capturing(dev):
             ws = make_workspace(need, dev)
         else:
             kept = _SCRATCH.__dict__

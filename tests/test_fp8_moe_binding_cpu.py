@@ -154,3 +154,21 @@ def test_capture_is_asked_of_the_tensors_gpu(monkeypatch, current):
     assert kept[0] is kept[1] and all(kept[0] is not c for c in captured)
     gpus.capturing = {0: True, 1: True}
     assert q._scratch(None, 512, dev) is not kept[0]
+
+
+def test_large_workspaces_are_given_back(monkeypatch):
+    """Only workspaces up to a limit are kept between calls: one large call does
+    not hold its memory from then on."""
+    q = pytest.importorskip("bit_nf4_quantized_20_amd")
+    dev = torch.device("cuda", 0)
+    gpus = _Gpus(monkeypatch, q, 0, {0: False})
+    most = q._KEEP_MOST
+    small = q._scratch(None, 512, dev)
+    large = q._scratch(None, most + 1, dev)
+    assert large.numel() >= most + 1
+    assert q._scratch(None, 512, dev) is small           # the large one did not take its place
+    full = q._scratch(None, most, dev)
+    assert q._scratch(None, 512, dev) is full
+    assert q._scratch(None, most + 1, dev) is not large
+    assert max(t.numel() for t in q._SCRATCH.__dict__.values()) == most
+    assert gpus.made == [(512, 0), (most + 1, 0), (most, 0), (most + 1, 0)]
