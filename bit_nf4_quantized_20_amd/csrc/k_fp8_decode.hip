@@ -148,8 +148,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void k_fp8_decode(DecodeF8 p) {
       v.x[q] = load16(rx, ((xrow & ~kPastEnd) + at) | off | (xrow & kPastEnd));
     }
   };
-  // blocks of activations in flight: four while few codes are held, then two
-  constexpr int kRing = 4;
+  constexpr int kRing = 4;  // blocks of activations in flight
   Acts xa[kRing];
 #pragma unroll
   for (int i = 0; i < kRing; ++i) load_x(xa[i], i);
@@ -191,8 +190,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void k_fp8_decode(DecodeF8 p) {
     // are free before the next load takes them
     __asm__ volatile("" : "+v"(fx[i]), "+v"(sx[i / 4]));
     __builtin_amdgcn_sched_barrier(0);
-    if (i < 8 && i + 4 < NBW) load_x(xa[i % kRing], i + 4);
-    if (i >= 10 && i + 2 < NBW) load_x(xa[(i + 2) % kRing], i + 2);
+    if (i + kRing < NBW) load_x(xa[i % kRing], i + kRing);
     __builtin_amdgcn_sched_barrier(0);
   }
   // s U of this wave's 32 ranks: lane (token n, g) ranks 8 g .. + 7, hi and lo

@@ -244,8 +244,7 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_fp8_gemm(F8Args p) {
     DtlTile<BM, NW> ta;
     std::conditional_t<kTr, F8TileT<BN, NW>, F8Tile<BN, NW>> tw;
     ta.init(reinterpret_cast<const uint16_t*>(p.xq), p.ldx / 2, m0, p.M, wv, lane);
-    if constexpr (kTr) tw.init(p.w, p.ldw, n0, p.wrows, wv, lane);
-    else tw.init(p.w, p.ldw, n0, p.wrows, wv, lane);
+    tw.init(p.w, p.ldw, n0, p.wrows, wv, lane);
     auto copy_act = [&](int64_t e, uint16_t* sa) {  // steps past the end re-read the last one
       ta.load(sa, wv, (e < last ? e : last - 1) * (kStep / 2));
     };
