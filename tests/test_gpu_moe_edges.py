@@ -10,6 +10,7 @@ import synth
 from oracle import moe as omoe
 from oracle import nf4 as onf4
 
+import test_gpu_moe
 from gpu_util import banner, dev_bf16, dev_f32, host, host_bits, require_gpu
 
 pytestmark = pytest.mark.gpu
@@ -128,3 +129,52 @@ def test_experts_hidden_values_past_bf16(T, E, k, H, I):
     drift = np.abs(w).sum(1) * I * d * 4 * np.abs(g) * c * np.abs(x).sum(1) * H * 2.0 ** -24
     bound = 2.0 ** -8 * np.abs(ref) + 2.0 ** -13 * mag + drift + 1e-37
     assert (np.abs(Y - ref[:, None]) <= bound[:, None])[fine].all()
+
+
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("E", [8, 60, 300])
+def test_route_gradient_of_zeros_is_zero(E, renorm):
+    q = require_gpu()
+    banner(f"route gradient of zeros E={E} renorm={renorm}")
+    l = synth.normal_f32(207, (9, E), 3.0)
+    l[4] = -np.inf
+    l[5, 2:] = -np.inf
+    ids, _ = q.qlora_moe_route(dev_f32(l), 4, renormalize=renorm)
+    assert not _grad(q, l, host(ids), np.zeros((9, 4), np.float32), renorm).any()
+
+
+@pytest.mark.parametrize("T,E,k,H,I", [
+    (5, 8, 2, 256, 320),      # at most 64 pairs, the down product in one launch
+    (9, 8, 4, 448, 1024),     # in two launches
+    (40, 60, 4, 320, 192),    # more than 64 pairs
+    (64, 4, 8, 256, 320),     # two column tiles at a time, more of them than one
+    (61, 4, 4, 576, 256),     # column tiles shared by several workgroups
+])
+def test_experts_workspace_contents(T, E, k, H, I):
+    """The pairs that are no choice leave their part of the workspace unwritten:
+    whatever it holds, the result is the same bit for bit, and a row of nothing
+    but such pairs is 0."""
+    q = require_gpu()
+    banner(f"moe workspace contents T={T} E={E} k={k} H={H} I={I}")
+    gu = q.nf4_quantize_weight(dev_f32(synth.normal_f32(208, (E * 2 * I, H), H ** -0.5)))
+    dn = q.nf4_quantize_weight(dev_f32(synth.normal_f32(209, (E * H, I), I ** -0.5)))
+    rng = np.random.Generator(np.random.PCG64(T * E))
+    ids = rng.integers(0, E, (T, k)).astype(np.int32)
+    ids[rng.random((T, k)) < 0.3] = -1
+    ids[0] = [E, -1, -7, 1 << 30][:k] + [-1] * (k - 4)
+    ids[T - 1] = -1
+    ids, X = torch.from_numpy(ids).cuda(), dev_bf16(synth.bf16_bits(synth.normal_f32(210, (T, H), 1.0)))
+    w = dev_f32(synth.normal_f32(211, (T, k), 1.0))
+    need = q.qlora_moe_workspace_bytes(T, H, I, k)
+    Y = q.qlora_moe_fwd(gu, dn, E, X, ids, w)
+    assert bool(torch.isfinite(Y).all()) and not Y[[0, T - 1]].any() and bool(Y[1:T - 1].any())
+    for fill in (0x00, 0x7f, 0xff):
+        ws = torch.full((need,), fill, dtype=torch.uint8, device="cuda")
+        assert torch.equal(q.qlora_moe_fwd(gu, dn, E, X, ids, w, ws=ws), Y), fill
+
+
+@pytest.mark.parametrize("T,E,k,H,I", [(64, 600, 8, 128, 128), (20, 1024, 16, 128, 256), (13, 80, 6, 128, 128)])
+def test_more_experts_than_pairs(T, E, k, H, I):
+    """More than 64 pairs over even more experts: a workgroup's slot is a pair,
+    and only an expert's first pair works."""
+    test_gpu_moe.test_experts_where_the_kernels_change(T, E, k, H, I)
