@@ -296,3 +296,70 @@ def test_workspace_contents_streams_and_graphs(T, n_in, n_out, r):
             g.replay()
             torch.cuda.synchronize()
             assert same(out, want), turn
+
+
+# ------------------------------------------------------------------ the largest sides
+WIDEST = (1 << 24) - 64  # the other side 64: the expanded weight stays below 2^31 bytes
+
+
+def _one_hot(T, n, at):
+    x = torch.zeros(T, n, dtype=torch.bfloat16, device="cuda")
+    x[torch.arange(T, device="cuda"), at] = 1.0
+    return x
+
+
+@pytest.mark.parametrize("n_in,n_out", [(WIDEST, 64), (64, WIDEST)])
+def test_widest_weights_are_read_exactly(n_in, n_out):
+    """Offsets up to 2^31 within a tile, an output or a workspace: one value of 1 a
+    row shows rows and columns of the weight, exactly."""
+    q = require_gpu()
+    banner(f"fp8 widest {n_in}x{n_out}")
+    g = torch.Generator("cuda").manual_seed(351)
+    W = q.qlora_fp8_quantize_weight(torch.randn(n_out, n_in, generator=g, device="cuda") * 0.02)
+    wh = q.qlora_fp8_dequantize(W.codes, W.scales, n_out, n_in)
+    for T in (1, 17, 33):
+        for n, back in ((n_in, False), (n_out, True)):
+            at = (torch.arange(T, device="cuda") * 2 + 1) * (n // (2 * T + 1))
+            at[0], at[T - 1] = 0 if T > 1 else n - 1, n - 1
+            X = _one_hot(T, n, at)
+            if back:
+                got, want = q.qlora_fp8_linear_bwd(W, None, X, None, None, 0, 0.0)[0], wh[at]
+            else:
+                got, want = q.qlora_fp8_linear_fwd(W, X, None, None, 0, 0.0), wh.t()[at]
+            assert torch.equal(got, want), (T, back)  # (-0 equals 0)
+            del X, got, want
+
+
+@pytest.mark.parametrize("n_in,n_out", [((1 << 23) - 64, 64), (64, (1 << 23) - 64)])
+@pytest.mark.parametrize("T", [3, 17])
+def test_widest_adapters(T, n_in, n_out):
+    """The adapter at the largest side it takes above 16 tokens.  X and dY have
+    one value of 1 a row, so that U's and V's rows are columns of A and rows of B:
+    Y and dX are sums of one weight and r products, dA and dB rows of V and U."""
+    q = require_gpu()
+    banner(f"fp8 widest adapter T={T} {n_in}x{n_out}")
+    r, g = 8, torch.Generator("cuda").manual_seed(352)
+    W = q.qlora_fp8_quantize_weight(torch.randn(n_out, n_in, generator=g, device="cuda") * 0.02)
+    wh = q.qlora_fp8_dequantize(W.codes, W.scales, n_out, n_in)
+    A = torch.randn(r, n_in, generator=g, device="cuda").to(torch.bfloat16)
+    B = torch.randn(n_out, r, generator=g, device="cuda").to(torch.bfloat16)
+    kx = torch.arange(T, device="cuda") * 3 % n_in if n_in == 64 else (n_in - 1 - torch.arange(T, device="cuda") * (n_in // T))
+    my = torch.arange(T, device="cuda") * 3 % n_out if n_out == 64 else (n_out - 1 - torch.arange(T, device="cuda") * (n_out // T))
+    assert len(set(kx.tolist())) == T and len(set(my.tolist())) == T
+    X, dY = _one_hot(T, n_in, kx), _one_hot(T, n_out, my)
+    Y = q.qlora_fp8_linear_fwd(W, X, A, B, r, float(r))
+    dX, dA, dB = q.qlora_fp8_linear_bwd(W, X, dY, A, B, r, float(r))
+    U, V = A.double().t()[kx], B.double()[my]
+
+    def close(got, base, left, right):
+        for t in range(T):  # a row at a time: the widest are 64 MiB in 64 bits
+            terms = left[t][:, None] * right
+            ref, mag = base[t].double() + terms.sum(0), base[t].double().abs() + terms.abs().sum(0)
+            bound = 2.0 ** -8 * ref.abs() + 2.0 ** -12 * mag  # as in test_gpu_fp8.py
+            assert bool(((got[t].double() - ref).abs() <= bound).all()), t
+    close(Y, wh.t()[kx], U, B.double().t())
+    close(dX, wh[my], V, A.double())
+    # one term a sum, held to 32 bits: exact
+    assert torch.equal(dA[:, kx], V.t().float()) and torch.equal(dB[my], U.float())
+    dA[:, kx], dB[my] = 0.0, 0.0
+    assert not bool(dA.any()) and not bool(dB.any())

@@ -178,3 +178,37 @@ def test_more_experts_than_pairs(T, E, k, H, I):
     """More than 64 pairs over even more experts: a workgroup's slot is a pair,
     and only an expert's first pair works."""
     test_gpu_moe.test_experts_where_the_kernels_change(T, E, k, H, I)
+
+
+@pytest.mark.parametrize("T,k,H,I", [(1, 1, (1 << 20) - 64, 64), (17, 2, (1 << 20) - 64, 64), (17, 2, 64, (1 << 20) - 64),
+                                     (64, 3, (1 << 20) - 64, 128)])
+def test_experts_widest_sides(T, k, H, I):
+    """hidden and inter next to their limit of 2^20."""
+    q = require_gpu()
+    banner(f"moe widest T={T} k={k} H={H} I={I}")
+    E, g = 3, torch.Generator("cuda").manual_seed(221)
+    gu = q.nf4_quantize_weight(torch.randn(E * 2 * I, H, generator=g, device="cuda") * H ** -0.5)
+    dn = q.nf4_quantize_weight(torch.randn(E * H, I, generator=g, device="cuda") * I ** -0.5)
+    X = torch.randn(T, H, generator=g, device="cuda").to(torch.bfloat16)
+    ids = torch.stack([torch.randperm(E, generator=g, device="cuda")[:k] for _ in range(T)]).to(torch.int32)
+    w = torch.randn(T, k, generator=g, device="cuda")
+    Y = q.qlora_moe_fwd(gu, dn, E, X, ids, w)
+
+    vg = q.nf4_dequantize(gu.codes, gu.absmax_q, gu.absmax_scale, E * 2 * I * H).view(E, 2 * I, H)
+    vd = q.nf4_dequantize(dn.codes, dn.absmax_q, dn.absmax_scale, E * H * I).view(E, H, I)
+    ref, mag = (torch.zeros(T, H, dtype=torch.float64, device="cuda") for _ in range(2))
+    for e in range(E):
+        took = (w.double() * (ids == e)).sum(1)
+        rows = (ids == e).any(1).nonzero().view(-1)
+        if not rows.numel():
+            continue
+        gate = X[rows].double() @ vg[e].double().t().contiguous()
+        h = gate[:, :I] * torch.sigmoid(gate[:, :I]) * gate[:, I:]
+        down = vd[e].double().t().contiguous()
+        ref[rows] += took[rows, None] * (h @ down)
+        mag[rows] += took[rows, None].abs() * (h.abs() @ down.abs())
+    # the bound of test_gpu_moe.py, whose 2^-13 stands for two chained sums of at most
+    # 1024 terms, 2^-14 each; here the sums of a wave are longer, but what its matrix
+    # instructions add is random in sign: n terms err by about sqrt(n) 2^-24 of their
+    # root mean square, 2^-14 at n = 2^20
+    assert bool(((Y.double() - ref).abs() <= 2.0 ** -8 * ref.abs() + 2.0 ** -13 * mag).all())
