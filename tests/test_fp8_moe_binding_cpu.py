@@ -108,9 +108,27 @@ def test_transposed_tensors_are_refused_elsewhere(q):
                 call()
 
 
+def test_host_memory_is_refused_by_every_call(q):
+    u8, f32, i32, b16 = torch.uint8, torch.float32, torch.int32, torch.bfloat16
+    host = lambda *shape, dtype=b16: torch.zeros(*shape, dtype=dtype)
+    W = q.FP8Weight(host(64, 64, dtype=u8), host(1, 1, dtype=u8), 64, 64)
+    N4 = q.NF4Weight(host(4096, dtype=u8), host(128, dtype=u8), host(1, dtype=f32), 128, 64)
+    X, A, B, ids, wt = host(4, 64), host(8, 64), host(64, 8), host(4, 2, dtype=i32), host(4, 2, dtype=f32)
+    for call in (lambda: q.qlora_fp8_quantize(host(64, 64, dtype=f32)), lambda: q.qlora_fp8_quantize_weight(host(64, 64, dtype=f32)),
+                 lambda: q.qlora_fp8_dequantize(W.codes, W.scales, 64, 64),
+                 lambda: q.qlora_fp8_linear_fwd(W, X, A, B, 8, 16.0), lambda: q.qlora_fp8_linear_fwd(W, X, None, None, 0, 0.0),
+                 lambda: q.qlora_fp8_linear_bwd(W, X, X, A, B, 8, 16.0),
+                 lambda: q.qlora_fp8_linear_bwd(W, None, X, None, None, 0, 0.0),
+                 lambda: q.qlora_moe_route(host(4, 8, dtype=f32), 2),
+                 lambda: q.qlora_moe_route_bwd(host(4, 8, dtype=f32), ids, wt),
+                 lambda: q.qlora_moe_fwd(N4, N4, 1, X, ids, wt)):
+        with pytest.raises(ValueError, match="GPU"):
+            call()
+
+
 # ------------------------------------------------------------------ workspaces
 class _Gpus:
-    """torch.cuda as far as the workspaces ask it: which GPU is current and
+    """torch's GPUs as far as the workspaces ask them: which GPU is current and
     whether each one's current stream is being captured."""
 
     def __init__(self, monkeypatch, q, current, capturing):
@@ -126,8 +144,8 @@ class _Gpus:
 
             def __exit__(self, *_):
                 gpus.current = self.back
-        monkeypatch.setattr(torch.cuda, "current_device", lambda: gpus.current)
-        monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: gpus.capturing[gpus.current])
+        monkeypatch.setattr(q, "_current_gpu", lambda: gpus.current)
+        monkeypatch.setattr(q, "_captures", lambda: gpus.capturing[gpus.current])
         monkeypatch.setattr(torch.cuda, "device", Guard)
         monkeypatch.setattr(q, "_raw_stream", lambda index: 100 + index)
         self.made = []
