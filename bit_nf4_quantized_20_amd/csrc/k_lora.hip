@@ -284,7 +284,8 @@ __device__ __forceinline__ void down_fin_tile(FinStage<NP>& stage, const float* 
     }
     s_t[jl][tl] = hb | (lb << 16);  // tokens >= T hold zero
     if constexpr (NP == 3)
-      s_t3[jl][tl] = static_cast<uint16_t>(pack_bf16x2(is_finite(v) ? v - bf16_lo(hb) - bf16_lo(lb) : 0.f, 0.f));
+      s_t3[jl][tl] = static_cast<uint16_t>(  // what is not finite is in lo already
+          pack_bf16x2(__builtin_fabsf(v) < __builtin_inff() ? v - bf16_lo(hb) - bf16_lo(lb) : 0.f, 0.f));
   }
   if (hilo_t == nullptr) return;
   __syncthreads();
@@ -374,12 +375,12 @@ hipError_t launch_lora_down_fin(const float* part, int64_t T, int64_t K, int nP,
 
 // ---------------------------------------------------------------------------
 // lora_grad: G[j][c] = sum_t Pt[j][t] Q[t][c] + sum_t Pt[rp+j][t] Q[t][c]
-// (the hi and lo halves of the transposed rank factor) for ranks
-// [j0, j0 + 32*JT), 128 columns per workgroup and a slice of tokens; slices
-// add into the zeroed fp32 output with atomics.  Bound by streaming Q (dY or
-// X) from HBM once.
+// (the hi and lo planes of the transposed rank factor, and a third one with NP
+// = 3) for ranks [j0, j0 + 32*JT), 128 columns per workgroup and a slice of
+// tokens; each slice writes its own sums, which are added in order afterwards.
+// Bound by streaming Q (dY or X) from HBM once.
 //
-// Per 64-token step the Q tile [64 t][128 c] and the Pt tile [64*JT rows][64 t]
+// Per 64-token step the Q tile [64 t][128 c] and the Pt tile [32*NP*JT rows][64 t]
 // are loaded contiguously into registers one step ahead and written into a
 // double-buffered LDS stage.  Q is transposed on the way: a thread holds two
 // token rows of 8 columns, pairs them with v_perm and writes one dword
@@ -431,7 +432,7 @@ __device__ __forceinline__ void grad_tile(GradStage<JT, NP>& stage, const uint16
   const int nsteps = static_cast<int>((te - ts + 63) / 64);
 
   // Q resource starts at this slice and ends at row T (or 2^31 - 1 bytes;
-  // the host keeps a slice under 2^30 bytes)
+  // all of Q is below that)
   const uint64_t q_bytes = static_cast<uint64_t>(T - ts) * ldq * 2;
   const __amdgpu_buffer_rsrc_t rs_q = __builtin_amdgcn_make_buffer_rsrc(
       const_cast<uint16_t*>(Q + ts * ldq), 0, static_cast<int>(q_bytes < 0x7fffffffu ? q_bytes : 0x7fffffffu),
@@ -442,7 +443,7 @@ __device__ __forceinline__ void grad_tile(GradStage<JT, NP>& stage, const uint16
       const_cast<uint16_t*>(Pt), 0, static_cast<int>(static_cast<uint64_t>(nproj) * NP * rp * ldt * 2),
       kBufferWord3);
   // Rank J of the call is rank J % rproj of projection J / rproj, whose hi and
-  // lo rows are i 2rp + J % rproj and i 2rp + rp + J % rproj; ranks past r read zeros.
+  // lo rows are i NP rp + J % rproj and i NP rp + rp + J % rproj; ranks past r read zeros.
   int64_t prow_base[NP * JT];
 #pragma unroll
   for (int i = 0; i < NP * JT; ++i) {
@@ -1028,7 +1029,8 @@ namespace {
 int64_t grad_two_tokens(int64_t T, int64_t C0, int64_t C1, int64_t r) {
   const int64_t ct = ceil_div(C0, kGradCT) + ceil_div(C1, kGradCT), most = C0 > C1 ? C0 : C1;
   const int64_t steps = ceil_div(T, 64), room = r > 32 ? 256 : 512;
-  // 32-bit buffer offsets: a slice of Q stays under 2^30 bytes
+  // 32-bit buffer offsets: more than one slice above 2^30 bytes of Q (with an even
+  // number of steps one may pass that, but all of Q is below 2^31)
   int64_t best = 1;
   double least = -1.0;
   for (int64_t S = ceil_div(T * most * 2, int64_t(1) << 30); S <= 64; ++S) {

@@ -166,15 +166,13 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
 __device__ __forceinline__ float bf16_lo(uint32_t p) { return __builtin_bit_cast(float, p << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t p) { return __builtin_bit_cast(float, p & 0xffff0000u); }
 
-// Two fp32 values as bf16 pairs hi + lo (16 bits of fraction).  A finite value
-// that would round past bf16's largest takes that as its hi, so that lo holds
-// the rest; an infinite one has no rest (inf - inf is NaN).
-__device__ __forceinline__ bool is_finite(float v) { return __builtin_fabsf(v) < __builtin_inff(); }
+// Two fp32 values as bf16 pairs hi + lo (16 bits of fraction).  hi is held to
+// bf16's largest, so that lo has the rest of a value that would round past it,
+// and carries an infinity or a NaN (with an infinite hi it would be inf - inf).
 __device__ __forceinline__ void split_bf16x2(float a, float b, uint32_t& hi, uint32_t& lo) {
   constexpr float kMost = 0x1.fep127f;
-  const bool fa = is_finite(a), fb = is_finite(b);
-  hi = pack_bf16x2(fa ? __builtin_amdgcn_fmed3f(a, -kMost, kMost) : a, fb ? __builtin_amdgcn_fmed3f(b, -kMost, kMost) : b);
-  lo = pack_bf16x2(fa ? a - bf16_lo(hi) : 0.f, fb ? b - bf16_hi(hi) : 0.f);
+  hi = pack_bf16x2(__builtin_amdgcn_fmed3f(a, -kMost, kMost), __builtin_amdgcn_fmed3f(b, -kMost, kMost));
+  lo = pack_bf16x2(a - bf16_lo(hi), b - bf16_hi(hi));
 }
 
 // ---------------------------------------------------------------------------
