@@ -164,9 +164,11 @@ struct F8Args {
 // read anew behind its last use).  The scale bytes of four steps sit in one
 // register per activation fragment (op_sel picks the byte) and are fetched four
 // steps ahead.  4096 x 4096 -> 14336: 262 us with the barrier at the step's end
-// and both operands' fragments doubled, 230 this way (2.1 PF/s; without copies
-// and LDS reads the matrix instructions alone took 183, at the 2.0 GHz that the
-// power limit leaves them); 4 waves of 128 x 128 took 252.
+// and both operands' fragments doubled, 230 this way (2.1 PF/s); 4 waves of 128 x
+// 128 took 252.  What bounds it is the issue of this sequence: the matrix cores
+// are busy for 244 k cycles, 122 us at the 2.0 GHz of these runs, and with
+// neither copies nor LDS reads the same instruction order still took 183; the
+// LDS reads and the copies with their one wait a step are the rest.
 template <int BM, int BN, int WM, int WN, bool kTr>
 __global__ __launch_bounds__(64 * WM * WN, 1) void k_fp8_gemm(F8Args p) {
   constexpr int NW = WM * WN;

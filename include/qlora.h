@@ -438,7 +438,9 @@ const char* qlora_status_string(int status);
  * an all-zero block has byte 0.
  *   code = e4m3_rne(w 2^-e);   w_hat = code 2^e
  * Blocks at the right and lower edge may be smaller; rows and cols are
- * multiples of 64.  8 + 8 / 16384 bits per weight.
+ * multiples of 64.  8 + 8 / 16384 bits per weight.  (Weights that come with
+ * free fp32 scales per block are no codes of this format: they have to be
+ * multiplied out and quantized again.)
  *   codes  [rows * cols]                            row-major, one byte each
  *   scales [ceil(rows / 128) * ceil(cols / 128)]    row-major
  *   flags  reserved, must be 0 (QLORA_ERR_VALUE otherwise)
@@ -491,7 +493,8 @@ size_t qlora_fp8_workspace_bytes(int64_t T, int64_t in_features, int64_t out_fea
  *   A  [r, in] bf16;  B [out, r] bf16;  0 <= r <= 256 (r = 0: no adapter, A, B
  *   and alpha are not read and A, B may be NULL);  alpha finite
  *   ws of ws_bytes >= qlora_fp8_workspace_bytes(T, in, out, r, 0)
- * A row of X that holds an infinity or a NaN gives a row of Y of NaN.
+ * A row of X that holds an infinity or a NaN gives a row of Y of NaN; the other
+ * rows do not change.  A value of s X A^T that is infinite or NaN counts as such.
  * T = 0 is a no-op.  Size limits as for qlora_linear_fwd; with r > 0, above 16
  * tokens or 8192 columns also in, out < 2^23 and 6 rp tp < 2^31, rp being r
  * rounded up to 64 and tp T rounded up to 8 (both calls).
@@ -507,7 +510,9 @@ int qlora_fp8_linear_fwd(const qlora_fp8_weight* W, const qlora_bf16* X, int64_t
  *   dX = dY_hat W_hat + s (dY B) A    [T, in]  bf16 (one rounding)
  *   dA = s (dY B)^T X                 [r, in]  fp32
  *   dB = s dY^T (X A^T)               [out, r] fp32
- * dY_hat is dY quantized per row and 128 columns like X in the forward.  dA
+ * dY_hat is dY quantized per row and 128 columns like X in the forward.  A row of
+ * dY that is not finite gives a row of dX of NaN; one of X or dY reaches dA and
+ * dB as the sums above say.  dA
  * and dB are overwritten and bit-reproducible, as in qlora_linear_bwd; with
  * r = 0 only dX is written (X, A, B, dA, dB may be NULL).  T = 0 writes zeros
  * to dA and dB.
@@ -540,7 +545,9 @@ int qlora_fp8_linear_bwd(const qlora_fp8_weight* W, const qlora_bf16* X, const q
  * weights 0.  A row with a NaN or +inf has NaN weights.
  *   logits  [T, E] fp32;  1 <= E <= 1024;  1 <= k <= min(16, E);  T >= 0
  *           (0 is a no-op), T * E < 2^31
- * qlora_moe_route_bwd -- the gradient of the logits for dweights [T, k]: with p
+ * qlora_moe_route_bwd -- the gradient of the logits for dweights [T, k] (for a
+ * layer Y_t = sum_j weights[t, j] y_tj that is the products dY_t . y_tj; the
+ * caller forms them, qlora_moe_fwd keeps no y_tj): with p
  * the softmax the weights were taken from (over the chosen, or over all) and
  * g_e the gradient of e's weight (0 where e was not chosen),
  *   dlogits [T, E] fp32 = p_e (g_e - sum_i g_i p_i), overwritten; 0 in a row of

@@ -1,7 +1,11 @@
 """The 8-bit linear layer where its inputs leave the ordinary (rows that are
 not finite, adapter products past bf16's largest, transposed tensors), where
 its products are exact, and with any contents of its workspace, on another
-stream and in graphs, at sizes that split the sums."""
+stream and in graphs, at sizes that split the sums.
+
+Above 16 tokens sU and sV meet dB and dA as three bf16 parts, up to 16 as fp32
+values: the relative Frobenius bound of 2e-5 in test_gpu_fp8.py has room for
+two parts (2^-17), the one for exact values here has not."""
 
 import numpy as np
 import pytest
