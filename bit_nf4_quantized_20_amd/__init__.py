@@ -13,8 +13,12 @@ Names and semantics follow include/qlora.h:
     qlora_noalloc_scratch_bytes, qlora_linear_fwd_noalloc, qlora_workspace_bytes_flags,
     nf4_quantize_weight_nodq, nf4_code_buckets,
     qlora_fp8_storage_bytes, qlora_fp8_quantize, qlora_fp8_quantize_weight, qlora_fp8_dequantize,
-    qlora_fp8_workspace_bytes, qlora_fp8_linear_fwd, qlora_fp8_linear_bwd,
+    qlora_fp8_workspace_bytes, qlora_fp8_linear_fwd, qlora_fp8_linear_bwd, qlora_fp8_rows_bytes,
+    qlora_fp8_linear_fwd_rows,
     qlora_moe_route, qlora_moe_route_bwd, qlora_moe_workspace_bytes, qlora_moe_fwd,
+    qlora_rmsnorm_fwd, qlora_rmsnorm_workspace_bytes, qlora_rmsnorm_bwd,
+    qlora_head_workspace_bytes, qlora_head_loss, qlora_head_loss_grad,
+    qlora_adamw_state_len, qlora_adamw_state, qlora_adamw_plan, qlora_adamw_step,
     nf4_codebook, nf4_code_thresholds, qlora_status_string
 """
 
@@ -150,6 +154,54 @@ _lib.qlora_moe_workspace_bytes.restype = _sz
 _lib.qlora_moe_fwd.argtypes = [ctypes.POINTER(_NF4WeightC), ctypes.POINTER(_NF4WeightC), _i64, _p, _i64, _p, _p,
                                _i64, _p, _p, _sz, _p]
 _lib.qlora_moe_fwd.restype = ctypes.c_int
+_lib.qlora_fp8_rows_bytes.argtypes = [_i64, _i64, ctypes.POINTER(_sz), ctypes.POINTER(_sz)]
+_lib.qlora_fp8_rows_bytes.restype = ctypes.c_int
+_lib.qlora_fp8_linear_fwd_rows.argtypes = [ctypes.POINTER(_FP8WeightC), _p, _p, _p, _i64, _p, _p, _i64, ctypes.c_float,
+                                           _p, _p, _sz, _p]
+_lib.qlora_fp8_linear_fwd_rows.restype = ctypes.c_int
+_lib.qlora_rmsnorm_fwd.argtypes = [_p, _p, _p, _i64, _i64, ctypes.c_float, _p, _p, _p, _p, _p, _p]
+_lib.qlora_rmsnorm_fwd.restype = ctypes.c_int
+_lib.qlora_rmsnorm_workspace_bytes.argtypes = [_i64, _i64]
+_lib.qlora_rmsnorm_workspace_bytes.restype = _sz
+_lib.qlora_rmsnorm_bwd.argtypes = [_p, _p, _p, _p, _p, _i64, _i64, _p, _p, _p, _sz, _p]
+_lib.qlora_rmsnorm_bwd.restype = ctypes.c_int
+
+
+class _HeadC(ctypes.Structure):
+    _fields_ = [("bf16", _p), ("nf4", ctypes.POINTER(_NF4WeightC)), ("fp8", ctypes.POINTER(_FP8WeightC)),
+                ("vocab", _i64), ("hidden", _i64)]
+
+
+_lib.qlora_head_workspace_bytes.argtypes = [_i64, _i64, _i64, ctypes.c_int, ctypes.c_int]
+_lib.qlora_head_workspace_bytes.restype = _sz
+_lib.qlora_head_loss.argtypes = [ctypes.POINTER(_HeadC), _p, _i64, _p, _p, _p, _p, _sz, _p]
+_lib.qlora_head_loss.restype = ctypes.c_int
+_lib.qlora_head_loss_grad.argtypes = [ctypes.POINTER(_HeadC), _p, _i64, _p, _p, _p, _p, _p, _p, _sz, _p]
+_lib.qlora_head_loss_grad.restype = ctypes.c_int
+
+
+class _AdamWTensorC(ctypes.Structure):
+    _fields_ = [("param", _p), ("master", _p), ("grad", _p), ("numel", _i64)]
+
+
+class _AdamWTableC(ctypes.Structure):
+    _fields_ = [("table", _p), ("chunks", _i64), ("state_len", _i64)]
+
+
+class _AdamWRatesC(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double), ("step", _i64), ("seed", ctypes.c_uint32)]
+
+
+_lib.qlora_adamw_state_len.argtypes = [ctypes.POINTER(_i64), _i64]
+_lib.qlora_adamw_state_len.restype = _i64
+_lib.qlora_adamw_table_bytes.argtypes = [ctypes.POINTER(_i64), _i64]
+_lib.qlora_adamw_table_bytes.restype = _sz
+_lib.qlora_adamw_plan.argtypes = [ctypes.POINTER(_AdamWTensorC), _i64, _p, _sz, ctypes.POINTER(_AdamWTableC), _p]
+_lib.qlora_adamw_plan.restype = ctypes.c_int
+_lib.qlora_adamw_step.argtypes = [ctypes.POINTER(_AdamWTableC), ctypes.c_int, _p, _p, _p, _p, _p,
+                                  ctypes.POINTER(_AdamWRatesC), _p]
+_lib.qlora_adamw_step.restype = ctypes.c_int
 
 
 def _status_string(status: int) -> str:
@@ -867,3 +919,309 @@ def qlora_moe_fwd(gate_up: NF4Weight, down: NF4Weight, experts: int, X, ids, wei
         X.data_ptr(), T, ids.data_ptr(), weights.data_ptr(), k, Y.data_ptr(), ws.data_ptr(),
         ws.numel() * ws.element_size())
     return Y
+
+
+# ---------------------------------------------------------------------------
+# Around the layers of a training step: norm, loss through the output head,
+# optimizer.  As above, a call runs on its tensors' GPU and that GPU's current
+# stream.
+# ---------------------------------------------------------------------------
+@dataclass
+class FP8Rows:
+    """Quantized rows of a matrix [T, cols]: e4m3 codes, padded with 0 to whole
+    blocks of 128 columns, and scale bytes by groups of four blocks (block b of
+    row t: scales[b // 4, t, b % 4])."""
+    codes: torch.Tensor   # uint8 [T, cols rounded up to 128]
+    scales: torch.Tensor  # uint8 [ceil(cols/512), T rounded up to 256, 4]
+    T: int
+    cols: int
+
+
+def qlora_fp8_rows_bytes(T: int, cols: int):
+    c, s = _sz(), _sz()
+    _check(_lib.qlora_fp8_rows_bytes(T, cols, ctypes.byref(c), ctypes.byref(s)), "qlora_fp8_rows_bytes")
+    return c.value, s.value
+
+
+def _rows8_arg(rows, T: int, cols: int, dev):
+    if not isinstance(rows, FP8Rows):
+        raise TypeError(f"rows: expected FP8Rows, got {type(rows).__name__}")
+    if rows.T != T or rows.cols != cols:
+        raise ValueError(f"rows: expected [{T}, {cols}], got [{rows.T}, {rows.cols}]")
+    _arg(rows.codes, torch.uint8, (T, -(-cols // 128) * 128), "rows.codes", dev)
+    _arg(rows.scales, torch.uint8, (-(-cols // 512), -(-T // 256) * 256, 4), "rows.scales", dev)
+
+
+def qlora_fp8_linear_fwd_rows(W: FP8Weight, rows: FP8Rows, X, A, B, r: int, alpha: float, Y=None, ws=None):
+    """qlora_fp8_linear_fwd of an X whose quantized rows are at hand (the same
+    Y bit for bit); X None: r = 0, and more than 16 tokens or 8192 columns."""
+    if not isinstance(rows, FP8Rows):
+        raise TypeError(f"rows: expected FP8Rows, got {type(rows).__name__}")
+    T, dev = rows.T, rows.codes.device
+    _rows8_arg(rows, T, W.cols, dev)
+    if X is not None:
+        _arg(X, torch.bfloat16, (T, W.cols), "X", dev)
+    _fp8_args(W, A, B, r, dev)
+    if Y is None:
+        Y = torch.empty(T, W.rows, dtype=torch.bfloat16, device=dev)
+    else:
+        _rows_arg(Y, torch.bfloat16, T, W.rows, "Y", dev)
+    ws = _scratch(ws, qlora_fp8_workspace_bytes(T, W.cols, W.rows, r, False), dev)
+    _on(dev, _lib.qlora_fp8_linear_fwd_rows, "qlora_fp8_linear_fwd_rows", ctypes.byref(W._c()), rows.codes.data_ptr(),
+        rows.scales.data_ptr(), X.data_ptr() if X is not None else None, T, A.data_ptr() if r > 0 else None,
+        B.data_ptr() if r > 0 else None, r, float(alpha), Y.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size())
+    return Y
+
+
+def qlora_rmsnorm_fwd(x, weight, residual=None, eps: float = 1e-6, y16: bool = True, rows8: bool = False, h=None, y=None,
+                      rows=None, rstd=None):
+    """-> (y bf16 [T, H] or None, FP8Rows of y or None, h bf16 [T, H], rstd fp32
+    [T]): h = bf16(x + residual) (x itself without one), rstd = 1 / sqrt(mean
+    h^2 + eps), y = bf16(h rstd weight), weight fp32 [H].  y16, rows8: which
+    forms of y are wanted.  h may be x or residual."""
+    T, H = _matrix(x, "x")
+    dev = x.device
+    _arg(x, torch.bfloat16, (T, H), "x", dev)
+    _arg(weight, torch.float32, H, "weight", dev)
+    if residual is not None:
+        _arg(residual, torch.bfloat16, (T, H), "residual", dev)
+        if h is None:
+            h = torch.empty(T, H, dtype=torch.bfloat16, device=dev)
+        else:
+            _rows_arg(h, torch.bfloat16, T, H, "h", dev)
+    elif h is not None and h is not x:
+        raise ValueError("h: is x without a residual")
+    y16, rows8 = y16 or y is not None, rows8 or rows is not None
+    if not y16 and not rows8:
+        raise ValueError("y16, rows8: one of them is needed")
+    if y is not None:
+        _rows_arg(y, torch.bfloat16, T, H, "y", dev)
+    elif y16:
+        y = torch.empty(T, H, dtype=torch.bfloat16, device=dev)
+    if rows is not None:
+        _rows8_arg(rows, T, H, dev)
+    elif rows8:
+        rows = FP8Rows(torch.empty(T, -(-H // 128) * 128, dtype=torch.uint8, device=dev),
+                       torch.empty(-(-H // 512), -(-T // 256) * 256, 4, dtype=torch.uint8, device=dev), T, H)
+    if rstd is None:
+        rstd = torch.empty(T, dtype=torch.float32, device=dev)
+    else:
+        _arg(rstd, torch.float32, T, "rstd", dev)
+    _on(dev, _lib.qlora_rmsnorm_fwd, "qlora_rmsnorm_fwd", x.data_ptr(), residual.data_ptr() if residual is not None else None,
+        weight.data_ptr(), T, H, float(eps), h.data_ptr() if residual is not None else None,
+        y.data_ptr() if y is not None else None, rows.codes.data_ptr() if rows8 else None,
+        rows.scales.data_ptr() if rows8 else None, rstd.data_ptr())
+    return y, rows, x if residual is None else h, rstd
+
+
+@functools.lru_cache(maxsize=4096)
+def qlora_rmsnorm_workspace_bytes(T: int, H: int) -> int:
+    return int(_lib.qlora_rmsnorm_workspace_bytes(T, H))
+
+
+def qlora_rmsnorm_bwd(dy, h, weight, rstd, dres=None, want_dweight: bool = True, dh=None, dweight=None, ws=None):
+    """-> (dh bf16 [T, H], dweight fp32 [H] or None), h and rstd as the forward
+    gave them; dres: the gradient that reaches h past the norm.  dh may be dy or
+    dres."""
+    T, H = _matrix(dy, "dy")
+    dev = dy.device
+    _arg(dy, torch.bfloat16, (T, H), "dy", dev)
+    _arg(h, torch.bfloat16, (T, H), "h", dev)
+    _arg(weight, torch.float32, H, "weight", dev)
+    _arg(rstd, torch.float32, T, "rstd", dev)
+    if dres is not None:
+        _arg(dres, torch.bfloat16, (T, H), "dres", dev)
+    if dh is None:
+        dh = torch.empty(T, H, dtype=torch.bfloat16, device=dev)
+    else:
+        _rows_arg(dh, torch.bfloat16, T, H, "dh", dev)
+    ws_ptr, ws_bytes = None, 0
+    if dweight is not None:
+        _arg(dweight, torch.float32, H, "dweight", dev)
+    elif want_dweight:
+        dweight = torch.empty(H, dtype=torch.float32, device=dev)
+    if dweight is not None:
+        ws = _scratch(ws, qlora_rmsnorm_workspace_bytes(T, H), dev)
+        ws_ptr, ws_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
+    _on(dev, _lib.qlora_rmsnorm_bwd, "qlora_rmsnorm_bwd", dy.data_ptr(), h.data_ptr(), weight.data_ptr(), rstd.data_ptr(),
+        dres.data_ptr() if dres is not None else None, T, H, dh.data_ptr(),
+        dweight.data_ptr() if dweight is not None else None, ws_ptr, ws_bytes)
+    return dh, dweight
+
+
+@functools.lru_cache(maxsize=4096)
+def qlora_head_workspace_bytes(T: int, vocab: int, hidden: int, expand: bool, grad: bool) -> int:
+    return int(_lib.qlora_head_workspace_bytes(T, vocab, hidden, 1 if expand else 0, 1 if grad else 0))
+
+
+def _head_args(W, X, labels, grad: bool, loss, lse, ws):
+    """Checks what both calls take -> (T, H, the head's C struct, loss, lse, workspace)."""
+    T, H = _matrix(X, "X")
+    dev = X.device
+    _arg(X, torch.bfloat16, (T, H), "X", dev)
+    head = _HeadC(hidden=H)
+    if isinstance(W, NF4Weight):
+        vocab = W.rows
+        if W.flags == QLORA_NF4_ABSMAX_FP32:
+            _arg(W.codes, torch.uint8, vocab * W.cols // 2, "W.codes", dev)
+            _arg(W.absmax_scale, torch.float32, vocab * W.cols // 64, "W.absmax_scale", dev)
+        else:
+            _nf4_arg(W, "W", dev)
+        head.nf4 = ctypes.pointer(W._c())
+    elif isinstance(W, FP8Weight):
+        vocab = W.rows
+        _fp8_args(W, None, None, 0, dev)
+        head.fp8 = ctypes.pointer(W._c())
+    else:
+        vocab, _ = _matrix(W, "W")
+        _arg(W, torch.bfloat16, (vocab, H), "W", dev)
+        head.bf16 = W.data_ptr()
+    head.vocab = vocab
+    _arg(labels, torch.int64, T, "labels", dev)
+    if loss is None:
+        loss = torch.empty(T, dtype=torch.float32, device=dev)
+    else:
+        _arg(loss, torch.float32, T, "loss", dev)
+    if lse is None:
+        lse = torch.empty(T, dtype=torch.float32, device=dev)
+    else:
+        _arg(lse, torch.float32, T, "lse", dev)
+    ws = _scratch(ws, qlora_head_workspace_bytes(T, vocab, H, not head.bf16, grad), dev)
+    return T, H, head, loss, lse, ws
+
+
+def qlora_head_loss(W, X, labels, loss=None, lse=None, ws=None):
+    """-> (loss fp32 [T], lse fp32 [T]) of the logits X W^T: loss = lse -
+    logit[label], 0 where the label is outside [0, vocab).  W: the frozen output
+    head [vocab, hidden], a bf16 tensor, an NF4Weight or an FP8Weight; X bf16 [T,
+    hidden]; labels int64 [T]."""
+    T, _, head, loss, lse, ws = _head_args(W, X, labels, False, loss, lse, ws)
+    _on(X.device, _lib.qlora_head_loss, "qlora_head_loss", ctypes.byref(head), X.data_ptr(), T, labels.data_ptr(),
+        loss.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size())
+    return loss, lse
+
+
+def qlora_head_loss_grad(W, X, labels, dloss, loss=None, lse=None, dX=None, ws=None):
+    """-> (loss, lse, dX bf16 [T, hidden]): qlora_head_loss and the gradient of X
+    for dloss fp32 [T], the gradient of each row's loss; the logits are formed
+    once for both."""
+    T, H, head, loss, lse, ws = _head_args(W, X, labels, True, loss, lse, ws)
+    dev = X.device
+    _arg(dloss, torch.float32, T, "dloss", dev)
+    if dX is None:
+        dX = torch.empty(T, H, dtype=torch.bfloat16, device=dev)
+    else:
+        _rows_arg(dX, torch.bfloat16, T, H, "dX", dev)
+    _on(dev, _lib.qlora_head_loss_grad, "qlora_head_loss_grad", ctypes.byref(head), X.data_ptr(), T, labels.data_ptr(),
+        dloss.data_ptr(), loss.data_ptr(), lse.data_ptr(), dX.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size())
+    return loss, lse, dX
+
+
+@dataclass
+class AdamWState:
+    """The states of all tensors of a plan, one tensor's after another's, each
+    rounded up to 128 elements.  32 bits: m, v fp32.  8 bits: m, v uint8 (e4m3
+    codes of m and of sqrt(v)) with scale bytes, one per 128 elements."""
+    m: torch.Tensor
+    v: torch.Tensor
+    m_scales: torch.Tensor = None
+    v_scales: torch.Tensor = None
+
+
+@dataclass
+class AdamWPlan:
+    """Tensors bound to an optimizer's step.  It keeps them (their memory is
+    read and written at every step; a tensor whose storage is replaced needs a new
+    plan)."""
+    state: AdamWState
+    bits: int
+    offsets: list     # each tensor's first element in the states
+    tensors: list     # what the table points to
+    table: torch.Tensor
+    _c: _AdamWTableC
+
+
+def _numels(numel):
+    return (_i64 * max(len(numel), 1))(*[int(n) for n in numel])
+
+
+def qlora_adamw_state_len(numel) -> int:
+    """Elements of m and of v for tensors of these sizes."""
+    n = int(_lib.qlora_adamw_state_len(_numels(numel), len(numel)))
+    if n < 0:
+        raise QloraError(-2, "qlora_adamw_state_len")
+    return n
+
+
+def qlora_adamw_state(numel, bits: int, device) -> AdamWState:
+    """Zero states for tensors of these sizes."""
+    if bits not in (8, 32):
+        raise ValueError(f"bits: 8 or 32, got {bits}")
+    n = qlora_adamw_state_len(numel)
+    if bits == 32:
+        return AdamWState(torch.zeros(n, dtype=torch.float32, device=device),
+                          torch.zeros(n, dtype=torch.float32, device=device))
+    return AdamWState(*[torch.zeros(k, dtype=torch.uint8, device=device) for k in (n, n, n // 128, n // 128)])
+
+
+def qlora_adamw_plan(params, masters, grads, state: AdamWState) -> AdamWPlan:
+    """Binds tensors to their states.  params: bf16 tensors or None, masters: fp32
+    tensors or None (one of the two per tensor, or both: the master and the copy
+    that the layers read; either list may be None), grads: fp32, of the same sizes.
+    The dA, dB of the layers are written into grads with their output arguments."""
+    n = len(grads)
+    params, masters = params if params is not None else [None] * n, masters if masters is not None else [None] * n
+    if len(params) != n or len(masters) != n:
+        raise ValueError(f"params, masters, grads: {len(params)}, {len(masters)} and {n} tensors")
+    if not isinstance(state, AdamWState) or not isinstance(state.m, torch.Tensor):
+        raise TypeError(f"state: expected an AdamWState, got {type(state).__name__}")
+    dev = state.m.device
+    bits = 8 if state.m.dtype == torch.uint8 else 32
+    numel, offsets, total = [], [], 0
+    for i, (p, f, g) in enumerate(zip(params, masters, grads)):
+        if not isinstance(g, torch.Tensor):
+            raise TypeError(f"grads[{i}]: expected a tensor, got {type(g).__name__}")
+        if p is None and f is None:
+            raise TypeError(f"params[{i}], masters[{i}]: one of them is needed")
+        _arg(g, torch.float32, tuple(g.shape), f"grads[{i}]", dev)
+        if p is not None:
+            _arg(p, torch.bfloat16, tuple(g.shape), f"params[{i}]", dev)
+        if f is not None:
+            _arg(f, torch.float32, tuple(g.shape), f"masters[{i}]", dev)
+        numel.append(g.numel())
+        offsets.append(total)
+        total += -(-g.numel() // 128) * 128
+    length = qlora_adamw_state_len(numel)
+    kind = torch.uint8 if bits == 8 else torch.float32
+    _arg(state.m, kind, length, "state.m", dev)
+    _arg(state.v, kind, length, "state.v", dev)
+    if bits == 8:
+        _arg(state.m_scales, torch.uint8, length // 128, "state.m_scales", dev)
+        _arg(state.v_scales, torch.uint8, length // 128, "state.v_scales", dev)
+    need = int(_lib.qlora_adamw_table_bytes(_numels(numel), n))
+    table = torch.empty(need, dtype=torch.uint8, device=dev)
+    ptr = (lambda t: t.data_ptr() if t is not None else None)
+    rows = (_AdamWTensorC * max(n, 1))(*[_AdamWTensorC(ptr(p), ptr(f), g.data_ptr(), k)
+                                         for p, f, g, k in zip(params, masters, grads, numel)])
+    out = _AdamWTableC()
+    _on(dev, _lib.qlora_adamw_plan, "qlora_adamw_plan", rows, n, table.data_ptr(), need, ctypes.byref(out))
+    # aliases of the tensors: what they point to stays allocated
+    kept = [t.detach() for ts in (params, masters, grads) for t in ts if t is not None]
+    return AdamWPlan(AdamWState(*[t.detach() if t is not None else None for t in
+                                  (state.m, state.v, state.m_scales, state.v_scales)]), bits, offsets, kept, table, out)
+
+
+def qlora_adamw_step(plan: AdamWPlan, step: int, lr: float, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
+                     weight_decay: float = 0.0, grad_scale=None, seed: int = None):
+    """One AdamW step (the step-th, from 1 on) over all tensors of a plan, in
+    place.  grad_scale: fp32 tensor of one element on the GPU, multiplied into every
+    gradient; seed: of the 8-bit states' rounding (the step's number if None)."""
+    st = plan.state
+    dev = plan.table.device
+    if grad_scale is not None:
+        _arg(grad_scale, torch.float32, 1, "grad_scale", dev)
+    small = plan.bits == 8
+    rates = _AdamWRatesC(lr, beta1, beta2, eps, weight_decay, step, (step if seed is None else seed) & 0xffffffff)
+    _on(dev, _lib.qlora_adamw_step, "qlora_adamw_step", ctypes.byref(plan._c), plan.bits, st.m.data_ptr(), st.v.data_ptr(),
+        st.m_scales.data_ptr() if small else None, st.v_scales.data_ptr() if small else None,
+        grad_scale.data_ptr() if grad_scale is not None else None, ctypes.byref(rates))

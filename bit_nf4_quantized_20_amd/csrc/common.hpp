@@ -299,6 +299,110 @@ hipError_t launch_fp8_decode(const uint8_t* codes, const uint8_t* scales, int64_
                              int64_t T, const uint16_t* A, const uint16_t* B, int64_t r, float s, const float* u,
                              uint16_t* Y, hipStream_t st);
 
+// Root-mean-square norm (k_norm.hip): h = bf16(x + res) (res null: h = x, not
+// written), y = bf16(h rstd w), codes [T][Kp] and scale bytes of y as
+// launch_fp8_rows lays them out (pitch = fp8_row_pitch(T)); y, codes with
+// scales, and rstd may be null.  H % 64 == 0, 64 <= H <= kNormMaxCols.
+constexpr int64_t kNormMaxCols = 16384;
+struct NormFwd {
+  const uint16_t *x, *res;
+  const float* w;
+  int64_t T, pitch;
+  uint32_t H, Kp;
+  float eps;
+  uint16_t *h, *y;
+  uint8_t *codes, *scales;
+  float* rstd;
+};
+hipError_t launch_norm_fwd(const NormFwd& a, hipStream_t s);
+// Its gradient: dh (dres may be null) and, where part is given
+// (norm_bwd_parts(T, H) rows of H floats), dw.
+struct NormBwd {
+  const uint16_t *dy, *h, *dres;
+  const float *w, *rstd;
+  int64_t T;
+  uint32_t H;
+  uint16_t* dh;
+  float* part;
+};
+int64_t norm_bwd_parts(int64_t T, int64_t H);
+hipError_t launch_norm_bwd(const NormBwd& a, float* dw, hipStream_t s);
+
+// Cross entropy through a frozen output head W [V][H] (k_head.hip), a piece of
+// the vocabulary at a time: columns [v0, v0 + n) of the logits X W^T with the
+// piece's rows in bf16.  Per row the sum over the vocabulary but the label's
+// column is held as run_s 2^(kHeadCell run_c); a row's label is outside [0, V)
+// where it has none.
+constexpr int kHeadTile = 256;   // columns of the logits that one workgroup reduces
+constexpr float kHeadCell = 128.f;
+struct HeadPiece {
+  const uint16_t* X;      // [T][H]
+  int64_t T, H;
+  const uint16_t* W;      // [n][H], the piece's rows
+  int64_t v0, n;          // v0 a multiple of kHeadTile
+  const int64_t* labels;  // [T]
+  float* target;          // [T] the label's logit times log2 e, written by the piece that has it
+  uint16_t* E;            // [T][lde] bf16 2^(logit log2 e - kHeadCell c), or null; 0 at the label and behind n
+  int64_t lde;            // n rounded up to whole tiles
+  float *tile_c, *tile_s;  // [tiles of the piece][T]
+  // sums over the pieces before (first: none) and with this one, and the factor
+  // 2^(kHeadCell (c before - c now)) of what was accumulated before
+  bool first;
+  const float *c_in, *s_in;
+  float *c_out, *s_out, *factor;
+};
+hipError_t launch_head_logits(const HeadPiece& p, hipStream_t s);
+// the tiles' sums into the rows' and, with E, every row of E to its row's cell
+hipError_t launch_head_rows(const HeadPiece& p, hipStream_t s);
+// part [splits][T][H] fp32 = factor part (not first) + E W
+int head_splits(int64_t T, int64_t H, int64_t n);
+hipError_t launch_head_grad(const HeadPiece& p, float* part, int splits, hipStream_t s);
+// What is left: loss, lse (may be null) and, with dX, dX = dloss (sum of the
+// parts / total - (others / total) W_label).  The label's row of W in its own format.
+struct HeadWeight {
+  const uint16_t* w16;
+  const uint8_t *codes, *absmax_q;  // NF4 (absmax_q null: fp32 absmax), or 8-bit codes
+  const float* scale;
+  const uint8_t* scale8;            // 8-bit: block scales
+};
+struct HeadFinish {
+  int64_t T, H, V;
+  const int64_t* labels;
+  const float *target, *c, *s, *part, *dloss;
+  int splits;
+  HeadWeight W;
+  float *loss, *lse;
+  uint16_t* dX;
+};
+hipError_t launch_head_finish(const HeadFinish& f, hipStream_t s);
+
+// AdamW over many tensors (k_adamw.hip).  The tensors' elements are cut into
+// chunks of kAdamChunk; the table in device memory has one entry a chunk.
+constexpr int kAdamChunk = 2048;
+constexpr int kAdamBlock = 128;  // elements of a tensor that share a scale of the 8-bit states
+struct AdamChunk {
+  uint16_t* p; float* master; const float* g;  // p or master may be null, not both
+  int64_t state;  // the chunk's first element in m and v, a multiple of kAdamBlock
+  int32_t n, pad;
+};
+struct AdamTensor {
+  uint16_t* p; float* master; const float* g;
+  int64_t numel, chunk0, state0;
+};
+// writes the entries of count tensors
+hipError_t launch_adamw_plan(const AdamTensor* t, int64_t count, AdamChunk* table, hipStream_t s);
+struct AdamStep {
+  const AdamChunk* table;
+  int64_t chunks;
+  void *m, *v;
+  uint8_t *ms, *vs;         // 8-bit states: scale bytes
+  const float* grad_scale;  // one value, or null
+  float b1, c1, b2, c2;     // beta and 1 - beta
+  float rate, root, eps, decay;  // lr / (1 - b1^t), 1 / sqrt(1 - b2^t), eps, lr * weight decay
+  uint32_t key;             // hash of the seed
+};
+hipError_t launch_adamw(const AdamStep& a, bool bits8, hipStream_t s);
+
 // W_merged[m][n] = bf16(W_hat[m][n] + s * sum_j Bp[m][j] Atp[n][j]) for the
 // NF4 weight [out][in] (out % 64 == 0, in % 64 == 0); Bp [out][ldp] and Atp
 // [in][ldp] hold B and A^T zero-padded to rp (a multiple of 16) columns.

@@ -68,6 +68,36 @@ __device__ __forceinline__ bf16x8 lds_frag(const uint16_t* lds, int row, int chu
   return __builtin_bit_cast(bf16x8, v);
 }
 
+// Transposed weight tiles (K along W's rows) are stored K-row-major: row k
+// of W (a K index) holds the tile's BN columns, 16-byte chunk c of row k at
+// chunk c ^ tswz(k).  tswz(k) = 4 (k % 4) + (k / 4) % 4 keeps both accesses
+// conflict-free on the 64-bank LDS: a dequantize write (16 lanes, 16
+// consecutive rows, one chunk) lands in 16 distinct chunk slots, and a
+// transposed fragment read (32 lanes: 4 consecutive rows x 4 consecutive
+// chunks, 8 bytes per lane) covers 16 distinct slots.
+__device__ __forceinline__ int tswz(int k) { return 4 * (k & 3) + ((k >> 2) & 3); }
+
+// MFMA operand fragment of rows n = n0 .. n0 + 31 (n0 wave-uniform), K
+// sub-step j, from a transposed tile of BN columns: lane l holds n = n0 + l % 32
+// and k = 16 j + 8 (l / 32) + 0..7.  ds_read_b64_tr_b16 hands each group of
+// 16 lanes a 16 x 4 block transposed: lane i of the group supplies the address
+// of row i / 4 (of four consecutive rows) at columns 4 (i % 4) .. + 3, and
+// receives column i of the four rows.  Two such reads give the eight k.
+template <int BN>
+__device__ __forceinline__ bf16x8 lds_frag_tr(const uint16_t* lds, int n0, int j) {
+  typedef short v4s __attribute__((ext_vector_type(4)));
+  const int l = threadIdx.x & 63, i = l & 15, G = l >> 4;
+  const int n = n0 + 16 * (G & 1) + 4 * (i & 3);
+  v4s v[2];
+#pragma unroll
+  for (int s2 = 0; s2 < 2; ++s2) {
+    const int k = 16 * j + 8 * (G >> 1) + 4 * s2 + (i >> 2);
+    const int e = k * BN + (((n >> 3) ^ tswz(k)) << 3) + (n & 4);
+    v[s2] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        (__attribute__((address_space(3))) v4s*)(const_cast<uint16_t*>(lds) + e));
+  }
+  return __builtin_bit_cast(bf16x8, __builtin_shufflevector(v[0], v[1], 0, 1, 2, 3, 4, 5, 6, 7));
+}
 // XCD-aware tile order.  Workgroups are dispatched round-robin over the 8
 // XCDs (linear id % 8), and each XCD has its own L2.  The tiles are renumbered
 // so that XCD x runs a contiguous stretch of the tile sequence, and the

@@ -4,9 +4,12 @@
 // HIP call (so validation can be exercised on a machine without a GPU),
 // then checks once per device that the device is gfx950, then enqueues its
 // kernels on the caller's stream.
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstring>
+#include <memory>
+#include <new>
 
 #include "../../include/qlora.h"
 #include "common.hpp"
@@ -925,15 +928,21 @@ size_t qlora_fp8_workspace_bytes(int64_t T, int64_t in_features, int64_t out_fea
   return need > kMinWorkspace ? need : kMinWorkspace;
 }
 
-int qlora_fp8_linear_fwd(const qlora_fp8_weight* W, const qlora_bf16* X, int64_t T, const qlora_bf16* A,
-                         const qlora_bf16* B, int64_t r, float alpha, qlora_bf16* Y, void* ws, size_t ws_bytes,
-                         qlora_stream stream) {
+}  // extern "C"
+
+namespace {
+
+// codes, scales: X's rows, already quantized (NULL: they are quantized here).
+// X may then be missing where nothing reads it.
+int fp8_fwd_impl(const qlora_fp8_weight* W, const uint8_t* codes, const uint8_t* scales, const qlora_bf16* X, int64_t T,
+                 const qlora_bf16* A, const qlora_bf16* B, int64_t r, float alpha, qlora_bf16* Y, void* ws,
+                 size_t ws_bytes, qlora_stream stream) {
   if (int st = check_fp8_weight(W)) return st;
   const int64_t out = W->rows, in = W->cols;
   if (!fp8_shapes_ok(T, in, out, r)) return QLORA_ERR_SHAPE;
   if (r > 0 && (!A || !B)) return QLORA_ERR_NULL;
   if (r > 0 && (!aligned16(A) || !aligned16(B))) return QLORA_ERR_ALIGN;
-  if (T > 0 && (!X || !Y)) return QLORA_ERR_NULL;
+  if (T > 0 && (!Y || (!X && (codes == nullptr || r > 0 || fp8_small(T, in, false))))) return QLORA_ERR_NULL;
   if (!aligned16(X) || !aligned16(Y)) return QLORA_ERR_ALIGN;
   if (r > 0 && !std::isfinite(alpha)) return QLORA_ERR_VALUE;
   if (T == 0) return QLORA_OK;
@@ -968,7 +977,7 @@ int qlora_fp8_linear_fwd(const qlora_fp8_weight* W, const qlora_bf16* X, int64_t
     LoraFront f{};
     f.in = X; f.P = A; f.T = T; f.K = in; f.r = r; f.rp = rp;
     f.part = reinterpret_cast<float*>(base + lay.part);
-    f.rows = rows;
+    if (codes == nullptr) f.rows = rows;
     f.src = B; f.dst = b_pad; f.R = out; f.ldd = 2 * rp;
     e = launch_lora_front(f, s);
     if (e == hipSuccess)
@@ -976,7 +985,7 @@ int qlora_fp8_linear_fwd(const qlora_fp8_weight* W, const qlora_bf16* X, int64_t
     g.act1 = u_pad;
     g.wt1 = b_pad;
     g.lda1 = g.ldw1 = g.K1 = 2 * rp;
-  } else {
+  } else if (codes == nullptr) {
     e = launch_fp8_rows(rows, s);
   }
   g.M = T;
@@ -984,12 +993,30 @@ int qlora_fp8_linear_fwd(const qlora_fp8_weight* W, const qlora_bf16* X, int64_t
   g.scales = W->scales;
   g.rows = out;
   g.cols = in;
-  g.xq = base + lay.xq;
-  g.xs = base + lay.xs;
+  g.xq = codes != nullptr ? codes : base + lay.xq;
+  g.xs = codes != nullptr ? scales : base + lay.xs;
   g.C = Y;
   g.part = reinterpret_cast<float*>(base + lay.split);
   if (e == hipSuccess) e = launch_fp8_gemm(g, s);
   return launched(e);
+}
+
+}  // namespace
+
+extern "C" {
+
+int qlora_fp8_linear_fwd(const qlora_fp8_weight* W, const qlora_bf16* X, int64_t T, const qlora_bf16* A,
+                         const qlora_bf16* B, int64_t r, float alpha, qlora_bf16* Y, void* ws, size_t ws_bytes,
+                         qlora_stream stream) {
+  return fp8_fwd_impl(W, nullptr, nullptr, X, T, A, B, r, alpha, Y, ws, ws_bytes, stream);
+}
+
+int qlora_fp8_linear_fwd_rows(const qlora_fp8_weight* W, const uint8_t* codes, const uint8_t* scales,
+                              const qlora_bf16* X, int64_t T, const qlora_bf16* A, const qlora_bf16* B, int64_t r,
+                              float alpha, qlora_bf16* Y, void* ws, size_t ws_bytes, qlora_stream stream) {
+  if (T > 0 && (!codes || !scales)) return QLORA_ERR_NULL;
+  if (!aligned16(codes) || !aligned16(scales)) return QLORA_ERR_ALIGN;
+  return fp8_fwd_impl(W, codes, scales, X, T, A, B, r, alpha, Y, ws, ws_bytes, stream);
 }
 
 int qlora_fp8_linear_bwd(const qlora_fp8_weight* W, const qlora_bf16* X, const qlora_bf16* dY, int64_t T,
@@ -1207,6 +1234,395 @@ int qlora_moe_fwd(const qlora_nf4_weight* gate_up, const qlora_nf4_weight* down,
   a.H = static_cast<int>(hidden);
   a.I = static_cast<int>(inter);
   return launched(launch_moe(a, static_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"
+
+namespace {
+
+// ---------------------------------------------------------------- norm
+bool norm_shapes_ok(int64_t T, int64_t H) {
+  return T >= 0 && T < (int64_t(1) << 31) && H >= 64 && H <= kNormMaxCols && H % 64 == 0;
+}
+
+// ---------------------------------------------------------------- output head
+// Tokens of one round over the vocabulary, and the most logits (rows by columns)
+// of one piece: E, 2 bytes a logit, then stays within the 256 MiB last-level
+// cache between the two products, and the fp32 sums of dX are read and written
+// once in n columns of work.
+constexpr int64_t kHeadTokens = 4096, kHeadLogits = int64_t(1) << 26;
+// Weights of one piece that are written out in bf16.
+constexpr int64_t kHeadWeights = int64_t(1) << 26;
+constexpr int64_t kHeadMaxHidden = 16384, kHeadMaxVocab = int64_t(1) << 24;
+
+bool head_shapes_ok(int64_t T, int64_t V, int64_t H) {
+  return T >= 0 && T < (int64_t(1) << 31) && V >= 1 && V <= kHeadMaxVocab && H >= 64 && H <= kHeadMaxHidden &&
+         H % 64 == 0;
+}
+
+struct HeadLayout {
+  int64_t tokens, n;  // rows of a round, columns of a piece
+  int splits;
+  size_t w, e, part, tile_c, tile_s, target, c[2], s[2], factor, total;
+};
+HeadLayout head_layout(int64_t T, int64_t V, int64_t H, bool expand, bool grad) {
+  HeadLayout l{};
+  const int64_t rounds = T > 0 ? ceil_div(T, kHeadTokens) : 1;
+  l.tokens = rounds > 1 ? round_up(ceil_div(T, rounds), 256) : T;
+  const int64_t rows = l.tokens > 0 ? l.tokens : 1;
+  int64_t most = round_up(V, kHeadTile);
+  if (grad && most > kHeadLogits / rows) most = kHeadLogits / rows;
+  if (expand && most > kHeadWeights / H) most = kHeadWeights / H;
+  // the second product addresses a piece's rows with 32-bit offsets
+  if (grad && most > (int64_t(1) << 29) / H) most = (int64_t(1) << 29) / H;
+  most = most / kHeadTile * kHeadTile;
+  l.n = round_up(ceil_div(V, ceil_div(V, most)), kHeadTile);
+  const int64_t tiles = l.n / kHeadTile;
+  Carve c;
+  const size_t row = static_cast<size_t>(l.tokens) * 4;
+  l.w = c.take(expand ? static_cast<size_t>(l.n * H * 2) : 0);
+  if (grad) {
+    l.splits = head_splits(rows, H, l.n);
+    l.e = c.take(static_cast<size_t>(l.tokens * l.n * 2));
+    l.part = c.take(row * H * l.splits);
+  }
+  l.tile_c = c.take(row * tiles);
+  l.tile_s = c.take(row * tiles);
+  l.target = c.take(row);
+  for (int i = 0; i < 2; ++i) {
+    l.c[i] = c.take(row);
+    l.s[i] = c.take(row);
+  }
+  l.factor = c.take(row);
+  l.total = c.off;
+  return l;
+}
+
+int check_head(const qlora_head* W) {
+  if (!W) return QLORA_ERR_NULL;
+  const int given = (W->bf16 != nullptr) + (W->nf4 != nullptr) + (W->fp8 != nullptr);
+  if (given == 0) return QLORA_ERR_NULL;
+  if (given > 1) return QLORA_ERR_VALUE;
+  if (W->nf4 != nullptr) {
+    if (int st = check_weight(W->nf4)) return st;
+    if (W->nf4->rows != W->vocab || W->nf4->cols != W->hidden) return QLORA_ERR_SHAPE;
+  } else if (W->fp8 != nullptr) {
+    if (int st = check_fp8_weight(W->fp8)) return st;
+    if (W->fp8->rows != W->vocab || W->fp8->cols != W->hidden || !fp8_matrix_ok(W->vocab, W->hidden))
+      return QLORA_ERR_SHAPE;
+  } else if (!aligned16(W->bf16)) {
+    return QLORA_ERR_ALIGN;
+  }
+  return QLORA_OK;
+}
+
+// rows [v0, v0 + n) of the head in bf16 (v0 a multiple of 256)
+hipError_t head_piece(const qlora_head& W, int64_t v0, int64_t n, uint16_t* out, hipStream_t s) {
+  const int64_t H = W.hidden, at = v0 * H;
+  if (W.fp8 != nullptr)
+    return launch_fp8_dequantize(W.fp8->codes + at, W.fp8->scales + v0 / QLORA_FP8_BLOCK * ceil_div(H, QLORA_FP8_BLOCK), n,
+                                 H, out, s);
+  const qlora_nf4_weight& q = *W.nf4;
+  if (absmax_fp32(q)) return launch_nf4_dequantize_nodq(q.codes + at / 2, q.absmax_scale + at / 64, n * H, out, s);
+  return launch_nf4_dequantize(q.codes + at / 2, q.absmax_q + at / 64, q.absmax_scale + at / 16384, n * H, out, s);
+}
+
+int head_loss_impl(const qlora_head* W, const qlora_bf16* X, int64_t T, const int64_t* labels, const float* dloss,
+                   float* loss, float* lse, qlora_bf16* dX, bool grad, void* ws, size_t ws_bytes, qlora_stream stream) {
+  if (int st = check_head(W)) return st;
+  const int64_t V = W->vocab, H = W->hidden;
+  if (!head_shapes_ok(T, V, H)) return QLORA_ERR_SHAPE;
+  if (T == 0) return QLORA_OK;
+  if (!X || !labels || !loss || (grad && (!dloss || !dX))) return QLORA_ERR_NULL;
+  if (!aligned16(X) || !aligned16(labels) || !aligned16(loss) || !aligned16(lse) ||
+      (grad && (!aligned16(dloss) || !aligned16(dX))))
+    return QLORA_ERR_ALIGN;
+  const bool expand = W->bf16 == nullptr;
+  const HeadLayout lay = head_layout(T, V, H, expand, grad);
+  if (ws == nullptr || ws_bytes < lay.total) return QLORA_ERR_WORKSPACE;
+  if (!aligned16(ws)) return QLORA_ERR_ALIGN;
+  if (int st = check_device()) return st;
+
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  auto f32 = [&](size_t at) { return reinterpret_cast<float*>(base + at); };
+  hipError_t e = hipSuccess;
+  for (int64_t t0 = 0; t0 < T && e == hipSuccess; t0 += lay.tokens) {
+    HeadPiece p{};
+    p.X = X + t0 * H;
+    p.T = T - t0 < lay.tokens ? T - t0 : lay.tokens;
+    p.H = H;
+    p.labels = labels + t0;
+    p.target = f32(lay.target);
+    p.E = grad ? reinterpret_cast<uint16_t*>(base + lay.e) : nullptr;
+    p.tile_c = f32(lay.tile_c);
+    p.tile_s = f32(lay.tile_s);
+    p.factor = f32(lay.factor);
+    int turn = 0;
+    for (int64_t v0 = 0; v0 < V && e == hipSuccess; v0 += lay.n, turn ^= 1) {
+      p.v0 = v0;
+      p.n = V - v0 < lay.n ? V - v0 : lay.n;
+      p.lde = round_up(p.n, kHeadTile);
+      p.first = v0 == 0;
+      p.c_in = f32(lay.c[turn]);
+      p.s_in = f32(lay.s[turn]);
+      p.c_out = f32(lay.c[turn ^ 1]);
+      p.s_out = f32(lay.s[turn ^ 1]);
+      if (expand) {
+        uint16_t* w = reinterpret_cast<uint16_t*>(base + lay.w);
+        e = head_piece(*W, v0, p.n, w, s);
+        p.W = w;
+      } else {
+        p.W = W->bf16 + v0 * H;
+      }
+      if (e == hipSuccess) e = launch_head_logits(p, s);
+      if (e == hipSuccess) e = launch_head_rows(p, s);
+      if (e == hipSuccess && grad) e = launch_head_grad(p, f32(lay.part), lay.splits, s);
+    }
+    HeadFinish f{};
+    f.T = p.T;
+    f.H = H;
+    f.V = V;
+    f.labels = p.labels;
+    f.target = p.target;
+    f.c = f32(lay.c[turn]);
+    f.s = f32(lay.s[turn]);
+    f.loss = loss + t0;
+    f.lse = lse != nullptr ? lse + t0 : nullptr;
+    if (grad) {
+      f.part = f32(lay.part);
+      f.splits = lay.splits;
+      f.dloss = dloss + t0;
+      f.dX = dX + t0 * H;
+      f.W.w16 = W->bf16;
+      if (W->nf4 != nullptr) {
+        f.W.codes = W->nf4->codes;
+        f.W.absmax_q = absmax_fp32(*W->nf4) ? nullptr : W->nf4->absmax_q;
+        f.W.scale = W->nf4->absmax_scale;
+      } else if (W->fp8 != nullptr) {
+        f.W.codes = W->fp8->codes;
+        f.W.scale8 = W->fp8->scales;
+      }
+    }
+    if (e == hipSuccess) e = launch_head_finish(f, s);
+  }
+  return launched(e);
+}
+
+// ---------------------------------------------------------------- AdamW
+// state elements and chunks of n tensors; false: a size out of range
+bool adamw_sizes(const int64_t* numel, int64_t n, int64_t* state, int64_t* chunks) {
+  constexpr int64_t kMost = int64_t(1) << 32;  // elements over all tensors
+  if (n < 0 || n > QLORA_ADAMW_MAX_TENSORS || (n > 0 && !numel)) return false;
+  *state = *chunks = 0;
+  for (int64_t i = 0; i < n; ++i) {
+    if (numel[i] < 0 || numel[i] > kMost) return false;
+    *state += round_up(numel[i], kAdamBlock);
+    *chunks += ceil_div(numel[i], kAdamChunk);
+    if (*state > kMost) return false;
+  }
+  return true;
+}
+
+// whether two of the n ranges share a byte (they are sorted for it)
+struct AdamRange {
+  uintptr_t at, end;
+};
+bool overlap(AdamRange* r, int64_t n) {
+  std::sort(r, r + n, [](const AdamRange& a, const AdamRange& b) { return a.at < b.at; });
+  for (int64_t i = 1; i < n; ++i)
+    if (r[i].at < r[i - 1].end) return true;
+  return false;
+}
+// whether x shares a byte with one of the n sorted ranges, which are apart
+bool meets(const AdamRange* r, int64_t n, const AdamRange& x) {
+  const AdamRange* at = std::lower_bound(r, r + n, x, [](const AdamRange& a, const AdamRange& b) { return a.end <= b.at; });
+  return at != r + n && at->at < x.end;
+}
+
+}  // namespace
+
+extern "C" {
+
+int qlora_fp8_rows_bytes(int64_t T, int64_t cols, size_t* codes_bytes, size_t* scale_bytes) {
+  if (T < 0 || cols < 0 || cols % 64 != 0 || T >= (int64_t(1) << 31) || cols >= (int64_t(1) << 31)) return QLORA_ERR_SHAPE;
+  if (codes_bytes) *codes_bytes = static_cast<size_t>(T * round_up(cols, QLORA_FP8_BLOCK));
+  if (scale_bytes) *scale_bytes = fp8_row_scale_bytes(T, cols);
+  return QLORA_OK;
+}
+
+int qlora_rmsnorm_fwd(const qlora_bf16* x, const qlora_bf16* residual, const float* weight, int64_t T, int64_t H,
+                      float eps, qlora_bf16* h, qlora_bf16* y, uint8_t* codes, uint8_t* scales, float* rstd,
+                      qlora_stream stream) {
+  if (!norm_shapes_ok(T, H)) return QLORA_ERR_SHAPE;
+  if (!std::isfinite(eps) || eps < 0.f) return QLORA_ERR_VALUE;
+  if (T == 0) return QLORA_OK;
+  if (!x || !weight || (residual != nullptr) != (h != nullptr) || (codes != nullptr) != (scales != nullptr) ||
+      (!y && !codes))
+    return QLORA_ERR_NULL;
+  if (!aligned16(x) || !aligned16(residual) || !aligned16(weight) || !aligned16(h) || !aligned16(y) ||
+      !aligned16(codes) || !aligned16(scales) || !aligned16(rstd))
+    return QLORA_ERR_ALIGN;
+  if (int st = check_device()) return st;
+  NormFwd a{};
+  a.x = x;
+  a.res = residual;
+  a.w = weight;
+  a.T = T;
+  a.pitch = fp8_row_pitch(T);
+  a.H = static_cast<uint32_t>(H);
+  a.Kp = static_cast<uint32_t>(round_up(H, QLORA_FP8_BLOCK));
+  a.eps = eps;
+  a.h = h;
+  a.y = y;
+  a.codes = codes;
+  a.scales = scales;
+  a.rstd = rstd;
+  return launched(launch_norm_fwd(a, static_cast<hipStream_t>(stream)));
+}
+
+size_t qlora_rmsnorm_workspace_bytes(int64_t T, int64_t H) {
+  if (!norm_shapes_ok(T, H)) return 0;
+  const size_t need = T > 0 ? static_cast<size_t>(norm_bwd_parts(T, H) * H * 4) : 0;
+  return need > kMinWorkspace ? need : kMinWorkspace;
+}
+
+int qlora_rmsnorm_bwd(const qlora_bf16* dy, const qlora_bf16* h, const float* weight, const float* rstd,
+                      const qlora_bf16* dres, int64_t T, int64_t H, qlora_bf16* dh, float* dweight, void* ws,
+                      size_t ws_bytes, qlora_stream stream) {
+  if (!norm_shapes_ok(T, H)) return QLORA_ERR_SHAPE;
+  if (T > 0 && (!dy || !h || !weight || !rstd || !dh)) return QLORA_ERR_NULL;
+  if (!aligned16(dy) || !aligned16(h) || !aligned16(weight) || !aligned16(rstd) || !aligned16(dres) ||
+      !aligned16(dh) || !aligned16(dweight))
+    return QLORA_ERR_ALIGN;
+  if (T == 0 && !dweight) return QLORA_OK;
+  if (T > 0 && dweight && (ws == nullptr || ws_bytes < qlora_rmsnorm_workspace_bytes(T, H))) return QLORA_ERR_WORKSPACE;
+  if (T > 0 && dweight && !aligned16(ws)) return QLORA_ERR_ALIGN;
+  if (int st = check_device()) return st;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (T == 0) return launched(launch_fill_f32(dweight, H, 0.f, s));
+  NormBwd a{};
+  a.dy = dy;
+  a.h = h;
+  a.dres = dres;
+  a.w = weight;
+  a.rstd = rstd;
+  a.T = T;
+  a.H = static_cast<uint32_t>(H);
+  a.dh = dh;
+  a.part = dweight != nullptr ? static_cast<float*>(ws) : nullptr;
+  return launched(launch_norm_bwd(a, dweight, s));
+}
+
+size_t qlora_head_workspace_bytes(int64_t T, int64_t vocab, int64_t hidden, int expand, int grad) {
+  if (!head_shapes_ok(T, vocab, hidden)) return 0;
+  const size_t need = head_layout(T, vocab, hidden, expand != 0, grad != 0).total;
+  return need > kMinWorkspace ? need : kMinWorkspace;
+}
+
+int qlora_head_loss(const qlora_head* W, const qlora_bf16* X, int64_t T, const int64_t* labels, float* loss, float* lse,
+                    void* ws, size_t ws_bytes, qlora_stream stream) {
+  return head_loss_impl(W, X, T, labels, nullptr, loss, lse, nullptr, false, ws, ws_bytes, stream);
+}
+
+int qlora_head_loss_grad(const qlora_head* W, const qlora_bf16* X, int64_t T, const int64_t* labels, const float* dloss,
+                         float* loss, float* lse, qlora_bf16* dX, void* ws, size_t ws_bytes, qlora_stream stream) {
+  return head_loss_impl(W, X, T, labels, dloss, loss, lse, dX, true, ws, ws_bytes, stream);
+}
+
+int64_t qlora_adamw_state_len(const int64_t* numel, int64_t n) {
+  int64_t state, chunks;
+  return adamw_sizes(numel, n, &state, &chunks) ? state : -1;
+}
+
+size_t qlora_adamw_table_bytes(const int64_t* numel, int64_t n) {
+  int64_t state, chunks;
+  if (!adamw_sizes(numel, n, &state, &chunks)) return 0;
+  const size_t need = static_cast<size_t>(chunks) * sizeof(AdamChunk);
+  return need > kMinWorkspace ? need : kMinWorkspace;
+}
+
+int qlora_adamw_plan(const qlora_adamw_tensor* tensors, int64_t n, void* table, size_t table_bytes,
+                     qlora_adamw_table* out, qlora_stream stream) {
+  if (n < 0 || n > QLORA_ADAMW_MAX_TENSORS) return QLORA_ERR_SHAPE;
+  if (!out || !table || (n > 0 && !tensors)) return QLORA_ERR_NULL;
+  if (!aligned16(table)) return QLORA_ERR_ALIGN;
+  // (nothrow: an exception must not leave a C entry point)
+  std::unique_ptr<AdamTensor[]> list(new (std::nothrow) AdamTensor[n > 0 ? n : 1]);
+  std::unique_ptr<int64_t[]> numel(new (std::nothrow) int64_t[n > 0 ? n : 1]);
+  std::unique_ptr<AdamRange[]> written(new (std::nothrow) AdamRange[n > 0 ? 3 * n : 1]);
+  if (!list || !numel || !written) return QLORA_ERR_LAUNCH;
+  for (int64_t i = 0; i < n; ++i) numel[i] = tensors[i].numel;
+  int64_t state, chunks;
+  if (!adamw_sizes(numel.get(), n, &state, &chunks)) return QLORA_ERR_SHAPE;
+  int64_t ranges = 0;
+  int64_t chunk0 = 0, state0 = 0;
+  for (int64_t i = 0; i < n; ++i) {
+    const qlora_adamw_tensor& t = tensors[i];
+    if (t.numel > 0) {
+      if ((!t.param && !t.master) || !t.grad) return QLORA_ERR_NULL;
+      if (!aligned16(t.param) || !aligned16(t.master) || !aligned16(t.grad)) return QLORA_ERR_ALIGN;
+      const auto add = [&](const void* p, int64_t bytes) {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+        if (p != nullptr) written[ranges++] = AdamRange{at, at + static_cast<uintptr_t>(bytes)};
+      };
+      add(t.param, 2 * t.numel);
+      add(t.master, 4 * t.numel);
+    }
+    list[i] = AdamTensor{t.param, t.master, t.grad, t.numel, chunk0, state0};
+    chunk0 += ceil_div(t.numel, kAdamChunk);
+    state0 += round_up(t.numel, kAdamBlock);
+  }
+  if (overlap(written.get(), ranges)) return QLORA_ERR_VALUE;
+  for (int64_t i = 0; i < n; ++i) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(tensors[i].grad);
+    if (tensors[i].numel > 0 &&
+        meets(written.get(), ranges, AdamRange{at, at + 4 * static_cast<uintptr_t>(tensors[i].numel)}))
+      return QLORA_ERR_VALUE;
+  }
+  if (table_bytes < static_cast<size_t>(chunks) * sizeof(AdamChunk)) return QLORA_ERR_WORKSPACE;
+  if (int st = check_device()) return st;
+  if (const hipError_t e = launch_adamw_plan(list.get(), n, static_cast<AdamChunk*>(table), static_cast<hipStream_t>(stream));
+      e != hipSuccess)
+    return QLORA_ERR_LAUNCH;
+  *out = qlora_adamw_table{table, chunks, state};
+  return QLORA_OK;
+}
+
+int qlora_adamw_step(const qlora_adamw_table* table, int bits, void* m, void* v, uint8_t* m_scales, uint8_t* v_scales,
+                     const float* grad_scale, const qlora_adamw_rates* rates, qlora_stream stream) {
+  if (!table || !rates) return QLORA_ERR_NULL;
+  if (table->chunks < 0 || table->chunks >= (int64_t(1) << 31)) return QLORA_ERR_SHAPE;
+  if (bits != 32 && bits != 8) return QLORA_ERR_VALUE;
+  if (rates->step < 1 || !std::isfinite(rates->lr) || !std::isfinite(rates->weight_decay) ||
+      !(rates->eps >= 0.) || !std::isfinite(rates->eps) || !(rates->beta1 >= 0. && rates->beta1 < 1.) ||
+      !(rates->beta2 >= 0. && rates->beta2 < 1.))
+    return QLORA_ERR_VALUE;
+  if (table->chunks == 0) return QLORA_OK;
+  if (!table->table || !m || !v || (bits == 8 && (!m_scales || !v_scales))) return QLORA_ERR_NULL;
+  if (!aligned16(table->table) || !aligned16(m) || !aligned16(v) ||
+      (bits == 8 && (!aligned16(m_scales) || !aligned16(v_scales))) || (reinterpret_cast<uintptr_t>(grad_scale) & 3u) != 0)
+    return QLORA_ERR_ALIGN;
+  if (int st = check_device()) return st;
+  const double t = static_cast<double>(rates->step);
+  AdamStep a{};
+  a.table = static_cast<const AdamChunk*>(table->table);
+  a.chunks = table->chunks;
+  a.m = m;
+  a.v = v;
+  a.ms = m_scales;
+  a.vs = v_scales;
+  a.grad_scale = grad_scale;
+  a.b1 = static_cast<float>(rates->beta1);
+  a.c1 = static_cast<float>(1. - rates->beta1);
+  a.b2 = static_cast<float>(rates->beta2);
+  a.c2 = static_cast<float>(1. - rates->beta2);
+  a.rate = static_cast<float>(rates->lr / (1. - std::pow(rates->beta1, t)));
+  a.root = static_cast<float>(1. / std::sqrt(1. - std::pow(rates->beta2, t)));
+  a.eps = static_cast<float>(rates->eps);
+  a.decay = static_cast<float>(rates->lr * rates->weight_decay);
+  a.key = rates->seed;
+  return launched(launch_adamw(a, bits == 8, static_cast<hipStream_t>(stream)));
 }
 
 void nf4_codebook(float out[16]) {

@@ -505,6 +505,25 @@ int qlora_fp8_linear_fwd(const qlora_fp8_weight* W, const qlora_bf16* X, int64_t
                          qlora_stream stream);
 
 /*
+ * Quantized rows.  X_hat above as a caller may hold it, codes and scales of X
+ * [T, cols] (qlora_rmsnorm_fwd writes them):
+ *   codes   [T, Kp] e4m3, Kp = cols rounded up to 128, 0 behind cols
+ *   scales  [ceil(cols / 512), P, 4] bytes, P = T rounded up to 256: block b of
+ *           row t is byte ((b / 4) P + t) 4 + b % 4; rows from T on are not read
+ * qlora_fp8_rows_bytes: their sizes (host only; any output pointer may be NULL;
+ * SHAPE for negative sizes or cols % 64 != 0).
+ * qlora_fp8_linear_fwd_rows -- qlora_fp8_linear_fwd with the rows' codes at hand:
+ * the same Y bit for bit, without a pass over X to quantize it.  The codes have
+ * to be X's own.  X may be NULL with r = 0 where T > 16 or in > 8192 (up to 16
+ * tokens the layer reads X itself, which is no more than its codes' launch).
+ * Workspace and errors as qlora_fp8_linear_fwd.
+ */
+int qlora_fp8_rows_bytes(int64_t T, int64_t cols, size_t* codes_bytes, size_t* scale_bytes);
+int qlora_fp8_linear_fwd_rows(const qlora_fp8_weight* W, const uint8_t* codes, const uint8_t* scales,
+                              const qlora_bf16* X, int64_t T, const qlora_bf16* A, const qlora_bf16* B, int64_t r,
+                              float alpha, qlora_bf16* Y, void* ws, size_t ws_bytes, qlora_stream stream);
+
+/*
  * qlora_fp8_linear_bwd -- the gradients of the forward above with the
  * quantization of X taken as the identity, s = alpha/r:
  *   dX = dY_hat W_hat + s (dY B) A    [T, in]  bf16 (one rounding)
@@ -590,6 +609,161 @@ size_t qlora_moe_workspace_bytes(int64_t T, int64_t hidden, int64_t inter, int64
 int qlora_moe_fwd(const qlora_nf4_weight* gate_up, const qlora_nf4_weight* down, int64_t experts,
                   const qlora_bf16* X, int64_t T, const int32_t* ids, const float* weights, int64_t k,
                   qlora_bf16* Y, void* ws, size_t ws_bytes, qlora_stream stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Around the layers of a training step: the norm in front of them, the loss
+ * through the output head, the optimizer of the adapters.
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * qlora_rmsnorm_fwd -- root-mean-square norm of bf16 rows, after the residual's
+ * addition and with 8-bit rows for the layer behind it:
+ *   h    = bf16(x + residual)            [T, H] bf16 (residual NULL: h is x, and
+ *                                        the argument h must be NULL)
+ *   rstd = 1 / sqrt(mean h^2 + eps)      [T] fp32, or NULL
+ *   y    = bf16(h rstd weight)           [T, H] bf16, or NULL with codes
+ *   codes, scales: y as quantized rows (above), or both NULL
+ *   x, residual [T, H] bf16;  weight [H] fp32;  eps >= 0
+ *   H a multiple of 64, 64 .. 16384;  0 <= T < 2^31 (0 is a no-op)
+ * h may be x or residual themselves; otherwise outputs are apart from inputs.  The
+ * square sums are fp32: |h| below 2^60.  A row that holds an infinity or a NaN
+ * has a y of NaN where the formula says so; the other rows do not change.
+ * Errors: NULL, SHAPE, ALIGN, VALUE, DEVICE, LAUNCH.
+ */
+int qlora_rmsnorm_fwd(const qlora_bf16* x, const qlora_bf16* residual, const float* weight, int64_t T, int64_t H,
+                      float eps, qlora_bf16* h, qlora_bf16* y, uint8_t* codes, uint8_t* scales, float* rstd,
+                      qlora_stream stream);
+
+/*
+ * qlora_rmsnorm_bwd -- its gradients, with h and rstd of the forward and n = h
+ * rstd (the quantization of y taken as the identity):
+ *   dh      = bf16(dres + rstd (weight dy - n mean(weight dy n)))   [T, H] bf16,
+ *             the gradient of x and of residual alike
+ *   dweight = sum over the rows of dy n                             [H] fp32, or NULL
+ *   dy [T, H] bf16;  dres [T, H] bf16, the gradient that reaches h past the norm,
+ *   or NULL;  ws of ws_bytes >= qlora_rmsnorm_workspace_bytes(T, H), read and
+ *   needed with dweight only
+ * dh may be dy or dres themselves.  dweight is overwritten, added in a fixed
+ * order (bit-reproducible), 0 for T = 0.
+ * Errors: as the forward, and WORKSPACE.
+ */
+size_t qlora_rmsnorm_workspace_bytes(int64_t T, int64_t H);
+int qlora_rmsnorm_bwd(const qlora_bf16* dy, const qlora_bf16* h, const float* weight, const float* rstd,
+                      const qlora_bf16* dres, int64_t T, int64_t H, qlora_bf16* dh, float* dweight, void* ws,
+                      size_t ws_bytes, qlora_stream stream);
+
+/*
+ * A frozen output head [vocab, hidden], in one of the formats (the others NULL).
+ * NF4 and 8-bit weights are written out in bf16 a piece at a time; their rows and
+ * cols are vocab and hidden.
+ */
+typedef struct {
+  const qlora_bf16* bf16;
+  const qlora_nf4_weight* nf4;
+  const qlora_fp8_weight* fp8;
+  int64_t vocab, hidden;
+} qlora_head;
+
+/*
+ * qlora_head_loss -- softmax cross entropy of logits = X W^T, which are formed a
+ * piece of the vocabulary at a time and never stored:
+ *   loss [T] fp32 = lse - logit[label];   lse [T] fp32 = log sum exp logits, or NULL
+ * qlora_head_loss_grad -- the same, and the gradient of X for dloss [T] fp32, the
+ * gradient of each row's loss:
+ *   dX [T, hidden] bf16 = dloss (softmax(logits) W - W_label), one rounding
+ * The logits are formed once for both.  W is frozen and has no gradient.
+ *   X [T, hidden] bf16;  labels [T] int64: a label outside [0, vocab) is none (a
+ *   prompt, a padded row): loss 0 and a dX row of zeros, whatever the row holds
+ *   hidden a multiple of 64, 64 .. 16384;  1 <= vocab <= 2^24 (NF4, 8 bits: a
+ *   multiple of 64);  0 <= T < 2^31 (0 is a no-op)
+ *   ws  workspace of ws_bytes >= qlora_head_workspace_bytes(T, vocab, hidden,
+ *       expand, grad), expand: W is not bf16, grad: of the second call (scratch: no
+ *       initialisation, nothing kept between calls; calls that overlap in time
+ *       must not share one)
+ * fp32 accumulation; the softmax's terms meet W in bf16, the label's own in fp32, so that
+ * 1 - p of a row that is nearly sure keeps its digits.  A row with a logit of
+ * +inf (finite ones: below 2^127) or NaN has a loss, lse and dX of NaN; a logit of -inf counts for nothing.
+ * All outputs are bit-reproducible.
+ * Errors: NULL (also: no format given), VALUE (two formats), SHAPE, ALIGN,
+ * WORKSPACE, DEVICE, LAUNCH.
+ */
+size_t qlora_head_workspace_bytes(int64_t T, int64_t vocab, int64_t hidden, int expand, int grad);
+int qlora_head_loss(const qlora_head* W, const qlora_bf16* X, int64_t T, const int64_t* labels, float* loss, float* lse,
+                    void* ws, size_t ws_bytes, qlora_stream stream);
+int qlora_head_loss_grad(const qlora_head* W, const qlora_bf16* X, int64_t T, const int64_t* labels, const float* dloss,
+                         float* loss, float* lse, qlora_bf16* dX, void* ws, size_t ws_bytes, qlora_stream stream);
+
+/*
+ * AdamW over many tensors in one launch.  A tensor is a bf16 parameter, an fp32
+ * one (master), or both: an fp32 master and the bf16 copy that the layers read,
+ * written from it.  Its gradient is fp32 (dA, dB, dweight).  Of a bf16 parameter
+ * alone each step's result is rounded to nearest.
+ */
+#define QLORA_ADAMW_MAX_TENSORS 65536
+#define QLORA_ADAMW_BLOCK 128 /* elements of a tensor that share a scale of the 8-bit states */
+
+typedef struct {
+  qlora_bf16* param;  /* or NULL */
+  float* master;      /* or NULL, not both */
+  const float* grad;
+  int64_t numel;      /* >= 0 */
+} qlora_adamw_tensor;
+
+/* A plan: the tensors' addresses, cut into pieces of work, in device memory. */
+typedef struct {
+  const void* table;
+  int64_t chunks, state_len;
+} qlora_adamw_table;
+
+typedef struct {
+  double lr, beta1, beta2, eps, weight_decay; /* 0 <= beta < 1, eps >= 0 */
+  int64_t step;                               /* from 1 on */
+  uint32_t seed;                              /* of the 8-bit states' rounding */
+} qlora_adamw_rates;
+
+/*
+ * qlora_adamw_state_len: elements of m and of v for n tensors: each tensor's
+ * numel rounded up to 128, one after another (-1: a size out of range; at most
+ * 2^32 in all).  qlora_adamw_table_bytes: bytes of the plan's device memory (0:
+ * out of range).  Host only.
+ * qlora_adamw_plan: writes the plan of the n tensors (host array) into `table`
+ * (device memory, which the caller keeps for as long as the plan is used, like
+ * the tensors) and fills out.  Refused with VALUE: two tensors whose param or
+ * master share memory, or a gradient that shares memory with one.  No copy from
+ * the host: it can be captured.
+ */
+int64_t qlora_adamw_state_len(const int64_t* numel, int64_t n);
+size_t qlora_adamw_table_bytes(const int64_t* numel, int64_t n);
+int qlora_adamw_plan(const qlora_adamw_tensor* tensors, int64_t n, void* table, size_t table_bytes,
+                     qlora_adamw_table* out, qlora_stream stream);
+
+/*
+ * qlora_adamw_step -- one step over all tensors of a plan, t = rates->step:
+ *   g = grad_scale grad;   m = beta1 m + (1 - beta1) g;   v = beta2 v + (1 - beta2) g^2
+ *   p = p - lr weight_decay p - lr / (1 - beta1^t) m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+ * (p: master, or the bf16 parameter where there is none.)
+ *   bits = 32: m, v fp32 [state_len]
+ *   bits = 8:  m, v uint8 [state_len], e4m3 codes of m and of sqrt(v); m_scales,
+ *       v_scales uint8 [state_len / 128], one power of two per 128 elements of a tensor
+ *       as in the 8-bit format above (0 bytes everywhere: zero states).  A code is
+ *       floor(|x| / step + u) steps, step the distance of codes at |x|, u = (byte + 1/2) /
+ *       256 with a byte of a hash of (seed, element): its expectation is x, where
+ *       the nearest code would stand still under beta2 near 1; pass another seed
+ *       each step.  sqrt(v) that is not 0 keeps at least the smallest code.  The
+ *       step's own update takes m and v before that rounding.  A state that is not
+ *       finite becomes NaN, alone in its block.
+ *   state elements between a tensor's end and its next multiple of 128 are written as 0
+ *   grad_scale: one fp32 in device memory (a factor that clips the gradients'
+ *       norm), or NULL
+ * The numbers in rates are taken by value: a captured step repeats its t and seed.
+ * Two steps of one plan must not overlap in time.  An element's result depends
+ * on nothing but its own values and, in 8 bits, its block's.
+ * Errors: NULL, SHAPE, ALIGN, VALUE (bits, rates), DEVICE, LAUNCH.
+ */
+int qlora_adamw_step(const qlora_adamw_table* table, int bits, void* m, void* v, uint8_t* m_scales, uint8_t* v_scales,
+                     const float* grad_scale, const qlora_adamw_rates* rates, qlora_stream stream);
 
 #ifdef __cplusplus
 }

@@ -29,6 +29,9 @@ Modules:
     native    -- ctypes loader for the plain-C brute-force nearest-level search
     fp8       -- the 8-bit block format (e4m3, power-of-two scales) and its linear layer
     moe       -- the router with its gradient, and the expert layer
+    norm      -- the root-mean-square norm and its gradient
+    head      -- cross entropy through an output head and its gradient
+    adamw     -- the AdamW step, states in 32 or 8 bits
 
 Pins (what each part is checked against) live in tests/test_oracle_*.py.
 Parity unpinned: none of the functions here; the page figures that need
