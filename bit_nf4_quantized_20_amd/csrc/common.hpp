@@ -333,7 +333,8 @@ hipError_t launch_norm_bwd(const NormBwd& a, float* dw, hipStream_t s);
 // piece's rows in bf16.  Per row the sum over the vocabulary but the label's
 // column is held as run_s 2^(kHeadCell run_c); a row's label is outside [0, V)
 // where it has none.
-constexpr int kHeadTile = 256;   // columns of the logits that one workgroup reduces
+constexpr int kHeadTile = 256;   // columns of the logits a workgroup forms
+constexpr int kHeadCols = 128;   // columns that one wave reduces
 constexpr float kHeadCell = 128.f;
 struct HeadPiece {
   const uint16_t* X;      // [T][H]
@@ -344,7 +345,7 @@ struct HeadPiece {
   float* target;          // [T] the label's logit times log2 e, written by the piece that has it
   uint16_t* E;            // [T][lde] bf16 2^(logit log2 e - kHeadCell c), or null; 0 at the label and behind n
   int64_t lde;            // n rounded up to whole tiles
-  float *tile_c, *tile_s;  // [tiles of the piece][T]
+  float *tile_c, *tile_s;  // [lde / kHeadCols][T]
   // sums over the pieces before (first: none) and with this one, and the factor
   // 2^(kHeadCell (c before - c now)) of what was accumulated before
   bool first;

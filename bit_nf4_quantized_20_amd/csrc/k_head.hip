@@ -22,7 +22,7 @@
 // k_head_logits (X W^T, weight rows as the matrix cores' first operand, then the
 // softmax's part in the epilogue) and k_head_grad (E W, the weight read
 // K-row-major through transposing LDS loads) share one main loop: BM x 256 x 64
-// tiles, eight waves of BM/2 x 64, two LDS stages filled by copies straight from
+// tiles, four waves of BM/2 x 128, LDS stages filled by copies straight from
 // global memory, fragments of a sub-step read during the one before.
 #include <type_traits>
 
@@ -37,7 +37,7 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kInf = __builtin_inff();
-constexpr int kNW = 8, kBN = 256;
+constexpr int kNW = 4, kBN = 256, kWN = 128;  // waves (2 x 2), tile and wave columns
 
 // x 2^(kHeadCell d), d <= 0 a whole number of cells (two cells and more give 0
 // or, of an infinity or a NaN, what it was)
@@ -58,192 +58,301 @@ __device__ __forceinline__ void join(float& c, float& s, float c2, float s2) {
   }
 }
 
+// Tiles of 64 columns (K), copied straight from global memory into LDS, 1 KB a wave
+// instruction and whole 128-byte lines: in halves of lines the second-level cache gets
+// twice the requests and bounds the kernel (4096 x 4096 x 16128: 485 us).  live
+// false: the resource is empty, so that the copy reads nothing and writes zeros.
+//
+// Rows [row0, row0 + ROWS) of a K-contiguous matrix, as lds_frag reads them.
+template <int ROWS>
+struct RowTile {
+  static constexpr int kPerWave = ROWS / 8 / kNW;
+  const uint16_t* base;
+  int bytes;
+  uint32_t voff[kPerWave];
+  __device__ __forceinline__ void init(const uint16_t* p, int64_t ld, int64_t row0, int64_t rows, int wv, int lane) {
+    base = p + row0 * ld;
+    const int64_t n = (rows - row0) * ld * 2;
+    bytes = static_cast<int>(n < 0x7fffffff ? n : 0x7fffffff);
+#pragma unroll
+    for (int i = 0; i < kPerWave; ++i) {
+      const int row = (i * kNW + wv) * 8 + (lane >> 3);
+      voff[i] = static_cast<uint32_t>((row * ld + swz(row, lane & 7) * 8) * 2);
+    }
+  }
+  // pieces [first, first + count) of the kPerWave
+  __device__ __forceinline__ void load(uint16_t* lds, int wv, int k0, bool live, int first = 0, int count = kPerWave) const {
+    const __amdgpu_buffer_rsrc_t rs =
+        __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(base), 0, live ? bytes : 0, kBufferWord3);
+#pragma unroll
+    for (int i = first; i < first + count && i < kPerWave; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          rs, (__attribute__((address_space(3))) void*)(lds + (i * kNW + wv) * 512), 16, voff[i], live ? k0 * 2 : 0, 0, 0);
+  }
+};
+
 // K-row-major weight tile: 64 rows of W (K) by kBN columns from n0, swizzled by
 // tswz for lds_frag_tr.  A wave instruction copies two rows; lane L lands at
 // 16-byte chunk L % 32 of row L / 32 and loads the chunk that belongs there.
 // Columns past H read the next row (never stored), rows past the piece read 0:
-// the resource starts at the step's first row.
-struct DtlTileT {
+// the resource starts at the step's first row (a piece is below 2^31 bytes).
+struct ColTile {
   static constexpr int kPerWave = kBK / 2 / kNW;
   const uint16_t* base;
-  int64_t H, rows;
+  int pitch, bytes;
   uint32_t voff[kPerWave];
-  __device__ __forceinline__ void init(const uint16_t* W, int64_t ld, int64_t n0, int64_t nrows, int wv, int lane) {
+  __device__ __forceinline__ void init(const uint16_t* W, int64_t ld, int64_t n0, int64_t rows, int wv, int lane) {
     base = W;
-    H = ld;
-    rows = nrows;
+    pitch = static_cast<int>(ld * 2);
+    bytes = static_cast<int>(rows * ld * 2);
 #pragma unroll
     for (int i = 0; i < kPerWave; ++i) {
       const int k = (i * kNW + wv) * 2 + (lane >> 5);
       voff[i] = static_cast<uint32_t>((k * ld + n0 + ((lane & 31) ^ tswz(k)) * 8) * 2);
     }
   }
-  __device__ __forceinline__ void load(uint16_t* lds, int wv, int64_t k0) const {
-    const __amdgpu_buffer_rsrc_t rs = rows_rsrc(base, H, k0, rows, 2);
+  __device__ __forceinline__ void load(uint16_t* lds, int wv, int k0, bool live, int first = 0, int count = kPerWave) const {
+    const int64_t at = static_cast<int64_t>(live ? k0 : 0) * pitch;
+    const int64_t left = live && at < bytes ? bytes - at : 0;
+    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<uint8_t*>(reinterpret_cast<const uint8_t*>(base) + at), 0, static_cast<int>(left), kBufferWord3);
 #pragma unroll
-    for (int i = 0; i < kPerWave; ++i)
+    for (int i = first; i < first + count && i < kPerWave; ++i)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
           rs, (__attribute__((address_space(3))) void*)(lds + (i * kNW + wv) * 512), 16, voff[i], 0, 0, 0);
   }
 };
 
+// Fragments of v_mfma_f32_16x16x32_bf16: lane l holds row l % 16 and the eight k from
+// 32 j + 8 (l / 16) on.  (This shape and not 32 x 32 x 16: per product it moves half
+// of the accumulators and draws less power, which is what bounds the matrix
+// cores on random operands: 2050 against 1765 TFLOP/s of nothing but matrix instructions.)
+__device__ __forceinline__ bf16x8 row_frag(const uint16_t* lds, int row0, int j) {
+  const int l = threadIdx.x & 63;
+  return lds_frag(lds, row0 + (l & 15), 4 * j + (l >> 4));
+}
+// of columns n0 .. n0 + 15 of a ColTile: each group of 16 lanes gets the transposed
+// blocks of its eight k (as lds_frag_tr)
+__device__ __forceinline__ bf16x8 col_frag(const uint16_t* lds, int n0, int j) {
+  typedef short v4s __attribute__((ext_vector_type(4)));
+  const int l = threadIdx.x & 63, i = l & 15, n = n0 + 4 * (i & 3);
+  v4s v[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int k = 32 * j + 8 * (l >> 4) + 4 * h + (i >> 2);
+    v[h] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        (__attribute__((address_space(3))) v4s*)(const_cast<uint16_t*>(lds) + k * kBN + (((n >> 3) ^ tswz(k)) << 3) + (n & 4)));
+  }
+  return __builtin_bit_cast(bf16x8, __builtin_shufflevector(v[0], v[1], 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
 // acc[a][c] += weight fragments times activation fragments over K-steps [k0,
-// k0 + steps); acc[a][c][e] holds row m = wm BM/2 + 32 c + lane % 32 of the
-// tile and column n = 64 wn + 32 a + 8 (e / 4) + 4 (lane / 32) + e % 4.
+// k0 + steps) of 64; acc[a][c][i] holds row m = wm BM/2 + 16 c + lane % 16 of the
+// tile and column n = 128 wn + 16 a + 4 (lane / 16) + i.
+//
+// Two LDS stages of activations and three of weights, each an array of its own and
+// its index a compile-time constant, so that the compiler sees that the copies into one
+// stage do not alias the fragment reads of another.  A step is two sub-steps of FN = 8
+// groups of matrix instructions, one group per weight fragment.  Fragments are read
+// ahead: a weight's six groups before its use, into the register of one that is used
+// up, the activations' under the middle of the sub-step before.  After group 1 of the
+// second sub-step all of the step's fragments have been read and a barrier frees its
+// stages; it also waits for what the next step reads.  The copies of two steps on
+// (activations) go out behind it and have a sub-step to land, those of three steps on
+// (weights) under the next sub-step and have three.
 template <int BM, class TW>
 struct HeadLoop {
-  static constexpr int FN = 2, FM = BM / 64;
-  static constexpr bool kTr = std::is_same_v<TW, DtlTileT>;
-  typedef bf16x8 Frags[FN + FM];
-  uint16_t *s_act[2], *s_wt[2];
-  int wv, lane;
+  static constexpr int FN = kWN / 16, FM = BM / 32;
+  static_assert(FN == 8, "the order of the reads below");
+  static constexpr bool kTr = std::is_same_v<TW, ColTile>;
+  typedef f32x4 Acc[FN][FM];
+  uint16_t *s_act[2], *s_wt[3];
+  int wv;
 
-  __device__ __forceinline__ void read(Frags& f, int b, int j) const {
-    const int half = lane >> 5, r32 = lane & 31, chunk = 2 * j + half, wm = wv & 1, wn = wv >> 1;
-#pragma unroll
-    for (int a = 0; a < FN; ++a) {
-      if constexpr (kTr) f[a] = lds_frag_tr<kBN>(s_wt[b], wn * 64 + a * 32, j);
-      else f[a] = lds_frag(s_wt[b], wn * 64 + a * 32 + r32, chunk);
-    }
-#pragma unroll
-    for (int c = 0; c < FM; ++c) f[FN + c] = lds_frag(s_act[b], wm * (BM / 2) + c * 32 + r32, chunk);
+  __device__ __forceinline__ bf16x8 act(int b, int j, int i) const {
+    return row_frag(s_act[b], (wv & 1) * (BM / 2) + i * 16, j);
   }
-  __device__ __forceinline__ static void mfmas(f32x16 (&acc)[FN][FM], const Frags& f) {
+  __device__ __forceinline__ bf16x8 wt(int b, int j, int i) const {
+    const int n0 = (wv >> 1) * kWN + i * 16;
+    if constexpr (kTr) return col_frag(s_wt[b], n0, j);
+    else return row_frag(s_wt[b], n0, j);
+  }
+  // In assembly, so that the accumulators stay where they are: of the builtin's the
+  // compiler moves some at every turn of the loop.  It knows what the operands wait
+  // for, but not when the result is there: settle() before the first and after the last.
+  __device__ __forceinline__ static void mfma(f32x4& acc, const bf16x8& w, const bf16x8& x) {
+    asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(w), "v"(x));
+  }
+  __device__ __forceinline__ static void settle(Acc& acc) {
 #pragma unroll
     for (int a = 0; a < FN; ++a)
 #pragma unroll
-      for (int c = 0; c < FM; ++c)
-        acc[a][c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f[a], f[FN + c], acc[a][c], 0, 0, 0);
-    // each matrix instruction followed by at most two LDS reads, a copy and
-    // address arithmetic
+      for (int c = 0; c < FM; ++c) asm volatile("" : "+a"(acc[a][c]));
+    asm volatile("s_nop 15\n\ts_nop 15");
 #pragma unroll
-    for (int i = 0; i < FN * FM; ++i) {
-      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-      __builtin_amdgcn_sched_group_barrier(0x100, kTr ? 2 : 1, 0);
-      __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
-      __builtin_amdgcn_sched_group_barrier(0x002, 8, 0);
-    }
-    __builtin_amdgcn_sched_barrier(0);
+    for (int a = 0; a < FN; ++a)
+#pragma unroll
+      for (int c = 0; c < FM; ++c) asm volatile("" : "+a"(acc[a][c]));
   }
-  __device__ __forceinline__ void run(f32x16 (&acc)[FN][FM], const DtlTile<BM, kNW>& ta, const TW& tw, int64_t k0,
-                                      int64_t steps) const {
-    const int64_t last = steps - 1;
-    auto copy = [&](int64_t e, int b) {  // a step past the end copies the last one again
-      const int64_t k = (k0 + (e < last ? e : last)) * kBK;
-      ta.load(s_act[b], wv, k);
-      tw.load(s_wt[b], wv, k);
+  // (not __syncthreads, which would wait for every copy)
+  __device__ __forceinline__ static void barrier() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  }
+  static constexpr int wait_code(int copies) { return (copies & 15) | ((copies >> 4) << 14) | 0x70; }  // lgkmcnt(0) too
+
+  __device__ __forceinline__ void run(Acc& acc, const RowTile<BM>& ta, const TW& tw, int k0, int steps) const {
+    constexpr int kA = RowTile<BM>::kPerWave, kW = TW::kPerWave;  // copies of a wave and step
+    auto copy_a = [&](int e, int b, int first, int count) {
+      ta.load(s_act[b], wv, (k0 + e) * kBK, e < steps, first, count);
     };
-    copy(0, 0);
-    __builtin_amdgcn_s_waitcnt(0);
-    __syncthreads();
-    Frags f0, f1;
-    read(f0, 0, 0);
-    auto step = [&](int64_t e, auto bc) {
-      constexpr int B = decltype(bc)::value;
-      copy(e + 1, B ^ 1);
-      __builtin_amdgcn_s_setprio(1);
-      read(f1, B, 1);
-      mfmas(acc, f0);
-      read(f0, B, 2);
-      mfmas(acc, f1);
-      read(f1, B, 3);
-      mfmas(acc, f0);
-      mfmas(acc, f1);
-      __builtin_amdgcn_s_setprio(0);
-      __builtin_amdgcn_s_waitcnt(0);
-      __syncthreads();
-      read(f0, B ^ 1, 0);
+    auto copy_w = [&](int e, int b, int first, int count) {
+      tw.load(s_wt[b], wv, (k0 + e) * kBK, e < steps, first, count);
     };
-    int64_t e = 0;
-    for (; e + 2 <= steps; e += 2) {
-      step(e, std::integral_constant<int, 0>{});
-      step(e + 1, std::integral_constant<int, 1>{});
+    copy_a(0, 0, 0, kA);
+    copy_w(0, 0, 0, kW);
+    copy_w(1, 1, 0, kW);
+    copy_a(1, 1, 0, kA);
+    __builtin_amdgcn_s_waitcnt(wait_code(kA + kW));
+    barrier();
+    bf16x8 fw[FN], fa[2][FM];
+#pragma unroll
+    for (int i = 0; i < 6; ++i) fw[i] = wt(0, 0, i);
+#pragma unroll
+    for (int i = 0; i < FM; ++i) fa[0][i] = act(0, 0, i);
+    settle(acc);
+    // step e; A, W: its stages
+    auto step = [&](int e, auto ac, auto wc) {
+      constexpr int A = decltype(ac)::value, W = decltype(wc)::value, NA = A ^ 1, NW = (W + 1) % 3;
+      constexpr int kPer = (FM + 3) / 4, kWG = (kW + FN - 1) / FN, kAG = (kA + 3) / 4;
+#pragma unroll
+      for (int g = 0; g < FN; ++g) {
+        if (g < 2) fw[g + 6] = wt(W, 0, g + 6);
+        else fw[g - 2] = wt(W, 1, g - 2);
+        if (g >= 2 && g < 6)
+#pragma unroll
+          for (int i = (g - 2) * kPer; i < (g - 1) * kPer && i < FM; ++i) fa[1][i] = act(A, 1, i);
+        copy_w(e + 2, (W + 2) % 3, g * kWG, kWG);
+#pragma unroll
+        for (int c = 0; c < FM; ++c) mfma(acc[g][c], fw[g], fa[0][c]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+#pragma unroll
+      for (int g = 0; g < FN; ++g) {
+        if (g == 0) {
+          fw[6] = wt(W, 1, 6);
+          fw[7] = wt(W, 1, 7);
+        }
+        if (g == 2) {
+          __builtin_amdgcn_s_waitcnt(wait_code(kW));
+          barrier();
+        }
+        if (g >= 2) fw[g - 2] = wt(NW, 0, g - 2);
+        if (g >= 2 && g < 6)
+#pragma unroll
+          for (int i = (g - 2) * kPer; i < (g - 1) * kPer && i < FM; ++i) fa[0][i] = act(NA, 0, i);
+        if (g >= 4) copy_a(e + 2, A, (g - 4) * kAG, kAG);
+#pragma unroll
+        for (int c = 0; c < FM; ++c) mfma(acc[g][c], fw[g], fa[1][c]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+    using I0 = std::integral_constant<int, 0>;
+    using I1 = std::integral_constant<int, 1>;
+    using I2 = std::integral_constant<int, 2>;
+    for (int e = 0; e < steps; e += 6) {
+      step(e, I0{}, I0{});
+      step(e + 1, I1{}, I1{});
+      step(e + 2, I0{}, I2{});
+      step(e + 3, I1{}, I0{});
+      step(e + 4, I0{}, I1{});
+      step(e + 5, I1{}, I2{});
     }
-    if (e < steps) step(e, std::integral_constant<int, 0>{});
+    settle(acc);
+    __builtin_amdgcn_s_waitcnt(0);  // copies of zeros behind the last step
   }
 };
 
 template <int FN, int FM>
-__device__ __forceinline__ void clear(f32x16 (&acc)[FN][FM]) {
+__device__ __forceinline__ void clear(f32x4 (&acc)[FN][FM]) {
 #pragma unroll
   for (int a = 0; a < FN; ++a)
 #pragma unroll
-    for (int c = 0; c < FM; ++c)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) acc[a][c][e] = 0.f;
+    for (int c = 0; c < FM; ++c) acc[a][c] = f32x4{0.f, 0.f, 0.f, 0.f};
 }
 
 }  // namespace
 
-template <int BM>
-__global__ __launch_bounds__(512, 1) void k_head_logits(HeadPiece p) {
-  constexpr int FN = 2, FM = BM / 64, WM = BM / 2;
-  __shared__ __attribute__((aligned(1024))) uint16_t s_act0[BM * kBK];
-  __shared__ __attribute__((aligned(1024))) uint16_t s_act1[BM * kBK];
-  __shared__ __attribute__((aligned(1024))) uint16_t s_wt0[kBN * kBK];
-  __shared__ __attribute__((aligned(1024))) uint16_t s_wt1[kBN * kBK];
-  __shared__ float s_max[4][BM], s_sum[4][BM];
+// kE: with E (the gradient's call); else the sums alone.
+template <int BM, bool kE>
+__global__ __launch_bounds__(256, 1) void k_head_logits(HeadPiece p) {
+  constexpr int FN = kWN / 16, FM = BM / 32, WM = BM / 2;
+  __shared__ __attribute__((aligned(1024))) uint16_t s_a0[BM * kBK], s_a1[BM * kBK];
+  __shared__ __attribute__((aligned(1024))) uint16_t s_w0[kBN * kBK], s_w1[kBN * kBK], s_w2[kBN * kBK];
 
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wm = wv & 1, wn = wv >> 1, r32 = lane & 31, half = lane >> 5;
+  const int wm = wv & 1, wn = wv >> 1, r16 = lane & 15, quarter = lane >> 4;
   int64_t mt, nt;
   xcd_tile(gridDim.x, gridDim.y, mt, nt);
   const int64_t m0 = mt * BM, n0 = nt * kBN;
 
-  f32x16 acc[FN][FM];
+  f32x4 acc[FN][FM];
   clear(acc);
   {
-    using TW = DtlTile<kBN, kNW>;
-    DtlTile<BM, kNW> ta;
+    using TW = RowTile<kBN>;
+    RowTile<BM> ta;
     TW tw;
     ta.init(p.X, p.H, m0, p.T, wv, lane);
     tw.init(p.W, p.H, n0, p.n, wv, lane);
-    HeadLoop<BM, TW>{{s_act0, s_act1}, {s_wt0, s_wt1}, wv, lane}.run(acc, ta, tw, 0, p.H / kBK);
+    HeadLoop<BM, TW>{{s_a0, s_a1}, {s_w0, s_w1, s_w2}, wv}.run(acc, ta, tw, 0, static_cast<int>(p.H / kBK));
   }
 
-  // columns behind the vocabulary count as -inf
-  const int64_t left = p.n - n0 - wn * 64;  // valid columns from this wave's first
-  if (left < 64) {
+  // Every wave reduces its own 128 columns; E goes to LDS as a BM/2 x 128 block a
+  // wave (as large as a stage of activations), rows of sixteen 16-byte pieces, piece k
+  // of row r at slot k ^ (r % 16).
+  uint16_t* const s_e = wv == 0 ? s_w0 : wv == 1 ? s_w1 : wv == 2 ? s_w2 : s_a0;
+  const int64_t left = p.n - n0 - wn * kWN;  // valid columns from this wave's first; behind them -inf
+  const int64_t block = nt * 2 + wn;
+  __syncthreads();  // every wave is done reading the stages
+#pragma unroll
+  for (int c = 0; c < FM; ++c) {
+    const int row = c * 16 + r16;
+    const int64_t m = m0 + wm * WM + row;
+    float s[FN][4];
 #pragma unroll
     for (int a = 0; a < FN; ++a)
 #pragma unroll
-      for (int c = 0; c < FM; ++c)
-#pragma unroll
-        for (int e = 0; e < 16; ++e)
-          if (32 * a + 8 * (e >> 2) + 4 * half + (e & 3) >= left) acc[a][c][e] = -kInf;
-  }
-#pragma unroll
-  for (int c = 0; c < FM; ++c) {
-    const int row = wm * WM + c * 32 + r32;
-    const int64_t m = m0 + row;
-    const int64_t at = m < p.T ? p.labels[m] - p.v0 - n0 - wn * 64 : -1;
-    if (__any(at >= 0 && at < 64)) {  // the label's logit goes aside
+      for (int i = 0; i < 4; ++i) s[a][i] = acc[a][c][i];
+    if (left < kWN) {
 #pragma unroll
       for (int a = 0; a < FN; ++a)
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-          if (at == 32 * a + 8 * (e >> 2) + 4 * half + (e & 3)) {
-            if (at < left) p.target[m] = acc[a][c][e] * kLog2e;
-            acc[a][c][e] = -kInf;
-          }
+        for (int i = 0; i < 4; ++i)
+          if (16 * a + 4 * quarter + i >= left) s[a][i] = -kInf;
+    }
+    const int64_t at = m < p.T ? p.labels[m] - p.v0 - n0 - wn * kWN : -1;
+    const bool here = at >= 0 && at < kWN && at < left;
+    if (__any(here)) {  // the label's logit goes aside
+      float target = 0.f;
+      const int mine = here ? static_cast<int>(at) - 4 * quarter : -1;
+#pragma unroll
+      for (int a = 0; a < FN; ++a)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const bool hit = mine == 16 * a + i;
+          target = hit ? s[a][i] : target;
+          s[a][i] = hit ? -kInf : s[a][i];
+        }
+      if (here && ((at >> 2) & 3) == quarter) p.target[m] = target * kLog2e;
     }
     float top = -kInf;
 #pragma unroll
     for (int a = 0; a < FN; ++a)
 #pragma unroll
-      for (int e = 0; e < 16; ++e) top = fmaxf(top, acc[a][c][e]);
+      for (int i = 0; i < 4; ++i) top = fmaxf(top, s[a][i]);
+    top = fmaxf(top, __shfl_xor(top, 16));
     top = fmaxf(top, __shfl_xor(top, 32));
-    if (half == 0) s_max[wn][row] = top;
-  }
-  __syncthreads();  // also: every wave is done reading the stages
-  // this wave's 128 x 64 block of E in LDS, rows of eight 16-byte pieces, piece k
-  // of row r at slot k ^ (r % 8)
-  uint16_t* const s_e = (wv < 2 ? s_act0 : wv < 4 ? s_act1 : wv < 6 ? s_wt0 : s_wt1) + (wv & 1) * (WM * 64);
-#pragma unroll
-  for (int c = 0; c < FM; ++c) {
-    const int row = wm * WM + c * 32 + r32;
-    const int64_t m = m0 + row;
-    const float top = fmaxf(fmaxf(s_max[0][row], s_max[1][row]), fmaxf(s_max[2][row], s_max[3][row]));
     float cell = top == -kInf ? -kInf : cell_of(top * kLog2e);
     if (!p.first && m < p.T) cell = fmaxf(cell, p.c_in[m]);
     const float ref = cell == -kInf ? 0.f : cell * kHeadCell;
@@ -256,38 +365,36 @@ __global__ __launch_bounds__(512, 1) void k_head_logits(HeadPiece p) {
 #pragma unroll
       for (int a = 0; a < FN; ++a)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) acc[a][c][e] *= kLog2e;
+        for (int i = 0; i < 4; ++i) s[a][i] *= kLog2e;
     }
     float sum = 0.f;
 #pragma unroll
-    for (int a = 0; a < FN; ++a)
+    for (int a = 0; a < FN; ++a) {
+      float e[4];
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        float e[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[a][c][4 * g + i], scale, -ref));
-          sum += e[i];
-        }
-        if (p.E != nullptr)
-          *reinterpret_cast<u32x2*>(s_e + (c * 32 + r32) * 64 + (((4 * a + g) ^ (row & 7)) * 8) + 4 * half) =
-              u32x2{pack_bf16x2(e[0], e[1]), pack_bf16x2(e[2], e[3])};
+      for (int i = 0; i < 4; ++i) {
+        e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[a][i], scale, -ref));
+        sum += e[i];
       }
+      if constexpr (kE)
+        *reinterpret_cast<u32x2*>(s_e + row * kWN + (((2 * a + (quarter >> 1)) ^ r16) * 8) + 4 * (quarter & 1)) =
+            u32x2{pack_bf16x2(e[0], e[1]), pack_bf16x2(e[2], e[3])};
+    }
+    sum += __shfl_xor(sum, 16);
     sum += __shfl_xor(sum, 32);
-    if (half == 0) s_sum[wn][row] = sum;
-    if (wn == 0 && half == 0 && m < p.T) p.tile_c[nt * p.T + m] = cell;
+    if (quarter == 0 && m < p.T) {
+      p.tile_c[block * p.T + m] = cell;
+      p.tile_s[block * p.T + m] = sum;
+    }
   }
-  __syncthreads();
-  if (threadIdx.x < BM && m0 + threadIdx.x < p.T)
-    p.tile_s[nt * p.T + m0 + threadIdx.x] = s_sum[0][threadIdx.x] + s_sum[1][threadIdx.x] + s_sum[2][threadIdx.x] +
-                                            s_sum[3][threadIdx.x];
-  if (p.E == nullptr) return;
+  if constexpr (!kE) return;
+  __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): this wave's block is in LDS
 #pragma unroll
-  for (int i = 0; i < WM / 8; ++i) {
-    const int row = 8 * i + (lane >> 3), piece = lane & 7;
+  for (int i = 0; i < WM / 4; ++i) {
+    const int row = 4 * i + (lane >> 4), piece = lane & 15;
     const int64_t m = m0 + wm * WM + row;
-    const u32x4 v = *reinterpret_cast<const u32x4*>(s_e + row * 64 + ((piece ^ (row & 7)) * 8));
-    if (m < p.T) *reinterpret_cast<u32x4*>(p.E + m * p.lde + n0 + wn * 64 + 8 * piece) = v;
+    const u32x4 v = *reinterpret_cast<const u32x4*>(s_e + row * kWN + ((piece ^ (row & 15)) * 8));
+    if (m < p.T) *reinterpret_cast<u32x4*>(p.E + m * p.lde + n0 + wn * kWN + 8 * piece) = v;
   }
 }
 
@@ -299,7 +406,7 @@ __global__ __launch_bounds__(256) void k_head_rows(HeadPiece p) {
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
   const int64_t m = static_cast<int64_t>(blockIdx.x) * 64 + lane;
   const bool live = m < p.T;
-  const int tiles = static_cast<int>(ceil_div(p.n, kHeadTile));
+  const int tiles = static_cast<int>(p.lde / kHeadCols);
   float c = -kInf, s = 0.f;
   for (int t = wv; t < tiles; t += 16) {
     float tc[4], ts[4];
@@ -333,61 +440,56 @@ __global__ __launch_bounds__(256) void k_head_rows(HeadPiece p) {
       const int l = __builtin_ctzll(todo);
       todo &= todo - 1;
       const float d = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, tc - c), l));
-      u32x2* at = reinterpret_cast<u32x2*>(p.E + (static_cast<int64_t>(blockIdx.x) * 64 + l) * p.lde +
-                                           static_cast<int64_t>(t) * kHeadTile + 4 * lane);
-      const u32x2 v = *at;
-      *at = u32x2{pack_bf16x2(down_cells(bf16_lo(v[0]), d), down_cells(bf16_hi(v[0]), d)),
-                  pack_bf16x2(down_cells(bf16_lo(v[1]), d), down_cells(bf16_hi(v[1]), d))};
+      uint32_t* at = reinterpret_cast<uint32_t*>(p.E + (static_cast<int64_t>(blockIdx.x) * 64 + l) * p.lde +
+                                                 static_cast<int64_t>(t) * kHeadCols + 2 * lane);
+      const uint32_t v = *at;
+      *at = pack_bf16x2(down_cells(bf16_lo(v), d), down_cells(bf16_hi(v), d));
     }
   }
 }
 
 template <int BM>
-__global__ __launch_bounds__(512, 1) void k_head_grad(HeadPiece p, float* part, int64_t ks) {
-  constexpr int FN = 2, FM = BM / 64, WM = BM / 2;
-  __shared__ __attribute__((aligned(1024))) uint16_t s_act0[BM * kBK];
-  __shared__ __attribute__((aligned(1024))) uint16_t s_act1[BM * kBK];
-  __shared__ __attribute__((aligned(1024))) uint16_t s_wt0[kBN * kBK];
-  __shared__ __attribute__((aligned(1024))) uint16_t s_wt1[kBN * kBK];
+__global__ __launch_bounds__(256, 1) void k_head_grad(HeadPiece p, float* part, int ks) {
+  constexpr int FN = kWN / 16, FM = BM / 32, WM = BM / 2;
+  __shared__ __attribute__((aligned(1024))) uint16_t s_a0[BM * kBK], s_a1[BM * kBK];
+  __shared__ __attribute__((aligned(1024))) uint16_t s_w0[kBN * kBK], s_w1[kBN * kBK], s_w2[kBN * kBK];
 
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wm = wv & 1, wn = wv >> 1, r32 = lane & 31, half = lane >> 5;
+  const int wm = wv & 1, wn = wv >> 1, r16 = lane & 15, quarter = lane >> 4;
   int64_t mt, nt;
   xcd_tile(gridDim.x, gridDim.y, mt, nt);
   const int64_t m0 = mt * BM, n0 = nt * kBN;
-  const int64_t k0 = blockIdx.z * ks, end = p.lde / kBK;
-  const int64_t steps = k0 + ks < end ? ks : end > k0 ? end - k0 : 0;
+  const int k0 = static_cast<int>(blockIdx.z) * ks, end = static_cast<int>(p.lde / kBK);
+  const int steps = k0 + ks < end ? ks : end > k0 ? end - k0 : 0;
 
-  f32x16 acc[FN][FM];
+  f32x4 acc[FN][FM];
   clear(acc);
   if (steps > 0) {
-    DtlTile<BM, kNW> ta;
-    DtlTileT tw;
+    RowTile<BM> ta;
+    ColTile tw;
     ta.init(p.E, p.lde, m0, p.T, wv, lane);
     tw.init(p.W, p.H, n0, p.n, wv, lane);
-    HeadLoop<BM, DtlTileT>{{s_act0, s_act1}, {s_wt0, s_wt1}, wv, lane}.run(acc, ta, tw, k0, steps);
+    HeadLoop<BM, ColTile>{{s_a0, s_a1}, {s_w0, s_w1, s_w2}, wv}.run(acc, ta, tw, k0, steps);
   }
   float* const dst = part + blockIdx.z * p.T * p.H;
 #pragma unroll
   for (int c = 0; c < FM; ++c) {
-    const int64_t m = m0 + wm * WM + c * 32 + r32;
+    const int64_t m = m0 + wm * WM + c * 16 + r16;
     if (m >= p.T) continue;
     const float f = p.first ? 0.f : p.factor[m];
 #pragma unroll
-    for (int a = 0; a < FN; ++a)
+    for (int a = 0; a < FN; ++a) {
+      const int64_t n = n0 + wn * kWN + a * 16 + 4 * quarter;
+      if (n >= p.H) continue;
+      f32x4* at = reinterpret_cast<f32x4*>(dst + m * p.H + n);
+      f32x4 v = acc[a][c];
+      if (!p.first) {
+        const f32x4 old = *at;
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const int64_t n = n0 + wn * 64 + a * 32 + 8 * g + 4 * half;
-        if (n >= p.H) continue;
-        f32x4* at = reinterpret_cast<f32x4*>(dst + m * p.H + n);
-        f32x4 v = {acc[a][c][4 * g], acc[a][c][4 * g + 1], acc[a][c][4 * g + 2], acc[a][c][4 * g + 3]};
-        if (!p.first) {
-          const f32x4 old = *at;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] += f == 1.f ? old[i] : f * old[i];
-        }
-        *at = v;
+        for (int i = 0; i < 4; ++i) v[i] += f == 1.f ? old[i] : f * old[i];
       }
+      *at = v;
+    }
   }
 }
 
@@ -476,12 +578,15 @@ __global__ __launch_bounds__(256) void k_head_finish(HeadFinish f) {
   }
 }
 
-template __global__ void k_head_logits<256>(HeadPiece);
-template __global__ void k_head_logits<128>(HeadPiece);
-template __global__ void k_head_logits<64>(HeadPiece);
-template __global__ void k_head_grad<256>(HeadPiece, float*, int64_t);
-template __global__ void k_head_grad<128>(HeadPiece, float*, int64_t);
-template __global__ void k_head_grad<64>(HeadPiece, float*, int64_t);
+template __global__ void k_head_logits<256, true>(HeadPiece);
+template __global__ void k_head_logits<128, true>(HeadPiece);
+template __global__ void k_head_logits<64, true>(HeadPiece);
+template __global__ void k_head_logits<256, false>(HeadPiece);
+template __global__ void k_head_logits<128, false>(HeadPiece);
+template __global__ void k_head_logits<64, false>(HeadPiece);
+template __global__ void k_head_grad<256>(HeadPiece, float*, int);
+template __global__ void k_head_grad<128>(HeadPiece, float*, int);
+template __global__ void k_head_grad<64>(HeadPiece, float*, int);
 
 namespace {
 constexpr int64_t kHeadCus = 256;  // of the part; fixed, so that sizes depend on shapes only
@@ -491,24 +596,29 @@ int head_rows(int64_t T) { return T <= 64 ? 64 : T <= 128 ? 128 : 256; }
 hipError_t launch_head_logits(const HeadPiece& p, hipStream_t s) {
   const int bm = head_rows(p.T);
   const dim3 grid(static_cast<uint32_t>(ceil_div(p.T, bm)), static_cast<uint32_t>(ceil_div(p.n, kBN)));
-  if (bm == 64) hipLaunchKernelGGL((k_head_logits<64>), grid, dim3(512), 0, s, p);
-  else if (bm == 128) hipLaunchKernelGGL((k_head_logits<128>), grid, dim3(512), 0, s, p);
-  else hipLaunchKernelGGL((k_head_logits<256>), grid, dim3(512), 0, s, p);
+  const auto go = [&](auto b) {
+    constexpr int BM = decltype(b)::value;
+    if (p.E != nullptr) hipLaunchKernelGGL((k_head_logits<BM, true>), grid, dim3(256), 0, s, p);
+    else hipLaunchKernelGGL((k_head_logits<BM, false>), grid, dim3(256), 0, s, p);
+  };
+  if (bm == 64) go(std::integral_constant<int, 64>{});
+  else if (bm == 128) go(std::integral_constant<int, 128>{});
+  else go(std::integral_constant<int, 256>{});
   return hipGetLastError();
 }
 
 hipError_t launch_head_rows(const HeadPiece& p, hipStream_t s) {
-  const int64_t tiles = ceil_div(p.n, kHeadTile);
+  const int64_t tiles = p.lde / kHeadCols;
   const int64_t ys = p.E == nullptr ? 1 : tiles < 32 ? ceil_div(tiles, 4) : 8;
   hipLaunchKernelGGL(k_head_rows, dim3(static_cast<uint32_t>(ceil_div(p.T, 64)), static_cast<uint32_t>(ys)), dim3(256),
                      0, s, p);
   return hipGetLastError();
 }
 
-// as many ranges of the vocabulary as give every CU a workgroup, each of 16
-// steps or more
+// as many ranges of the vocabulary as give every CU a workgroup, each of
+// 1024 columns or more
 int head_splits(int64_t T, int64_t H, int64_t n) {
-  const int64_t tiles = ceil_div(T, head_rows(T)) * ceil_div(H, kBN), steps = round_up(n, kHeadTile) / kBK;
+  const int64_t tiles = ceil_div(T, head_rows(T)) * ceil_div(H, kBN), steps = round_up(n, kHeadTile) / 64;
   int64_t S = kHeadCus / tiles;
   if (S > steps / 16) S = steps / 16;
   return S > 1 ? static_cast<int>(S) : 1;
@@ -518,10 +628,10 @@ hipError_t launch_head_grad(const HeadPiece& p, float* part, int splits, hipStre
   const int bm = head_rows(p.T);
   const dim3 grid(static_cast<uint32_t>(ceil_div(p.T, bm)), static_cast<uint32_t>(ceil_div(p.H, kBN)),
                   static_cast<uint32_t>(splits));
-  const int64_t ks = ceil_div(p.lde / kBK, splits);
-  if (bm == 64) hipLaunchKernelGGL((k_head_grad<64>), grid, dim3(512), 0, s, p, part, ks);
-  else if (bm == 128) hipLaunchKernelGGL((k_head_grad<128>), grid, dim3(512), 0, s, p, part, ks);
-  else hipLaunchKernelGGL((k_head_grad<256>), grid, dim3(512), 0, s, p, part, ks);
+  const int ks = static_cast<int>(ceil_div(p.lde / kBK, splits));
+  if (bm == 64) hipLaunchKernelGGL((k_head_grad<64>), grid, dim3(256), 0, s, p, part, ks);
+  else if (bm == 128) hipLaunchKernelGGL((k_head_grad<128>), grid, dim3(256), 0, s, p, part, ks);
+  else hipLaunchKernelGGL((k_head_grad<256>), grid, dim3(256), 0, s, p, part, ks);
   return hipGetLastError();
 }
 

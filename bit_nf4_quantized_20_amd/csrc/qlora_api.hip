@@ -1277,7 +1277,7 @@ HeadLayout head_layout(int64_t T, int64_t V, int64_t H, bool expand, bool grad) 
   if (grad && most > (int64_t(1) << 29) / H) most = (int64_t(1) << 29) / H;
   most = most / kHeadTile * kHeadTile;
   l.n = round_up(ceil_div(V, ceil_div(V, most)), kHeadTile);
-  const int64_t tiles = l.n / kHeadTile;
+  const int64_t tiles = l.n / kHeadCols;
   Carve c;
   const size_t row = static_cast<size_t>(l.tokens) * 4;
   l.w = c.take(expand ? static_cast<size_t>(l.n * H * 2) : 0);
