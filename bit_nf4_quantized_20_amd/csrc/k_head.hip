@@ -60,62 +60,65 @@ __device__ __forceinline__ void join(float& c, float& s, float c2, float s2) {
 
 // Tiles of 64 columns (K), copied straight from global memory into LDS, 1 KB a wave
 // instruction and whole 128-byte lines: in halves of lines the second-level cache gets
-// twice the requests and bounds the kernel (4096 x 4096 x 16128: 485 us).  live
-// false: the resource is empty, so that the copy reads nothing and writes zeros.
+// twice the requests and bounds the kernel (4096 x 4096 x 16128: 485 us).
 //
-// Rows [row0, row0 + ROWS) of a K-contiguous matrix, as lds_frag reads them.
+// Where a tile's data begin and how many bytes from there may be read (the rest
+// reads as 0; bytes = 0: nothing is read).
+struct Source {
+  const uint16_t* base;
+  int bytes;
+};
+__device__ __forceinline__ Source rows_source(const uint16_t* p, int64_t ld, int64_t row0, int64_t rows, int64_t col0) {
+  const int64_t n = ((rows - row0) * ld - col0) * 2;
+  return Source{p + row0 * ld + col0, static_cast<int>(n < 0x7fffffff ? n : 0x7fffffff)};
+}
+
+// ROWS rows of a K-contiguous matrix, as lds_frag reads them.
 template <int ROWS>
 struct RowTile {
   static constexpr int kPerWave = ROWS / 8 / kNW;
-  const uint16_t* base;
-  int bytes;
   uint32_t voff[kPerWave];
-  __device__ __forceinline__ void init(const uint16_t* p, int64_t ld, int64_t row0, int64_t rows, int wv, int lane) {
-    base = p + row0 * ld;
-    const int64_t n = (rows - row0) * ld * 2;
-    bytes = static_cast<int>(n < 0x7fffffff ? n : 0x7fffffff);
+  __device__ __forceinline__ void init(int64_t ld, int wv, int lane) {
 #pragma unroll
     for (int i = 0; i < kPerWave; ++i) {
       const int row = (i * kNW + wv) * 8 + (lane >> 3);
       voff[i] = static_cast<uint32_t>((row * ld + swz(row, lane & 7) * 8) * 2);
     }
   }
-  // pieces [first, first + count) of the kPerWave
-  __device__ __forceinline__ void load(uint16_t* lds, int wv, int k0, bool live, int first = 0, int count = kPerWave) const {
+  // step k's pieces [first, first + count) of the kPerWave
+  __device__ __forceinline__ void load(uint16_t* lds, int wv, const Source& s, int k, int first, int count) const {
     const __amdgpu_buffer_rsrc_t rs =
-        __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(base), 0, live ? bytes : 0, kBufferWord3);
+        __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(s.base), 0, s.bytes, kBufferWord3);
+    const int at = s.bytes != 0 ? k * kBK * 2 : 0;
 #pragma unroll
     for (int i = first; i < first + count && i < kPerWave; ++i)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          rs, (__attribute__((address_space(3))) void*)(lds + (i * kNW + wv) * 512), 16, voff[i], live ? k0 * 2 : 0, 0, 0);
+          rs, (__attribute__((address_space(3))) void*)(lds + (i * kNW + wv) * 512), 16, voff[i], at, 0, 0);
   }
 };
 
-// K-row-major weight tile: 64 rows of W (K) by kBN columns from n0, swizzled by
-// tswz for lds_frag_tr.  A wave instruction copies two rows; lane L lands at
-// 16-byte chunk L % 32 of row L / 32 and loads the chunk that belongs there.
-// Columns past H read the next row (never stored), rows past the piece read 0:
-// the resource starts at the step's first row (a piece is below 2^31 bytes).
+// K-row-major weight tile: 64 rows of W (K) by kBN columns, swizzled by tswz for
+// col_frag.  A wave instruction copies two rows; lane L lands at 16-byte chunk L % 32 of
+// row L / 32 and loads the chunk that belongs there.  Columns past H read the next
+// row (never stored), rows past the piece read 0: the resource starts at the step's
+// first row (a piece is below 2^31 bytes).
 struct ColTile {
   static constexpr int kPerWave = kBK / 2 / kNW;
-  const uint16_t* base;
-  int pitch, bytes;
+  int pitch;  // bytes of a row
   uint32_t voff[kPerWave];
-  __device__ __forceinline__ void init(const uint16_t* W, int64_t ld, int64_t n0, int64_t rows, int wv, int lane) {
-    base = W;
+  __device__ __forceinline__ void init(int64_t ld, int wv, int lane) {
     pitch = static_cast<int>(ld * 2);
-    bytes = static_cast<int>(rows * ld * 2);
 #pragma unroll
     for (int i = 0; i < kPerWave; ++i) {
       const int k = (i * kNW + wv) * 2 + (lane >> 5);
-      voff[i] = static_cast<uint32_t>((k * ld + n0 + ((lane & 31) ^ tswz(k)) * 8) * 2);
+      voff[i] = static_cast<uint32_t>((k * ld + ((lane & 31) ^ tswz(k)) * 8) * 2);
     }
   }
-  __device__ __forceinline__ void load(uint16_t* lds, int wv, int k0, bool live, int first = 0, int count = kPerWave) const {
-    const int64_t at = static_cast<int64_t>(live ? k0 : 0) * pitch;
-    const int64_t left = live && at < bytes ? bytes - at : 0;
+  __device__ __forceinline__ void load(uint16_t* lds, int wv, const Source& s, int k, int first, int count) const {
+    const int64_t at = static_cast<int64_t>(k) * (kBK * pitch);
     const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<uint8_t*>(reinterpret_cast<const uint8_t*>(base) + at), 0, static_cast<int>(left), kBufferWord3);
+        const_cast<uint8_t*>(reinterpret_cast<const uint8_t*>(s.base) + at), 0,
+        static_cast<int>(at < s.bytes ? s.bytes - at : 0), kBufferWord3);
 #pragma unroll
     for (int i = first; i < first + count && i < kPerWave; ++i)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
@@ -146,7 +149,7 @@ __device__ __forceinline__ bf16x8 col_frag(const uint16_t* lds, int n0, int j) {
   return __builtin_bit_cast(bf16x8, __builtin_shufflevector(v[0], v[1], 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
-// acc[a][c] += weight fragments times activation fragments over K-steps [k0,
+// acc[a][c] += weight fragments times activation fragments over a tile's K-steps [k0,
 // k0 + steps) of 64; acc[a][c][i] holds row m = wm BM/2 + 16 c + lane % 16 of the
 // tile and column n = 128 wn + 16 a + 4 (lane / 16) + i.
 //
@@ -160,6 +163,11 @@ __device__ __forceinline__ bf16x8 col_frag(const uint16_t* lds, int n0, int j) {
 // stages; it also waits for what the next step reads.  The copies of two steps on
 // (activations) go out behind it and have a sub-step to land, those of three steps on
 // (weights) under the next sub-step and have three.
+//
+// A workgroup takes one tile after another without a break in this: the steps count on
+// into the next tile (steps is rounded up to the six after which both rings are back
+// where they began, with copies of zeros), so that its first copies and fragments
+// are under way during the last steps and the epilogue.
 template <int BM, class TW>
 struct HeadLoop {
   static constexpr int FN = kWN / 16, FM = BM / 32;
@@ -168,6 +176,11 @@ struct HeadLoop {
   typedef f32x4 Acc[FN][FM];
   uint16_t *s_act[2], *s_wt[3];
   int wv;
+  RowTile<BM> ta;
+  TW tw;
+  int k0, steps;          // of this tile (and of the next, where there is one)
+  Source a[2], w[2];      // this tile's and the next one's (bytes 0: none)
+  bf16x8 fw[FN], fa[2][FM];
 
   __device__ __forceinline__ bf16x8 act(int b, int j, int i) const {
     return row_frag(s_act[b], (wv & 1) * (BM / 2) + i * 16, j);
@@ -202,25 +215,35 @@ struct HeadLoop {
   }
   static constexpr int wait_code(int copies) { return (copies & 15) | ((copies >> 4) << 14) | 0x70; }  // lgkmcnt(0) too
 
-  __device__ __forceinline__ void run(Acc& acc, const RowTile<BM>& ta, const TW& tw, int k0, int steps) const {
-    constexpr int kA = RowTile<BM>::kPerWave, kW = TW::kPerWave;  // copies of a wave and step
-    auto copy_a = [&](int e, int b, int first, int count) {
-      ta.load(s_act[b], wv, (k0 + e) * kBK, e < steps, first, count);
-    };
-    auto copy_w = [&](int e, int b, int first, int count) {
-      tw.load(s_wt[b], wv, (k0 + e) * kBK, e < steps, first, count);
-    };
+  __device__ __forceinline__ static int padded(int n) { return (n + 5) / 6 * 6; }
+  static constexpr int kA = RowTile<BM>::kPerWave, kW = TW::kPerWave;  // copies of a wave and step
+  // step e counted from this tile's first
+  __device__ __forceinline__ static Source source(const Source (&s)[2], int e, int steps, int turn) {
+    return Source{e < turn ? s[0].base : s[1].base, e < steps ? s[0].bytes : e < turn || e - turn >= steps ? 0 : s[1].bytes};
+  }
+  __device__ __forceinline__ void copy_a(int e, int b, int first, int count) const {
+    const int turn = padded(steps);
+    ta.load(s_act[b], wv, source(a, e, steps, turn), e < turn ? k0 + e : e - turn, first, count);
+  }
+  __device__ __forceinline__ void copy_w(int e, int b, int first, int count) const {
+    const int turn = padded(steps);
+    tw.load(s_wt[b], wv, source(w, e, steps, turn), e < turn ? k0 + e : e - turn, first, count);
+  }
+
+  // the first copies and fragments of a workgroup's first tile
+  __device__ __forceinline__ void begin() {
     copy_a(0, 0, 0, kA);
     copy_w(0, 0, 0, kW);
     copy_w(1, 1, 0, kW);
     copy_a(1, 1, 0, kA);
     __builtin_amdgcn_s_waitcnt(wait_code(kA + kW));
     barrier();
-    bf16x8 fw[FN], fa[2][FM];
 #pragma unroll
     for (int i = 0; i < 6; ++i) fw[i] = wt(0, 0, i);
 #pragma unroll
     for (int i = 0; i < FM; ++i) fa[0][i] = act(0, 0, i);
+  }
+  __device__ __forceinline__ void tile(Acc& acc) {
     settle(acc);
     // step e; A, W: its stages
     auto step = [&](int e, auto ac, auto wc) {
@@ -270,7 +293,6 @@ struct HeadLoop {
       step(e + 5, I1{}, I2{});
     }
     settle(acc);
-    __builtin_amdgcn_s_waitcnt(0);  // copies of zeros behind the last step
   }
 };
 
@@ -280,6 +302,140 @@ __device__ __forceinline__ void clear(f32x4 (&acc)[FN][FM]) {
   for (int a = 0; a < FN; ++a)
 #pragma unroll
     for (int c = 0; c < FM; ++c) acc[a][c] = f32x4{0.f, 0.f, 0.f, 0.f};
+}
+
+__device__ __forceinline__ void tile_at(int64_t t, int64_t gm, int64_t gn, int64_t& mt, int64_t& nt) {
+  const int64_t per_group = kGroupM * gn, g = t / per_group, left = gm - g * kGroupM;
+  const int64_t rows = left < kGroupM ? left : kGroupM, in_g = t - g * per_group;
+  mt = g * kGroupM + in_g % rows;
+  nt = in_g / rows;
+}
+
+// max of three (fmaxf would quiet each operand with an instruction of its own; a NaN is
+// passed over either way)
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+  return r;
+}
+// over the four lanes l, l ^ 16, l ^ 32, l ^ 48
+__device__ __forceinline__ float max_quarters(float v) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, v);
+  const auto x = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  v = max3(__builtin_bit_cast(float, static_cast<uint32_t>(x[0])), __builtin_bit_cast(float, static_cast<uint32_t>(x[1])), v);
+  const uint32_t w = __builtin_bit_cast(uint32_t, v);
+  const auto y = __builtin_amdgcn_permlane32_swap(w, w, false, false);
+  return max3(__builtin_bit_cast(float, static_cast<uint32_t>(y[0])), __builtin_bit_cast(float, static_cast<uint32_t>(y[1])), v);
+}
+__device__ __forceinline__ float sum_quarters(float v) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, v);
+  const auto x = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  v = __builtin_bit_cast(float, static_cast<uint32_t>(x[0])) + __builtin_bit_cast(float, static_cast<uint32_t>(x[1]));
+  const uint32_t w = __builtin_bit_cast(uint32_t, v);
+  const auto y = __builtin_amdgcn_permlane32_swap(w, w, false, false);
+  return __builtin_bit_cast(float, static_cast<uint32_t>(y[0])) + __builtin_bit_cast(float, static_cast<uint32_t>(y[1]));
+}
+
+// The softmax's part of a wave's BM/2 x 128 logits, rows from m0 and columns from n0
+// on: the row's cell and sum, the label's logit, E.  (Stores of 16 bytes a lane, 64 a
+// row and instruction.  Through LDS they would be whole rows, but the stages already
+// hold the next tile.)  Bound by the vector unit, a third of it exponentials.
+template <int BM, bool kE>
+__device__ __forceinline__ void reduce_tile(const HeadPiece& p, const f32x4 (&acc)[kWN / 16][BM / 32], int64_t m0, int64_t n0) {
+  constexpr int FN = kWN / 16, FM = BM / 32;
+  const int lane = threadIdx.x & 63, r16 = lane & 15, quarter = lane >> 4;
+  const int left = static_cast<int>(p.n - n0 < kWN ? p.n - n0 : kWN);  // valid columns; behind them -inf
+  const int64_t block = n0 / kHeadCols;
+  // the rows' labels and cells, all loads ahead of the first store (rows past the
+  // last one read its)
+  const int rows = static_cast<int>(p.T - m0 < BM / 2 ? p.T - m0 : BM / 2);  // this wave's; <= 0: none
+  if (rows <= 0) return;
+  int label[FM];  // the label's column here, -1: elsewhere
+  float before[FM];
+#pragma unroll
+  for (int c = 0; c < FM; ++c) {
+    const int row = c * 16 + r16, at_row = row < rows ? row : rows - 1;
+    const uint64_t at = static_cast<uint64_t>(p.labels[m0 + at_row]) - static_cast<uint64_t>(p.v0 + n0);
+    label[c] = at < static_cast<uint64_t>(left) && row < rows ? static_cast<int>(at) : -1;
+    before[c] = p.first ? -kInf : p.c_in[m0 + at_row];
+  }
+  // E's rows from m0 on; stores behind the last are dropped
+  const uint64_t e_bytes = static_cast<uint64_t>(rows) * p.lde * 2;
+  const __amdgpu_buffer_rsrc_t e_rs = __builtin_amdgcn_make_buffer_rsrc(
+      kE ? p.E + m0 * p.lde : nullptr, 0, static_cast<int>(e_bytes < 0x7fffffff ? e_bytes : 0x7fffffff), kBufferWord3);
+  const uint32_t e_pitch = static_cast<uint32_t>(p.lde * 2);
+  const uint32_t e_off = r16 * e_pitch + static_cast<uint32_t>(n0 * 2) + 32 * (quarter & 1) + 16 * (quarter >> 1);
+#pragma unroll
+  for (int c = 0; c < FM; ++c) {
+    // E and sum of the logits s, in units of 2^ref
+    const auto finish = [&](const float (&s)[FN][4], float scale, float cell) {
+      const float ref = cell == -kInf ? 0.f : cell * kHeadCell;
+      float sum[2] = {0.f, 0.f};
+#pragma unroll
+      for (int a = 0; a < FN; a += 2) {
+        uint32_t q[2][2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          float e[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[a + k][i], scale, -ref));
+            sum[k] += e[i];
+          }
+          q[k][0] = pack_bf16x2(e[0], e[1]);
+          q[k][1] = pack_bf16x2(e[2], e[3]);
+        }
+        if constexpr (kE) {
+          // lanes 16 .. 31 and 48 .. 63 of fragment a change places with lanes 0 .. 15
+          // and 32 .. 47 of a + 1: each lane then has eight columns in a row
+          const auto x = __builtin_amdgcn_permlane16_swap(q[0][0], q[1][0], false, false);
+          const auto y = __builtin_amdgcn_permlane16_swap(q[0][1], q[1][1], false, false);
+          __builtin_amdgcn_raw_buffer_store_b128(u32x4{x[0], y[0], x[1], y[1]}, e_rs, e_off + c * 16 * e_pitch + 32 * a, 0, 0);
+        }
+      }
+      const float total = sum_quarters(sum[0] + sum[1]);
+      if (quarter == 0 && c * 16 + r16 < rows) {
+        p.tile_c[block * p.T + m0 + c * 16 + r16] = cell;
+        p.tile_s[block * p.T + m0 + c * 16 + r16] = total;
+      }
+    };
+    const auto largest = [&](const float (&s)[FN][4]) {
+      float top = -kInf;
+#pragma unroll
+      for (int a = 0; a < FN; ++a) top = max3(s[a][2], s[a][3], max3(s[a][0], s[a][1], top));
+      return max_quarters(top);
+    };
+    float s[FN][4];
+#pragma unroll
+    for (int a = 0; a < FN; ++a)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[a][i] = acc[a][c][i];
+    const float top = largest(s);
+    // s - ref is one fused multiply-add.  Its product is not rounded, the cell's was:
+    // from 2^31 on they would be further apart than a cell, so of such rows (from
+    // 2^23 on) the products are rounded first.
+    if (left == kWN && !__any(label[c] >= 0 || fabsf(top) >= 0x1p23f)) {
+      finish(s, kLog2e, fmaxf(before[c], cell_of(top * kLog2e)));
+    } else {
+      // (the accumulators are left as they are: changed in a branch, all of them would
+      // be copied out of the matrix cores' registers)
+      float target = 0.f, u[FN][4];
+      const int mine = label[c] >= 0 ? label[c] - 4 * quarter : -1;
+#pragma unroll
+      for (int a = 0; a < FN; ++a)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const bool hit = mine == 16 * a + i;
+          const float v = acc[a][c][i] * kLog2e;
+          target = hit ? v : target;  // the label's logit goes aside
+          u[a][i] = hit || 16 * a + 4 * quarter + i >= left ? -kInf : v;
+        }
+      if (label[c] >= 0 && ((label[c] >> 2) & 3) == quarter) p.target[m0 + c * 16 + r16] = target;
+      const float most = largest(u);
+      finish(u, 1.f, most == -kInf ? before[c] : fmaxf(before[c], cell_of(most)));
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  }
 }
 
 }  // namespace
@@ -292,110 +448,55 @@ __global__ __launch_bounds__(256, 1) void k_head_logits(HeadPiece p) {
   __shared__ __attribute__((aligned(1024))) uint16_t s_w0[kBN * kBK], s_w1[kBN * kBK], s_w2[kBN * kBK];
 
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wm = wv & 1, wn = wv >> 1, r16 = lane & 15, quarter = lane >> 4;
-  int64_t mt, nt;
-  xcd_tile(gridDim.x, gridDim.y, mt, nt);
-  const int64_t m0 = mt * BM, n0 = nt * kBN;
+  const int wm = wv & 1, wn = wv >> 1;
+  // This workgroup's tiles: XCD x (workgroups x, x + 8, ...) has a contiguous eighth
+  // of the sequence, which walks groups of kGroupM row tiles column by column.
+  const int64_t gm = ceil_div(p.T, BM), gn = ceil_div(p.n, kBN), total = gm * gn;
+  const int64_t xcd = blockIdx.x % kXcds, stride = gridDim.x / kXcds, end = total * (xcd + 1) / kXcds;
+  int64_t t = total * xcd / kXcds + blockIdx.x / kXcds;
+  if (t >= end) return;
 
-  f32x4 acc[FN][FM];
-  clear(acc);
-  {
-    using TW = RowTile<kBN>;
-    RowTile<BM> ta;
-    TW tw;
-    ta.init(p.X, p.H, m0, p.T, wv, lane);
-    tw.init(p.W, p.H, n0, p.n, wv, lane);
-    HeadLoop<BM, TW>{{s_a0, s_a1}, {s_w0, s_w1, s_w2}, wv}.run(acc, ta, tw, 0, static_cast<int>(p.H / kBK));
+  using TW = RowTile<kBN>;
+  HeadLoop<BM, TW> loop{{s_a0, s_a1}, {s_w0, s_w1, s_w2}, wv};
+  loop.ta.init(p.H, wv, lane);
+  loop.tw.init(p.H, wv, lane);
+  loop.k0 = 0;
+  loop.steps = static_cast<int>(p.H / kBK);
+  int64_t m0, n0, m1 = 0, n1 = 0;
+  tile_at(t, gm, gn, m0, n0);
+  m0 *= BM;
+  n0 *= kBN;
+  loop.a[0] = rows_source(p.X, p.H, m0, p.T, 0);
+  loop.w[0] = rows_source(p.W, p.H, n0, p.n, 0);
+  bool more = false;
+  const auto look_ahead = [&]() {
+    more = t + stride < end;
+    loop.a[1] = Source{p.X, 0};
+    loop.w[1] = Source{p.W, 0};
+    if (more) {
+      tile_at(t + stride, gm, gn, m1, n1);
+      m1 *= BM;
+      n1 *= kBN;
+      loop.a[1] = rows_source(p.X, p.H, m1, p.T, 0);
+      loop.w[1] = rows_source(p.W, p.H, n1, p.n, 0);
+    }
+  };
+  look_ahead();
+  loop.begin();
+  for (;;) {
+    f32x4 acc[FN][FM];
+    clear(acc);
+    loop.tile(acc);
+    reduce_tile<BM, kE>(p, acc, m0 + wm * WM, n0 + wn * kWN);
+    if (!more) break;
+    m0 = m1;
+    n0 = n1;
+    loop.a[0] = loop.a[1];
+    loop.w[0] = loop.w[1];
+    t += stride;
+    look_ahead();
   }
-
-  // Every wave reduces its own 128 columns; E goes to LDS as a BM/2 x 128 block a
-  // wave (as large as a stage of activations), rows of sixteen 16-byte pieces, piece k
-  // of row r at slot k ^ (r % 16).
-  uint16_t* const s_e = wv == 0 ? s_w0 : wv == 1 ? s_w1 : wv == 2 ? s_w2 : s_a0;
-  const int64_t left = p.n - n0 - wn * kWN;  // valid columns from this wave's first; behind them -inf
-  const int64_t block = nt * 2 + wn;
-  __syncthreads();  // every wave is done reading the stages
-#pragma unroll
-  for (int c = 0; c < FM; ++c) {
-    const int row = c * 16 + r16;
-    const int64_t m = m0 + wm * WM + row;
-    float s[FN][4];
-#pragma unroll
-    for (int a = 0; a < FN; ++a)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) s[a][i] = acc[a][c][i];
-    if (left < kWN) {
-#pragma unroll
-      for (int a = 0; a < FN; ++a)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (16 * a + 4 * quarter + i >= left) s[a][i] = -kInf;
-    }
-    const int64_t at = m < p.T ? p.labels[m] - p.v0 - n0 - wn * kWN : -1;
-    const bool here = at >= 0 && at < kWN && at < left;
-    if (__any(here)) {  // the label's logit goes aside
-      float target = 0.f;
-      const int mine = here ? static_cast<int>(at) - 4 * quarter : -1;
-#pragma unroll
-      for (int a = 0; a < FN; ++a)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const bool hit = mine == 16 * a + i;
-          target = hit ? s[a][i] : target;
-          s[a][i] = hit ? -kInf : s[a][i];
-        }
-      if (here && ((at >> 2) & 3) == quarter) p.target[m] = target * kLog2e;
-    }
-    float top = -kInf;
-#pragma unroll
-    for (int a = 0; a < FN; ++a)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) top = fmaxf(top, s[a][i]);
-    top = fmaxf(top, __shfl_xor(top, 16));
-    top = fmaxf(top, __shfl_xor(top, 32));
-    float cell = top == -kInf ? -kInf : cell_of(top * kLog2e);
-    if (!p.first && m < p.T) cell = fmaxf(cell, p.c_in[m]);
-    const float ref = cell == -kInf ? 0.f : cell * kHeadCell;
-    // s - ref is one fused multiply-add.  Its product is not rounded, the cell's was:
-    // from 2^31 on they would be further apart than a cell, so a wave that holds
-    // such a row (from 2^23 on) rounds its products first.
-    float scale = kLog2e;
-    if (__any(fabsf(top) >= 0x1p23f)) {
-      scale = 1.f;
-#pragma unroll
-      for (int a = 0; a < FN; ++a)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s[a][i] *= kLog2e;
-    }
-    float sum = 0.f;
-#pragma unroll
-    for (int a = 0; a < FN; ++a) {
-      float e[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[a][i], scale, -ref));
-        sum += e[i];
-      }
-      if constexpr (kE)
-        *reinterpret_cast<u32x2*>(s_e + row * kWN + (((2 * a + (quarter >> 1)) ^ r16) * 8) + 4 * (quarter & 1)) =
-            u32x2{pack_bf16x2(e[0], e[1]), pack_bf16x2(e[2], e[3])};
-    }
-    sum += __shfl_xor(sum, 16);
-    sum += __shfl_xor(sum, 32);
-    if (quarter == 0 && m < p.T) {
-      p.tile_c[block * p.T + m] = cell;
-      p.tile_s[block * p.T + m] = sum;
-    }
-  }
-  if constexpr (!kE) return;
-  __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): this wave's block is in LDS
-#pragma unroll
-  for (int i = 0; i < WM / 4; ++i) {
-    const int row = 4 * i + (lane >> 4), piece = lane & 15;
-    const int64_t m = m0 + wm * WM + row;
-    const u32x4 v = *reinterpret_cast<const u32x4*>(s_e + row * kWN + ((piece ^ (row & 15)) * 8));
-    if (m < p.T) *reinterpret_cast<u32x4*>(p.E + m * p.lde + n0 + wn * kWN + 8 * piece) = v;
-  }
+  __builtin_amdgcn_s_waitcnt(0);  // copies behind the last step
 }
 
 // Workgroup x: 64 rows; its four waves share the piece's tiles.  Workgroup y
@@ -465,11 +566,18 @@ __global__ __launch_bounds__(256, 1) void k_head_grad(HeadPiece p, float* part, 
   f32x4 acc[FN][FM];
   clear(acc);
   if (steps > 0) {
-    RowTile<BM> ta;
-    ColTile tw;
-    ta.init(p.E, p.lde, m0, p.T, wv, lane);
-    tw.init(p.W, p.H, n0, p.n, wv, lane);
-    HeadLoop<BM, ColTile>{{s_a0, s_a1}, {s_w0, s_w1, s_w2}, wv}.run(acc, ta, tw, k0, steps);
+    HeadLoop<BM, ColTile> loop{{s_a0, s_a1}, {s_w0, s_w1, s_w2}, wv};
+    loop.ta.init(p.lde, wv, lane);
+    loop.tw.init(p.H, wv, lane);
+    loop.k0 = k0;
+    loop.steps = steps;
+    loop.a[0] = rows_source(p.E, p.lde, m0, p.T, 0);
+    loop.w[0] = rows_source(p.W, p.H, 0, p.n, n0);
+    loop.a[1] = Source{p.E, 0};
+    loop.w[1] = Source{p.W, 0};
+    loop.begin();
+    loop.tile(acc);
+    __builtin_amdgcn_s_waitcnt(0);  // copies behind the last step
   }
   float* const dst = part + blockIdx.z * p.T * p.H;
 #pragma unroll
@@ -595,7 +703,7 @@ int head_rows(int64_t T) { return T <= 64 ? 64 : T <= 128 ? 128 : 256; }
 
 hipError_t launch_head_logits(const HeadPiece& p, hipStream_t s) {
   const int bm = head_rows(p.T);
-  const dim3 grid(static_cast<uint32_t>(ceil_div(p.T, bm)), static_cast<uint32_t>(ceil_div(p.n, kBN)));
+  const dim3 grid(static_cast<uint32_t>(kHeadCus));  // a multiple of the XCDs' number
   const auto go = [&](auto b) {
     constexpr int BM = decltype(b)::value;
     if (p.E != nullptr) hipLaunchKernelGGL((k_head_logits<BM, true>), grid, dim3(256), 0, s, p);
