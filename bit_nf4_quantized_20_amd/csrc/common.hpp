@@ -353,8 +353,6 @@ struct HeadPiece {
   float *c_out, *s_out, *factor;
 };
 hipError_t launch_head_logits(const HeadPiece& p, hipStream_t s);
-// the tiles' sums into the rows' and, with E, every row of E to its row's cell
-hipError_t launch_head_rows(const HeadPiece& p, hipStream_t s);
 // part [splits][T][H] fp32 = factor part (not first) + E W
 int head_splits(int64_t T, int64_t H, int64_t n);
 hipError_t launch_head_grad(const HeadPiece& p, float* part, int splits, hipStream_t s);
@@ -375,6 +373,9 @@ struct HeadFinish {
   float *loss, *lse;
   uint16_t* dX;
 };
+// the blocks' sums into the rows' and, with E, every row of E to its row's cell; with
+// f.loss loss and lse instead (without E, behind the last piece)
+hipError_t launch_head_rows(const HeadPiece& p, const HeadFinish& f, hipStream_t s);
 hipError_t launch_head_finish(const HeadFinish& f, hipStream_t s);
 
 // AdamW over many tensors (k_adamw.hip).  The tensors' elements are cut into

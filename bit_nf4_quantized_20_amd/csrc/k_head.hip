@@ -499,26 +499,52 @@ __global__ __launch_bounds__(256, 1) void k_head_logits(HeadPiece p) {
   __builtin_amdgcn_s_waitcnt(0);  // copies behind the last step
 }
 
-// Workgroup x: 64 rows; its four waves share the piece's tiles.  Workgroup y
-// scales the E of tiles y, y + gridDim.y, ... of those rows where the tile's cell
-// is below the row's (one wave instruction a row and tile; rare).
-__global__ __launch_bounds__(256) void k_head_rows(HeadPiece p) {
-  __shared__ float sc[4][64], ss[4][64];
+// loss and lse of a row from its label's logit t and the sum over the others,
+// and what the gradient takes: the others' share of the total, and the factor of what
+// was accumulated in units of the others' cell over the total
+struct RowLoss {
+  float loss, lse, rest, factor;
+};
+__device__ __forceinline__ RowLoss row_loss(float c, float s, bool has, float t) {
+  RowLoss r{0.f, 0.f, 0.f, 0.f};
+  float cell = c, total = s;
+  if (has) {
+    cell = fmaxf(c, t == -kInf ? c : cell_of(t));
+    const float d = t - (cell == -kInf ? 0.f : cell * kHeadCell);
+    const float scale = c == cell ? 1.f : down_cells(1.f, c - cell), others = c == cell ? s : s * scale;
+    total = others + __builtin_amdgcn_exp2f(d);
+    // 2^-d times the others, where that is in range
+    r.loss = d > -40.f ? log1pf(others * __builtin_amdgcn_exp2f(-d)) : (__builtin_amdgcn_logf(total) - d) * kLn2;
+    const float inv = 1.f / total;
+    r.rest = others * inv;
+    r.factor = scale * inv;
+  }
+  r.lse = ((cell == -kInf ? 0.f : cell * kHeadCell) + __builtin_amdgcn_logf(total)) * kLn2;
+  return r;
+}
+
+// Workgroup x: 64 rows; its 16 waves share the piece's blocks of 128 columns.
+// Workgroup y scales the E of blocks 16 y, ... of those rows where the block's cell is
+// below the row's (one wave instruction a row and block; rare).  Without E the last
+// piece's launch writes loss and lse.  Bound by the latency of one round of loads.
+constexpr int kRowWaves = 16;
+__global__ __launch_bounds__(64 * kRowWaves) void k_head_rows(HeadPiece p, HeadFinish f) {
+  __shared__ float sc[kRowWaves][64], ss[kRowWaves][64];
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
   const int64_t m = static_cast<int64_t>(blockIdx.x) * 64 + lane;
   const bool live = m < p.T;
-  const int tiles = static_cast<int>(p.lde / kHeadCols);
+  const int blocks = static_cast<int>(p.lde / kHeadCols);
   float c = -kInf, s = 0.f;
-  for (int t = wv; t < tiles; t += 16) {
-    float tc[4], ts[4];
+  for (int t = wv; t < blocks; t += 8 * kRowWaves) {
+    float tc[8], ts[8];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const bool in = live && t + 4 * u < tiles;
-      tc[u] = in ? p.tile_c[(t + 4 * u) * p.T + m] : -kInf;
-      ts[u] = in ? p.tile_s[(t + 4 * u) * p.T + m] : 0.f;
+    for (int u = 0; u < 8; ++u) {
+      const bool in = live && t + kRowWaves * u < blocks;
+      tc[u] = in ? p.tile_c[(t + kRowWaves * u) * p.T + m] : -kInf;
+      ts[u] = in ? p.tile_s[(t + kRowWaves * u) * p.T + m] : 0.f;
     }
 #pragma unroll
-    for (int u = 0; u < 4; ++u) join(c, s, tc[u], ts[u]);
+    for (int u = 0; u < 8; ++u) join(c, s, tc[u], ts[u]);
   }
   sc[wv][lane] = c;
   ss[wv][lane] = s;
@@ -527,14 +553,22 @@ __global__ __launch_bounds__(256) void k_head_rows(HeadPiece p) {
   c = before;
   s = live && !p.first ? p.s_in[m] : 0.f;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) join(c, s, sc[i][lane], ss[i][lane]);
+  for (int i = 0; i < kRowWaves; ++i) join(c, s, sc[i][lane], ss[i][lane]);
   if (blockIdx.y == 0 && wv == 0 && live) {
-    p.c_out[m] = c;
-    p.s_out[m] = s;
-    if (p.E != nullptr) p.factor[m] = before == c ? 1.f : down_cells(1.f, before - c);
+    if (f.loss != nullptr) {
+      const int64_t y = f.labels[m];
+      const bool has = y >= 0 && y < f.V;
+      const RowLoss r = row_loss(c, s, has, has ? f.target[m] : 0.f);
+      f.loss[m] = r.loss;
+      if (f.lse != nullptr) f.lse[m] = r.lse;
+    } else {
+      p.c_out[m] = c;
+      p.s_out[m] = s;
+      if (p.E != nullptr) p.factor[m] = before == c ? 1.f : down_cells(1.f, before - c);
+    }
   }
   if (p.E == nullptr) return;
-  for (int t = blockIdx.y * 4 + wv; t < tiles; t += gridDim.y * 4) {
+  for (int t = blockIdx.y * kRowWaves + wv; t < blocks; t += gridDim.y * kRowWaves) {
     const float tc = live ? p.tile_c[t * p.T + m] : c;
     uint64_t todo = __ballot(live && tc != c && tc != -kInf);
     while (todo != 0) {
@@ -637,30 +671,17 @@ __device__ __forceinline__ void label_row(const HeadFinish& f, int64_t y, int64_
   }
 }
 
-// One workgroup a row.
+// dX, loss and lse, one workgroup a row.
 __global__ __launch_bounds__(256) void k_head_finish(HeadFinish f) {
   const int64_t m = blockIdx.x;
   const int64_t y = f.labels[m];
   const bool has = y >= 0 && y < f.V;
-  const float c = f.c[m], s = f.s[m];
-  float cell = c, others = s, total = s, loss = 0.f, scale = 1.f;
-  if (has) {
-    const float t = f.target[m];
-    cell = fmaxf(c, t == -kInf ? c : cell_of(t));
-    const float d = t - (cell == -kInf ? 0.f : cell * kHeadCell);
-    scale = c == cell ? 1.f : down_cells(1.f, c - cell);
-    others = c == cell ? s : s * scale;
-    total = others + __builtin_amdgcn_exp2f(d);
-    // 2^-d times the others, where that is in range
-    loss = d > -40.f ? log1pf(others * __builtin_amdgcn_exp2f(-d)) : (__builtin_amdgcn_logf(total) - d) * kLn2;
-  }
+  const RowLoss r = row_loss(f.c[m], f.s[m], has, has ? f.target[m] : 0.f);
   if (threadIdx.x == 0) {
-    f.loss[m] = loss;
-    if (f.lse != nullptr)
-      f.lse[m] = ((cell == -kInf ? 0.f : cell * kHeadCell) + __builtin_amdgcn_logf(total)) * kLn2;
+    f.loss[m] = r.loss;
+    if (f.lse != nullptr) f.lse[m] = r.lse;
   }
-  if (f.dX == nullptr) return;
-  const float g = has ? f.dloss[m] : 0.f, inv = 1.f / total, rest = others * inv;
+  const float g = has ? f.dloss[m] : 0.f;
   for (int64_t col = threadIdx.x * 8; col < f.H; col += 2048) {
     u32x4 o = {0u, 0u, 0u, 0u};
     if (has) {
@@ -679,67 +700,108 @@ __global__ __launch_bounds__(256) void k_head_finish(HeadFinish f) {
       label_row(f, y, col, w);
 #pragma unroll
       for (int d = 0; d < 4; ++d)
-        o[d] = pack_bf16x2(g * (v[2 * d] * scale * inv - rest * w[2 * d]),
-                           g * (v[2 * d + 1] * scale * inv - rest * w[2 * d + 1]));
+        o[d] = pack_bf16x2(g * (v[2 * d] * r.factor - r.rest * w[2 * d]), g * (v[2 * d + 1] * r.factor - r.rest * w[2 * d + 1]));
     }
     *reinterpret_cast<u32x4*>(f.dX + m * f.H + col) = o;
   }
 }
 
 template __global__ void k_head_logits<256, true>(HeadPiece);
+template __global__ void k_head_logits<192, true>(HeadPiece);
 template __global__ void k_head_logits<128, true>(HeadPiece);
 template __global__ void k_head_logits<64, true>(HeadPiece);
 template __global__ void k_head_logits<256, false>(HeadPiece);
+template __global__ void k_head_logits<192, false>(HeadPiece);
 template __global__ void k_head_logits<128, false>(HeadPiece);
 template __global__ void k_head_logits<64, false>(HeadPiece);
 template __global__ void k_head_grad<256>(HeadPiece, float*, int);
+template __global__ void k_head_grad<192>(HeadPiece, float*, int);
 template __global__ void k_head_grad<128>(HeadPiece, float*, int);
 template __global__ void k_head_grad<64>(HeadPiece, float*, int);
 
 namespace {
 constexpr int64_t kHeadCus = 256;  // of the part; fixed, so that sizes depend on shapes only
-int head_rows(int64_t T) { return T <= 64 ? 64 : T <= 128 ? 128 : 256; }
+
+// Rows of a tile.  A round of tiles (one a CU) of 64, 128, 192 and 256 rows takes 53,
+// 68, 95 and 107 us at 4096 columns: the shorter ones read more weights a
+// product, so which is best goes by how they fill the rounds.  Measured with one height
+// throughout (64 / 128 / 192 / 256), gradient calls: 40 x 50021 x 2304 136 / 140 / 146 /
+// 150 us, 200 x 32000 x 4096 203 / 174 / 192 / 200, 301 x 50021 x 2304 350 / 285 / 226 /
+// 250, 1024 x 32000 x 4096 722 / 495 / 508 / 440.
+struct HeadHeight {
+  int rows, cost;
+};
+constexpr HeadHeight kHeights[] = {{64, 53}, {128, 68}, {192, 95}, {256, 107}};
+
+int logits_rows(int64_t T, int64_t n) {
+  int best = 0;
+  int64_t least = 0;
+  for (const HeadHeight& h : kHeights) {
+    const int64_t cost = ceil_div(ceil_div(T, h.rows) * ceil_div(n, kBN), kHeadCus) * h.cost;
+    if (best == 0 || cost < least) best = h.rows, least = cost;
+  }
+  return best;
+}
+
+// The rows of a tile of E W and the ranges of the vocabulary, each of 1024 columns or
+// more: as many as give every CU a workgroup.
+struct GradShape {
+  int rows, splits;
+};
+GradShape grad_shape(int64_t T, int64_t H, int64_t n) {
+  GradShape best{0, 1};
+  int64_t least = 0;
+  const int64_t steps = round_up(n, kHeadTile) / kBK;
+  for (const HeadHeight& h : kHeights) {
+    const int64_t tiles = ceil_div(T, h.rows) * ceil_div(H, kBN);
+    int64_t S = kHeadCus / tiles;
+    if (S > steps / 16) S = steps / 16;
+    if (S < 1) S = 1;
+    const int64_t cost = ceil_div(tiles * S, kHeadCus) * ceil_div(steps, S) * h.cost;
+    if (best.rows == 0 || cost < least) best = GradShape{h.rows, static_cast<int>(S)}, least = cost;
+  }
+  return best;
+}
+
+template <class F>
+void with_rows(int rows, F f) {
+  if (rows == 64) f(std::integral_constant<int, 64>{});
+  else if (rows == 128) f(std::integral_constant<int, 128>{});
+  else if (rows == 192) f(std::integral_constant<int, 192>{});
+  else f(std::integral_constant<int, 256>{});
+}
 }  // namespace
 
 hipError_t launch_head_logits(const HeadPiece& p, hipStream_t s) {
-  const int bm = head_rows(p.T);
   const dim3 grid(static_cast<uint32_t>(kHeadCus));  // a multiple of the XCDs' number
-  const auto go = [&](auto b) {
+  with_rows(logits_rows(p.T, p.n), [&](auto b) {
     constexpr int BM = decltype(b)::value;
     if (p.E != nullptr) hipLaunchKernelGGL((k_head_logits<BM, true>), grid, dim3(256), 0, s, p);
     else hipLaunchKernelGGL((k_head_logits<BM, false>), grid, dim3(256), 0, s, p);
-  };
-  if (bm == 64) go(std::integral_constant<int, 64>{});
-  else if (bm == 128) go(std::integral_constant<int, 128>{});
-  else go(std::integral_constant<int, 256>{});
+  });
   return hipGetLastError();
 }
 
-hipError_t launch_head_rows(const HeadPiece& p, hipStream_t s) {
-  const int64_t tiles = p.lde / kHeadCols;
-  const int64_t ys = p.E == nullptr ? 1 : tiles < 32 ? ceil_div(tiles, 4) : 8;
-  hipLaunchKernelGGL(k_head_rows, dim3(static_cast<uint32_t>(ceil_div(p.T, 64)), static_cast<uint32_t>(ys)), dim3(256),
-                     0, s, p);
+hipError_t launch_head_rows(const HeadPiece& p, const HeadFinish& f, hipStream_t s) {
+  const int64_t blocks = p.lde / kHeadCols;
+  const int64_t ys = p.E == nullptr ? 1 : blocks < 8 * kRowWaves ? ceil_div(blocks, kRowWaves) : 8;
+  hipLaunchKernelGGL(k_head_rows, dim3(static_cast<uint32_t>(ceil_div(p.T, 64)), static_cast<uint32_t>(ys)),
+                     dim3(64 * kRowWaves), 0, s, p, f);
   return hipGetLastError();
 }
 
-// as many ranges of the vocabulary as give every CU a workgroup, each of
-// 1024 columns or more
-int head_splits(int64_t T, int64_t H, int64_t n) {
-  const int64_t tiles = ceil_div(T, head_rows(T)) * ceil_div(H, kBN), steps = round_up(n, kHeadTile) / 64;
-  int64_t S = kHeadCus / tiles;
-  if (S > steps / 16) S = steps / 16;
-  return S > 1 ? static_cast<int>(S) : 1;
-}
+int head_splits(int64_t T, int64_t H, int64_t n) { return grad_shape(T, H, n).splits; }
 
 hipError_t launch_head_grad(const HeadPiece& p, float* part, int splits, hipStream_t s) {
-  const int bm = head_rows(p.T);
-  const dim3 grid(static_cast<uint32_t>(ceil_div(p.T, bm)), static_cast<uint32_t>(ceil_div(p.H, kBN)),
+  // (the last piece and the last round may be smaller: the number of splits stays)
+  const int rows = grad_shape(p.T, p.H, p.n).rows;
+  const dim3 grid(static_cast<uint32_t>(ceil_div(p.T, rows)), static_cast<uint32_t>(ceil_div(p.H, kBN)),
                   static_cast<uint32_t>(splits));
   const int ks = static_cast<int>(ceil_div(p.lde / kBK, splits));
-  if (bm == 64) hipLaunchKernelGGL((k_head_grad<64>), grid, dim3(256), 0, s, p, part, ks);
-  else if (bm == 128) hipLaunchKernelGGL((k_head_grad<128>), grid, dim3(256), 0, s, p, part, ks);
-  else hipLaunchKernelGGL((k_head_grad<256>), grid, dim3(256), 0, s, p, part, ks);
+  with_rows(rows, [&](auto b) {
+    constexpr int BM = decltype(b)::value;
+    hipLaunchKernelGGL((k_head_grad<BM>), grid, dim3(256), 0, s, p, part, ks);
+  });
   return hipGetLastError();
 }
 

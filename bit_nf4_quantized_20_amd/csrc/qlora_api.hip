@@ -1250,9 +1250,9 @@ bool norm_shapes_ok(int64_t T, int64_t H) {
 // of one piece: E, 2 bytes a logit, then stays within the 256 MiB last-level
 // cache between the two products, and the fp32 sums of dX are read and written
 // once in n columns of work.
-constexpr int64_t kHeadTokens = 4096, kHeadLogits = int64_t(1) << 26;
+constexpr int64_t kHeadTokens = 4096, kHeadLogits = int64_t(1) << 27;
 // Weights of one piece that are written out in bf16.
-constexpr int64_t kHeadWeights = int64_t(1) << 26;
+constexpr int64_t kHeadWeights = int64_t(1) << 27;
 constexpr int64_t kHeadMaxHidden = 16384, kHeadMaxVocab = int64_t(1) << 24;
 
 bool head_shapes_ok(int64_t T, int64_t V, int64_t H) {
@@ -1358,6 +1358,14 @@ int head_loss_impl(const qlora_head* W, const qlora_bf16* X, int64_t T, const in
     p.tile_c = f32(lay.tile_c);
     p.tile_s = f32(lay.tile_s);
     p.factor = f32(lay.factor);
+    HeadFinish f{};
+    f.T = p.T;
+    f.H = H;
+    f.V = V;
+    f.labels = p.labels;
+    f.target = p.target;
+    f.loss = loss + t0;
+    f.lse = lse != nullptr ? lse + t0 : nullptr;
     int turn = 0;
     for (int64_t v0 = 0; v0 < V && e == hipSuccess; v0 += lay.n, turn ^= 1) {
       p.v0 = v0;
@@ -1376,33 +1384,24 @@ int head_loss_impl(const qlora_head* W, const qlora_bf16* X, int64_t T, const in
         p.W = W->bf16 + v0 * H;
       }
       if (e == hipSuccess) e = launch_head_logits(p, s);
-      if (e == hipSuccess) e = launch_head_rows(p, s);
+      if (e == hipSuccess) e = launch_head_rows(p, !grad && v0 + lay.n >= V ? f : HeadFinish{}, s);
       if (e == hipSuccess && grad) e = launch_head_grad(p, f32(lay.part), lay.splits, s);
     }
-    HeadFinish f{};
-    f.T = p.T;
-    f.H = H;
-    f.V = V;
-    f.labels = p.labels;
-    f.target = p.target;
+    if (!grad) continue;
     f.c = f32(lay.c[turn]);
     f.s = f32(lay.s[turn]);
-    f.loss = loss + t0;
-    f.lse = lse != nullptr ? lse + t0 : nullptr;
-    if (grad) {
-      f.part = f32(lay.part);
-      f.splits = lay.splits;
-      f.dloss = dloss + t0;
-      f.dX = dX + t0 * H;
-      f.W.w16 = W->bf16;
-      if (W->nf4 != nullptr) {
-        f.W.codes = W->nf4->codes;
-        f.W.absmax_q = absmax_fp32(*W->nf4) ? nullptr : W->nf4->absmax_q;
-        f.W.scale = W->nf4->absmax_scale;
-      } else if (W->fp8 != nullptr) {
-        f.W.codes = W->fp8->codes;
-        f.W.scale8 = W->fp8->scales;
-      }
+    f.part = f32(lay.part);
+    f.splits = lay.splits;
+    f.dloss = dloss + t0;
+    f.dX = dX + t0 * H;
+    f.W.w16 = W->bf16;
+    if (W->nf4 != nullptr) {
+      f.W.codes = W->nf4->codes;
+      f.W.absmax_q = absmax_fp32(*W->nf4) ? nullptr : W->nf4->absmax_q;
+      f.W.scale = W->nf4->absmax_scale;
+    } else if (W->fp8 != nullptr) {
+      f.W.codes = W->fp8->codes;
+      f.W.scale8 = W->fp8->scales;
     }
     if (e == hipSuccess) e = launch_head_finish(f, s);
   }

@@ -139,15 +139,15 @@ def test_quantized_heads(kind, T, V, H):
 
 
 def test_vocabulary_in_pieces_16_bit():
-    """4096 rows and 40000 columns: three pieces, a last one that ends inside a
-    tile; rows in one round, then 4100 rows in two."""
+    """4096 rows and 70001 columns: three pieces, a last one that ends inside a
+    tile; rows in one round, then 4100 rows in two (with fewer pieces)."""
     q = require_gpu()
-    V, H = 40001, 64
+    V, H = 70001, 64
     W, Wv = _head(q, "bf16", 5, V, H, 0.5)
     for T in (4096, 4100):
         banner(f"head pieces {T}x{V}x{H}")
         X, y = dev_bf16(_bf16(6, (T, H))), _labels(7, T, V)
-        y[10], y[11], y[12], y[13] = 16127, 16128, 13568, V - 1  # next to where pieces meet
+        y[10:16] = 23551, 23552, 35071, 35072, 47104, V - 1  # next to where pieces meet
         g = np.abs(synth.normal_f32(8, (T,), 1.0))
         out = q.qlora_head_loss_grad(W, X, _dev(y), dev_f32(g), ws=_poisoned(q, T, V, H, False, True))
         rows = np.concatenate([np.arange(0, 20), np.arange(2040, 2060), np.arange(T - 30, T)])
@@ -157,13 +157,13 @@ def test_vocabulary_in_pieces_16_bit():
 
 @pytest.mark.parametrize("kind", ["nf4", "nodq", "fp8"])
 def test_vocabulary_in_pieces_quantized(kind):
-    """Rows of 16384 columns: pieces of 2^26 weights, 4096 rows of the head; 128-row
-    blocks and 16384-weight groups begin anew in each piece."""
+    """Rows of 16384 columns: pieces of at most 2^27 weights, two of 4352 and 3904 rows
+    of the head; 128-row blocks and 16384-weight groups begin anew in each piece."""
     q = require_gpu()
-    T, V, H = 3, 4544, 16384
+    T, V, H = 3, 8256, 16384
     banner(f"head pieces {kind} {T}x{V}x{H}")
     W, Wv = _head(q, kind, 9, V, H, 0.03)
-    X, y = dev_bf16(_bf16(10, (T, H))), np.array([4095, 4543, 2304])
+    X, y = dev_bf16(_bf16(10, (T, H))), np.array([4351, 4352, 8255])
     g = np.array([1.0, -2.0, 0.5], dtype=np.float32)
     _compare(X, Wv, y, g, *q.qlora_head_loss_grad(W, X, _dev(y), dev_f32(g), ws=_poisoned(q, T, V, H, True, True)))
     _compare(X, Wv, y, g, *q.qlora_head_loss(W, X, _dev(y)))
@@ -200,11 +200,12 @@ def test_cells_across_pieces():
     both sides of a cell's border (64 in powers of two)."""
     q = require_gpu()
     banner("head cells across pieces")
-    T, V, H = 4096, 40000, 64
+    T, V, H = 4096, 70000, 64
     W = dev_bf16(_bf16(14, (V, H), 0.05))
     W[:, 0] = 0
     W[16000:16010, 0] = 1
     W[30000:30010, 0] = 2
+    W[60000:60010, 0] = 4
     W[300:303, 1] = 8
     Wv = _wide(W)
     X = dev_bf16(_bf16(15, (T, H), 0.5))
@@ -214,7 +215,8 @@ def test_cells_across_pieces():
     X[1000:1100, 1] = 44.0 / 8      # logits of 44: powers of two of 63.5
     X[1100:1200, 1] = 44.75 / 8     # 64.6
     y = _labels(16, T, V)
-    y[2000:2040] = 30000
+    y[2000:2020] = 30000
+    y[2020:2040] = 60003
     y[3000:3040] = 16003
     y[1000:1020] = 301
     g = np.ones(T, dtype=np.float32)

@@ -230,7 +230,7 @@ def test_head_workspace_is_bounded(lib):
     workspace does not grow with either."""
     lib.qlora_head_workspace_bytes.restype = ctypes.c_size_t
     w = lambda T, v, h, e, g: lib.qlora_head_workspace_bytes(i64(T), i64(v), i64(h), e, g)
-    assert w(4096, 128000, 4096, 0, 1) < 256 << 20
+    assert w(4096, 128000, 4096, 0, 1) < 512 << 20
     assert w(1 << 20, 1 << 24, 4096, 1, 1) < 1 << 30
     assert w(1 << 20, 128000, 4096, 0, 1) <= w(4096, 128000, 4096, 0, 1)
     # no rows: the smallest there is, no division by their number
