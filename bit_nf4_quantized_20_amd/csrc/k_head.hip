@@ -671,74 +671,71 @@ __device__ __forceinline__ void label_row(const HeadFinish& f, int64_t y, int64_
   }
 }
 
-// dX, loss and lse, one workgroup a row.
+// dX, loss and lse: workgroup (row, 2048 columns).
 __global__ __launch_bounds__(256) void k_head_finish(HeadFinish f) {
-  const int64_t m = blockIdx.x;
+  const int64_t m = blockIdx.x, col = blockIdx.y * 2048 + threadIdx.x * 8;
   const int64_t y = f.labels[m];
   const bool has = y >= 0 && y < f.V;
   const RowLoss r = row_loss(f.c[m], f.s[m], has, has ? f.target[m] : 0.f);
-  if (threadIdx.x == 0) {
+  if (threadIdx.x == 0 && blockIdx.y == 0) {
     f.loss[m] = r.loss;
     if (f.lse != nullptr) f.lse[m] = r.lse;
   }
-  const float g = has ? f.dloss[m] : 0.f;
-  for (int64_t col = threadIdx.x * 8; col < f.H; col += 2048) {
-    u32x4 o = {0u, 0u, 0u, 0u};
-    if (has) {
-      float v[8], w[8];
+  if (col >= f.H) return;
+  u32x4 o = {0u, 0u, 0u, 0u};
+  if (has) {
+    const float g = f.dloss[m];
+    float v[8], w[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = 0.f;
-      for (int z = 0; z < f.splits; ++z) {
-        const float* src = f.part + (z * f.T + m) * f.H + col;
-        const f32x4 a = *reinterpret_cast<const f32x4*>(src), b = *reinterpret_cast<const f32x4*>(src + 4);
+    for (int e = 0; e < 8; ++e) v[e] = 0.f;
+    for (int z = 0; z < f.splits; z += 8) {  // in order, eight splits in flight
+      f32x4 u[8][2];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          v[e] += a[e];
-          v[4 + e] += b[e];
-        }
+      for (int k = 0; k < 8; ++k) {
+        const float* src = f.part + ((z + k < f.splits ? z + k : 0) * f.T + m) * f.H + col;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          u[k][h] = z + k < f.splits ? *reinterpret_cast<const f32x4*>(src + 4 * h) : f32x4{0.f, 0.f, 0.f, 0.f};
       }
-      label_row(f, y, col, w);
 #pragma unroll
-      for (int d = 0; d < 4; ++d)
-        o[d] = pack_bf16x2(g * (v[2 * d] * r.factor - r.rest * w[2 * d]), g * (v[2 * d + 1] * r.factor - r.rest * w[2 * d + 1]));
+      for (int k = 0; k < 8; ++k)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[4 * h + e] += u[k][h][e];
     }
-    *reinterpret_cast<u32x4*>(f.dX + m * f.H + col) = o;
+    label_row(f, y, col, w);
+#pragma unroll
+    for (int d = 0; d < 4; ++d)
+      o[d] = pack_bf16x2(g * (v[2 * d] * r.factor - r.rest * w[2 * d]), g * (v[2 * d + 1] * r.factor - r.rest * w[2 * d + 1]));
   }
+  *reinterpret_cast<u32x4*>(f.dX + m * f.H + col) = o;
 }
 
-template __global__ void k_head_logits<256, true>(HeadPiece);
-template __global__ void k_head_logits<192, true>(HeadPiece);
-template __global__ void k_head_logits<128, true>(HeadPiece);
-template __global__ void k_head_logits<64, true>(HeadPiece);
-template __global__ void k_head_logits<256, false>(HeadPiece);
-template __global__ void k_head_logits<192, false>(HeadPiece);
-template __global__ void k_head_logits<128, false>(HeadPiece);
-template __global__ void k_head_logits<64, false>(HeadPiece);
-template __global__ void k_head_grad<256>(HeadPiece, float*, int);
-template __global__ void k_head_grad<192>(HeadPiece, float*, int);
-template __global__ void k_head_grad<128>(HeadPiece, float*, int);
-template __global__ void k_head_grad<64>(HeadPiece, float*, int);
+#define HEAD_KERNELS(BM)                                       \
+  template __global__ void k_head_logits<BM, true>(HeadPiece);  \
+  template __global__ void k_head_logits<BM, false>(HeadPiece); \
+  template __global__ void k_head_grad<BM>(HeadPiece, float*, int);
+HEAD_KERNELS(64) HEAD_KERNELS(96) HEAD_KERNELS(128) HEAD_KERNELS(160) HEAD_KERNELS(192) HEAD_KERNELS(224) HEAD_KERNELS(256)
 
 namespace {
 constexpr int64_t kHeadCus = 256;  // of the part; fixed, so that sizes depend on shapes only
 
 // Rows of a tile.  A round of tiles (one a CU) of 64, 128, 192 and 256 rows takes 53,
-// 68, 95 and 107 us at 4096 columns: the shorter ones read more weights a
-// product, so which is best goes by how they fill the rounds.  Measured with one height
-// throughout (64 / 128 / 192 / 256), gradient calls: 40 x 50021 x 2304 136 / 140 / 146 /
-// 150 us, 200 x 32000 x 4096 203 / 174 / 192 / 200, 301 x 50021 x 2304 350 / 285 / 226 /
-// 250, 1024 x 32000 x 4096 722 / 495 / 508 / 440.
-struct HeadHeight {
-  int rows, cost;
-};
-constexpr HeadHeight kHeights[] = {{64, 53}, {128, 68}, {192, 95}, {256, 107}};
+// 68, 95 and 107 us at 4096 columns, about 36 + 0.28 rows: the shorter ones read more
+// weights a product, so which is best goes by how they fill the rounds.  Measured with
+// one height throughout (64 / 128 / 192 / 256), gradient calls: 40 x 50021 x 2304 136 /
+// 140 / 146 / 150 us, 200 x 32000 x 4096 203 / 174 / 192 / 200, 301 x 50021 x 2304 350 /
+// 285 / 226 / 250, 1024 x 32000 x 4096 722 / 495 / 508 / 440.
+constexpr int kHeights[] = {64, 96, 128, 160, 192, 224, 256};
+constexpr int64_t height_cost(int rows) { return 128 + rows; }
 
 int logits_rows(int64_t T, int64_t n) {
   int best = 0;
   int64_t least = 0;
-  for (const HeadHeight& h : kHeights) {
-    const int64_t cost = ceil_div(ceil_div(T, h.rows) * ceil_div(n, kBN), kHeadCus) * h.cost;
-    if (best == 0 || cost < least) best = h.rows, least = cost;
+  for (int rows : kHeights) {
+    const int64_t cost = ceil_div(ceil_div(T, rows) * ceil_div(n, kBN), kHeadCus) * height_cost(rows);
+    if (best == 0 || cost < least) best = rows, least = cost;
   }
   return best;
 }
@@ -752,13 +749,13 @@ GradShape grad_shape(int64_t T, int64_t H, int64_t n) {
   GradShape best{0, 1};
   int64_t least = 0;
   const int64_t steps = round_up(n, kHeadTile) / kBK;
-  for (const HeadHeight& h : kHeights) {
-    const int64_t tiles = ceil_div(T, h.rows) * ceil_div(H, kBN);
+  for (int rows : kHeights) {
+    const int64_t tiles = ceil_div(T, rows) * ceil_div(H, kBN);
     int64_t S = kHeadCus / tiles;
     if (S > steps / 16) S = steps / 16;
     if (S < 1) S = 1;
-    const int64_t cost = ceil_div(tiles * S, kHeadCus) * ceil_div(steps, S) * h.cost;
-    if (best.rows == 0 || cost < least) best = GradShape{h.rows, static_cast<int>(S)}, least = cost;
+    const int64_t cost = ceil_div(tiles * S, kHeadCus) * ceil_div(steps, S) * height_cost(rows);
+    if (best.rows == 0 || cost < least) best = GradShape{rows, static_cast<int>(S)}, least = cost;
   }
   return best;
 }
@@ -766,8 +763,11 @@ GradShape grad_shape(int64_t T, int64_t H, int64_t n) {
 template <class F>
 void with_rows(int rows, F f) {
   if (rows == 64) f(std::integral_constant<int, 64>{});
+  else if (rows == 96) f(std::integral_constant<int, 96>{});
   else if (rows == 128) f(std::integral_constant<int, 128>{});
+  else if (rows == 160) f(std::integral_constant<int, 160>{});
   else if (rows == 192) f(std::integral_constant<int, 192>{});
+  else if (rows == 224) f(std::integral_constant<int, 224>{});
   else f(std::integral_constant<int, 256>{});
 }
 }  // namespace
@@ -806,7 +806,8 @@ hipError_t launch_head_grad(const HeadPiece& p, float* part, int splits, hipStre
 }
 
 hipError_t launch_head_finish(const HeadFinish& f, hipStream_t s) {
-  hipLaunchKernelGGL(k_head_finish, dim3(static_cast<uint32_t>(f.T)), dim3(256), 0, s, f);
+  hipLaunchKernelGGL(k_head_finish, dim3(static_cast<uint32_t>(f.T), static_cast<uint32_t>(ceil_div(f.H, 2048))), dim3(256),
+                     0, s, f);
   return hipGetLastError();
 }
 
