@@ -175,6 +175,17 @@ def test_rows_that_are_not_finite_stay_alone(H):
     assert bool(torch.isnan(q.qlora_rmsnorm_fwd(zero, w, eps=0.0)[0]).all())
 
 
+def test_more_rows_than_workgroups():
+    """Rows behind the last workgroup's first are those of a call of their own."""
+    q = require_gpu()
+    T, H, n = 16500, 2112, 16300
+    x, r, w = _rows(41, 200, H).repeat(83, 1)[:T].contiguous(), _rows(42, T, H), _weight(43, H)
+    y, rows, h, rstd = q.qlora_rmsnorm_fwd(x, w, residual=r, rows8=True)
+    z, tail, g, s = q.qlora_rmsnorm_fwd(x[n:], w, residual=r[n:], rows8=True)
+    assert torch.equal(y[n:], z) and torch.equal(h[n:], g) and torch.equal(rstd[n:], s)
+    assert torch.equal(rows.codes[n:], tail.codes) and torch.equal(rows.scales[:, n:T], tail.scales[:, :T - n])
+
+
 def test_empty():
     q = require_gpu()
     banner("norm T=0")
