@@ -627,15 +627,17 @@ class FP8Weight:
         return _FP8WeightC(self.codes.data_ptr(), self.scales.data_ptr(), self.rows, self.cols, 0)
 
 
-def _arg(t, dtype, shape, name: str, dev):
+def _arg(t, dtype, shape, name: str, dev, index: int = None):
     """A contiguous tensor of this type, device and size (shape: its sizes, or
-    its element count).  One chain of tests for the call that is right; what
+    its element count); index: its place in a list.  One chain of tests for the call that is right; what
     is wrong is found out afterwards."""
     if (t is not None and t.dtype is dtype and t.device == dev and t.is_contiguous() and dev.type == "cuda"
             and (t.numel() == shape if type(shape) is int else t.shape == shape)):
         return
+    if index is not None:
+        name = f"{name}[{index}]"
     _arg_rest(t, dtype, name, dev)
-    raise ValueError(f"{name}: expected {shape} elements, got {tuple(t.shape)}")
+    raise ValueError(f"{name}: expected {tuple(shape) if type(shape) is torch.Size else shape} elements, got {tuple(t.shape)}")
 
 
 def _rows_arg(t, dtype, rows: int, cols: int, name: str, dev):
@@ -1168,7 +1170,8 @@ def qlora_adamw_plan(params, masters, grads, state: AdamWState) -> AdamWPlan:
     """Binds tensors to their states.  params: bf16 tensors or None, masters: fp32
     tensors or None (one of the two per tensor, or both: the master and the copy
     that the layers read; either list may be None), grads: fp32, of the same sizes.
-    The dA, dB of the layers are written into grads with their output arguments."""
+    The dA, dB of the layers are written into grads with their output arguments.
+    Waits for the current stream; not while it is being captured."""
     n = len(grads)
     params, masters = params if params is not None else [None] * n, masters if masters is not None else [None] * n
     if len(params) != n or len(masters) != n:
@@ -1183,14 +1186,15 @@ def qlora_adamw_plan(params, masters, grads, state: AdamWState) -> AdamWPlan:
             raise TypeError(f"grads[{i}]: expected a tensor, got {type(g).__name__}")
         if p is None and f is None:
             raise TypeError(f"params[{i}], masters[{i}]: one of them is needed")
-        _arg(g, torch.float32, tuple(g.shape), f"grads[{i}]", dev)
+        shape, k = g.shape, g.numel()
+        _arg(g, torch.float32, shape, "grads", dev, i)
         if p is not None:
-            _arg(p, torch.bfloat16, tuple(g.shape), f"params[{i}]", dev)
+            _arg(p, torch.bfloat16, shape, "params", dev, i)
         if f is not None:
-            _arg(f, torch.float32, tuple(g.shape), f"masters[{i}]", dev)
-        numel.append(g.numel())
+            _arg(f, torch.float32, shape, "masters", dev, i)
+        numel.append(k)
         offsets.append(total)
-        total += -(-g.numel() // 128) * 128
+        total += -(-k // 128) * 128
     length = qlora_adamw_state_len(numel)
     kind = torch.uint8 if bits == 8 else torch.float32
     _arg(state.m, kind, length, "state.m", dev)
@@ -1198,6 +1202,8 @@ def qlora_adamw_plan(params, masters, grads, state: AdamWState) -> AdamWPlan:
     if bits == 8:
         _arg(state.m_scales, torch.uint8, length // 128, "state.m_scales", dev)
         _arg(state.v_scales, torch.uint8, length // 128, "state.v_scales", dev)
+    if _capturing(dev):
+        raise RuntimeError("qlora_adamw_plan: the current stream is being captured")
     need = int(_lib.qlora_adamw_table_bytes(_numels(numel), n))
     table = torch.empty(need, dtype=torch.uint8, device=dev)
     ptr = (lambda t: t.data_ptr() if t is not None else None)

@@ -387,12 +387,6 @@ struct AdamChunk {
   int64_t state;  // the chunk's first element in m and v, a multiple of kAdamBlock
   int32_t n, pad;
 };
-struct AdamTensor {
-  uint16_t* p; float* master; const float* g;
-  int64_t numel, chunk0, state0;
-};
-// writes the entries of count tensors
-hipError_t launch_adamw_plan(const AdamTensor* t, int64_t count, AdamChunk* table, hipStream_t s);
 struct AdamStep {
   const AdamChunk* table;
   int64_t chunks;

@@ -4,6 +4,8 @@
 //   p' = p - lr wd p - lr / (1 - b1^t) m' / (sqrt(v') / sqrt(1 - b2^t) + eps)
 // Every element is read and written once: bound by HBM (30 bytes an element
 // with fp32 states, a master copy and its bf16 parameter; 18 with 8-bit states).
+// The factors of seven projections in 32 layers, 41.9 million elements: 232 us and
+// 140 us in 8 bits, 5.4 TB/s both (a 2 GiB copy reaches 4.8).
 //
 // The 8-bit states are m and r = sqrt(v) as e4m3 codes with one power-of-two
 // scale per 128 elements of a tensor (fp8_format.hpp).  r instead of v halves
@@ -42,32 +44,8 @@ __device__ __forceinline__ uint32_t code_with_noise(float y, uint32_t byte) {
 
 }  // namespace
 
-// The chunk's tensor is found by its number's range; kAdamTensors of them are
-// passed by value.
-constexpr int kAdamTensors = 56;
-struct AdamTensors {
-  AdamTensor t[kAdamTensors];
-  int count;
-  int64_t chunks;  // of these tensors
-};
-__global__ __launch_bounds__(256) void k_adamw_plan(AdamTensors a, AdamChunk* table) {
-  const int64_t id = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (id >= a.chunks) return;
-  const int64_t chunk = a.t[0].chunk0 + id;
-  int i = 0;
-  while (i + 1 < a.count && chunk >= a.t[i + 1].chunk0) ++i;
-  const AdamTensor t = a.t[i];
-  const int64_t first = (chunk - t.chunk0) * kAdamChunk;
-  AdamChunk c{};
-  c.p = t.p != nullptr ? t.p + first : nullptr;
-  c.master = t.master != nullptr ? t.master + first : nullptr;
-  c.g = t.g + first;
-  c.state = t.state0 + first;
-  c.n = static_cast<int32_t>(t.numel - first < kAdamChunk ? t.numel - first : kAdamChunk);
-  table[chunk] = c;
-}
-
-// One workgroup a chunk, eight elements a lane; 16 lanes hold a block of 128.
+// One workgroup a chunk, eight elements a lane; 16 lanes hold a block of 128.  The
+// chunks come from a table in device memory: one launch for any number of tensors.
 // The state sums are formed without fused multiply-adds: each is then the two
 // rounded products' rounded sum, as fp32 tensor operations form it, and the
 // codes of a state do not depend on how the sum was compiled.
@@ -220,21 +198,6 @@ __global__ __launch_bounds__(256) void k_adamw(AdamStep a) {
       a.vs[at / kAdamBlock] = static_cast<uint8_t>(vb);
     }
   }
-}
-
-hipError_t launch_adamw_plan(const AdamTensor* t, int64_t count, AdamChunk* table, hipStream_t s) {
-  for (int64_t i = 0; i < count; i += kAdamTensors) {
-    AdamTensors a{};
-    a.count = static_cast<int>(count - i < kAdamTensors ? count - i : kAdamTensors);
-    for (int k = 0; k < a.count; ++k) {
-      a.t[k] = t[i + k];
-      a.chunks += ceil_div(t[i + k].numel, kAdamChunk);
-    }
-    if (a.chunks == 0) continue;
-    hipLaunchKernelGGL(k_adamw_plan, dim3(static_cast<uint32_t>(ceil_div(a.chunks, 256))), dim3(256), 0, s, a, table);
-    if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-  }
-  return hipSuccess;
 }
 
 hipError_t launch_adamw(const AdamStep& a, bool bits8, hipStream_t s) {

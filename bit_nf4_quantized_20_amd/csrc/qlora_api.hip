@@ -58,6 +58,9 @@ void* device_scratch() {
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+// of what is read or written an element at a time (a slice of a longer vector)
+template <class T>
+bool aligned1(const T* p) { return (reinterpret_cast<uintptr_t>(p) & (sizeof(T) - 1)) == 0; }
 
 int launched(hipError_t e) { return e == hipSuccess ? QLORA_OK : QLORA_ERR_LAUNCH; }
 
@@ -1249,7 +1252,8 @@ bool norm_shapes_ok(int64_t T, int64_t H) {
 // Tokens of one round over the vocabulary, and the most logits (rows by columns)
 // of one piece: E, 2 bytes a logit, then stays within the 256 MiB last-level
 // cache between the two products, and the fp32 sums of dX are read and written
-// once in n columns of work.
+// once in n columns of work.  Without a gradient it is the blocks' cells and sums
+// that want an end, 8 bytes for 128 logits: 64 times as many take 512 MiB.
 constexpr int64_t kHeadTokens = 4096, kHeadLogits = int64_t(1) << 27;
 // Weights of one piece that are written out in bf16.
 constexpr int64_t kHeadWeights = int64_t(1) << 27;
@@ -1271,7 +1275,8 @@ HeadLayout head_layout(int64_t T, int64_t V, int64_t H, bool expand, bool grad) 
   l.tokens = rounds > 1 ? round_up(ceil_div(T, rounds), 256) : T;
   const int64_t rows = l.tokens > 0 ? l.tokens : 1;
   int64_t most = round_up(V, kHeadTile);
-  if (grad && most > kHeadLogits / rows) most = kHeadLogits / rows;
+  const int64_t logits = grad ? kHeadLogits : kHeadLogits * 64;
+  if (most > logits / rows) most = logits / rows;
   if (expand && most > kHeadWeights / H) most = kHeadWeights / H;
   // the second product addresses a piece's rows with 32-bit offsets
   if (grad && most > (int64_t(1) << 29) / H) most = (int64_t(1) << 29) / H;
@@ -1334,8 +1339,8 @@ int head_loss_impl(const qlora_head* W, const qlora_bf16* X, int64_t T, const in
   if (!head_shapes_ok(T, V, H)) return QLORA_ERR_SHAPE;
   if (T == 0) return QLORA_OK;
   if (!X || !labels || !loss || (grad && (!dloss || !dX))) return QLORA_ERR_NULL;
-  if (!aligned16(X) || !aligned16(labels) || !aligned16(loss) || !aligned16(lse) ||
-      (grad && (!aligned16(dloss) || !aligned16(dX))))
+  if (!aligned16(X) || !aligned1(labels) || !aligned1(loss) || !aligned1(lse) ||
+      (grad && (!aligned1(dloss) || !aligned16(dX))))
     return QLORA_ERR_ALIGN;
   const bool expand = W->bf16 == nullptr;
   const HeadLayout lay = head_layout(T, V, H, expand, grad);
@@ -1423,10 +1428,14 @@ bool adamw_sizes(const int64_t* numel, int64_t n, int64_t* state, int64_t* chunk
   return true;
 }
 
-// whether two of the n ranges share a byte (they are sorted for it)
 struct AdamRange {
   uintptr_t at, end;
 };
+AdamRange adamw_range(const void* p, int64_t bytes) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+  return AdamRange{at, at + static_cast<uintptr_t>(bytes)};
+}
+// whether two of the n ranges share a byte (they are sorted for it)
 bool overlap(AdamRange* r, int64_t n) {
   std::sort(r, r + n, [](const AdamRange& a, const AdamRange& b) { return a.at < b.at; });
   for (int64_t i = 1; i < n; ++i)
@@ -1460,7 +1469,7 @@ int qlora_rmsnorm_fwd(const qlora_bf16* x, const qlora_bf16* residual, const flo
       (!y && !codes))
     return QLORA_ERR_NULL;
   if (!aligned16(x) || !aligned16(residual) || !aligned16(weight) || !aligned16(h) || !aligned16(y) ||
-      !aligned16(codes) || !aligned16(scales) || !aligned16(rstd))
+      !aligned16(codes) || !aligned16(scales) || !aligned1(rstd))
     return QLORA_ERR_ALIGN;
   if (int st = check_device()) return st;
   NormFwd a{};
@@ -1491,7 +1500,7 @@ int qlora_rmsnorm_bwd(const qlora_bf16* dy, const qlora_bf16* h, const float* we
                       size_t ws_bytes, qlora_stream stream) {
   if (!norm_shapes_ok(T, H)) return QLORA_ERR_SHAPE;
   if (T > 0 && (!dy || !h || !weight || !rstd || !dh)) return QLORA_ERR_NULL;
-  if (!aligned16(dy) || !aligned16(h) || !aligned16(weight) || !aligned16(rstd) || !aligned16(dres) ||
+  if (!aligned16(dy) || !aligned16(h) || !aligned16(weight) || !aligned1(rstd) || !aligned16(dres) ||
       !aligned16(dh) || !aligned16(dweight))
     return QLORA_ERR_ALIGN;
   if (T == 0 && !dweight) return QLORA_OK;
@@ -1547,42 +1556,50 @@ int qlora_adamw_plan(const qlora_adamw_tensor* tensors, int64_t n, void* table, 
   if (!out || !table || (n > 0 && !tensors)) return QLORA_ERR_NULL;
   if (!aligned16(table)) return QLORA_ERR_ALIGN;
   // (nothrow: an exception must not leave a C entry point)
-  std::unique_ptr<AdamTensor[]> list(new (std::nothrow) AdamTensor[n > 0 ? n : 1]);
   std::unique_ptr<int64_t[]> numel(new (std::nothrow) int64_t[n > 0 ? n : 1]);
-  std::unique_ptr<AdamRange[]> written(new (std::nothrow) AdamRange[n > 0 ? 3 * n : 1]);
-  if (!list || !numel || !written) return QLORA_ERR_LAUNCH;
+  std::unique_ptr<AdamRange[]> written(new (std::nothrow) AdamRange[n > 0 ? 2 * n : 1]);
+  if (!numel || !written) return QLORA_ERR_LAUNCH;
   for (int64_t i = 0; i < n; ++i) numel[i] = tensors[i].numel;
-  int64_t state, chunks;
+  int64_t state, chunks, ranges = 0;
   if (!adamw_sizes(numel.get(), n, &state, &chunks)) return QLORA_ERR_SHAPE;
-  int64_t ranges = 0;
-  int64_t chunk0 = 0, state0 = 0;
   for (int64_t i = 0; i < n; ++i) {
     const qlora_adamw_tensor& t = tensors[i];
-    if (t.numel > 0) {
-      if ((!t.param && !t.master) || !t.grad) return QLORA_ERR_NULL;
-      if (!aligned16(t.param) || !aligned16(t.master) || !aligned16(t.grad)) return QLORA_ERR_ALIGN;
-      const auto add = [&](const void* p, int64_t bytes) {
-        const uintptr_t at = reinterpret_cast<uintptr_t>(p);
-        if (p != nullptr) written[ranges++] = AdamRange{at, at + static_cast<uintptr_t>(bytes)};
-      };
-      add(t.param, 2 * t.numel);
-      add(t.master, 4 * t.numel);
-    }
-    list[i] = AdamTensor{t.param, t.master, t.grad, t.numel, chunk0, state0};
-    chunk0 += ceil_div(t.numel, kAdamChunk);
-    state0 += round_up(t.numel, kAdamBlock);
+    if (t.numel == 0) continue;
+    if ((!t.param && !t.master) || !t.grad) return QLORA_ERR_NULL;
+    if (!aligned16(t.param) || !aligned16(t.master) || !aligned16(t.grad)) return QLORA_ERR_ALIGN;
+    if (t.param) written[ranges++] = adamw_range(t.param, 2 * t.numel);
+    if (t.master) written[ranges++] = adamw_range(t.master, 4 * t.numel);
   }
   if (overlap(written.get(), ranges)) return QLORA_ERR_VALUE;
-  for (int64_t i = 0; i < n; ++i) {
-    const uintptr_t at = reinterpret_cast<uintptr_t>(tensors[i].grad);
-    if (tensors[i].numel > 0 &&
-        meets(written.get(), ranges, AdamRange{at, at + 4 * static_cast<uintptr_t>(tensors[i].numel)}))
-      return QLORA_ERR_VALUE;
-  }
+  for (int64_t i = 0; i < n; ++i)
+    if (numel[i] > 0 && meets(written.get(), ranges, adamw_range(tensors[i].grad, 4 * numel[i]))) return QLORA_ERR_VALUE;
   if (table_bytes < static_cast<size_t>(chunks) * sizeof(AdamChunk)) return QLORA_ERR_WORKSPACE;
   if (int st = check_device()) return st;
-  if (const hipError_t e = launch_adamw_plan(list.get(), n, static_cast<AdamChunk*>(table), static_cast<hipStream_t>(stream));
-      e != hipSuccess)
+  // Written by the time the call returns: a step on another stream, or one in front of
+  // the replay of a graph that holds the plan, would follow addresses that are not there.
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  hipStreamCaptureStatus capture = hipStreamCaptureStatusNone;
+  if (hipStreamIsCapturing(s, &capture) != hipSuccess || capture != hipStreamCaptureStatusNone) return QLORA_ERR_LAUNCH;
+  std::unique_ptr<AdamChunk[]> list(new (std::nothrow) AdamChunk[chunks > 0 ? chunks : 1]);
+  if (!list) return QLORA_ERR_LAUNCH;
+  AdamChunk* at = list.get();
+  int64_t state0 = 0;
+  for (int64_t i = 0; i < n; ++i) {
+    const qlora_adamw_tensor& t = tensors[i];
+    for (int64_t first = 0; first < t.numel; first += kAdamChunk) {
+      AdamChunk& c = *at++;
+      c.p = t.param ? t.param + first : nullptr;
+      c.master = t.master ? t.master + first : nullptr;
+      c.g = t.grad + first;
+      c.state = state0 + first;
+      c.n = static_cast<int32_t>(t.numel - first < kAdamChunk ? t.numel - first : kAdamChunk);
+      c.pad = 0;
+    }
+    state0 += round_up(t.numel, kAdamBlock);
+  }
+  if (chunks > 0 && (hipMemcpyAsync(table, list.get(), static_cast<size_t>(chunks) * sizeof(AdamChunk),
+                                    hipMemcpyHostToDevice, s) != hipSuccess ||
+                     hipStreamSynchronize(s) != hipSuccess))
     return QLORA_ERR_LAUNCH;
   *out = qlora_adamw_table{table, chunks, state};
   return QLORA_OK;
@@ -1600,8 +1617,9 @@ int qlora_adamw_step(const qlora_adamw_table* table, int bits, void* m, void* v,
   if (table->chunks == 0) return QLORA_OK;
   if (!table->table || !m || !v || (bits == 8 && (!m_scales || !v_scales))) return QLORA_ERR_NULL;
   if (!aligned16(table->table) || !aligned16(m) || !aligned16(v) ||
-      (bits == 8 && (!aligned16(m_scales) || !aligned16(v_scales))) || (reinterpret_cast<uintptr_t>(grad_scale) & 3u) != 0)
+      (bits == 8 && (!aligned16(m_scales) || !aligned16(v_scales))) || !aligned1(grad_scale))
     return QLORA_ERR_ALIGN;
+  if (m == v || (bits == 8 && m_scales == v_scales)) return QLORA_ERR_VALUE;
   if (int st = check_device()) return st;
   const double t = static_cast<double>(rates->step);
   AdamStep a{};

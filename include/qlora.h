@@ -622,7 +622,7 @@ int qlora_moe_fwd(const qlora_nf4_weight* gate_up, const qlora_nf4_weight* down,
  * addition and with 8-bit rows for the layer behind it:
  *   h    = bf16(x + residual)            [T, H] bf16 (residual NULL: h is x, and
  *                                        the argument h must be NULL)
- *   rstd = 1 / sqrt(mean h^2 + eps)      [T] fp32, or NULL
+ *   rstd = 1 / sqrt(mean h^2 + eps)      [T] fp32 (any alignment of a float), or NULL
  *   y    = bf16(h rstd weight)           [T, H] bf16, or NULL with codes
  *   codes, scales: y as quantized rows (above), or both NULL
  *   x, residual [T, H] bf16;  weight [H] fp32;  eps >= 0
@@ -676,6 +676,7 @@ typedef struct {
  * The logits are formed once for both.  W is frozen and has no gradient.
  *   X [T, hidden] bf16;  labels [T] int64: a label outside [0, vocab) is none (a
  *   prompt, a padded row): loss 0 and a dX row of zeros, whatever the row holds
+ *   labels, dloss, loss and lse may begin at any of their elements (labels + 1)
  *   hidden a multiple of 64, 64 .. 16384;  1 <= vocab <= 2^24 (NF4, 8 bits: a
  *   multiple of 64);  0 <= T < 2^31 (0 is a no-op)
  *   ws  workspace of ws_bytes >= qlora_head_workspace_bytes(T, vocab, hidden,
@@ -730,9 +731,10 @@ typedef struct {
  * out of range).  Host only.
  * qlora_adamw_plan: writes the plan of the n tensors (host array) into `table`
  * (device memory, which the caller keeps for as long as the plan is used, like
- * the tensors) and fills out.  Refused with VALUE: two tensors whose param or
- * master share memory, or a gradient that shares memory with one.  No copy from
- * the host: it can be captured.
+ * the tensors) and fills out.  It waits for the stream: once it returns, steps on
+ * any stream may use the plan.  Refused with VALUE: two tensors whose param or
+ * master share memory, or a gradient that shares memory with one; with LAUNCH:
+ * on a stream that is being captured (the steps can be).
  */
 int64_t qlora_adamw_state_len(const int64_t* numel, int64_t n);
 size_t qlora_adamw_table_bytes(const int64_t* numel, int64_t n);
@@ -760,7 +762,7 @@ int qlora_adamw_plan(const qlora_adamw_tensor* tensors, int64_t n, void* table, 
  * The numbers in rates are taken by value: a captured step repeats its t and seed.
  * Two steps of one plan must not overlap in time.  An element's result depends
  * on nothing but its own values and, in 8 bits, its block's.
- * Errors: NULL, SHAPE, ALIGN, VALUE (bits, rates), DEVICE, LAUNCH.
+ * Errors: NULL, SHAPE, ALIGN, VALUE (bits, rates, m that is v), DEVICE, LAUNCH.
  */
 int qlora_adamw_step(const qlora_adamw_table* table, int bits, void* m, void* v, uint8_t* m_scales, uint8_t* v_scales,
                      const float* grad_scale, const qlora_adamw_rates* rates, qlora_stream stream);

@@ -250,7 +250,7 @@ def test_states_that_are_not_finite_stay_alone():
 
 def test_many_tensors_streams_graphs_and_plans():
     """More tensors than one launch of the plan takes, of many sizes; the step is
-    the same bits on another stream, in graphs (the plan too), and for each tensor alone where
+    the same bits on another stream, in graphs, and for each tensor alone where
     its states start at the same place."""
     q = require_gpu()
     banner("adamw many tensors")
@@ -273,18 +273,21 @@ def test_many_tensors_streams_graphs_and_plans():
         ref = result(a[0], a[1], a[3])
         a = fresh()
         side = torch.cuda.Stream()
-        side.wait_stream(torch.cuda.current_stream())
+        # (the plan waits for the current stream: the side stream finds it whole)
+        plan = q.qlora_adamw_plan(*a[:3], a[3])
         with torch.cuda.stream(side):
-            two(q.qlora_adamw_plan(*a[:3], a[3]))
+            two(plan)
         side.synchronize()
         assert all(torch.equal(x, y) for x, y in zip(result(a[0], a[1], a[3]), ref))
-        # a captured plan and steps, replayed on restored values
+        # captured steps, replayed on restored values
         a = fresh()
         start = result(a[0], a[1], a[3])
         keep = [t for t in a[0] + a[1] + [a[3].m, a[3].v, a[3].m_scales, a[3].v_scales] if t is not None]
+        plan = q.qlora_adamw_plan(*a[:3], a[3])
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g):
-            plan = q.qlora_adamw_plan(*a[:3], a[3])
+            with pytest.raises(RuntimeError, match="captured"):
+                q.qlora_adamw_plan(*a[:3], a[3])
             two(plan)
         for turn in range(3):
             for t, s in zip(keep, start):
@@ -340,5 +343,8 @@ def test_refusals():
         q.qlora_adamw_step(ok, 0, lr=1e-3)
     with pytest.raises(ValueError):
         q.qlora_adamw_step(ok, 1, lr=1e-3, grad_scale=torch.ones(1))
+    twice = q.AdamWState(state.m, state.m, state.m_scales, state.v_scales)
+    with pytest.raises(q.QloraError):
+        q.qlora_adamw_step(q.qlora_adamw_plan([p], [f], [g], twice), 1, lr=1e-3)
     with pytest.raises(ValueError):
         q.qlora_adamw_state([5], 16, "cuda")

@@ -338,6 +338,43 @@ def test_streams_and_graphs(kind, T):
             assert all(torch.equal(a, b) for a, b in zip(out, want)), turn
 
 
+def test_slices_of_longer_vectors():
+    """labels shifted by one in front of their rows, as a causal model's are, and the
+    other vectors at odd elements: the bits of the call on copies."""
+    q = require_gpu()
+    banner("head slices")
+    T, V, H = 37, 2112, 320
+    W, _ = _head(q, "bf16", 41, V, H, 0.2)
+    X, y, g = dev_bf16(_bf16(42, (T + 1, H))), _dev(_labels(43, T + 1, V)), dev_f32(np.linspace(0.5, 1, T + 1).astype(np.float32))
+    got = q.qlora_head_loss_grad(W, X[:-1], y[1:], g[1:])
+    want = q.qlora_head_loss_grad(W, X[:-1].clone(), y[1:].clone(), g[1:].clone())
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert all(torch.equal(a, b) for a, b in zip(q.qlora_head_loss(W, X[:-1], y[1:]), want))
+
+
+def test_loss_in_pieces_16_bit():
+    """4096 rows and 2^21 + 300 columns are two pieces without a gradient; sixteen of the
+    rows are one.  A sum of positive terms is off by at most its longest chain times
+    2^-24: 16 terms a lane, 5 more over the wave, 16400 blocks by 16 waves and their 16
+    sums, 1063 in all: 6.4e-5 of the sum and as much of lse, twice that between two calls."""
+    q = require_gpu()
+    banner("head loss in pieces")
+    T, V, H = 4096, (1 << 21) + 300, 64
+    torch.manual_seed(5)
+    W = torch.randn(V, H, device="cuda").to(torch.bfloat16)
+    X = torch.randn(T, H, device="cuda").to(torch.bfloat16)
+    y = torch.randint(0, V, (T,), device="cuda")
+    y[::5], y[1] = -100, V - 1
+    loss, lse = q.qlora_head_loss(W, X, y)
+    rows = torch.arange(0, T, 256, device="cuda")
+    rows[0] = 1
+    one, base = q.qlora_head_loss(W, X[rows].contiguous(), y[rows])
+    assert (lse[rows] - base).abs().max() <= 1.3e-4 and (loss[rows] - one).abs().max() <= 1.3e-4
+    logits = (X[1].double() * W.double()).sum(-1)
+    assert abs(lse[1].item() - torch.logsumexp(logits, 0).item()) <= 1e-4
+    assert abs(loss[1].item() - (torch.logsumexp(logits, 0) - logits[-1]).item()) <= 1e-4
+
+
 def test_empty_and_refusals():
     q = require_gpu()
     banner("head T=0 and refusals")

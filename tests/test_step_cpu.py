@@ -140,7 +140,8 @@ def test_norm_refusals(lib):
     assert [_norm_fwd(lib, eps=e) for e in (-1e-9, float("nan"), float("inf"))] == [VALUE] * 3
     assert [_norm_fwd(lib, **{k: None}) for k in ("x", "w", "res", "h", "codes", "scales")] == [NULL] * 6
     assert _norm_fwd(lib, y=None, codes=None, scales=None) == NULL
-    assert [_norm_fwd(lib, **{k: ODD}) for k in ("x", "res", "w", "h", "y", "codes", "scales", "rstd")] == [ALIGN] * 8
+    assert [_norm_fwd(lib, **{k: ODD}) for k in ("x", "res", "w", "h", "y", "codes", "scales")] == [ALIGN] * 7
+    assert _norm_fwd(lib, rstd=F + 2) == ALIGN
     assert _norm_fwd(lib, T=0, x=None, w=None) == 0
 
     def bwd(T=4, H=128, dy=F, h=F, w=F, rstd=F, dres=F, dh=F, dw=F, ws=F, n=1 << 20):
@@ -148,7 +149,8 @@ def test_norm_refusals(lib):
                                      ctypes.c_size_t(n), None)
     assert [bwd(**k) for k in ({"H": 32}, {"T": -1}, {"H": 1 << 20})] == [SHAPE] * 3
     assert [bwd(**{k: None}) for k in ("dy", "h", "w", "rstd", "dh")] == [NULL] * 5
-    assert [bwd(**{k: ODD}) for k in ("dy", "h", "w", "rstd", "dres", "dh", "dw", "ws")] == [ALIGN] * 8
+    assert [bwd(**{k: ODD}) for k in ("dy", "h", "w", "dres", "dh", "dw", "ws")] == [ALIGN] * 7
+    assert bwd(rstd=F + 2) == ALIGN and bwd(rstd=F + 4, ws=None) == WORKSPACE
     lib.qlora_rmsnorm_workspace_bytes.restype = ctypes.c_size_t
     need = lib.qlora_rmsnorm_workspace_bytes(i64(4), i64(128))
     assert need >= 256 and bwd(n=need - 1) == WORKSPACE and bwd(ws=None) == WORKSPACE
@@ -208,7 +210,9 @@ def test_head_refusals(lib):
         assert [call(head(), T=t, grad=grad) for t in (-1, 1 << 31)] == [SHAPE] * 2
         assert [call(head(v, h, **k), grad=grad) for k in (ok4, ok8) for v, h in ((576, 128), (640, 192))] == [SHAPE] * 4
         assert [call(head(), grad=grad, **{k: None}) for k in ("X", "labels", "loss")] == [NULL] * 3
-        assert [call(head(), grad=grad, **{k: ODD}) for k in ("X", "labels", "loss", "lse", "ws")] == [ALIGN] * 5
+        assert [call(head(), grad=grad, **{k: ODD}) for k in ("X", "ws")] == [ALIGN] * 2
+        assert [call(head(), grad=grad, **{k: F + 2}) for k in ("labels", "loss", "lse")] == [ALIGN] * 3
+        assert call(head(), grad=grad, labels=F + 8, loss=F + 4, lse=F + 12, ws=None) == WORKSPACE
         assert call(head(bf16=ODD), grad=grad) == ALIGN
         assert call(head(), T=0, X=None, labels=None, grad=grad) == 0
         assert call(head(), ws=None, grad=grad) == WORKSPACE
@@ -217,7 +221,7 @@ def test_head_refusals(lib):
             need = lib.qlora_head_workspace_bytes(i64(4), i64(v), i64(128), expand, int(grad))
             assert need > 256 and call(head(v, **k), n=need - 1, grad=grad) == WORKSPACE
     assert [call(head(), **{k: None}) for k in ("dloss", "dX")] == [NULL] * 2
-    assert [call(head(), **{k: ODD}) for k in ("dloss", "dX")] == [ALIGN] * 2
+    assert call(head(), dX=ODD) == ALIGN and call(head(), dloss=F + 2) == ALIGN
     bad = Nf4(F, F, F, 640, 128, 8)
     assert call(head(640, bf16=None, nf4=ctypes.pointer(bad))) == VALUE
     bad = Fp8(F, F, 640, 128, 1)
@@ -233,6 +237,7 @@ def test_head_workspace_is_bounded(lib):
     assert w(4096, 128000, 4096, 0, 1) < 512 << 20
     assert w(1 << 20, 1 << 24, 4096, 1, 1) < 1 << 30
     assert w(1 << 20, 128000, 4096, 0, 1) <= w(4096, 128000, 4096, 0, 1)
+    assert w(4096, 1 << 24, 4096, 0, 0) <= 513 << 20
     # no rows: the smallest there is, no division by their number
     assert all(w(0, v, 64, e, g) >= 256 for v in (1, 1 << 24) for e in (0, 1) for g in (0, 1))
 
@@ -298,5 +303,7 @@ def test_adamw_refusals(lib):
                                 {"eps": inf}, {"weight_decay": nan}, {"step": 0}, {"step": -3})] == [VALUE] * 11
     assert [step(**{k: None}) for k in ("m", "v", "ms", "vs")] == [NULL] * 4
     assert [step(**{k: ODD}) for k in ("m", "v", "ms", "vs")] == [ALIGN] * 4 and step(gs=F + 2) == ALIGN
+    # the two states in one place
+    assert step(bits=32) == VALUE and step(v=F + 8192) == VALUE and step(ms=F + 8192) == VALUE
     assert step(table=Table(F, -1, 0)) == SHAPE and step(table=Table(F, 1 << 31, 0)) == SHAPE
     assert step(table=Table(F, 0, 0), m=None) == 0
