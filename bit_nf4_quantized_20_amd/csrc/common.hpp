@@ -333,37 +333,40 @@ hipError_t launch_norm_bwd(const NormBwd& a, float* dw, hipStream_t s);
 // piece's rows in bf16.  Per row the sum over the vocabulary but the label's
 // column is held as run_s 2^(kHeadCell run_c); a row's label is outside [0, V)
 // where it has none.
-constexpr int kHeadTile = 256;   // columns of the logits a workgroup forms
-constexpr int kHeadCols = 128;   // columns that one wave reduces
+constexpr int kHeadTile = 256;   // a piece's columns are a multiple of it (the last piece's may not be)
 constexpr float kHeadCell = 128.f;
-struct HeadPiece {
-  const uint16_t* X;      // [T][H]
-  int64_t T, H;
-  const uint16_t* W;      // [n][H], the piece's rows
-  int64_t v0, n;          // v0 a multiple of kHeadTile
-  const int64_t* labels;  // [T]
-  float* target;          // [T] the label's logit times log2 e, written by the piece that has it
-  uint16_t* E;            // [T][lde] bf16 2^(logit log2 e - kHeadCell c), or null; 0 at the label and behind n
-  int64_t lde;            // n rounded up to whole tiles
-  float *tile_c, *tile_s;  // [lde / kHeadCols][T]
-  // sums over the pieces before (first: none) and with this one, and the factor
-  // 2^(kHeadCell (c before - c now)) of what was accumulated before
-  bool first;
-  const float *c_in, *s_in;
-  float *c_out, *s_out, *factor;
-};
-hipError_t launch_head_logits(const HeadPiece& p, hipStream_t s);
-// part [splits][T][H] fp32 = factor part (not first) + E W
-int head_splits(int64_t T, int64_t H, int64_t n);
-hipError_t launch_head_grad(const HeadPiece& p, float* part, int splits, hipStream_t s);
-// What is left: loss, lse (may be null) and, with dX, dX = dloss (sum of the
-// parts / total - (others / total) W_label).  The label's row of W in its own format.
+// W in its own format.
 struct HeadWeight {
   const uint16_t* w16;
   const uint8_t *codes, *absmax_q;  // NF4 (absmax_q null: fp32 absmax), or 8-bit codes
   const float* scale;
   const uint8_t* scale8;            // 8-bit: block scales
 };
+struct HeadPiece {
+  const uint16_t* X;      // [T][H]
+  int64_t T, H;
+  const uint16_t* W;      // [n][H], the piece's rows, or null:
+  HeadWeight q;           // the piece's rows in 4 or 8 bits (v0 a multiple of 256)
+  int64_t v0, n;          // v0 a multiple of kHeadTile
+  const int64_t* labels;  // [T]
+  float* target;          // [T] the label's logit times log2 e, written by the piece that has it
+  uint16_t* E;            // [T][lde] bf16 2^(logit log2 e - kHeadCell c), or null; 0 at the label and behind n
+  int64_t lde;            // n rounded up to whole tiles
+  int cols;               // columns that one wave reduces: head_cols(T, n, q given), 64 or 128
+  float *tile_c, *tile_s;  // [lde / cols][T]
+  // sums over the pieces before (first: none) and with this one, and the factor
+  // 2^(kHeadCell (c before - c now)) of what was accumulated before
+  bool first;
+  const float *c_in, *s_in;
+  float *c_out, *s_out, *factor;
+};
+int head_cols(int64_t T, int64_t n, bool codes);
+hipError_t launch_head_logits(const HeadPiece& p, hipStream_t s);
+// part [splits][T][H] fp32 = factor part (not first) + E W
+int head_splits(int64_t T, int64_t H, int64_t n, bool codes);
+hipError_t launch_head_grad(const HeadPiece& p, float* part, int splits, hipStream_t s);
+// What is left: loss, lse (may be null) and, with dX, dX = dloss (sum of the
+// parts / total - (others / total) W_label).  W is the whole weight here.
 struct HeadFinish {
   int64_t T, H, V;
   const int64_t* labels;

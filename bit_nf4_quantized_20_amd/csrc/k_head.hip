@@ -21,9 +21,17 @@
 //
 // k_head_logits (X W^T, weight rows as the matrix cores' first operand, then the
 // softmax's part in the epilogue) and k_head_grad (E W, the weight read
-// K-row-major through transposing LDS loads) share one main loop: BM x 256 x 64
-// tiles, four waves of BM/2 x 128, LDS stages filled by copies straight from
-// global memory, fragments of a sub-step read during the one before.
+// K-row-major through transposing LDS loads) share one main loop: BM x BN x 64
+// tiles, four waves of BM/2 x BN/2, LDS stages filled by copies straight from
+// global memory, fragments of a sub-step read during the one before.  4- and 8-bit
+// weights come through registers instead and are turned into bf16 on their way into
+// LDS (up to kHeadCodesTokens rows; the caller writes them out in bf16 for more).
+//
+// Measured: loss of 1 x 32000 x 4096 62 us (262 MB, 4.2 TB/s), of 64 rows in NF4 58;
+// gradient of 301 x 50021 x 2304 204 us, of 4096 x 128000 x 4096 6.3 ms, 1360 TFLOP/s.  A
+// 256 x 256 tile takes 1.4 us a step of 64, 1.5 PFLOP/s, where the matrix cores on random
+// operands are bound by power, and 10 us in front of and behind its steps; with few rows HBM
+// or, of 4-bit weights, the vector unit bounds.
 #include <type_traits>
 
 #include "common.hpp"
@@ -37,7 +45,7 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kInf = __builtin_inff();
-constexpr int kNW = 4, kBN = 256, kWN = 128;  // waves (2 x 2), tile and wave columns
+constexpr int kNW = 4;  // waves, 2 x 2
 
 // x 2^(kHeadCell d), d <= 0 a whole number of cells (two cells and more give 0
 // or, of an infinity or a NaN, what it was)
@@ -69,13 +77,16 @@ struct Source {
   int bytes;
 };
 __device__ __forceinline__ Source rows_source(const uint16_t* p, int64_t ld, int64_t row0, int64_t rows, int64_t col0) {
-  const int64_t n = ((rows - row0) * ld - col0) * 2;
+  const int64_t n = rows > row0 ? ((rows - row0) * ld - col0) * 2 : 0;
   return Source{p + row0 * ld + col0, static_cast<int>(n < 0x7fffffff ? n : 0x7fffffff)};
 }
 
 // ROWS rows of a K-contiguous matrix, as lds_frag reads them.
 template <int ROWS>
 struct RowTile {
+  static constexpr bool kQuant = false, kTr = false;
+  using Src = Source;
+  struct Set {};
   static constexpr int kPerWave = ROWS / 8 / kNW;
   uint32_t voff[kPerWave];
   __device__ __forceinline__ void init(int64_t ld, int wv, int lane) {
@@ -97,21 +108,25 @@ struct RowTile {
   }
 };
 
-// K-row-major weight tile: 64 rows of W (K) by kBN columns, swizzled by tswz for
-// col_frag.  A wave instruction copies two rows; lane L lands at 16-byte chunk L % 32 of
-// row L / 32 and loads the chunk that belongs there.  Columns past H read the next
+// K-row-major weight tile: 64 rows of W (K) by BN columns, swizzled by tswz for
+// col_frag.  A wave instruction copies two or four rows; lane L lands at 16-byte chunk
+// L % kChunks of row L / kChunks and loads the chunk that belongs there.  Columns past H read the next
 // row (never stored), rows past the piece read 0: the resource starts at the step's
 // first row (a piece is below 2^31 bytes).
+template <int BN>
 struct ColTile {
-  static constexpr int kPerWave = kBK / 2 / kNW;
+  static constexpr bool kQuant = false, kTr = true;
+  using Src = Source;
+  struct Set {};
+  static constexpr int kChunks = BN / 8, kRows = 64 / kChunks, kPerWave = kBK / kRows / kNW;
   int pitch;  // bytes of a row
   uint32_t voff[kPerWave];
   __device__ __forceinline__ void init(int64_t ld, int wv, int lane) {
     pitch = static_cast<int>(ld * 2);
 #pragma unroll
     for (int i = 0; i < kPerWave; ++i) {
-      const int k = (i * kNW + wv) * 2 + (lane >> 5);
-      voff[i] = static_cast<uint32_t>((k * ld + ((lane & 31) ^ tswz(k)) * 8) * 2);
+      const int k = (i * kNW + wv) * kRows + lane / kChunks;
+      voff[i] = static_cast<uint32_t>((k * ld + ((lane % kChunks) ^ tswz(k)) * 8) * 2);
     }
   }
   __device__ __forceinline__ void load(uint16_t* lds, int wv, const Source& s, int k, int first, int count) const {
@@ -126,6 +141,112 @@ struct ColTile {
   }
 };
 
+// A tile of a 4- or 8-bit weight on its way into LDS: a lane has BN / 4 weights of a row
+// (within one NF4 block), loads their codes and scales into registers two steps ahead of the
+// step that writes them to LDS in bf16, where row_frag (kCols: col_frag) reads them.
+// Rows past the piece are codes of 0 with scales of 0.
+enum { kBf16, kNf4, kFp8 };
+struct CodeSource {
+  const uint8_t* codes;
+  const uint8_t* q;      // NF4: 8-bit absmax, or null; 8 bits: scale bytes
+  const float* scale;    // NF4
+  int bytes, q_bytes;    // of codes (0: nothing is read) and q
+  int phase;             // NF4: blocks of scale's first group in front of codes
+};
+template <int BN, int F, bool kCols>
+struct CodeTile {
+  static constexpr bool kQuant = true, kTr = kCols;
+  static constexpr int kOwn = BN / 4, kLoads = kOwn / (F == kNf4 ? 32 : 16);  // 16 bytes of codes each
+  static constexpr int kPerWave = kLoads + (F == kNf4 ? 2 : 1);  // loads of a step
+  static constexpr int kRowShift = F == kNf4 ? 1 : 0;            // 2^-kRowShift bytes a weight
+  using Src = CodeSource;
+  struct Set {
+    u32x4 codes[kLoads];
+    uint32_t q;
+    float s;
+  };
+  uint32_t H, voff, block;
+  int lds_row, lds_chunk;  // this lane's first element and first chunk
+  bool dq;
+  Nf4Table table;
+  float s8;
+  __device__ __forceinline__ void init(int64_t h, int wv, int lane, int64_t n0, bool q) {
+    H = static_cast<uint32_t>(h);
+    dq = q;
+    // (columns: 16 lanes have 16 rows and one chunk, so that their LDS writes meet
+    // no bank twice, and a wave reads 16 rows of 256 columns)
+    const uint32_t row = kCols ? wv * 16 + (lane & 15) : wv * kOwn + (lane & (kOwn - 1));
+    const uint32_t first = kOwn * (kCols ? lane >> 4 : lane / kOwn), col = static_cast<uint32_t>(n0) + first;
+    voff = (row * H + col) >> kRowShift;
+    if constexpr (F == kNf4) block = row * (H / 64) + col / 64;
+    else block = kCols ? col / kF8Block : row / kF8Block * ((H + kF8Block - 1) / kF8Block);
+    lds_row = row * (kCols ? BN : kBK);
+    lds_chunk = first / 8;
+    key = kCols ? tswz(row) : swz(row, 0);
+  }
+  int key;
+  __device__ __forceinline__ static __amdgpu_buffer_rsrc_t rsrc(const void* p, int64_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, static_cast<int>(bytes), kBufferWord3);
+  }
+  __device__ __forceinline__ void load(Set& c, const Src& s, int k) const {
+    const int64_t ahead = kCols ? static_cast<int64_t>(k) * kBK * H >> kRowShift : 0;
+    const __amdgpu_buffer_rsrc_t rs = rsrc(s.codes + ahead, s.bytes > ahead ? s.bytes - ahead : 0);
+    const int soff = kCols || s.bytes == 0 ? 0 : k * kBK >> kRowShift;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i)
+      c.codes[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, voff + 16 * i, soff, 0));
+    if constexpr (F == kNf4) {
+      const uint32_t b = block + (kCols ? static_cast<uint32_t>(k) * H : k);
+      const int blocks = s.bytes >> 5, scales = blocks != 0 ? (blocks + s.phase + kGroup - 1) / kGroup : 0;
+      c.q = __builtin_amdgcn_raw_buffer_load_b8(rsrc(s.q, dq ? blocks : 0), b, 0, 0);
+      c.s = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(
+                                          rsrc(s.scale, dq ? scales * 4 : blocks * 4),
+                                          (dq ? (b + s.phase) / kGroup : b) * 4, 0, 0));
+    } else {
+      const uint32_t b = block + (k >> 1) * (kCols ? (H + kF8Block - 1) / kF8Block : 1);
+      c.q = __builtin_amdgcn_raw_buffer_load_b8(rsrc(s.q, s.bytes != 0 ? s.q_bytes : 0), b, 0, 0);
+    }
+  }
+  // The lane's weights 8 g .. 8 g + 7 into LDS in eight parts of about four instructions,
+  // g and u in turn: as many as the matrix cores take in behind one of theirs.
+  static constexpr int kParts = 8;
+  __device__ __forceinline__ void write(uint16_t* lds, const Set& c, int g, int u) {
+    if constexpr (F == kNf4) {
+      const uint32_t w = c.codes[g / 4][g % 4];
+      if (g == 0 && u == 0) table = make_table(dq ? dq_absmax(c.q, c.s) : c.s);
+      if (u == 0 || u == 3) {
+        sel = (u == 0 ? w : w >> 4) & 0x07070707u;
+        pick = __builtin_amdgcn_bitop3_b32(u == 0 ? w >> 1 : w >> 5, 0x04040404u, 0x03020100u, 0xEA);
+      }
+      if (u == 1) o[0] = lookup_plane(table.lo, sel, pick);
+      if (u == 2) o[1] = lookup_plane(table.hi, sel, pick);
+      if (u == 4) o[2] = lookup_plane(table.lo, sel, pick);
+      if (u == 5) o[3] = lookup_plane(table.hi, sel, pick);
+      if (u == 6) {
+        const uint32_t e0 = perm(o[1], o[0], 0x05010400u), e1 = perm(o[1], o[0], 0x07030602u);  // (w0, w2), (w4, w6)
+        const uint32_t o0 = perm(o[3], o[2], 0x05010400u), o1 = perm(o[3], o[2], 0x07030602u);  // (w1, w3), (w5, w7)
+        o[0] = e0;
+        o[1] = e1;
+        o[2] = o0;
+        o[3] = o1;
+      }
+      if (u == 7)
+        *reinterpret_cast<u32x4*>(lds + lds_row + (((lds_chunk + g) ^ key) << 3)) =
+            u32x4{perm(o[2], o[0], 0x05040100u), perm(o[2], o[0], 0x07060302u), perm(o[3], o[1], 0x05040100u),
+                  perm(o[3], o[1], 0x07060302u)};
+    } else {
+      if (g == 0 && u == 0) s8 = f8_scale(c.q);
+      if (u % 2 == 0) {
+        const int v = static_cast<int>(c.codes[g / 2][g % 2 * 2 + u / 4]);
+        const auto a = u % 4 == 0 ? __builtin_amdgcn_cvt_pk_f32_fp8(v, false) : __builtin_amdgcn_cvt_pk_f32_fp8(v, true);
+        o[u / 2] = pack_bf16x2(a[0] * s8, a[1] * s8);
+      }
+      if (u == 7) *reinterpret_cast<u32x4*>(lds + lds_row + (((lds_chunk + g) ^ key) << 3)) = u32x4{o[0], o[1], o[2], o[3]};
+    }
+  }
+  uint32_t sel, pick, o[4];
+};
+
 // Fragments of v_mfma_f32_16x16x32_bf16: lane l holds row l % 16 and the eight k from
 // 32 j + 8 (l / 16) on.  (This shape and not 32 x 32 x 16: per product it moves half
 // of the accumulators and draws less power, which is what bounds the matrix
@@ -136,6 +257,7 @@ __device__ __forceinline__ bf16x8 row_frag(const uint16_t* lds, int row0, int j)
 }
 // of columns n0 .. n0 + 15 of a ColTile: each group of 16 lanes gets the transposed
 // blocks of its eight k (as lds_frag_tr)
+template <int BN>
 __device__ __forceinline__ bf16x8 col_frag(const uint16_t* lds, int n0, int j) {
   typedef short v4s __attribute__((ext_vector_type(4)));
   const int l = threadIdx.x & 63, i = l & 15, n = n0 + 4 * (i & 3);
@@ -144,50 +266,71 @@ __device__ __forceinline__ bf16x8 col_frag(const uint16_t* lds, int n0, int j) {
   for (int h = 0; h < 2; ++h) {
     const int k = 32 * j + 8 * (l >> 4) + 4 * h + (i >> 2);
     v[h] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-        (__attribute__((address_space(3))) v4s*)(const_cast<uint16_t*>(lds) + k * kBN + (((n >> 3) ^ tswz(k)) << 3) + (n & 4)));
+        (__attribute__((address_space(3))) v4s*)(const_cast<uint16_t*>(lds) + k * BN + (((n >> 3) ^ tswz(k)) << 3) + (n & 4)));
   }
   return __builtin_bit_cast(bf16x8, __builtin_shufflevector(v[0], v[1], 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
+// Stages of activations: three beside codes, where LDS holds them (the wait for a stage is
+// also one for the codes asked for before it, and those come from HBM).
+constexpr int act_stages(int BM, int BN, bool codes) { return codes && BM <= (BN == 128 ? 64 : 160) ? 3 : 2; }
+
 // acc[a][c] += weight fragments times activation fragments over a tile's K-steps [k0,
 // k0 + steps) of 64; acc[a][c][i] holds row m = wm BM/2 + 16 c + lane % 16 of the
-// tile and column n = 128 wn + 16 a + 4 (lane / 16) + i.
+// tile and column n = wn BN/2 + 16 a + 4 (lane / 16) + i.
 //
-// Two LDS stages of activations and three of weights, each an array of its own and
+// NA LDS stages of activations and three of weights, each an array of its own and
 // its index a compile-time constant, so that the compiler sees that the copies into one
-// stage do not alias the fragment reads of another.  A step is two sub-steps of FN = 8
+// stage do not alias the fragment reads of another.  A step is two sub-steps of FN
 // groups of matrix instructions, one group per weight fragment.  Fragments are read
-// ahead: a weight's six groups before its use, into the register of one that is used
+// ahead: a weight's FN - 2 groups before its use, into the register of one that is used
 // up, the activations' under the middle of the sub-step before.  After group 1 of the
 // second sub-step all of the step's fragments have been read and a barrier frees its
-// stages; it also waits for what the next step reads.  The copies of two steps on
-// (activations) go out behind it and have a sub-step to land, those of three steps on
-// (weights) under the next sub-step and have three.
+// stages; it also waits for what the next step reads.  The copies of NA steps on
+// (activations) go out behind it and have at least a sub-step to land, those of three
+// steps on (weights) under the next sub-step and have three.  Codes are asked for NA
+// steps before they go to LDS, two steps before their products.
 //
 // A workgroup takes one tile after another without a break in this: the steps count on
-// into the next tile (steps is rounded up to the six after which both rings are back
-// where they began, with copies of zeros), so that its first copies and fragments
-// are under way during the last steps and the epilogue.
-template <int BM, class TW>
+// into the next tile (steps is rounded up to the six, with NA = 3 to the three but at
+// least six, after which the rings are back where they began, with copies of zeros), so
+// that its first copies and fragments are under way during the last steps and the
+// epilogue.
+template <int BM, int BN, class TW>
 struct HeadLoop {
-  static constexpr int FN = kWN / 16, FM = BM / 32;
-  static_assert(FN == 8, "the order of the reads below");
-  static constexpr bool kTr = std::is_same_v<TW, ColTile>;
+  static constexpr int NA = act_stages(BM, BN, TW::kQuant);
+  // codes become bf16 between the products (of 64 rows: in front of them, there are too few)
+  static constexpr bool kSpread = BM > 64;
+  static constexpr int FN = BN / 32, FM = BM / 32, kHalf = FN / 2;
+  static_assert(FN == 8 || FN == 4, "the order of the reads below");
+  static constexpr bool kTr = TW::kTr, kQuant = TW::kQuant;
   typedef f32x4 Acc[FN][FM];
-  uint16_t *s_act[2], *s_wt[3];
+  uint16_t *s_act[NA], *s_wt[3];
   int wv;
   RowTile<BM> ta;
   TW tw;
   int k0, steps;          // of this tile (and of the next, where there is one)
-  Source a[2], w[2];      // this tile's and the next one's (bytes 0: none)
+  Source a[2];            // this tile's and the next one's (bytes 0: none)
+  typename TW::Src w[2];
+  typename TW::Set set[NA];
   bf16x8 fw[FN], fa[2][FM];
 
+  __device__ __forceinline__ void stages(uint16_t* a0, uint16_t* a1, uint16_t* a2, uint16_t* w0, uint16_t* w1, uint16_t* w2,
+                                         int wave) {
+    s_act[0] = a0;
+    s_act[1] = a1;
+    if constexpr (NA == 3) s_act[2] = a2;
+    s_wt[0] = w0;
+    s_wt[1] = w1;
+    s_wt[2] = w2;
+    wv = wave;
+  }
   __device__ __forceinline__ bf16x8 act(int b, int j, int i) const {
     return row_frag(s_act[b], (wv & 1) * (BM / 2) + i * 16, j);
   }
   __device__ __forceinline__ bf16x8 wt(int b, int j, int i) const {
-    const int n0 = (wv >> 1) * kWN + i * 16;
-    if constexpr (kTr) return col_frag(s_wt[b], n0, j);
+    const int n0 = (wv >> 1) * (BN / 2) + i * 16;
+    if constexpr (kTr) return col_frag<BN>(s_wt[b], n0, j);
     else return row_frag(s_wt[b], n0, j);
   }
   // In assembly, so that the accumulators stay where they are: of the builtin's the
@@ -215,11 +358,14 @@ struct HeadLoop {
   }
   static constexpr int wait_code(int copies) { return (copies & 15) | ((copies >> 4) << 14) | 0x70; }  // lgkmcnt(0) too
 
-  __device__ __forceinline__ static int padded(int n) { return (n + 5) / 6 * 6; }
+  __device__ __forceinline__ static int padded(int n) { return NA == 2 ? (n + 5) / 6 * 6 : n < 6 ? 6 : (n + 2) / 3 * 3; }
   static constexpr int kA = RowTile<BM>::kPerWave, kW = TW::kPerWave;  // copies of a wave and step
   // step e counted from this tile's first
-  __device__ __forceinline__ static Source source(const Source (&s)[2], int e, int steps, int turn) {
-    return Source{e < turn ? s[0].base : s[1].base, e < steps ? s[0].bytes : e < turn || e - turn >= steps ? 0 : s[1].bytes};
+  template <class S>
+  __device__ __forceinline__ static S source(const S (&s)[2], int e, int steps, int turn) {
+    S r = e < turn ? s[0] : s[1];
+    r.bytes = e < steps ? s[0].bytes : e < turn || e - turn >= steps ? 0 : s[1].bytes;
+    return r;
   }
   __device__ __forceinline__ void copy_a(int e, int b, int first, int count) const {
     const int turn = padded(steps);
@@ -227,19 +373,55 @@ struct HeadLoop {
   }
   __device__ __forceinline__ void copy_w(int e, int b, int first, int count) const {
     const int turn = padded(steps);
-    tw.load(s_wt[b], wv, source(w, e, steps, turn), e < turn ? k0 + e : e - turn, first, count);
+    if constexpr (!kQuant) tw.load(s_wt[b], wv, source(w, e, steps, turn), e < turn ? k0 + e : e - turn, first, count);
+  }
+  __device__ __forceinline__ void codes(int e, int b) {
+    const int turn = padded(steps);
+    if constexpr (kQuant) tw.load(set[b], source(w, e, steps, turn), e < turn ? k0 + e : e - turn);
+  }
+
+  // group g of sub-step j, with its share of the codes' way into LDS between the products
+  __device__ __forceinline__ void products(Acc& acc, int g, int j, uint16_t* lds, int b) {
+#pragma unroll
+    for (int c = 0; c < FM; ++c) {
+      mfma(acc[g][c], fw[g], fa[j][c]);
+      if constexpr (kQuant && kSpread) {
+        constexpr int kShare = TW::kParts / 2;  // a group's
+        const int G = j * FN + g;
+#pragma unroll
+        for (int i = (c * kShare + FM - 1) / FM; i < ((c + 1) * kShare + FM - 1) / FM; ++i)
+          tw.write(lds, set[b], G / 2, G % 2 * kShare + i);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
   }
 
   // the first copies and fragments of a workgroup's first tile
   __device__ __forceinline__ void begin() {
     copy_a(0, 0, 0, kA);
-    copy_w(0, 0, 0, kW);
-    copy_w(1, 1, 0, kW);
-    copy_a(1, 1, 0, kA);
-    __builtin_amdgcn_s_waitcnt(wait_code(kA + kW));
+    if constexpr (kQuant) {
+      codes(0, 0);
+      codes(1, 1);
+      copy_a(1, 1, 0, kA);
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+#pragma unroll
+        for (int g = 0; g < FN * TW::kParts; ++g) tw.write(s_wt[b], set[b], g / TW::kParts, g % TW::kParts);
+      }
+#pragma unroll
+      for (int b = 0; b < NA; ++b) codes(2 + b, b);
+      if constexpr (NA == 3) copy_a(2, 2, 0, kA);
+      __builtin_amdgcn_s_waitcnt(wait_code(0));
+    } else {
+      copy_w(0, 0, 0, kW);
+      copy_w(1, 1, 0, kW);
+      copy_a(1, 1, 0, kA);
+      __builtin_amdgcn_s_waitcnt(wait_code(kA + kW));
+    }
     barrier();
 #pragma unroll
-    for (int i = 0; i < 6; ++i) fw[i] = wt(0, 0, i);
+    for (int i = 0; i < FN - 2; ++i) fw[i] = wt(0, 0, i);
 #pragma unroll
     for (int i = 0; i < FM; ++i) fa[0][i] = act(0, 0, i);
   }
@@ -247,50 +429,60 @@ struct HeadLoop {
     settle(acc);
     // step e; A, W: its stages
     auto step = [&](int e, auto ac, auto wc) {
-      constexpr int A = decltype(ac)::value, W = decltype(wc)::value, NA = A ^ 1, NW = (W + 1) % 3;
-      constexpr int kPer = (FM + 3) / 4, kWG = (kW + FN - 1) / FN, kAG = (kA + 3) / 4;
+      constexpr int A = decltype(ac)::value, W = decltype(wc)::value, A1 = (A + 1) % NA, W1 = (W + 1) % 3;
+      constexpr int kPer = (FM + kHalf - 1) / kHalf, kWG = (kW + FN - 1) / FN, kAG = (kA + kHalf - 1) / kHalf;
 #pragma unroll
       for (int g = 0; g < FN; ++g) {
-        if (g < 2) fw[g + 6] = wt(W, 0, g + 6);
+        if (g < 2) fw[g + FN - 2] = wt(W, 0, g + FN - 2);
         else fw[g - 2] = wt(W, 1, g - 2);
-        if (g >= 2 && g < 6)
+        if (g >= 2 && g < 2 + kHalf)
 #pragma unroll
           for (int i = (g - 2) * kPer; i < (g - 1) * kPer && i < FM; ++i) fa[1][i] = act(A, 1, i);
         copy_w(e + 2, (W + 2) % 3, g * kWG, kWG);
+        if constexpr (kQuant && !kSpread) {
 #pragma unroll
-        for (int c = 0; c < FM; ++c) mfma(acc[g][c], fw[g], fa[0][c]);
-        __builtin_amdgcn_sched_barrier(0);
+          for (int u = 0; u < TW::kParts; ++u) tw.write(s_wt[(W + 2) % 3], set[A], g, u);
+          if (g == FN - 1) codes(e + 2 + NA, A);
+        }
+        products(acc, g, 0, s_wt[(W + 2) % 3], A);
       }
 #pragma unroll
       for (int g = 0; g < FN; ++g) {
         if (g == 0) {
-          fw[6] = wt(W, 1, 6);
-          fw[7] = wt(W, 1, 7);
+          fw[FN - 2] = wt(W, 1, FN - 2);
+          fw[FN - 1] = wt(W, 1, FN - 1);
         }
         if (g == 2) {
-          __builtin_amdgcn_s_waitcnt(wait_code(kW));
+          __builtin_amdgcn_s_waitcnt(wait_code(NA == 2 ? kW : 2 * kW + kA));
           barrier();
         }
-        if (g >= 2) fw[g - 2] = wt(NW, 0, g - 2);
-        if (g >= 2 && g < 6)
+        if (g >= 2) fw[g - 2] = wt(W1, 0, g - 2);
+        if (g >= 2 && g < 2 + kHalf)
 #pragma unroll
-          for (int i = (g - 2) * kPer; i < (g - 1) * kPer && i < FM; ++i) fa[0][i] = act(NA, 0, i);
-        if (g >= 4) copy_a(e + 2, A, (g - 4) * kAG, kAG);
-#pragma unroll
-        for (int c = 0; c < FM; ++c) mfma(acc[g][c], fw[g], fa[1][c]);
-        __builtin_amdgcn_sched_barrier(0);
+          for (int i = (g - 2) * kPer; i < (g - 1) * kPer && i < FM; ++i) fa[0][i] = act(A1, 0, i);
+        if (g >= kHalf) copy_a(e + NA, A, (g - kHalf) * kAG, kAG);
+        products(acc, g, 1, s_wt[(W + 2) % 3], A);
       }
+      if constexpr (kQuant && kSpread) codes(e + 2 + NA, A);
     };
     using I0 = std::integral_constant<int, 0>;
     using I1 = std::integral_constant<int, 1>;
     using I2 = std::integral_constant<int, 2>;
-    for (int e = 0; e < steps; e += 6) {
-      step(e, I0{}, I0{});
-      step(e + 1, I1{}, I1{});
-      step(e + 2, I0{}, I2{});
-      step(e + 3, I1{}, I0{});
-      step(e + 4, I0{}, I1{});
-      step(e + 5, I1{}, I2{});
+    if constexpr (NA == 2) {
+      for (int e = 0; e < steps; e += 6) {
+        step(e, I0{}, I0{});
+        step(e + 1, I1{}, I1{});
+        step(e + 2, I0{}, I2{});
+        step(e + 3, I1{}, I0{});
+        step(e + 4, I0{}, I1{});
+        step(e + 5, I1{}, I2{});
+      }
+    } else {
+      for (int e = 0, n = padded(steps); e < n; e += 3) {
+        step(e, I0{}, I0{});
+        step(e + 1, I1{}, I1{});
+        step(e + 2, I2{}, I2{});
+      }
     }
     settle(acc);
   }
@@ -304,11 +496,12 @@ __device__ __forceinline__ void clear(f32x4 (&acc)[FN][FM]) {
     for (int c = 0; c < FM; ++c) acc[a][c] = f32x4{0.f, 0.f, 0.f, 0.f};
 }
 
-__device__ __forceinline__ void tile_at(int64_t t, int64_t gm, int64_t gn, int64_t& mt, int64_t& nt) {
-  const int64_t per_group = kGroupM * gn, g = t / per_group, left = gm - g * kGroupM;
-  const int64_t rows = left < kGroupM ? left : kGroupM, in_g = t - g * per_group;
-  mt = g * kGroupM + in_g % rows;
-  nt = in_g / rows;
+// (there are below 2^31 tiles; the results are told to be the same in all lanes)
+__device__ __forceinline__ void tile_at(uint32_t t, uint32_t gm, uint32_t gn, int64_t& mt, int64_t& nt) {
+  const uint32_t per_group = kGroupM * gn, g = t / per_group, left = gm - g * kGroupM;
+  const uint32_t rows = left < kGroupM ? left : kGroupM, in_g = t - g * per_group;
+  mt = __builtin_amdgcn_readfirstlane(g * kGroupM + in_g % rows);
+  nt = __builtin_amdgcn_readfirstlane(in_g / rows);
 }
 
 // max of three (fmaxf would quiet each operand with an instruction of its own; a NaN is
@@ -340,12 +533,12 @@ __device__ __forceinline__ float sum_quarters(float v) {
 // on: the row's cell and sum, the label's logit, E.  (Stores of 16 bytes a lane, 64 a
 // row and instruction.  Through LDS they would be whole rows, but the stages already
 // hold the next tile.)  Bound by the vector unit, a third of it exponentials.
-template <int BM, bool kE>
-__device__ __forceinline__ void reduce_tile(const HeadPiece& p, const f32x4 (&acc)[kWN / 16][BM / 32], int64_t m0, int64_t n0) {
-  constexpr int FN = kWN / 16, FM = BM / 32;
+template <int BM, int BN, bool kE>
+__device__ __forceinline__ void reduce_tile(const HeadPiece& p, const f32x4 (&acc)[BN / 32][BM / 32], int64_t m0, int64_t n0) {
+  constexpr int FN = BN / 32, FM = BM / 32, WN = BN / 2;
   const int lane = threadIdx.x & 63, r16 = lane & 15, quarter = lane >> 4;
-  const int left = static_cast<int>(p.n - n0 < kWN ? p.n - n0 : kWN);  // valid columns; behind them -inf
-  const int64_t block = n0 / kHeadCols;
+  const int left = static_cast<int>(p.n <= n0 ? 0 : p.n - n0 < WN ? p.n - n0 : WN);  // valid columns; behind them -inf
+  const int64_t block = n0 / WN;
   // the rows' labels and cells, all loads ahead of the first store (rows past the
   // last one read its)
   const int rows = static_cast<int>(p.T - m0 < BM / 2 ? p.T - m0 : BM / 2);  // this wave's; <= 0: none
@@ -414,7 +607,7 @@ __device__ __forceinline__ void reduce_tile(const HeadPiece& p, const f32x4 (&ac
     // s - ref is one fused multiply-add.  Its product is not rounded, the cell's was:
     // from 2^31 on they would be further apart than a cell, so of such rows (from
     // 2^23 on) the products are rounded first.
-    if (left == kWN && !__any(label[c] >= 0 || fabsf(top) >= 0x1p23f)) {
+    if (left == WN && !__any(label[c] >= 0 || fabsf(top) >= 0x1p23f)) {
       finish(s, kLog2e, fmaxf(before[c], cell_of(top * kLog2e)));
     } else {
       // (the accumulators are left as they are: changed in a branch, all of them would
@@ -440,45 +633,72 @@ __device__ __forceinline__ void reduce_tile(const HeadPiece& p, const f32x4 (&ac
 
 }  // namespace
 
+// the piece's rows from n0 on
+template <int F>
+__device__ __forceinline__ auto weight_source(const HeadPiece& p, int64_t n0) {
+  if constexpr (F == kBf16) {
+    return rows_source(p.W, p.H, n0, p.n, 0);
+  } else {
+    const int64_t kb = ceil_div(p.H, int64_t(kF8Block)), at = n0 * p.H, rows = p.n > n0 ? p.n - n0 : 0;
+    const int64_t n = rows * p.H >> (F == kNf4 ? 1 : 0);
+    CodeSource s{};
+    s.codes = p.q.codes + (F == kNf4 ? at / 2 : at);
+    s.bytes = static_cast<int>(n < 0x7fffffff ? n : 0x7fffffff);
+    if constexpr (F == kNf4) {
+      s.q = p.q.absmax_q + at / kBlock;
+      s.phase = static_cast<int>(at / kBlock % kGroup);
+      s.scale = p.q.scale + at / (p.q.absmax_q != nullptr ? kGroupElems : kBlock);
+    } else {
+      s.q = p.q.scale8 + n0 / kF8Block * kb;
+      s.q_bytes = static_cast<int>(ceil_div(rows, int64_t(kF8Block)) * kb);
+    }
+    return s;
+  }
+}
+
 // kE: with E (the gradient's call); else the sums alone.
-template <int BM, bool kE>
-__global__ __launch_bounds__(256, 1) void k_head_logits(HeadPiece p) {
-  constexpr int FN = kWN / 16, FM = BM / 32, WM = BM / 2;
-  __shared__ __attribute__((aligned(1024))) uint16_t s_a0[BM * kBK], s_a1[BM * kBK];
-  __shared__ __attribute__((aligned(1024))) uint16_t s_w0[kBN * kBK], s_w1[kBN * kBK], s_w2[kBN * kBK];
+template <int BM, int BN, bool kE, int F>
+__global__ __launch_bounds__(256, BN == 128 ? 2 : 1) void k_head_logits(HeadPiece p) {
+  constexpr int FN = BN / 32, FM = BM / 32, WM = BM / 2;
+  constexpr bool kThird = act_stages(BM, BN, F != kBf16) == 3;
+  __shared__ __attribute__((aligned(1024))) uint16_t s_a0[BM * kBK], s_a1[BM * kBK], s_a2[kThird ? BM * kBK : 1];
+  __shared__ __attribute__((aligned(1024))) uint16_t s_w0[BN * kBK], s_w1[BN * kBK], s_w2[BN * kBK];
 
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wv & 1, wn = wv >> 1;
   // This workgroup's tiles: XCD x (workgroups x, x + 8, ...) has a contiguous eighth
   // of the sequence, which walks groups of kGroupM row tiles column by column.
-  const int64_t gm = ceil_div(p.T, BM), gn = ceil_div(p.n, kBN), total = gm * gn;
-  const int64_t xcd = blockIdx.x % kXcds, stride = gridDim.x / kXcds, end = total * (xcd + 1) / kXcds;
-  int64_t t = total * xcd / kXcds + blockIdx.x / kXcds;
+  const uint32_t gm = static_cast<uint32_t>(ceil_div(p.T, BM)), gn = static_cast<uint32_t>(p.lde / BN), total = gm * gn;
+  const uint32_t xcd = blockIdx.x % kXcds, stride = gridDim.x / kXcds;
+  const uint32_t end = static_cast<uint32_t>(static_cast<uint64_t>(total) * (xcd + 1) / kXcds);
+  uint32_t t = static_cast<uint32_t>(static_cast<uint64_t>(total) * xcd / kXcds) + blockIdx.x / kXcds;
   if (t >= end) return;
 
-  using TW = RowTile<kBN>;
-  HeadLoop<BM, TW> loop{{s_a0, s_a1}, {s_w0, s_w1, s_w2}, wv};
+  using TW = std::conditional_t<F == kBf16, RowTile<BN>, CodeTile<BN, F, false>>;
+  HeadLoop<BM, BN, TW> loop;
+  loop.stages(s_a0, s_a1, s_a2, s_w0, s_w1, s_w2, wv);
   loop.ta.init(p.H, wv, lane);
-  loop.tw.init(p.H, wv, lane);
+  if constexpr (F == kBf16) loop.tw.init(p.H, wv, lane);
+  else loop.tw.init(p.H, wv, lane, 0, p.q.absmax_q != nullptr);
   loop.k0 = 0;
   loop.steps = static_cast<int>(p.H / kBK);
   int64_t m0, n0, m1 = 0, n1 = 0;
   tile_at(t, gm, gn, m0, n0);
   m0 *= BM;
-  n0 *= kBN;
+  n0 *= BN;
   loop.a[0] = rows_source(p.X, p.H, m0, p.T, 0);
-  loop.w[0] = rows_source(p.W, p.H, n0, p.n, 0);
+  loop.w[0] = weight_source<F>(p, n0);
   bool more = false;
   const auto look_ahead = [&]() {
     more = t + stride < end;
     loop.a[1] = Source{p.X, 0};
-    loop.w[1] = Source{p.W, 0};
+    loop.w[1] = weight_source<F>(p, p.n);
     if (more) {
       tile_at(t + stride, gm, gn, m1, n1);
       m1 *= BM;
-      n1 *= kBN;
+      n1 *= BN;
       loop.a[1] = rows_source(p.X, p.H, m1, p.T, 0);
-      loop.w[1] = rows_source(p.W, p.H, n1, p.n, 0);
+      loop.w[1] = weight_source<F>(p, n1);
     }
   };
   look_ahead();
@@ -487,7 +707,7 @@ __global__ __launch_bounds__(256, 1) void k_head_logits(HeadPiece p) {
     f32x4 acc[FN][FM];
     clear(acc);
     loop.tile(acc);
-    reduce_tile<BM, kE>(p, acc, m0 + wm * WM, n0 + wn * kWN);
+    reduce_tile<BM, BN, kE>(p, acc, m0 + wm * WM, n0 + wn * (BN / 2));
     if (!more) break;
     m0 = m1;
     n0 = n1;
@@ -523,92 +743,109 @@ __device__ __forceinline__ RowLoss row_loss(float c, float s, bool has, float t)
   return r;
 }
 
-// Workgroup x: 64 rows; its 16 waves share the piece's blocks of 128 columns.
-// Workgroup y scales the E of blocks 16 y, ... of those rows where the block's cell is
-// below the row's (one wave instruction a row and block; rare).  Without E the last
-// piece's launch writes loss and lse.  Bound by the latency of one round of loads.
-constexpr int kRowWaves = 16;
+// Workgroup x: 16 rows, which its 16 waves have four times each: 64 shares of the
+// piece's blocks of p.cols columns.  Workgroup y scales the E of blocks 64 y, ... of
+// those rows where the block's cell is below the row's (one wave instruction a row and
+// block; rare).  Without E the last piece's launch writes loss and lse.  Bound by the
+// latency of one round of loads.
+constexpr int kRowWaves = 16, kRowShares = 4 * kRowWaves;
 __global__ __launch_bounds__(64 * kRowWaves) void k_head_rows(HeadPiece p, HeadFinish f) {
-  __shared__ float sc[kRowWaves][64], ss[kRowWaves][64];
-  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-  const int64_t m = static_cast<int64_t>(blockIdx.x) * 64 + lane;
+  __shared__ float sc[kRowShares][16], ss[kRowShares][16];
+  const int lane = threadIdx.x & 63, r16 = lane & 15, share = threadIdx.x >> 4;
+  const int64_t m0 = static_cast<int64_t>(blockIdx.x) * 16, m = m0 + r16;
   const bool live = m < p.T;
-  const int blocks = static_cast<int>(p.lde / kHeadCols);
+  const int blocks = static_cast<int>(p.lde / p.cols);
   float c = -kInf, s = 0.f;
-  for (int t = wv; t < blocks; t += 8 * kRowWaves) {
+  for (int t = share; t < blocks; t += 8 * kRowShares) {
     float tc[8], ts[8];
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
-      const bool in = live && t + kRowWaves * u < blocks;
-      tc[u] = in ? p.tile_c[(t + kRowWaves * u) * p.T + m] : -kInf;
-      ts[u] = in ? p.tile_s[(t + kRowWaves * u) * p.T + m] : 0.f;
+      const bool in = live && t + kRowShares * u < blocks;
+      tc[u] = in ? p.tile_c[(t + kRowShares * u) * p.T + m] : -kInf;
+      ts[u] = in ? p.tile_s[(t + kRowShares * u) * p.T + m] : 0.f;
     }
 #pragma unroll
     for (int u = 0; u < 8; ++u) join(c, s, tc[u], ts[u]);
   }
-  sc[wv][lane] = c;
-  ss[wv][lane] = s;
+  sc[share][r16] = c;
+  ss[share][r16] = s;
   __syncthreads();
-  const float before = live && !p.first ? p.c_in[m] : -kInf;
-  c = before;
-  s = live && !p.first ? p.s_in[m] : 0.f;
+  // each wave for itself: a quarter of the shares a lane, then the quarters in order
+  const int first = (lane >> 4) * (kRowShares / 4);
+  c = -kInf;
+  s = 0.f;
 #pragma unroll
-  for (int i = 0; i < kRowWaves; ++i) join(c, s, sc[i][lane], ss[i][lane]);
-  if (blockIdx.y == 0 && wv == 0 && live) {
+  for (int i = 0; i < kRowShares / 4; ++i) join(c, s, sc[first + i][r16], ss[first + i][r16]);
+  const float before = live && !p.first ? p.c_in[m] : -kInf;
+  float rc = before, rs = live && !p.first ? p.s_in[m] : 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) join(rc, rs, __shfl(c, 16 * i + r16), __shfl(s, 16 * i + r16));
+  if (blockIdx.y == 0 && threadIdx.x < 16 && live) {
     if (f.loss != nullptr) {
       const int64_t y = f.labels[m];
       const bool has = y >= 0 && y < f.V;
-      const RowLoss r = row_loss(c, s, has, has ? f.target[m] : 0.f);
+      const RowLoss r = row_loss(rc, rs, has, has ? f.target[m] : 0.f);
       f.loss[m] = r.loss;
       if (f.lse != nullptr) f.lse[m] = r.lse;
     } else {
-      p.c_out[m] = c;
-      p.s_out[m] = s;
-      if (p.E != nullptr) p.factor[m] = before == c ? 1.f : down_cells(1.f, before - c);
+      p.c_out[m] = rc;
+      p.s_out[m] = rs;
+      if (p.E != nullptr) p.factor[m] = before == rc ? 1.f : down_cells(1.f, before - rc);
     }
   }
   if (p.E == nullptr) return;
-  for (int t = blockIdx.y * kRowWaves + wv; t < blocks; t += gridDim.y * kRowWaves) {
-    const float tc = live ? p.tile_c[t * p.T + m] : c;
-    uint64_t todo = __ballot(live && tc != c && tc != -kInf);
+  for (int t0 = blockIdx.y * kRowShares + share / 4 * 4; t0 < blocks; t0 += gridDim.y * kRowShares) {
+    const int t = t0 + (lane >> 4);
+    const float tc = live && t < blocks ? p.tile_c[t * p.T + m] : -kInf;
+    uint64_t todo = __ballot(tc != rc && tc != -kInf);
     while (todo != 0) {
       const int l = __builtin_ctzll(todo);
       todo &= todo - 1;
-      const float d = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, tc - c), l));
-      uint32_t* at = reinterpret_cast<uint32_t*>(p.E + (static_cast<int64_t>(blockIdx.x) * 64 + l) * p.lde +
-                                                 static_cast<int64_t>(t) * kHeadCols + 2 * lane);
+      const float d = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, tc - rc), l));
+      if (2 * lane >= p.cols) continue;
+      uint32_t* at = reinterpret_cast<uint32_t*>(p.E + (m0 + (l & 15)) * p.lde + static_cast<int64_t>(t0 + (l >> 4)) * p.cols +
+                                                 2 * lane);
       const uint32_t v = *at;
       *at = pack_bf16x2(down_cells(bf16_lo(v), d), down_cells(bf16_hi(v), d));
     }
   }
 }
 
-template <int BM>
-__global__ __launch_bounds__(256, 1) void k_head_grad(HeadPiece p, float* part, int ks) {
-  constexpr int FN = kWN / 16, FM = BM / 32, WM = BM / 2;
-  __shared__ __attribute__((aligned(1024))) uint16_t s_a0[BM * kBK], s_a1[BM * kBK];
-  __shared__ __attribute__((aligned(1024))) uint16_t s_w0[kBN * kBK], s_w1[kBN * kBK], s_w2[kBN * kBK];
+template <int BM, int BN, int F>
+__global__ __launch_bounds__(256, BN == 128 ? 2 : 1) void k_head_grad(HeadPiece p, float* part, int ks) {
+  constexpr int FN = BN / 32, FM = BM / 32, WM = BM / 2;
+  constexpr bool kThird = act_stages(BM, BN, F != kBf16) == 3;
+  __shared__ __attribute__((aligned(1024))) uint16_t s_a0[BM * kBK], s_a1[BM * kBK], s_a2[kThird ? BM * kBK : 1];
+  __shared__ __attribute__((aligned(1024))) uint16_t s_w0[BN * kBK], s_w1[BN * kBK], s_w2[BN * kBK];
 
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wv & 1, wn = wv >> 1, r16 = lane & 15, quarter = lane >> 4;
   int64_t mt, nt;
   xcd_tile(gridDim.x, gridDim.y, mt, nt);
-  const int64_t m0 = mt * BM, n0 = nt * kBN;
+  const int64_t m0 = mt * BM, n0 = nt * BN;
   const int k0 = static_cast<int>(blockIdx.z) * ks, end = static_cast<int>(p.lde / kBK);
   const int steps = k0 + ks < end ? ks : end > k0 ? end - k0 : 0;
 
   f32x4 acc[FN][FM];
   clear(acc);
   if (steps > 0) {
-    HeadLoop<BM, ColTile> loop{{s_a0, s_a1}, {s_w0, s_w1, s_w2}, wv};
+    using TW = std::conditional_t<F == kBf16, ColTile<BN>, CodeTile<BN, F, true>>;
+    HeadLoop<BM, BN, TW> loop;
+    loop.stages(s_a0, s_a1, s_a2, s_w0, s_w1, s_w2, wv);
     loop.ta.init(p.lde, wv, lane);
-    loop.tw.init(p.H, wv, lane);
+    if constexpr (F == kBf16) loop.tw.init(p.H, wv, lane);
+    else loop.tw.init(p.H, wv, lane, n0, p.q.absmax_q != nullptr);
     loop.k0 = k0;
     loop.steps = steps;
     loop.a[0] = rows_source(p.E, p.lde, m0, p.T, 0);
-    loop.w[0] = rows_source(p.W, p.H, 0, p.n, n0);
+    if constexpr (F == kBf16) {
+      loop.w[0] = rows_source(p.W, p.H, 0, p.n, n0);
+      loop.w[1] = Source{p.W, 0};
+    } else {
+      loop.w[0] = loop.w[1] = weight_source<F>(p, 0);
+      loop.w[1].bytes = 0;
+    }
     loop.a[1] = Source{p.E, 0};
-    loop.w[1] = Source{p.W, 0};
     loop.begin();
     loop.tile(acc);
     __builtin_amdgcn_s_waitcnt(0);  // copies behind the last step
@@ -621,7 +858,7 @@ __global__ __launch_bounds__(256, 1) void k_head_grad(HeadPiece p, float* part, 
     const float f = p.first ? 0.f : p.factor[m];
 #pragma unroll
     for (int a = 0; a < FN; ++a) {
-      const int64_t n = n0 + wn * kWN + a * 16 + 4 * quarter;
+      const int64_t n = n0 + wn * (BN / 2) + a * 16 + 4 * quarter;
       if (n >= p.H) continue;
       f32x4* at = reinterpret_cast<f32x4*>(dst + m * p.H + n);
       f32x4 v = acc[a][c];
@@ -712,95 +949,144 @@ __global__ __launch_bounds__(256) void k_head_finish(HeadFinish f) {
   *reinterpret_cast<u32x4*>(f.dX + m * f.H + col) = o;
 }
 
-#define HEAD_KERNELS(BM)                                       \
-  template __global__ void k_head_logits<BM, true>(HeadPiece);  \
-  template __global__ void k_head_logits<BM, false>(HeadPiece); \
-  template __global__ void k_head_grad<BM>(HeadPiece, float*, int);
-HEAD_KERNELS(64) HEAD_KERNELS(96) HEAD_KERNELS(128) HEAD_KERNELS(160) HEAD_KERNELS(192) HEAD_KERNELS(224) HEAD_KERNELS(256)
+#define HEAD_LOGITS(BM, BN, F)                                        \
+  template __global__ void k_head_logits<BM, BN, true, F>(HeadPiece);  \
+  template __global__ void k_head_logits<BM, BN, false, F>(HeadPiece);
+#define HEAD_KERNELS(BM, BN, F) \
+  HEAD_LOGITS(BM, BN, F) template __global__ void k_head_grad<BM, BN, F>(HeadPiece, float*, int);
+#define HEAD_CODES(F)                                                                                     \
+  HEAD_KERNELS(64, 128, F) HEAD_KERNELS(128, 128, F) HEAD_KERNELS(96, 256, F) HEAD_KERNELS(128, 256, F) \
+  HEAD_KERNELS(160, 256, F) HEAD_KERNELS(192, 256, F) HEAD_KERNELS(256, 256, F)
+HEAD_LOGITS(64, 128, kBf16)
+HEAD_KERNELS(64, 256, kBf16) HEAD_KERNELS(96, 256, kBf16) HEAD_KERNELS(128, 256, kBf16) HEAD_KERNELS(160, 256, kBf16)
+HEAD_KERNELS(192, 256, kBf16) HEAD_KERNELS(224, 256, kBf16) HEAD_KERNELS(256, 256, kBf16)
+HEAD_CODES(kNf4)
+HEAD_CODES(kFp8)
 
 namespace {
 constexpr int64_t kHeadCus = 256;  // of the part; fixed, so that sizes depend on shapes only
 
-// Rows of a tile.  A round of tiles (one a CU) of 64, 128, 192 and 256 rows takes 53,
-// 68, 95 and 107 us at 4096 columns, about 36 + 0.28 rows: the shorter ones read more
-// weights a product, so which is best goes by how they fill the rounds.  Measured with
-// one height throughout (64 / 128 / 192 / 256), gradient calls: 40 x 50021 x 2304 136 /
-// 140 / 146 / 150 us, 200 x 32000 x 4096 203 / 174 / 192 / 200, 301 x 50021 x 2304 350 /
-// 285 / 226 / 250, 1024 x 32000 x 4096 722 / 495 / 508 / 440.
+// Rows of a tile of 256 columns.  A round of tiles (one a CU) of 64, 128, 192 and 256
+// rows takes 53, 68, 95 and 107 us at 4096 columns, about 36 + 0.28 rows: the shorter ones
+// read more weights a product, so which is best goes by how they fill the rounds.
+// Measured with one height throughout (64 / 128 / 192 / 256), gradient calls: 40 x 50021 x
+// 2304 136 / 140 / 146 / 150 us, 200 x 32000 x 4096 203 / 174 / 192 / 200, 301 x 50021 x
+// 2304 350 / 285 / 226 / 250, 1024 x 32000 x 4096 722 / 495 / 508 / 440.  (Of 4- and
+// 8-bit weights 64 rows have the tiles below, and with 224 the registers do not suffice.)
 constexpr int kHeights[] = {64, 96, 128, 160, 192, 224, 256};
 constexpr int64_t height_cost(int rows) { return 128 + rows; }
+constexpr bool height_fits(int rows, bool codes) { return !codes || (rows != 64 && rows != 224); }
 
-int logits_rows(int64_t T, int64_t n) {
+// Few rows: tiles of 128 columns, two workgroups a CU, so that one works while the
+// other waits for its LDS reads and turns codes into bf16 (128 rows of an 8-bit
+// weight 32000 x 4096: 82 us with 256 columns, 64 with 128, gradient 143 and 125).  A bf16
+// weight's tiles wait for HBM instead; there the logits of up to 64 rows take them where
+// tiles of 256 columns would fill no more than half of the CUs (16 x 32000 x 4096: 69
+// us, 77 with 256 columns; 16 x 128000 x 4096: 223 and 213).
+bool half_tiles(int64_t T, int64_t n, bool codes) {
+  return codes ? T <= 128 : T <= 64 && ceil_div(n, int64_t(256)) <= kHeadCus / 2;
+}
+int half_rows(int64_t T) { return T <= 64 ? 64 : 128; }
+
+struct TileShape {
+  int rows, cols;
+};
+TileShape logits_shape(int64_t T, int64_t n, bool codes) {
+  if (half_tiles(T, n, codes)) return {half_rows(T), 128};
   int best = 0;
   int64_t least = 0;
   for (int rows : kHeights) {
-    const int64_t cost = ceil_div(ceil_div(T, rows) * ceil_div(n, kBN), kHeadCus) * height_cost(rows);
+    if (!height_fits(rows, codes)) continue;
+    const int64_t cost = ceil_div(ceil_div(T, rows) * ceil_div(n, int64_t(256)), kHeadCus) * height_cost(rows);
     if (best == 0 || cost < least) best = rows, least = cost;
   }
-  return best;
+  return {best, 256};
 }
 
-// The rows of a tile of E W and the ranges of the vocabulary, each of 1024 columns or
-// more: as many as give every CU a workgroup.
+// The tiles of E W and the ranges of the vocabulary, each of 1024 columns or more: as
+// many as give every CU its workgroups.
 struct GradShape {
-  int rows, splits;
+  TileShape tile;
+  int splits;
 };
-GradShape grad_shape(int64_t T, int64_t H, int64_t n) {
-  GradShape best{0, 1};
-  int64_t least = 0;
+GradShape grad_shape(int64_t T, int64_t H, int64_t n, bool codes) {
   const int64_t steps = round_up(n, kHeadTile) / kBK;
-  for (int rows : kHeights) {
-    const int64_t tiles = ceil_div(T, rows) * ceil_div(H, kBN);
-    int64_t S = kHeadCus / tiles;
+  const auto splits = [&](int64_t workgroups, int64_t tiles) {
+    int64_t S = workgroups / tiles;
     if (S > steps / 16) S = steps / 16;
-    if (S < 1) S = 1;
+    return S < 1 ? int64_t(1) : S;
+  };
+  if (codes && half_tiles(T, n, codes))
+    return {{half_rows(T), 128}, static_cast<int>(splits(2 * kHeadCus, ceil_div(H, int64_t(128))))};
+  GradShape best{{0, 256}, 1};
+  int64_t least = 0;
+  for (int rows : kHeights) {
+    if (!height_fits(rows, codes)) continue;
+    const int64_t tiles = ceil_div(T, rows) * ceil_div(H, int64_t(256)), S = splits(kHeadCus, tiles);
     const int64_t cost = ceil_div(tiles * S, kHeadCus) * ceil_div(steps, S) * height_cost(rows);
-    if (best.rows == 0 || cost < least) best = GradShape{rows, static_cast<int>(S)}, least = cost;
+    if (best.tile.rows == 0 || cost < least) best = GradShape{{rows, 256}, static_cast<int>(S)}, least = cost;
   }
   return best;
 }
 
-template <class F>
-void with_rows(int rows, F f) {
-  if (rows == 64) f(std::integral_constant<int, 64>{});
-  else if (rows == 96) f(std::integral_constant<int, 96>{});
-  else if (rows == 128) f(std::integral_constant<int, 128>{});
-  else if (rows == 160) f(std::integral_constant<int, 160>{});
-  else if (rows == 192) f(std::integral_constant<int, 192>{});
-  else if (rows == 224) f(std::integral_constant<int, 224>{});
-  else f(std::integral_constant<int, 256>{});
+template <int N>
+using Int = std::integral_constant<int, N>;
+// f(tile rows, tile columns, format)
+template <class Fn>
+void with_kernel(TileShape t, const HeadWeight& q, Fn f) {
+  const auto with = [&](auto fmt) {
+    if constexpr (decltype(fmt)::value == kBf16) {
+      if (t.cols == 128) return f(Int<64>{}, Int<128>{}, fmt);
+      if (t.rows == 64) return f(Int<64>{}, Int<256>{}, fmt);
+      if (t.rows == 224) return f(Int<224>{}, Int<256>{}, fmt);
+    } else {
+      if (t.cols == 128 && t.rows == 64) return f(Int<64>{}, Int<128>{}, fmt);
+      if (t.cols == 128) return f(Int<128>{}, Int<128>{}, fmt);
+    }
+    if (t.rows == 96) return f(Int<96>{}, Int<256>{}, fmt);
+    if (t.rows == 128) return f(Int<128>{}, Int<256>{}, fmt);
+    if (t.rows == 160) return f(Int<160>{}, Int<256>{}, fmt);
+    if (t.rows == 192) return f(Int<192>{}, Int<256>{}, fmt);
+    f(Int<256>{}, Int<256>{}, fmt);
+  };
+  if (q.codes == nullptr) with(Int<kBf16>{});
+  else if (q.scale8 == nullptr) with(Int<kNf4>{});
+  else with(Int<kFp8>{});
 }
 }  // namespace
 
+int head_cols(int64_t T, int64_t n, bool codes) { return logits_shape(T, n, codes).cols / 2; }
+
 hipError_t launch_head_logits(const HeadPiece& p, hipStream_t s) {
-  const dim3 grid(static_cast<uint32_t>(kHeadCus));  // a multiple of the XCDs' number
-  with_rows(logits_rows(p.T, p.n), [&](auto b) {
-    constexpr int BM = decltype(b)::value;
-    if (p.E != nullptr) hipLaunchKernelGGL((k_head_logits<BM, true>), grid, dim3(256), 0, s, p);
-    else hipLaunchKernelGGL((k_head_logits<BM, false>), grid, dim3(256), 0, s, p);
+  const TileShape t = logits_shape(p.T, p.n, p.q.codes != nullptr);
+  const dim3 grid(static_cast<uint32_t>(t.cols == 128 ? 2 * kHeadCus : kHeadCus));  // a multiple of the XCDs' number
+  with_kernel(t, p.q, [&](auto bm, auto bn, auto fmt) {
+    constexpr int BM = decltype(bm)::value, BN = decltype(bn)::value, F = decltype(fmt)::value;
+    if (p.E != nullptr) hipLaunchKernelGGL((k_head_logits<BM, BN, true, F>), grid, dim3(256), 0, s, p);
+    else hipLaunchKernelGGL((k_head_logits<BM, BN, false, F>), grid, dim3(256), 0, s, p);
   });
   return hipGetLastError();
 }
 
 hipError_t launch_head_rows(const HeadPiece& p, const HeadFinish& f, hipStream_t s) {
-  const int64_t blocks = p.lde / kHeadCols;
-  const int64_t ys = p.E == nullptr ? 1 : blocks < 8 * kRowWaves ? ceil_div(blocks, kRowWaves) : 8;
-  hipLaunchKernelGGL(k_head_rows, dim3(static_cast<uint32_t>(ceil_div(p.T, 64)), static_cast<uint32_t>(ys)),
+  const int64_t blocks = p.lde / p.cols;
+  const int64_t ys = p.E == nullptr ? 1 : blocks < 8 * kRowShares ? ceil_div(blocks, kRowShares) : 8;
+  hipLaunchKernelGGL(k_head_rows, dim3(static_cast<uint32_t>(ceil_div(p.T, 16)), static_cast<uint32_t>(ys)),
                      dim3(64 * kRowWaves), 0, s, p, f);
   return hipGetLastError();
 }
 
-int head_splits(int64_t T, int64_t H, int64_t n) { return grad_shape(T, H, n).splits; }
+int head_splits(int64_t T, int64_t H, int64_t n, bool codes) { return grad_shape(T, H, n, codes).splits; }
 
 hipError_t launch_head_grad(const HeadPiece& p, float* part, int splits, hipStream_t s) {
   // (the last piece and the last round may be smaller: the number of splits stays)
-  const int rows = grad_shape(p.T, p.H, p.n).rows;
-  const dim3 grid(static_cast<uint32_t>(ceil_div(p.T, rows)), static_cast<uint32_t>(ceil_div(p.H, kBN)),
+  const TileShape t = grad_shape(p.T, p.H, p.n, p.q.codes != nullptr).tile;
+  const dim3 grid(static_cast<uint32_t>(ceil_div(p.T, t.rows)), static_cast<uint32_t>(ceil_div(p.H, t.cols)),
                   static_cast<uint32_t>(splits));
   const int ks = static_cast<int>(ceil_div(p.lde / kBK, splits));
-  with_rows(rows, [&](auto b) {
-    constexpr int BM = decltype(b)::value;
-    hipLaunchKernelGGL((k_head_grad<BM>), grid, dim3(256), 0, s, p, part, ks);
+  with_kernel(t, p.q, [&](auto bm, auto bn, auto fmt) {
+    constexpr int BM = decltype(bm)::value, BN = decltype(bn)::value, F = decltype(fmt)::value;
+    if constexpr (F != kBf16 || BN == 256) hipLaunchKernelGGL((k_head_grad<BM, BN, F>), grid, dim3(256), 0, s, p, part, ks);
   });
   return hipGetLastError();
 }

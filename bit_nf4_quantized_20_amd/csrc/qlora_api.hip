@@ -1255,6 +1255,11 @@ bool norm_shapes_ok(int64_t T, int64_t H) {
 // once in n columns of work.  Without a gradient it is the blocks' cells and sums
 // that want an end, 8 bytes for 128 logits: 64 times as many take 512 MiB.
 constexpr int64_t kHeadTokens = 4096, kHeadLogits = int64_t(1) << 27;
+// Up to here 4- and 8-bit weights are turned into bf16 on their way into the products;
+// for more rows, whose tiles each do that, they are written out first, a piece at a time.
+// Loss of 512 x 65536 x 4096: NF4 290 us and 356, 8 bits 275 and 370, with gradient 576 and
+// 640, 553 and 653; 1024 x 32000 x 4096: 283 and 267, 256 and 269, 541 and 486, 508 and 497.
+constexpr int64_t kHeadCodesTokens = 512;
 // Weights of one piece that are written out in bf16.
 constexpr int64_t kHeadWeights = int64_t(1) << 27;
 constexpr int64_t kHeadMaxHidden = 16384, kHeadMaxVocab = int64_t(1) << 24;
@@ -1266,6 +1271,7 @@ bool head_shapes_ok(int64_t T, int64_t V, int64_t H) {
 
 struct HeadLayout {
   int64_t tokens, n;  // rows of a round, columns of a piece
+  bool codes;         // W read in its own format by the products themselves
   int splits;
   size_t w, e, part, tile_c, tile_s, target, c[2], s[2], factor, total;
 };
@@ -1274,6 +1280,8 @@ HeadLayout head_layout(int64_t T, int64_t V, int64_t H, bool expand, bool grad) 
   const int64_t rounds = T > 0 ? ceil_div(T, kHeadTokens) : 1;
   l.tokens = rounds > 1 ? round_up(ceil_div(T, rounds), 256) : T;
   const int64_t rows = l.tokens > 0 ? l.tokens : 1;
+  l.codes = expand && rows <= kHeadCodesTokens;
+  expand = expand && !l.codes;
   int64_t most = round_up(V, kHeadTile);
   const int64_t logits = grad ? kHeadLogits : kHeadLogits * 64;
   if (most > logits / rows) most = logits / rows;
@@ -1282,12 +1290,12 @@ HeadLayout head_layout(int64_t T, int64_t V, int64_t H, bool expand, bool grad) 
   if (grad && most > (int64_t(1) << 29) / H) most = (int64_t(1) << 29) / H;
   most = most / kHeadTile * kHeadTile;
   l.n = round_up(ceil_div(V, ceil_div(V, most)), kHeadTile);
-  const int64_t tiles = l.n / kHeadCols;
+  const int64_t tiles = l.n / (rows <= 128 ? 64 : 128);  // (at least; a shorter last round's fit in it)
   Carve c;
   const size_t row = static_cast<size_t>(l.tokens) * 4;
   l.w = c.take(expand ? static_cast<size_t>(l.n * H * 2) : 0);
   if (grad) {
-    l.splits = head_splits(rows, H, l.n);
+    l.splits = head_splits(rows, H, l.n, l.codes);
     l.e = c.take(static_cast<size_t>(l.tokens * l.n * 2));
     l.part = c.take(row * H * l.splits);
   }
@@ -1319,6 +1327,23 @@ int check_head(const qlora_head* W) {
     return QLORA_ERR_ALIGN;
   }
   return QLORA_OK;
+}
+
+// the head from row v0 on (a multiple of 256) in its own format
+HeadWeight head_rows(const qlora_head& W, int64_t v0) {
+  const int64_t H = W.hidden, at = v0 * H;
+  HeadWeight w{};
+  if (W.bf16 != nullptr) {
+    w.w16 = W.bf16 + at;
+  } else if (W.nf4 != nullptr) {
+    w.codes = W.nf4->codes + at / 2;
+    w.absmax_q = absmax_fp32(*W.nf4) ? nullptr : W.nf4->absmax_q + at / 64;
+    w.scale = W.nf4->absmax_scale + (absmax_fp32(*W.nf4) ? at / 64 : at / 16384);
+  } else {
+    w.codes = W.fp8->codes + at;
+    w.scale8 = W.fp8->scales + v0 / QLORA_FP8_BLOCK * ceil_div(H, QLORA_FP8_BLOCK);
+  }
+  return w;
 }
 
 // rows [v0, v0 + n) of the head in bf16 (v0 a multiple of 256)
@@ -1381,7 +1406,10 @@ int head_loss_impl(const qlora_head* W, const qlora_bf16* X, int64_t T, const in
       p.s_in = f32(lay.s[turn]);
       p.c_out = f32(lay.c[turn ^ 1]);
       p.s_out = f32(lay.s[turn ^ 1]);
-      if (expand) {
+      p.cols = head_cols(p.T, p.n, lay.codes);
+      if (lay.codes) {
+        p.q = head_rows(*W, v0);
+      } else if (expand) {
         uint16_t* w = reinterpret_cast<uint16_t*>(base + lay.w);
         e = head_piece(*W, v0, p.n, w, s);
         p.W = w;
@@ -1399,15 +1427,7 @@ int head_loss_impl(const qlora_head* W, const qlora_bf16* X, int64_t T, const in
     f.splits = lay.splits;
     f.dloss = dloss + t0;
     f.dX = dX + t0 * H;
-    f.W.w16 = W->bf16;
-    if (W->nf4 != nullptr) {
-      f.W.codes = W->nf4->codes;
-      f.W.absmax_q = absmax_fp32(*W->nf4) ? nullptr : W->nf4->absmax_q;
-      f.W.scale = W->nf4->absmax_scale;
-    } else if (W->fp8 != nullptr) {
-      f.W.codes = W->fp8->codes;
-      f.W.scale8 = W->fp8->scales;
-    }
+    f.W = head_rows(*W, 0);
     if (e == hipSuccess) e = launch_head_finish(f, s);
   }
   return launched(e);

@@ -656,8 +656,8 @@ int qlora_rmsnorm_bwd(const qlora_bf16* dy, const qlora_bf16* h, const float* we
 
 /*
  * A frozen output head [vocab, hidden], in one of the formats (the others NULL).
- * NF4 and 8-bit weights are written out in bf16 a piece at a time; their rows and
- * cols are vocab and hidden.
+ * NF4 and 8-bit weights enter the products in bf16; their rows and cols are vocab
+ * and hidden.
  */
 typedef struct {
   const qlora_bf16* bf16;

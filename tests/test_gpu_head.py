@@ -126,7 +126,8 @@ def test_loss_and_gradient(T, V, H):
 
 
 @pytest.mark.parametrize("kind", ["nf4", "nodq", "fp8"])
-@pytest.mark.parametrize("T,V,H", [(1, 64, 64), (5, 320, 128), (70, 1088, 192), (300, 704, 320)])
+@pytest.mark.parametrize("T,V,H", [(1, 64, 64), (5, 320, 128), (64, 1088, 192), (70, 1088, 192), (128, 704, 1088),
+                                   (300, 704, 320), (512, 2112, 320), (513, 2112, 320)])
 def test_quantized_heads(kind, T, V, H):
     q = require_gpu()
     banner(f"head {kind} {T}x{V}x{H}")
@@ -136,6 +137,23 @@ def test_quantized_heads(kind, T, V, H):
     out = q.qlora_head_loss_grad(W, X, _dev(y), dev_f32(g), ws=_poisoned(q, T, V, H, True, True))
     _compare(X, Wv, y, g, *out)
     _compare(X, Wv, y, g, *q.qlora_head_loss(W, X, _dev(y), ws=_poisoned(q, T, V, H, True, False)))
+
+
+@pytest.mark.parametrize("kind", ["nf4", "fp8"])
+@pytest.mark.parametrize("T,V,H", [(256, 32768, 64), (160, 33024, 64), (192, 33024, 64), (250, 33024, 64), (250, 8256, 4160),
+                                   (160, 4160, 16384), (190, 4160, 16384), (250, 4160, 16384)])
+def test_quantized_heads_of_each_tile(kind, T, V, H):
+    """Sizes that take each height of a tile of the logits (many vocabulary rows) and
+    of dX (long rows), up to 512 rows in the weight's own format."""
+    q = require_gpu()
+    banner(f"head tiles {kind} {T}x{V}x{H}")
+    W, Wv = _head(q, kind, V + H, V, H, 4 / np.sqrt(H))
+    X, y = dev_bf16(_bf16(V + 2, (T, H))), _labels(T, T, V)
+    g = np.abs(synth.normal_f32(T + 1, (T,), 1.0))
+    rows = np.unique(np.concatenate([np.arange(0, 8), np.arange(0, T, 9), np.arange(T - 3, T)]))
+    out = q.qlora_head_loss_grad(W, X, _dev(y), dev_f32(g), ws=_poisoned(q, T, V, H, True, True))
+    _compare(X, Wv, y, g, *out, rows=rows)
+    _compare(X, Wv, y, g, *q.qlora_head_loss(W, X, _dev(y), ws=_poisoned(q, T, V, H, True, False)), rows=rows)
 
 
 def test_vocabulary_in_pieces_16_bit():
@@ -157,26 +175,45 @@ def test_vocabulary_in_pieces_16_bit():
 
 @pytest.mark.parametrize("kind", ["nf4", "nodq", "fp8"])
 def test_vocabulary_in_pieces_quantized(kind):
-    """Rows of 16384 columns: pieces of at most 2^27 weights, two of 4352 and 3904 rows
-    of the head; 128-row blocks and 16384-weight groups begin anew in each piece."""
+    """Rows of 16384 columns: 520 of them make pieces of at most 2^27 weights, two of 4352
+    and 3904 rows of the head; 128-row blocks and 16384-weight groups begin anew in each
+    piece.  Three rows take the weight as it is, in one piece."""
     q = require_gpu()
-    T, V, H = 3, 8256, 16384
-    banner(f"head pieces {kind} {T}x{V}x{H}")
+    V, H = 8256, 16384
     W, Wv = _head(q, kind, 9, V, H, 0.03)
-    X, y = dev_bf16(_bf16(10, (T, H))), np.array([4351, 4352, 8255])
-    g = np.array([1.0, -2.0, 0.5], dtype=np.float32)
-    _compare(X, Wv, y, g, *q.qlora_head_loss_grad(W, X, _dev(y), dev_f32(g), ws=_poisoned(q, T, V, H, True, True)))
-    _compare(X, Wv, y, g, *q.qlora_head_loss(W, X, _dev(y)))
+    for T in (3, 520):
+        banner(f"head pieces {kind} {T}x{V}x{H}")
+        X, y = dev_bf16(_bf16(10, (T, H))), np.resize(np.array([4351, 4352, 8255]), T)
+        g = np.resize(np.array([1.0, -2.0, 0.5], dtype=np.float32), T)
+        rows = np.unique(np.concatenate([np.arange(3), np.arange(T - 3, T)]))
+        _compare(X, Wv, y, g, *q.qlora_head_loss_grad(W, X, _dev(y), dev_f32(g), ws=_poisoned(q, T, V, H, True, True)), rows=rows)
+        _compare(X, Wv, y, g, *q.qlora_head_loss(W, X, _dev(y)), rows=rows)
 
 
+@pytest.mark.parametrize("kind", ["nf4", "nodq", "fp8"])
+def test_long_vocabulary_in_its_own_format(kind):
+    """512 rows and 262464 columns are two pieces with a gradient, both read as codes."""
+    q = require_gpu()
+    T, V, H = 512, 262144 + 320, 64
+    banner(f"head codes in pieces {kind}")
+    W, Wv = _head(q, kind, 51, V, H, 0.5)
+    X, y = dev_bf16(_bf16(52, (T, H))), _labels(53, T, V)
+    y[10:16] = 131071, 131072, 131327, 131328, 262143, V - 1
+    g = np.abs(synth.normal_f32(54, (T,), 1.0))
+    rows = np.concatenate([np.arange(0, 20), np.arange(T - 4, T)])
+    _compare(X, Wv, y, g, *q.qlora_head_loss_grad(W, X, _dev(y), dev_f32(g), ws=_poisoned(q, T, V, H, True, True)), rows=rows)
+    _compare(X, Wv, y, g, *q.qlora_head_loss(W, X, _dev(y), ws=_poisoned(q, T, V, H, True, False)), rows=rows)
+
+
+@pytest.mark.parametrize("T", [96, 48])
 @pytest.mark.parametrize("size", [30.0, 100.0, 400.0, 3000.0, 1e6, 1e30])
-def test_logits_of_any_size(size):
+def test_logits_of_any_size(size, T):
     """Rows whose logits spread over +-size: their tiles, pieces and label lie in
     different powers of 2^128.  The first column tile holds the smaller logits for
     half of the rows and the larger for the others."""
     q = require_gpu()
     banner(f"head logits of {size}")
-    T, V, H = 96, 1300, 64
+    V, H = 1300, 64
     W, _ = _head(q, "bf16", 11, V, H, 0.5)
     W[:256] *= 0.125
     W[1290:] *= 2
