@@ -1628,7 +1628,7 @@ int qlora_adamw_plan(const qlora_adamw_tensor* tensors, int64_t n, void* table, 
 int qlora_adamw_step(const qlora_adamw_table* table, int bits, void* m, void* v, uint8_t* m_scales, uint8_t* v_scales,
                      const float* grad_scale, const qlora_adamw_rates* rates, qlora_stream stream) {
   if (!table || !rates) return QLORA_ERR_NULL;
-  if (table->chunks < 0 || table->chunks >= (int64_t(1) << 31)) return QLORA_ERR_SHAPE;
+  if (table->chunks < 0 || table->chunks >= (int64_t(1) << 31) || table->state_len < 0) return QLORA_ERR_SHAPE;
   if (bits != 32 && bits != 8) return QLORA_ERR_VALUE;
   if (rates->step < 1 || !std::isfinite(rates->lr) || !std::isfinite(rates->weight_decay) ||
       !(rates->eps >= 0.) || !std::isfinite(rates->eps) || !(rates->beta1 >= 0. && rates->beta1 < 1.) ||
@@ -1639,7 +1639,10 @@ int qlora_adamw_step(const qlora_adamw_table* table, int bits, void* m, void* v,
   if (!aligned16(table->table) || !aligned16(m) || !aligned16(v) ||
       (bits == 8 && (!aligned16(m_scales) || !aligned16(v_scales))) || !aligned1(grad_scale))
     return QLORA_ERR_ALIGN;
-  if (m == v || (bits == 8 && m_scales == v_scales)) return QLORA_ERR_VALUE;
+  const int64_t width = bits == 8 ? 1 : 4, scales = table->state_len / kAdamBlock;
+  AdamRange states[4] = {adamw_range(m, width * table->state_len), adamw_range(v, width * table->state_len),
+                         adamw_range(m_scales, scales), adamw_range(v_scales, scales)};
+  if (overlap(states, bits == 8 ? 4 : 2)) return QLORA_ERR_VALUE;
   if (int st = check_device()) return st;
   const double t = static_cast<double>(rates->step);
   AdamStep a{};

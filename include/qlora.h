@@ -16,13 +16,13 @@
  *
  * Conventions shared by every call:
  *   - All tensor pointers are DEVICE pointers to contiguous row-major data on
- *     the current HIP device, 16-byte aligned.  The caller owns every buffer,
+ *     the current HIP device, 16-byte aligned where a call does not say less.  The caller owns every buffer,
  *     including the workspace; the library allocates no device memory and
  *     keeps no pointer after returning.  Its only global state is a
  *     per-device cache of the architecture check (thread-safe).
  *   - `stream` is a hipStream_t (NULL = the null stream).  Each call checks
  *     its arguments on the host, enqueues its kernels on `stream` and
- *     returns; nothing is synchronised.  Device faults surface at the
+ *     returns; nothing is synchronised (but qlora_adamw_plan waits).  Device faults surface at the
  *     caller's next synchronisation.
  *   - Return value: QLORA_OK (0) or a negative qlora_status.  A call that
  *     fails validation enqueues nothing and leaves every output untouched.
@@ -762,7 +762,8 @@ int qlora_adamw_plan(const qlora_adamw_tensor* tensors, int64_t n, void* table, 
  * The numbers in rates are taken by value: a captured step repeats its t and seed.
  * Two steps of one plan must not overlap in time.  An element's result depends
  * on nothing but its own values and, in 8 bits, its block's.
- * Errors: NULL, SHAPE, ALIGN, VALUE (bits, rates, m that is v), DEVICE, LAUNCH.
+ * Errors: NULL, SHAPE, ALIGN, VALUE (bits, rates, states that share
+ * memory), DEVICE, LAUNCH.
  */
 int qlora_adamw_step(const qlora_adamw_table* table, int bits, void* m, void* v, uint8_t* m_scales, uint8_t* v_scales,
                      const float* grad_scale, const qlora_adamw_rates* rates, qlora_stream stream);

@@ -303,7 +303,10 @@ def test_adamw_refusals(lib):
                                 {"eps": inf}, {"weight_decay": nan}, {"step": 0}, {"step": -3})] == [VALUE] * 11
     assert [step(**{k: None}) for k in ("m", "v", "ms", "vs")] == [NULL] * 4
     assert [step(**{k: ODD}) for k in ("m", "v", "ms", "vs")] == [ALIGN] * 4 and step(gs=F + 2) == ALIGN
-    # the two states in one place
-    assert step(bits=32) == VALUE and step(v=F + 8192) == VALUE and step(ms=F + 8192) == VALUE
+    # states that share memory: 6144 elements and 48 scales each
+    apart = dict(m=F, v=F + 6144, ms=F + 12288, vs=F + 12336)
+    assert step(bits=32) == VALUE and step(bits=32, v=F + 6144) == VALUE
+    assert [step(**{**apart, **k}) for k in ({"v": F + 6128}, {"m": F + 16}, {"ms": F + 12272}, {"vs": F + 12320}, {"vs": F + 12288})] == [VALUE] * 5
+    assert step(table=Table(F, 3, -1)) == SHAPE
     assert step(table=Table(F, -1, 0)) == SHAPE and step(table=Table(F, 1 << 31, 0)) == SHAPE
     assert step(table=Table(F, 0, 0), m=None) == 0
