@@ -329,8 +329,8 @@ int64_t norm_bwd_parts(int64_t T, int64_t H);
 hipError_t launch_norm_bwd(const NormBwd& a, float* dw, hipStream_t s);
 
 // Cross entropy through a frozen output head W [V][H] (k_head.hip), a piece of
-// the vocabulary at a time: columns [v0, v0 + n) of the logits X W^T with the
-// piece's rows in bf16.  Per row the sum over the vocabulary but the label's
+// the vocabulary at a time: columns [v0, v0 + n) of the logits X W^T, with the
+// piece's rows in bf16 or as codes.  Per row the sum over the vocabulary but the label's
 // column is held as run_s 2^(kHeadCell run_c); a row's label is outside [0, V)
 // where it has none.
 constexpr int kHeadTile = 256;   // a piece's columns are a multiple of it (the last piece's may not be)

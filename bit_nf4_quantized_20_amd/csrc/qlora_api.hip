@@ -1598,8 +1598,12 @@ int qlora_adamw_plan(const qlora_adamw_tensor* tensors, int64_t n, void* table, 
   // Written by the time the call returns: a step on another stream, or one in front of
   // the replay of a graph that holds the plan, would follow addresses that are not there.
   hipStream_t s = static_cast<hipStream_t>(stream);
+  const auto failed = []() {
+    (void)hipGetLastError();  // not for the next call to find
+    return QLORA_ERR_LAUNCH;
+  };
   hipStreamCaptureStatus capture = hipStreamCaptureStatusNone;
-  if (hipStreamIsCapturing(s, &capture) != hipSuccess || capture != hipStreamCaptureStatusNone) return QLORA_ERR_LAUNCH;
+  if (hipStreamIsCapturing(s, &capture) != hipSuccess || capture != hipStreamCaptureStatusNone) return failed();
   std::unique_ptr<AdamChunk[]> list(new (std::nothrow) AdamChunk[chunks > 0 ? chunks : 1]);
   if (!list) return QLORA_ERR_LAUNCH;
   AdamChunk* at = list.get();
@@ -1620,7 +1624,7 @@ int qlora_adamw_plan(const qlora_adamw_tensor* tensors, int64_t n, void* table, 
   if (chunks > 0 && (hipMemcpyAsync(table, list.get(), static_cast<size_t>(chunks) * sizeof(AdamChunk),
                                     hipMemcpyHostToDevice, s) != hipSuccess ||
                      hipStreamSynchronize(s) != hipSuccess))
-    return QLORA_ERR_LAUNCH;
+    return failed();
   *out = qlora_adamw_table{table, chunks, state};
   return QLORA_OK;
 }
