@@ -271,15 +271,21 @@ __device__ __forceinline__ bf16x8 col_frag(const uint16_t* lds, int n0, int j) {
   return __builtin_bit_cast(bf16x8, __builtin_shufflevector(v[0], v[1], 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
-// Stages of activations: three beside codes, where LDS holds them (the wait for a stage is
-// also one for the codes asked for before it, and those come from HBM).
-constexpr int act_stages(int BM, int BN, bool codes) { return codes && BM <= (BN == 128 ? 64 : 160) ? 3 : 2; }
+// LDS stages.  Of activations three beside codes, where LDS holds them (the wait for a
+// stage is also one for the codes asked for before it, and those come from HBM).  Tiles of
+// 128 columns of a bf16 weight, one a CU, wait for HBM: four of both (64 x 32000 x 4096 70
+// us instead of 75, 1 x 16000 x 2048 18.8 and 21.6; five 70 and 19.5, six 71.5 and 20.4).
+constexpr int kDeep = 4;
+constexpr int act_stages(int BM, int BN, bool codes) {
+  return codes ? BM <= (BN == 128 ? 64 : 160) ? 3 : 2 : BN == 128 ? kDeep : 2;
+}
+constexpr int weight_stages(int BN, bool codes) { return !codes && BN == 128 ? kDeep : 3; }
 
 // acc[a][c] += weight fragments times activation fragments over a tile's K-steps [k0,
 // k0 + steps) of 64; acc[a][c][i] holds row m = wm BM/2 + 16 c + lane % 16 of the
 // tile and column n = wn BN/2 + 16 a + 4 (lane / 16) + i.
 //
-// NA LDS stages of activations and three of weights, each an array of its own and
+// NA LDS stages of activations and NW of weights, each an array of its own and
 // its index a compile-time constant, so that the compiler sees that the copies into one
 // stage do not alias the fragment reads of another.  A step is two sub-steps of FN
 // groups of matrix instructions, one group per weight fragment.  Fragments are read
@@ -287,25 +293,25 @@ constexpr int act_stages(int BM, int BN, bool codes) { return codes && BM <= (BN
 // up, the activations' under the middle of the sub-step before.  After group 1 of the
 // second sub-step all of the step's fragments have been read and a barrier frees its
 // stages; it also waits for what the next step reads.  The copies of NA steps on
-// (activations) go out behind it and have at least a sub-step to land, those of three
-// steps on (weights) under the next sub-step and have three.  Codes are asked for NA
+// (activations) go out behind it and have at least a sub-step to land, those of NW
+// steps on (weights) under the next sub-step and have at least three.  Codes are asked for NA
 // steps before they go to LDS, two steps before their products.
 //
 // A workgroup takes one tile after another without a break in this: the steps count on
-// into the next tile (steps is rounded up to the six, with NA = 3 to the three but at
+// into the next tile (steps is rounded up to the six, with NA > 2 to a multiple of NA of at
 // least six, after which the rings are back where they began, with copies of zeros), so
 // that its first copies and fragments are under way during the last steps and the
 // epilogue.
 template <int BM, int BN, class TW>
 struct HeadLoop {
-  static constexpr int NA = act_stages(BM, BN, TW::kQuant);
+  static constexpr int NA = act_stages(BM, BN, TW::kQuant), NW = weight_stages(BN, TW::kQuant);
   // codes become bf16 between the products (of 64 rows: in front of them, there are too few)
   static constexpr bool kSpread = BM > 64;
   static constexpr int FN = BN / 32, FM = BM / 32, kHalf = FN / 2;
   static_assert(FN == 8 || FN == 4, "the order of the reads below");
   static constexpr bool kTr = TW::kTr, kQuant = TW::kQuant;
   typedef f32x4 Acc[FN][FM];
-  uint16_t *s_act[NA], *s_wt[3];
+  uint16_t *s_act[NA], *s_wt[NW];
   int wv;
   RowTile<BM> ta;
   TW tw;
@@ -315,15 +321,11 @@ struct HeadLoop {
   typename TW::Set set[NA];
   bf16x8 fw[FN], fa[2][FM];
 
-  __device__ __forceinline__ void stages(uint16_t* a0, uint16_t* a1, uint16_t* a2, uint16_t* w0, uint16_t* w1, uint16_t* w2,
-                                         int wave) {
-    s_act[0] = a0;
-    s_act[1] = a1;
-    if constexpr (NA == 3) s_act[2] = a2;
-    s_wt[0] = w0;
-    s_wt[1] = w1;
-    s_wt[2] = w2;
-    wv = wave;
+  __device__ __forceinline__ void stages(uint16_t* const (&a)[kDeep], uint16_t* const (&w)[kDeep]) {
+#pragma unroll
+    for (int i = 0; i < NA; ++i) s_act[i] = a[i];
+#pragma unroll
+    for (int i = 0; i < NW; ++i) s_wt[i] = w[i];
   }
   __device__ __forceinline__ bf16x8 act(int b, int j, int i) const {
     return row_frag(s_act[b], (wv & 1) * (BM / 2) + i * 16, j);
@@ -358,7 +360,7 @@ struct HeadLoop {
   }
   static constexpr int wait_code(int copies) { return (copies & 15) | ((copies >> 4) << 14) | 0x70; }  // lgkmcnt(0) too
 
-  __device__ __forceinline__ static int padded(int n) { return NA == 2 ? (n + 5) / 6 * 6 : n < 6 ? 6 : (n + 2) / 3 * 3; }
+  __device__ __forceinline__ static int padded(int n) { return NA == 2 ? (n + 5) / 6 * 6 : (n < 6 ? 6 + NA - 1 : n + NA - 1) / NA * NA; }
   static constexpr int kA = RowTile<BM>::kPerWave, kW = TW::kPerWave;  // copies of a wave and step
   // step e counted from this tile's first
   template <class S>
@@ -413,6 +415,13 @@ struct HeadLoop {
       for (int b = 0; b < NA; ++b) codes(2 + b, b);
       if constexpr (NA == 3) copy_a(2, 2, 0, kA);
       __builtin_amdgcn_s_waitcnt(wait_code(0));
+    } else if constexpr (NA == kDeep) {
+#pragma unroll
+      for (int e = 0; e < kDeep; ++e) {
+        if (e > 0) copy_a(e, e, 0, kA);
+        if (e < kDeep - 1) copy_w(e, e, 0, kW);
+      }
+      __builtin_amdgcn_s_waitcnt(wait_code((kDeep - 2) * (kA + kW) + kA));
     } else {
       copy_w(0, 0, 0, kW);
       copy_w(1, 1, 0, kW);
@@ -429,7 +438,7 @@ struct HeadLoop {
     settle(acc);
     // step e; A, W: its stages
     auto step = [&](int e, auto ac, auto wc) {
-      constexpr int A = decltype(ac)::value, W = decltype(wc)::value, A1 = (A + 1) % NA, W1 = (W + 1) % 3;
+      constexpr int A = decltype(ac)::value, W = decltype(wc)::value, A1 = (A + 1) % NA, W1 = (W + 1) % NW, WL = (W + NW - 1) % NW;
       constexpr int kPer = (FM + kHalf - 1) / kHalf, kWG = (kW + FN - 1) / FN, kAG = (kA + kHalf - 1) / kHalf;
 #pragma unroll
       for (int g = 0; g < FN; ++g) {
@@ -438,13 +447,13 @@ struct HeadLoop {
         if (g >= 2 && g < 2 + kHalf)
 #pragma unroll
           for (int i = (g - 2) * kPer; i < (g - 1) * kPer && i < FM; ++i) fa[1][i] = act(A, 1, i);
-        copy_w(e + 2, (W + 2) % 3, g * kWG, kWG);
+        copy_w(e + NW - 1, WL, g * kWG, kWG);
         if constexpr (kQuant && !kSpread) {
 #pragma unroll
-          for (int u = 0; u < TW::kParts; ++u) tw.write(s_wt[(W + 2) % 3], set[A], g, u);
+          for (int u = 0; u < TW::kParts; ++u) tw.write(s_wt[WL], set[A], g, u);
           if (g == FN - 1) codes(e + 2 + NA, A);
         }
-        products(acc, g, 0, s_wt[(W + 2) % 3], A);
+        products(acc, g, 0, s_wt[WL], A);
       }
 #pragma unroll
       for (int g = 0; g < FN; ++g) {
@@ -453,7 +462,7 @@ struct HeadLoop {
           fw[FN - 1] = wt(W, 1, FN - 1);
         }
         if (g == 2) {
-          __builtin_amdgcn_s_waitcnt(wait_code(NA == 2 ? kW : 2 * kW + kA));
+          __builtin_amdgcn_s_waitcnt(wait_code(NA == 2 ? kW : NA == NW && !kQuant ? (NA - 2) * (kA + kW) : 2 * kW + kA));
           barrier();
         }
         if (g >= 2) fw[g - 2] = wt(W1, 0, g - 2);
@@ -461,7 +470,7 @@ struct HeadLoop {
 #pragma unroll
           for (int i = (g - 2) * kPer; i < (g - 1) * kPer && i < FM; ++i) fa[0][i] = act(A1, 0, i);
         if (g >= kHalf) copy_a(e + NA, A, (g - kHalf) * kAG, kAG);
-        products(acc, g, 1, s_wt[(W + 2) % 3], A);
+        products(acc, g, 1, s_wt[WL], A);
       }
       if constexpr (kQuant && kSpread) codes(e + 2 + NA, A);
     };
@@ -478,10 +487,11 @@ struct HeadLoop {
         step(e + 5, I1{}, I2{});
       }
     } else {
-      for (int e = 0, n = padded(steps); e < n; e += 3) {
+      for (int e = 0, n = padded(steps); e < n; e += NA) {
         step(e, I0{}, I0{});
         step(e + 1, I1{}, I1{});
         step(e + 2, I2{}, I2{});
+        if constexpr (NA > 3) step(e + 3, std::integral_constant<int, 3 % NA>{}, std::integral_constant<int, 3 % NW>{});
       }
     }
     settle(acc);
@@ -656,13 +666,18 @@ __device__ __forceinline__ auto weight_source(const HeadPiece& p, int64_t n0) {
   }
 }
 
+// A tile's stages, each an array of its own (those that are not used take no space)
+#define HEAD_STAGES(NA, NW)                                                                                          \
+  __shared__ __attribute__((aligned(1024))) uint16_t s_a0[BM * kBK], s_a1[BM * kBK], s_a2[NA > 2 ? BM * kBK : 1], s_a3[NA > 3 ? BM * kBK : 1]; \
+  __shared__ __attribute__((aligned(1024))) uint16_t s_w0[BN * kBK], s_w1[BN * kBK], s_w2[BN * kBK], s_w3[NW > 3 ? BN * kBK : 1]; \
+  uint16_t* const s_a[kDeep] = {s_a0, s_a1, s_a2, s_a3};                                                              \
+  uint16_t* const s_w[kDeep] = {s_w0, s_w1, s_w2, s_w3};
+
 // kE: with E (the gradient's call); else the sums alone.
 template <int BM, int BN, bool kE, int F>
-__global__ __launch_bounds__(256, BN == 128 ? 2 : 1) void k_head_logits(HeadPiece p) {
+__global__ __launch_bounds__(256, BN == 128 && F != kBf16 ? 2 : 1) void k_head_logits(HeadPiece p) {
   constexpr int FN = BN / 32, FM = BM / 32, WM = BM / 2;
-  constexpr bool kThird = act_stages(BM, BN, F != kBf16) == 3;
-  __shared__ __attribute__((aligned(1024))) uint16_t s_a0[BM * kBK], s_a1[BM * kBK], s_a2[kThird ? BM * kBK : 1];
-  __shared__ __attribute__((aligned(1024))) uint16_t s_w0[BN * kBK], s_w1[BN * kBK], s_w2[BN * kBK];
+  HEAD_STAGES(act_stages(BM, BN, F != kBf16), weight_stages(BN, F != kBf16))
 
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wv & 1, wn = wv >> 1;
@@ -676,7 +691,8 @@ __global__ __launch_bounds__(256, BN == 128 ? 2 : 1) void k_head_logits(HeadPiec
 
   using TW = std::conditional_t<F == kBf16, RowTile<BN>, CodeTile<BN, F, false>>;
   HeadLoop<BM, BN, TW> loop;
-  loop.stages(s_a0, s_a1, s_a2, s_w0, s_w1, s_w2, wv);
+  loop.stages(s_a, s_w);
+  loop.wv = wv;
   loop.ta.init(p.H, wv, lane);
   if constexpr (F == kBf16) loop.tw.init(p.H, wv, lane);
   else loop.tw.init(p.H, wv, lane, 0, p.q.absmax_q != nullptr);
@@ -814,9 +830,7 @@ __global__ __launch_bounds__(64 * kRowWaves) void k_head_rows(HeadPiece p, HeadF
 template <int BM, int BN, int F>
 __global__ __launch_bounds__(256, BN == 128 ? 2 : 1) void k_head_grad(HeadPiece p, float* part, int ks) {
   constexpr int FN = BN / 32, FM = BM / 32, WM = BM / 2;
-  constexpr bool kThird = act_stages(BM, BN, F != kBf16) == 3;
-  __shared__ __attribute__((aligned(1024))) uint16_t s_a0[BM * kBK], s_a1[BM * kBK], s_a2[kThird ? BM * kBK : 1];
-  __shared__ __attribute__((aligned(1024))) uint16_t s_w0[BN * kBK], s_w1[BN * kBK], s_w2[BN * kBK];
+  HEAD_STAGES(act_stages(BM, BN, F != kBf16), weight_stages(BN, F != kBf16))
 
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wv & 1, wn = wv >> 1, r16 = lane & 15, quarter = lane >> 4;
@@ -831,7 +845,8 @@ __global__ __launch_bounds__(256, BN == 128 ? 2 : 1) void k_head_grad(HeadPiece 
   if (steps > 0) {
     using TW = std::conditional_t<F == kBf16, ColTile<BN>, CodeTile<BN, F, true>>;
     HeadLoop<BM, BN, TW> loop;
-    loop.stages(s_a0, s_a1, s_a2, s_w0, s_w1, s_w2, wv);
+    loop.stages(s_a, s_w);
+    loop.wv = wv;
     loop.ta.init(p.lde, wv, lane);
     if constexpr (F == kBf16) loop.tw.init(p.H, wv, lane);
     else loop.tw.init(p.H, wv, lane, n0, p.q.absmax_q != nullptr);
@@ -982,7 +997,7 @@ constexpr bool height_fits(int rows, bool codes) { return !codes || (rows != 64 
 // weight 32000 x 4096: 82 us with 256 columns, 64 with 128, gradient 143 and 125).  A bf16
 // weight's tiles wait for HBM instead; there the logits of up to 64 rows take them where
 // tiles of 256 columns would fill no more than half of the CUs (16 x 32000 x 4096: 69
-// us, 77 with 256 columns; 16 x 128000 x 4096: 223 and 213).
+// us, 77 with 256 columns; 16 x 128000 x 4096: 223 and 213), with a CU to themselves.
 bool half_tiles(int64_t T, int64_t n, bool codes) {
   return codes ? T <= 128 : T <= 64 && ceil_div(n, int64_t(256)) <= kHeadCus / 2;
 }
@@ -1059,7 +1074,7 @@ int head_cols(int64_t T, int64_t n, bool codes) { return logits_shape(T, n, code
 
 hipError_t launch_head_logits(const HeadPiece& p, hipStream_t s) {
   const TileShape t = logits_shape(p.T, p.n, p.q.codes != nullptr);
-  const dim3 grid(static_cast<uint32_t>(t.cols == 128 ? 2 * kHeadCus : kHeadCus));  // a multiple of the XCDs' number
+  const dim3 grid(static_cast<uint32_t>(t.cols == 128 && p.q.codes != nullptr ? 2 * kHeadCus : kHeadCus));  // a multiple of the XCDs' number
   with_kernel(t, p.q, [&](auto bm, auto bn, auto fmt) {
     constexpr int BM = decltype(bm)::value, BN = decltype(bn)::value, F = decltype(fmt)::value;
     if (p.E != nullptr) hipLaunchKernelGGL((k_head_logits<BM, BN, true, F>), grid, dim3(256), 0, s, p);
