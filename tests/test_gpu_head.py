@@ -126,7 +126,7 @@ def test_loss_and_gradient(T, V, H):
 
 
 @pytest.mark.parametrize("kind", ["nf4", "nodq", "fp8"])
-@pytest.mark.parametrize("T,V,H", [(1, 64, 64), (5, 320, 128), (64, 1088, 192), (70, 1088, 192), (128, 704, 1088),
+@pytest.mark.parametrize("T,V,H", [(1, 64, 64), (5, 320, 128), (32, 704, 320), (33, 704, 320), (64, 1088, 192), (70, 1088, 192), (128, 704, 1088),
                                    (300, 704, 320), (512, 2112, 320), (513, 2112, 320)])
 def test_quantized_heads(kind, T, V, H):
     q = require_gpu()
