@@ -27,7 +27,7 @@
 // weights come through registers instead and are turned into bf16 on their way into
 // LDS (up to kHeadCodesTokens rows; the caller writes them out in bf16 for more).
 //
-// Measured: loss of 1 x 32000 x 4096 62 us (262 MB, 4.2 TB/s), of 64 rows in NF4 58;
+// Measured: loss of 1 x 32000 x 4096 58 to 62 us (262 MB, 4.2 to 4.5 TB/s), of 64 rows in NF4 59;
 // gradient of 301 x 50021 x 2304 204 us, of 4096 x 128000 x 4096 6.3 ms, 1360 TFLOP/s.  A
 // 256 x 256 tile takes 1.4 us a step of 64, 1.5 PFLOP/s, where the matrix cores on random
 // operands are bound by power, and 10 us in front of and behind its steps; with few rows HBM
