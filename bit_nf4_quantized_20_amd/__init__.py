@@ -1134,13 +1134,14 @@ class AdamWState:
 class AdamWPlan:
     """Tensors bound to an optimizer's step.  It keeps them (their memory is
     read and written at every step; a tensor whose storage is replaced needs a new
-    plan)."""
+    plan).  A graph that holds its steps needs it for as long as it is replayed."""
     state: AdamWState
     bits: int
     offsets: list     # each tensor's first element in the states
     tensors: list     # what the table points to
     table: torch.Tensor
     _c: _AdamWTableC
+    _stream: int = 0  # the table was allocated on
 
 
 def _numels(numel):
@@ -1214,7 +1215,8 @@ def qlora_adamw_plan(params, masters, grads, state: AdamWState) -> AdamWPlan:
     # aliases of the tensors: what they point to stays allocated
     kept = [t.detach() for ts in (params, masters, grads) for t in ts if t is not None]
     return AdamWPlan(AdamWState(*[t.detach() if t is not None else None for t in
-                                  (state.m, state.v, state.m_scales, state.v_scales)]), bits, offsets, kept, table, out)
+                                  (state.m, state.v, state.m_scales, state.v_scales)]), bits, offsets, kept, table, out,
+                     _raw_stream(dev.index))
 
 
 def qlora_adamw_step(plan: AdamWPlan, step: int, lr: float, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
@@ -1227,6 +1229,9 @@ def qlora_adamw_step(plan: AdamWPlan, step: int, lr: float, beta1: float = 0.9, 
     if grad_scale is not None:
         _arg(grad_scale, torch.float32, 1, "grad_scale", dev)
     small = plan.bits == 8
+    # a table that went back to the allocator under a step would lead it anywhere
+    if _raw_stream(dev.index) != plan._stream and not _capturing(dev):
+        plan.table.record_stream(torch.cuda.current_stream(dev))
     rates = _AdamWRatesC(lr, beta1, beta2, eps, weight_decay, step, (step if seed is None else seed) & 0xffffffff)
     _on(dev, _lib.qlora_adamw_step, "qlora_adamw_step", ctypes.byref(plan._c), plan.bits, st.m.data_ptr(), st.v.data_ptr(),
         st.m_scales.data_ptr() if small else None, st.v_scales.data_ptr() if small else None,

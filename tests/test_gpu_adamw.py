@@ -313,6 +313,25 @@ def test_plan_keeps_its_tensors():
     assert all(bool((t == 9).all()) for t in other) and bool(((alias + 0.5).abs() < 1e-4).all())
 
 
+def test_table_outlives_a_step_on_another_stream():
+    q = require_gpu()
+    banner("adamw table on another stream")
+    state = q.qlora_adamw_state([3 << 20], 32, "cuda")
+    p, g = torch.zeros(3 << 20, device="cuda"), torch.ones(3 << 20, device="cuda")
+    plan = q.qlora_adamw_plan(None, [p], [g], state)
+    at, size = plan.table.data_ptr(), plan.table.numel()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100_000_000)
+        q.qlora_adamw_step(plan, 1, lr=0.5)
+    del plan
+    others = [torch.empty(size, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    assert not side.query() and all(t.data_ptr() != at for t in others)
+    torch.cuda.synchronize()
+    assert bool(((p + 0.5).abs() < 1e-4).all())
+
+
 def test_refusals():
     q = require_gpu()
     banner("adamw refusals")
