@@ -342,7 +342,7 @@ def test_gradient_is_the_difference_of_the_loss():
         assert bool(((diff - dX[:, j].float()).abs() <= 2.0 ** -8 * dX[:, j].float().abs() + 5e-4).all())
 
 
-@pytest.mark.parametrize("kind,T", [("bf16", 40), ("bf16", 300), ("fp8", 300)])
+@pytest.mark.parametrize("kind,T", [("bf16", 40), ("bf16", 300), ("fp8", 300), ("nf4", 20), ("fp8", 100), ("nf4", 600)])
 def test_streams_and_graphs(kind, T):
     q = require_gpu()
     banner(f"head streams and graphs {kind} T={T}")
