@@ -310,6 +310,7 @@ struct NormFwd {
   int64_t T, pitch;
   uint32_t H, Kp;
   float eps;
+  double inv_h;  // 1 / H
   uint16_t *h, *y;
   uint8_t *codes, *scales;
   float* rstd;

@@ -22,8 +22,8 @@ namespace {
 // sum over the L lanes that share a row (L = 16, 64: within a wave; above: the
 // workgroup's waves through LDS, two buffers by the parity of the row so that
 // one barrier a row is enough)
-template <int L>
-__device__ __forceinline__ float row_sum(float v, float (*red)[8], int parity) {
+template <int L, class T>
+__device__ __forceinline__ T row_sum(T v, T (*red)[8], int parity) {
   constexpr int kIn = L < 64 ? L : 64;
 #pragma unroll
   for (int o = kIn / 2; o >= 1; o >>= 1) v += __shfl_xor(v, o);
@@ -70,7 +70,7 @@ constexpr int norm_threads(int L) { return L < 256 ? 256 : L; }
 template <int L, int C>
 __global__ __launch_bounds__(norm_threads(L)) void k_norm_fwd(NormFwd a) {
   constexpr int NT = norm_threads(L), kRows = NT / L;
-  __shared__ float red[2][8];
+  __shared__ double red[2][8];
   const int sub = threadIdx.x % L;
   float w[C][8];
 #pragma unroll
@@ -99,11 +99,15 @@ __global__ __launch_bounds__(norm_threads(L)) void k_norm_fwd(NormFwd a) {
         if (a.res != nullptr) u[c] = row_load(a.res + at + col);
       }
     }
-    float sum = 0.f;
+    // The square sum in 64 bits, which hold the squares of any bf16 values and a sum that is
+    // as good as exact: in fp32 a row of finite values from 2^57 on could sum to an infinity, its y
+    // to 0, and the sum's own error moved codes.  (8192 x 8192 104.5 us either way.)
+    double sum = 0.;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const uint32_t col = (c * L + sub) * 8;
       float f[8];
+      double part = 0.;
       if (a.res != nullptr) {
         float g[8];
         unpack8(v[c], f);
@@ -114,16 +118,19 @@ __global__ __launch_bounds__(norm_threads(L)) void k_norm_fwd(NormFwd a) {
       }
       unpack8(v[c], f);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) sum += f[e] * f[e];
+      for (int e = 0; e < 8; ++e) part = __builtin_fma(static_cast<double>(f[e]), static_cast<double>(f[e]), part);
+      sum += part;
     }
     sum = row_sum<L>(sum, red, parity);
     parity ^= 1;
-    // rstd as rh + rl, rl a Newton step's correction, and h rstd w without the products' own
-    // roundings: y is rounded to bf16 and on to a code, where a last bit decides over a whole
-    // step (2048 x 8192: 71 - 117 y off the rounded exact value instead of 117 - 161; 1% of the time)
-    const float x = sum / static_cast<float>(a.H) + a.eps, rh = 1.f / sqrtf(x), q = x * rh;
-    const float e = __builtin_fmaf(-q, rh, 1.f) - __builtin_fmaf(x, rh, -q) * rh;
-    const float rl = e == e ? 0.5f * rh * e : 0.f, rstd = rh + rl;
+    // rstd as rh + rl (v_rsq_f64 is within 2^-24, a Newton step squares that), and h rstd w without
+    // the products' own roundings: y is rounded to bf16 and on to a code, where a last bit decides
+    // over a whole step.
+    const double x = __builtin_fma(sum, a.inv_h, static_cast<double>(a.eps)), rough = __builtin_amdgcn_rsq(x);
+    const double e = __builtin_fma(-x * rough, rough, 1.);
+    const double r = e == e ? __builtin_fma(0.5 * rough, e, rough) : rough;
+    const float rstd = static_cast<float>(r), rh = rstd;
+    const float rl = rh < __builtin_inff() ? static_cast<float>(r - static_cast<double>(rh)) : 0.f;
     if (live && sub == 0 && a.rstd != nullptr) a.rstd[row] = rstd;
     uint32_t bytes = 0;  // L = 16: the row's only group of four blocks
 #pragma unroll

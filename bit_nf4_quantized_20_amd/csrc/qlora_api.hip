@@ -1501,6 +1501,7 @@ int qlora_rmsnorm_fwd(const qlora_bf16* x, const qlora_bf16* residual, const flo
   a.H = static_cast<uint32_t>(H);
   a.Kp = static_cast<uint32_t>(round_up(H, QLORA_FP8_BLOCK));
   a.eps = eps;
+  a.inv_h = 1. / static_cast<double>(H);
   a.h = h;
   a.y = y;
   a.codes = codes;

@@ -628,8 +628,10 @@ int qlora_moe_fwd(const qlora_nf4_weight* gate_up, const qlora_nf4_weight* down,
  *   x, residual [T, H] bf16;  weight [H] fp32;  eps >= 0
  *   H a multiple of 64, 64 .. 16384;  0 <= T < 2^31 (0 is a no-op)
  * h may be x or residual themselves; otherwise outputs are apart from inputs.  The
- * square sums are fp32: |h| below 2^60.  A row that holds an infinity or a NaN
- * has a y of NaN where the formula says so; the other rows do not change.
+ * square sums are held in 64 bits, so that any finite h is in range (an rstd past fp32's
+ * largest, of eps = 0 and a mean h^2 below 2^-256, is infinite and its y NaN).  A row that
+ * holds an infinity or a NaN has a y of NaN where the formula says so; the other
+ * rows do not change.
  * Errors: NULL, SHAPE, ALIGN, VALUE, DEVICE, LAUNCH.
  */
 int qlora_rmsnorm_fwd(const qlora_bf16* x, const qlora_bf16* residual, const float* weight, int64_t T, int64_t H,
