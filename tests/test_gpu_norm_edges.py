@@ -104,3 +104,39 @@ def test_gradient_of_large_and_small_rows(H):
     # (a dh below bf16's normal range: half of its smallest step, 2^-134)
     assert (np.abs(_wide(dh) - rdh) <= 2.0 ** -8 * np.abs(rdh) + 64 * u * mag + 2.0 ** -133).all()
     assert (np.abs(host(dw) - rdw) <= (T + 34) * u * magw + 1e-38).all()
+
+
+@pytest.mark.parametrize("H", [64, 576, 4096, 8256])
+def test_weights_that_are_not_finite(H):
+    """An infinite weight gives an infinite y of the product's sign, a NaN weight NaN, in its
+    column alone; 0 times infinity is NaN."""
+    q = require_gpu()
+    banner(f"norm infinite weight H={H}")
+    T, inf = 40, float("inf")
+    x = dev_bf16(_bits16(synth.normal_f32(8, (T, H), 1.0)))
+    x[3, 1] = 0
+    w = dev_f32(1 + 0.3 * synth.normal_f32(9, (H,), 1.0))
+    bad = w.clone()
+    bad[1], bad[H // 2], bad[H - 1] = inf, -inf, float("nan")
+    y, rows, _, rstd = q.qlora_rmsnorm_fwd(x, w, rows8=True)
+    yb, _, _, sb = q.qlora_rmsnorm_fwd(x, bad, rows8=True)
+    assert torch.equal(sb, rstd)
+    keep = torch.ones(H, dtype=torch.bool, device="cuda")
+    keep[[1, H // 2, H - 1]] = False
+    assert torch.equal(yb[:, keep], y[:, keep])
+    s = torch.sign(x.float())
+    assert bool(torch.isnan(yb[3, 1])) and bool(torch.isnan(yb[:, H - 1]).all())
+    rest = torch.arange(T, device="cuda") != 3
+    assert torch.equal(yb[rest, 1].float(), s[rest, 1] * inf) and torch.equal(yb[:, H // 2].float(), s[:, H // 2] * -inf)
+    # rows of +-1 without eps: rstd is 1, and no product has a remainder
+    ones = torch.where(x >= 0, 1.0, -1.0).to(torch.bfloat16)
+    y1, _, _, r1 = q.qlora_rmsnorm_fwd(ones, bad, eps=0.0)
+    assert bool((r1 == 1).all()) and torch.equal(y1[:, 1], ones[:, 1] * inf) and torch.equal(y1[:, H // 2], ones[:, H // 2] * -inf)
+    # the largest finite weights: y as the formula rounds it, an infinity past bf16's largest
+    big = torch.full_like(w, 2.0 ** 127)
+    yl = q.qlora_rmsnorm_fwd(x, big)[0]
+    ry, _ = onorm.fwd(_wide(x), host(big).astype(np.float64), float(np.float32(1e-6)))
+    inside = np.abs(ry) < 2.0 ** 127 * 1.98
+    assert (np.abs(_wide(yl)[inside] - ry[inside]) <= (2.0 ** -8 + 2.0 ** -22) * np.abs(ry[inside])).all()
+    past = np.abs(ry) > 2.0 ** 128
+    assert past.any() and np.array_equal(_wide(yl)[past], np.sign(ry[past]) * np.inf)
