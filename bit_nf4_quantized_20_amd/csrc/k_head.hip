@@ -749,8 +749,11 @@ __device__ __forceinline__ RowLoss row_loss(float c, float s, bool has, float t)
     const float d = t - (cell == -kInf ? 0.f : cell * kHeadCell);
     const float scale = c == cell ? 1.f : down_cells(1.f, c - cell), others = c == cell ? s : s * scale;
     total = others + __builtin_amdgcn_exp2f(d);
-    // 2^-d times the others, where that is in range
-    r.loss = d > -40.f ? log1pf(others * __builtin_amdgcn_exp2f(-d)) : (__builtin_amdgcn_logf(total) - d) * kLn2;
+    // The others over the label's own, wherever that quotient is finite: the difference of
+    // the logarithms is off by 2^-24 |d|, which is all of a small loss (label at -30, others at -60:
+    // -2.6e-6 or 0 instead of 3e-11).  It is not finite only where the loss is large.
+    const float ratio = others * __builtin_amdgcn_exp2f(-d);
+    r.loss = ratio < kInf ? log1pf(ratio) : (__builtin_amdgcn_logf(total) - d) * kLn2;
     const float inv = 1.f / total;
     r.rest = others * inv;
     r.factor = scale * inv;

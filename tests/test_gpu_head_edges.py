@@ -1,0 +1,48 @@
+"""The head loss on the GPU where a loss is small at any size of the logits, where
+weights are large, and through every tile height of a 16-bit head.  Oracle and
+bounds: tests/test_gpu_head.py."""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import head as ohead
+
+from gpu_util import banner, dev_bf16, dev_f32, host, require_gpu
+from test_gpu_head import _bf16, _compare, _dev, _head, _labels, _poisoned, _wide
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("V", [40, 300, 3500])
+def test_small_losses_at_any_logit(V):
+    """A row's logits are a, its label's a + b (whole numbers, exact in fp32), so that its
+    loss is log1p((V - 1) e^-b) whatever a is, down to 1e-15 and below.  In powers of two a
+    and a + b are off by 1.5 2^-24 of themselves (product and constant), both again by
+    2^-18 less their cell, exponentials and sums (at most V / 4 + 64 terms in a chain) by 2^-22 +
+    (V / 4 + 64) 2^-24: a relative error of loss and gradient."""
+    q = require_gpu()
+    banner(f"head small losses V={V}")
+    levels = np.array([-100, -88, -64, -60, -45, -44, -36, -31, -29, -27, -10, 0, 10, 28, 44, 45, 60, 64, 88, 100.0])
+    gaps = np.array([1, 2, 4, 7, 10, 14, 18, 20, 25, 30, 36.0])
+    a, b = (x.reshape(-1) for x in np.meshgrid(levels, gaps, indexing="ij"))
+    T, H, label = len(a), 64, 7
+    X, W = np.zeros((T, H)), np.zeros((V, H))
+    X[:, 0], X[:, 1] = a, b
+    W[:, 0] = 1
+    W[label, 1] = 1
+    X = torch.from_numpy(X).to(torch.bfloat16).cuda()
+    W = torch.from_numpy(W).to(torch.bfloat16).cuda()
+    y, g = np.full(T, label), np.ones(T, dtype=np.float32)
+    ref = np.log1p((V - 1) * np.exp(-b))
+    rel = np.log(2) * (1.5 * 2.0 ** -24 * 1.4427 * (np.abs(a) + np.abs(a + b)) + 2.0 ** -17) + 2.0 ** -22 + (V / 4 + 64) * 2.0 ** -24
+    loss, lse, dX = q.qlora_head_loss_grad(W, X, _dev(y), dev_f32(g))
+    for l, z in ((loss, lse), q.qlora_head_loss(W, X, _dev(y))):
+        err = np.abs(host(l) / ref - 1)
+        assert (err <= rel).all(), (a[err > rel], b[err > rel], host(l)[err > rel], ref[err > rel])
+        rz = a + np.log(V - 1 + np.exp(b))
+        assert (np.abs(host(z) - rz) <= 2.0 ** -20 * (1 + np.abs(rz))).all()
+    # column 1: - (1 - p) of the label, rounded to bf16
+    rest = -np.expm1(-ref)
+    d1 = _wide(dX)[:, 1]
+    assert (np.abs(-d1 / rest - 1) <= 2.0 ** -8 + 2 * rel).all()
