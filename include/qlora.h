@@ -688,6 +688,8 @@ typedef struct {
  * fp32 accumulation; the softmax's terms meet W in bf16, the label's own in fp32, so that
  * 1 - p of a row that is nearly sure keeps its digits.  A row with a logit of
  * +inf (finite ones: below 2^127) or NaN has a loss, lse and dX of NaN; a logit of -inf counts for nothing.
+ * With a gradient |W| below 2^39: a term, before it is divided by their sum, is at most
+ * 2^64 |W|, and up to 2^24 of them are added in fp32 (an infinite weight: NaN in its column of dX).
  * All outputs are bit-reproducible.
  * Errors: NULL (also: no format given), VALUE (two formats), SHAPE, ALIGN,
  * WORKSPACE, DEVICE, LAUNCH.

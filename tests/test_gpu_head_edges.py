@@ -46,3 +46,20 @@ def test_small_losses_at_any_logit(V):
     rest = -np.expm1(-ref)
     d1 = _wide(dX)[:, 1]
     assert (np.abs(-d1 / rest - 1) <= 2.0 ** -8 + 2 * rel).all()
+
+
+def test_large_weights_with_a_gradient():
+    """E, below 2^64 a term, times weights of up to 2^39: logits of 44 from rows
+    of about 2^-34 give finite gradients."""
+    q = require_gpu()
+    banner("head large weights")
+    T, V, H = 40, 1300, 64
+    W = torch.from_numpy(np.random.Generator(np.random.PCG64(3)).normal(0, 1, (V, H))).clamp(-3.9, 3.9).cuda()
+    W = (W * 2.0 ** 37).to(torch.bfloat16)
+    X = dev_bf16(_bf16(4, (T, H), 1.0)) * 2.0 ** -37 * 2
+    X[::2] *= 2.0 ** 0.5 * 1.6
+    Wv, y = _wide(W), _labels(5, T, V)
+    g = np.ones(T, dtype=np.float32)
+    loss, lse, dX = q.qlora_head_loss_grad(W, X, _dev(y), dev_f32(g), ws=_poisoned(q, T, V, H, False, True))
+    assert bool(torch.isfinite(dX).all()) and host(lse).max() > 44
+    _compare(X, Wv, y, g, loss, lse, dX, whole=False)
