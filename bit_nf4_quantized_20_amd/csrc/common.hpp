@@ -5,6 +5,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "sizes.hpp"
+
 namespace qlora {
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
@@ -32,9 +34,6 @@ __device__ __forceinline__ float max16(float v) {
   v = fmaxf(v, dpp_mov<kDppRowMirror>(v));
   return v;
 }
-
-__host__ __device__ constexpr int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-__host__ __device__ constexpr int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
 
 // ---------------------------------------------------------------------------
 // Launchers (host side).  Each returns hipSuccess or the launch error.
@@ -334,7 +333,6 @@ hipError_t launch_norm_bwd(const NormBwd& a, float* dw, hipStream_t s);
 // piece's rows in bf16 or as codes.  Per row the sum over the vocabulary but the label's
 // column is held as run_s 2^(kHeadCell run_c); a row's label is outside [0, V)
 // where it has none.
-constexpr int kHeadTile = 256;   // a piece's columns are a multiple of it (the last piece's may not be)
 constexpr float kHeadCell = 128.f;
 // W in its own format.
 struct HeadWeight {
@@ -361,10 +359,8 @@ struct HeadPiece {
   const float *c_in, *s_in;
   float *c_out, *s_out, *factor;
 };
-int head_cols(int64_t T, int64_t n, bool codes);
 hipError_t launch_head_logits(const HeadPiece& p, hipStream_t s);
 // part [splits][T][H] fp32 = factor part (not first) + E W
-int head_splits(int64_t T, int64_t H, int64_t n, bool codes);
 hipError_t launch_head_grad(const HeadPiece& p, float* part, int splits, hipStream_t s);
 // What is left: loss, lse (may be null) and, with dX, dX = dloss (sum of the
 // parts / total - (others / total) W_label).  W is the whole weight here.

@@ -13,6 +13,7 @@
 
 #include "../../include/qlora.h"
 #include "common.hpp"
+#include "head_shapes.hpp"
 #include "nf4_format.hpp"
 
 using namespace qlora;
