@@ -1254,12 +1254,16 @@ bool norm_shapes_ok(int64_t T, int64_t H) {
 // of one piece: E, 2 bytes a logit, then stays within the 256 MiB last-level
 // cache between the two products, and the fp32 sums of dX are read and written
 // once in n columns of work.  Without a gradient it is the blocks' cells and sums
-// that want an end, 8 bytes for 128 logits: 64 times as many take 512 MiB.
+// that want an end, 8 bytes for 128 logits: 64 times as many take 512 MiB.  Each part is
+// bounded by itself; in sum a call takes at most 521 MiB (E and dX's sums, 256 each), with
+// a weight that is written out 585 (E, the weight and 64 of dX's sums) and without a gradient
+// 769 (the blocks' sums and the weight).
 constexpr int64_t kHeadTokens = 4096, kHeadLogits = int64_t(1) << 27;
 // Up to here 4- and 8-bit weights are turned into bf16 on their way into the products;
 // for more rows, whose tiles each do that, they are written out first, a piece at a time.
 // Loss of 512 x 65536 x 4096: NF4 290 us and 356, 8 bits 275 and 370, with gradient 576 and
 // 640, 553 and 653; 1024 x 32000 x 4096: 283 and 267, 256 and 269, 541 and 486, 508 and 497.
+// (Where between the two the ways cross has not been measured.)
 constexpr int64_t kHeadCodesTokens = 512;
 // Weights of one piece that are written out in bf16.
 constexpr int64_t kHeadWeights = int64_t(1) << 27;

@@ -684,7 +684,8 @@ typedef struct {
  *   ws  workspace of ws_bytes >= qlora_head_workspace_bytes(T, vocab, hidden,
  *       expand, grad), expand: W is not bf16, grad: of the second call (scratch: no
  *       initialisation, nothing kept between calls; calls that overlap in time
- *       must not share one)
+ *       must not share one).  At any size at most 521 MiB for a bf16 head, 585 with a
+ *       gradient and 769 without one for the others
  * fp32 accumulation; the softmax's terms meet W in bf16, the label's own in fp32, so that
  * 1 - p of a row that is nearly sure keeps its digits.  A row with a logit of
  * +inf (finite ones: below 2^127) or NaN has a loss, lse and dX of NaN; a logit of -inf counts for nothing.
