@@ -1644,6 +1644,13 @@ int qlora_adamw_step(const qlora_adamw_table* table, int bits, void* m, void* v,
       !(rates->eps >= 0.) || !std::isfinite(rates->eps) || !(rates->beta1 >= 0. && rates->beta1 < 1.) ||
       !(rates->beta2 >= 0. && rates->beta2 < 1.))
     return QLORA_ERR_VALUE;
+  // what the kernel takes in fp32 has to be there: a rate of infinity, or an eps of 0 in the place of
+  // 1e-50, would make NaN of an element with a zero state
+  const double t = static_cast<double>(rates->step);
+  const float rate = static_cast<float>(rates->lr / (1. - std::pow(rates->beta1, t)));
+  const float decay = static_cast<float>(rates->lr * rates->weight_decay), eps = static_cast<float>(rates->eps);
+  if (!std::isfinite(rate) || !std::isfinite(decay) || !std::isfinite(eps) || (rates->eps > 0. && eps == 0.f))
+    return QLORA_ERR_VALUE;
   if (table->chunks == 0) return QLORA_OK;
   if (!table->table || !m || !v || (bits == 8 && (!m_scales || !v_scales))) return QLORA_ERR_NULL;
   if (!aligned16(table->table) || !aligned16(m) || !aligned16(v) ||
@@ -1654,7 +1661,6 @@ int qlora_adamw_step(const qlora_adamw_table* table, int bits, void* m, void* v,
                          adamw_range(m_scales, scales), adamw_range(v_scales, scales)};
   if (overlap(states, bits == 8 ? 4 : 2)) return QLORA_ERR_VALUE;
   if (int st = check_device()) return st;
-  const double t = static_cast<double>(rates->step);
   AdamStep a{};
   a.table = static_cast<const AdamChunk*>(table->table);
   a.chunks = table->chunks;
@@ -1667,10 +1673,10 @@ int qlora_adamw_step(const qlora_adamw_table* table, int bits, void* m, void* v,
   a.c1 = static_cast<float>(1. - rates->beta1);
   a.b2 = static_cast<float>(rates->beta2);
   a.c2 = static_cast<float>(1. - rates->beta2);
-  a.rate = static_cast<float>(rates->lr / (1. - std::pow(rates->beta1, t)));
+  a.rate = rate;
   a.root = static_cast<float>(1. / std::sqrt(1. - std::pow(rates->beta2, t)));
-  a.eps = static_cast<float>(rates->eps);
-  a.decay = static_cast<float>(rates->lr * rates->weight_decay);
+  a.eps = eps;
+  a.decay = decay;
   a.key = rates->seed;
   return launched(launch_adamw(a, bits == 8, static_cast<hipStream_t>(stream)));
 }

@@ -724,7 +724,7 @@ typedef struct {
 } qlora_adamw_table;
 
 typedef struct {
-  double lr, beta1, beta2, eps, weight_decay; /* 0 <= beta < 1, eps >= 0 */
+  double lr, beta1, beta2, eps, weight_decay; /* 0 <= beta < 1, eps >= 0; in fp32's range */
   int64_t step;                               /* from 1 on */
   uint32_t seed;                              /* of the 8-bit states' rounding */
 } qlora_adamw_rates;
@@ -767,6 +767,9 @@ int qlora_adamw_plan(const qlora_adamw_tensor* tensors, int64_t n, void* table, 
  * The numbers in rates are taken by value: a captured step repeats its t and seed.
  * Two steps of one plan must not overlap in time.  An element's result depends
  * on nothing but its own values and, in 8 bits, its block's.
+ * The kernel works in fp32: a square of g past its range is infinite.  Rates that
+ * have no finite fp32 value (lr / (1 - beta1^t), lr weight_decay, eps), and an eps above 0 that
+ * fp32 rounds to 0, are refused.
  * Errors: NULL, SHAPE, ALIGN, VALUE (bits, rates, states that share
  * memory), DEVICE, LAUNCH.
  */

@@ -310,3 +310,15 @@ def test_adamw_refusals(lib):
     assert step(table=Table(F, 3, -1)) == SHAPE
     assert step(table=Table(F, -1, 0)) == SHAPE and step(table=Table(F, 1 << 31, 0)) == SHAPE
     assert step(table=Table(F, 0, 0), m=None) == 0
+
+
+def test_adamw_rates_that_fp32_does_not_hold(lib):
+    def step(**r):
+        d = dict(lr=1e-3, beta1=.9, beta2=.999, eps=1e-8, weight_decay=0., step=1, seed=0)
+        d.update(r)
+        t = Table(F, 0, 0)  # no tensors: what is accepted ends here
+        return lib.qlora_adamw_step(ctypes.byref(t), 32, None, None, None, None, None, ctypes.byref(Rates(**d)), None)
+    assert step() == 0 and step(eps=0.) == 0 and step(eps=1e-45) == 0 and step(lr=0., weight_decay=1e30) == 0
+    assert step(eps=1e-46) == VALUE and step(eps=1e39) == VALUE
+    assert step(lr=1e38) == VALUE and step(lr=1e38, beta1=0.) == 0 and step(lr=1e38, step=1000) == 0
+    assert step(lr=1e20, weight_decay=-1e20) == VALUE and step(lr=-1e39, beta1=0.) == VALUE
