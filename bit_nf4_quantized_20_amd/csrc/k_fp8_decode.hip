@@ -113,6 +113,10 @@ __global__ __launch_bounds__(64 * kWaves, 2) void k_fp8_decode(DecodeF8 p) {
     return static_cast<int>(__builtin_amdgcn_raw_buffer_load_b8(
         rsrc(p.scales + static_cast<int64_t>(rows) * KB + b0, nb), lane, 0, 0));
   };
+  // Waits for this wave's reads of a stage, in front of the copies that overwrite it.  The
+  // matrix instructions that take what was read do not order the two: they touch no memory
+  // and may be issued behind the copies, whose data then land in rows still to be read.
+  auto reads_done = [&]() { __builtin_amdgcn_s_waitcnt(0xc07f); };  // lgkmcnt(0)
   int tile = blockIdx.x;
   int sw = load_s(tile);
   copy(tile, 0, s_w0);
@@ -157,7 +161,10 @@ __global__ __launch_bounds__(64 * kWaves, 2) void k_fp8_decode(DecodeF8 p) {
     const Acts& v = xa[i % kRing];
     if constexpr (kU)
       if (i % 2 == 0) {
-        if (i > 0) copy_a(i / 2);
+        if (i > 0) {
+          reads_done();
+          copy_a(i / 2);
+        }
         __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0): A's rows (and the first tile's codes) are in LDS
         __builtin_amdgcn_sched_barrier(0);
       }
@@ -238,6 +245,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void k_fp8_decode(DecodeF8 p) {
   auto chunk = [&](int t, auto cc, uint8_t* now, uint8_t* other) {
     constexpr int c = decltype(cc)::value;
     __builtin_amdgcn_sched_barrier(0);
+    reads_done();
     copy(c + 1 < NC ? t : t + step, c + 1 < NC ? c + 1 : 0, other);
     __builtin_amdgcn_sched_barrier(0);
     __builtin_amdgcn_s_waitcnt(0x0f78);  // vmcnt(8): all but the eight copies just issued have landed
