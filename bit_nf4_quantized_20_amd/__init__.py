@@ -980,7 +980,8 @@ def qlora_rmsnorm_fwd(x, weight, residual=None, eps: float = 1e-6, y16: bool = T
     """-> (y bf16 [T, H] or None, FP8Rows of y or None, h bf16 [T, H], rstd fp32
     [T]): h = bf16(x + residual) (x itself without one), rstd = 1 / sqrt(mean
     h^2 + eps), y = bf16(h rstd weight), weight fp32 [H].  y16, rows8: which
-    forms of y are wanted.  h may be x or residual."""
+    forms of y are wanted (up to 16 rows and 8192 columns the 8-bit layer reads y16
+    alone).  h may be x or residual."""
     T, H = _matrix(x, "x")
     dev = x.device
     _arg(x, torch.bfloat16, (T, H), "x", dev)

@@ -17,7 +17,10 @@ constexpr int64_t kHeadCus = 256;  // of the part; fixed, so that sizes depend o
 // Measured with one height throughout (64 / 128 / 192 / 256), gradient calls: 40 x 50021 x
 // 2304 136 / 140 / 146 / 150 us, 200 x 32000 x 4096 203 / 174 / 192 / 200, 301 x 50021 x
 // 2304 350 / 285 / 226 / 250, 1024 x 32000 x 4096 722 / 495 / 508 / 440.  (Of 4- and
-// 8-bit weights 64 rows have the tiles below, and with 224 the registers do not suffice.)
+// 8-bit weights 64 rows have the tiles below.  224 are left out: their kernels have up to
+// 118 vector registers too few, E W of 8 bits, and 24 to 43 in the logits.  Those of 256 have
+// 31 to 67 too few in the logits' epilogue, once a tile, and 7 in E W; the cost does not count
+// that, and the two have not been timed against each other.)
 constexpr int kHeights[] = {64, 96, 128, 160, 192, 224, 256};
 constexpr int64_t height_cost(int rows) { return 128 + rows; }
 constexpr bool height_fits(int rows, bool codes) { return !codes || (rows != 64 && rows != 224); }

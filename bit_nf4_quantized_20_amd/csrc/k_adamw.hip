@@ -24,6 +24,8 @@ namespace qlora {
 
 namespace {
 
+// Every bit of x spread over a word: two rounds of shift and odd factor and a last shift, with
+// Austin Appleby's published 32-bit constants (public domain).
 __host__ __device__ __forceinline__ uint32_t mix32(uint32_t x) {
   x ^= x >> 16;
   x *= 0x85ebca6bu;

@@ -16,8 +16,9 @@
 // the row's largest above 2^-64: what E loses is below 2^-62 of the largest.
 // Nearly all logits of a model are in cell 0; where a row's tiles differ,
 // k_head_rows scales its E, and what was accumulated before is scaled by the
-// next product.  (E's own rounding, 2^-9 of each term, is unbiased and stays
-// below dX's.)
+// next product.  (E's own rounding, up to 2^-8 of each term, is unbiased and over a whole
+// dX an eighth of dX's own, 2e-4 beside 1.7e-3; where one term is nearly all of a row's sum, it is
+// as large.  E W of 2^24 columns stays in fp32 for weights below 2^39.)
 //
 // k_head_logits (X W^T, weight rows as the matrix cores' first operand, then the
 // softmax's part in the epilogue) and k_head_grad (E W, the weight read
@@ -31,7 +32,9 @@
 // gradient of 301 x 50021 x 2304 204 us, of 4096 x 128000 x 4096 6.3 ms, 1360 TFLOP/s.  A
 // 256 x 256 tile takes 1.4 us a step of 64, 1.5 PFLOP/s, where the matrix cores on random
 // operands are bound by power, and 10 us in front of and behind its steps; with few rows HBM
-// or, of 4-bit weights, the vector unit bounds.
+// bounds or, of 4- and 8-bit weights, the codes' way to the products: through registers, put in
+// order, into LDS, past a barrier and out again (2.4 million weights of 4 bits a us; k_decode_stream,
+// which has none of that, reaches 5.3).
 #include <type_traits>
 
 #include "common.hpp"

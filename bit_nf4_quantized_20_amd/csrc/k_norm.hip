@@ -7,8 +7,8 @@
 // Both are one pass over their rows and bound by HBM: a row stays in the
 // registers of the L lanes that share it (C chunks of eight columns each), so
 // nothing is read twice.  8192 rows of 8192 with residual, sum, y and codes: 604 MB
-// in 106.5 us, 5.7 TB/s; the gradient of 8192 rows of 4096 with dres and dw: 268 MB in
-// 46.5 us, 5.8 TB/s, and 4.8 us of k_norm_dw (a 2 GiB copy reaches 4.8 TB/s).
+// in 104 to 106 us, 5.7 TB/s; the gradient of 8192 rows of 4096 with dres and dw: 268 MB in
+// 45 us, 6.0 TB/s, and 4.9 us of k_norm_dw (a 2 GiB copy reaches 4.8 TB/s, HBM's peak is 8).
 #include <type_traits>
 
 #include "common.hpp"
@@ -39,8 +39,8 @@ __device__ __forceinline__ T row_sum(T v, T (*red)[8], int parity) {
 
 // Rows are read once and, in the forward pass, written without being kept in
 // front of what the caches hold: 8192 rows of 8192 with residual and codes take
-// 108 us so and 117 with ordinary loads and stores, the gradient of 8192 rows of
-// 4096 51.3 and 53.6.  The gradient's own stores are ordinary ones (57 us if not).
+// 8% less time so than with ordinary loads and stores, the gradient of 8192 rows of
+// 4096 4% less.  The gradient's own stores are ordinary ones (11% more if not).
 __device__ __forceinline__ u32x4 row_load(const uint16_t* p) {
   return __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
 }
@@ -315,9 +315,9 @@ hipError_t with_shape(int64_t H, F f) {
 }
 
 // Workgroups of 256 threads.  Forward: one turn each up to 16384 of them (8192 x
-// 8192: 105.7 us, with eight workgroups a CU that go round 108).  Gradient: each
-// leaves H floats for dw, so two a CU (8192 x 4096: 51.3 us; 384 of them 52.6, 640
-// 55.3).
+// 8192: 2% less time than with eight workgroups a CU that go round).  Gradient: each
+// leaves H floats for dw, so two a CU (8192 x 4096: 384 of them take 3% more, 640
+// 8%).
 constexpr int64_t kNormFwdWgs = 16384;
 constexpr int64_t kNormBwdWgs = 512;
 

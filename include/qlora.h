@@ -624,7 +624,8 @@ int qlora_moe_fwd(const qlora_nf4_weight* gate_up, const qlora_nf4_weight* down,
  *                                        the argument h must be NULL)
  *   rstd = 1 / sqrt(mean h^2 + eps)      [T] fp32 (any alignment of a float), or NULL
  *   y    = bf16(h rstd weight)           [T, H] bf16, or NULL with codes
- *   codes, scales: y as quantized rows (above), or both NULL
+ *   codes, scales: y as quantized rows (above), or both NULL (for T <= 16 and H <= 8192 the
+ *                                        8-bit layer reads y itself and no codes)
  *   x, residual [T, H] bf16;  weight [H] fp32;  eps >= 0
  *   H a multiple of 64, 64 .. 16384;  0 <= T < 2^31 (0 is a no-op)
  * h may be x or residual themselves; otherwise outputs are apart from inputs.  The
@@ -674,7 +675,7 @@ typedef struct {
  *   loss [T] fp32 = lse - logit[label];   lse [T] fp32 = log sum exp logits, or NULL
  * qlora_head_loss_grad -- the same, and the gradient of X for dloss [T] fp32, the
  * gradient of each row's loss:
- *   dX [T, hidden] bf16 = dloss (softmax(logits) W - W_label), one rounding
+ *   dX [T, hidden] bf16 = dloss (softmax(logits) W - W_label)
  * The logits are formed once for both.  W is frozen and has no gradient.
  *   X [T, hidden] bf16;  labels [T] int64: a label outside [0, vocab) is none (a
  *   prompt, a padded row): loss 0 and a dX row of zeros, whatever the row holds
@@ -686,8 +687,9 @@ typedef struct {
  *       initialisation, nothing kept between calls; calls that overlap in time
  *       must not share one).  At any size at most 521 MiB for a bf16 head, 585 with a
  *       gradient and 769 without one for the others
- * fp32 accumulation; the softmax's terms meet W in bf16, the label's own in fp32, so that
- * 1 - p of a row that is nearly sure keeps its digits.  A row with a logit of
+ * fp32 accumulation; the softmax's terms meet W in bf16 (each rounded by up to 2^-8 of
+ * itself, dX once more), the label's own in fp32, so that 1 - p of a row that is nearly sure keeps
+ * its digits.  A row with a logit of
  * +inf (finite ones: below 2^127) or NaN has a loss, lse and dX of NaN; a logit of -inf counts for nothing.
  * With a gradient |W| below 2^39: a term, before it is divided by their sum, is at most
  * 2^64 |W|, and up to 2^24 of them are added in fp32 (an infinite weight: NaN in its column of dX).

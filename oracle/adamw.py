@@ -16,7 +16,8 @@ def step(p, g, m, v, t, lr, b1, b2, eps, wd):
 
 
 def mix32(x):
-    """Two rounds of shift and odd factor, which spread every bit over a word, on uint32 arrays."""
+    """Two rounds of shift and odd factor, which spread every bit over a word, on uint32 arrays
+    (the constants: Austin Appleby's published 32-bit ones, public domain)."""
     x = np.asarray(x, dtype=np.uint32)
     x = (x ^ (x >> np.uint32(16))) * np.uint32(0x85EBCA6B)
     x = (x ^ (x >> np.uint32(13))) * np.uint32(0xC2B2AE35)
