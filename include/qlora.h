@@ -630,7 +630,7 @@ int qlora_moe_fwd(const qlora_nf4_weight* gate_up, const qlora_nf4_weight* down,
  *   H a multiple of 64, 64 .. 16384;  0 <= T < 2^31 (0 is a no-op)
  * h may be x or residual themselves; otherwise outputs are apart from inputs.  The
  * square sums are held in 64 bits, so that any finite h is in range (an rstd past fp32's
- * largest, of eps = 0 and a mean h^2 below 2^-256, is infinite and its y NaN).  A row that
+ * largest, of eps = 0 and a mean h^2 below 2^-256, is infinite and its y is not finite).  A row that
  * holds an infinity or a NaN has a y of NaN where the formula says so; the other
  * rows do not change.
  * Errors: NULL, SHAPE, ALIGN, VALUE, DEVICE, LAUNCH.
